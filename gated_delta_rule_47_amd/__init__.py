@@ -22,7 +22,9 @@ __all__ = ["KdaError", "read_scale", "gate", "chunk_fwd", "chunk_fwd_scalar", "c
            "chunk_fwd_norm_workspace_bytes", "recurrent_step", "recurrent_step_scalar", "chunk_bwd",
            "chunk_bwd_workspace_bytes", "gate_bwd", "gate_bwd_workspace_bytes", "gate_bwd_noalloc",
            "GATE_BWD_SCRATCH_BYTES", "counters", "status_string",
-           "library_path"]
+           "library_path", "decay_attn_workspace_bytes", "decay_attn_fwd", "decay_attn_step",
+           "decay_attn_bwd_workspace_bytes", "decay_attn_bwd", "layer_norm_fwd", "layer_norm_bwd_workspace_bytes",
+           "layer_norm_bwd", "ckpt_pack", "ckpt_unpack"]
 
 
 class KdaError(RuntimeError):
@@ -357,3 +359,9 @@ def gate_bwd_noalloc(z, A_log, dt_bias, dg, dz_out=None, dA_out=None, ddb_out=No
     _call("kda_gate_bwd_noalloc", _ptr(z), _ptr(A_log), _ptr(dt_bias), _ptr(dg), _ptr(dz), _ptr(dA), _ptr(ddb),
           B, H, T, K, _dtype_code(z), _stream(dev))
     return dz, dA, ddb
+
+
+# Operators that stand beside the delta rule in a layer (they use the helpers above).
+from .layer_ops import (ckpt_pack, ckpt_unpack, decay_attn_bwd, decay_attn_bwd_workspace_bytes,  # noqa: E402
+                        decay_attn_fwd, decay_attn_step, decay_attn_workspace_bytes, layer_norm_bwd,
+                        layer_norm_bwd_workspace_bytes, layer_norm_fwd)

@@ -15,6 +15,9 @@ EXPORTED = ("kda_read_scale", "kda_gate", "kda_chunk_fwd_workspace_bytes", "kda_
             "kda_chunk_fwd_status", "kda_set_exchange_timeout_us", "kda_recurrent_step",
             "kda_recurrent_step_scalar",
             "kda_chunk_bwd_workspace_bytes", "kda_chunk_bwd", "kda_gate_bwd_workspace_bytes", "kda_gate_bwd", "kda_gate_bwd_noalloc", "kda_chunk_fwd_norm_workspace_bytes", "kda_chunk_fwd_norm",
+            "kda_decay_attn_workspace_bytes", "kda_decay_attn_fwd", "kda_decay_attn_step",
+            "kda_decay_attn_bwd_workspace_bytes", "kda_decay_attn_bwd", "kda_layer_norm_fwd",
+            "kda_layer_norm_bwd_workspace_bytes", "kda_layer_norm_bwd", "kda_ckpt_pack", "kda_ckpt_unpack",
             "kda_status_string", "kda_get_counters")
 
 _lib = None
@@ -23,6 +26,7 @@ _p = ctypes.c_void_p
 _i = ctypes.c_int
 _f = ctypes.c_float
 _sz = ctypes.c_size_t
+_ll = ctypes.c_longlong
 
 _PROTOS = {
     "kda_read_scale": (_f, [_i]),
@@ -44,6 +48,17 @@ _PROTOS = {
     "kda_gate_bwd_workspace_bytes": (_sz, [_i, _i, _i, _i]),
     "kda_gate_bwd": (_i, [_p, _p, _p, _p, _p, _p, _p, _p, _sz, _i, _i, _i, _i, _i, _p]),
     "kda_gate_bwd_noalloc": (_i, [_p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _p]),
+    "kda_decay_attn_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i]),
+    "kda_decay_attn_fwd": (_i, [_p, _p, _p, _p, _p, _p, _f, _p, _p, _p, _sz, _i, _i, _i, _i, _i, _i, _p]),
+    "kda_decay_attn_step": (_i, [_p, _p, _p, _p, _p, _f, _p, _i, _i, _i, _i, _i, _p]),
+    "kda_decay_attn_bwd_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i]),
+    "kda_decay_attn_bwd": (_i, [_p, _p, _p, _p, _p, _p, _p, _p, _p, _f, _p, _p, _p, _p, _p, _p, _p, _sz,
+                                _i, _i, _i, _i, _i, _i, _p]),
+    "kda_layer_norm_fwd": (_i, [_p, _p, _p, _f, _p, _p, _p, _i, _i, _i, _i, _i, _p]),
+    "kda_layer_norm_bwd_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
+    "kda_layer_norm_bwd": (_i, [_p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _sz, _i, _i, _i, _i, _i, _p]),
+    "kda_ckpt_pack": (_i, [_p, _p, _p, _ll, _i, _i, _p]),
+    "kda_ckpt_unpack": (_i, [_p, _p, _p, _ll, _i, _i, _p]),
     "kda_status_string": (ctypes.c_char_p, [_i]),
     "kda_get_counters": (_i, [ctypes.POINTER(ctypes.c_ulonglong), _i]),
 }

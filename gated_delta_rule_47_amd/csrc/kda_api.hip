@@ -11,10 +11,11 @@ namespace kda {
 
 static std::atomic<unsigned long long> g_counters[KDA_NUM_COUNTERS];
 
-static int reject(int status) {
+int reject(int status) {
   g_counters[KDA_COUNTER_REJECTED].fetch_add(1, std::memory_order_relaxed);
   return status;
 }
+void count_call(int counter) { g_counters[counter].fetch_add(1, std::memory_order_relaxed); }
 
 // Bound of every wait for the partner workgroup, in 100 MHz real-time ticks (1 s).
 static std::atomic<unsigned long long> g_spin_ticks{100000000ull};

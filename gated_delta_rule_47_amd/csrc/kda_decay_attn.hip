@@ -1,0 +1,240 @@
+// Decay attention: the plan of segments, the join of the segments' states, the single-token step and
+// the sequences of launches behind kda_decay_attn_fwd / _bwd (the walk itself: kda_decay_attn.h).
+#include "kda_decay_attn.h"
+#include "kda_launch.h"
+
+namespace kda {
+
+// ------------------------------------------------------------------ segments
+// A walk is sequential over its chunks, so heads x value tiles alone may leave most of the 256 CUs
+// idle; then the tokens are cut into segments.  The price is a second read of k and v (the segments'
+// local states), so no more segments are taken than fill the chip once, and none under 4 chunks.
+DecayPlan decay_plan(int B, int H, int T, int K, int V, bool bf16) {
+  const int C = bf16 ? 64 : 32;
+  const long long wgs = (long long)B * H * ((V + 63) / 64);
+  const int nchunks = (T + C - 1) / C;
+  const long long fill = 256;
+  long long n = (fill + wgs - 1) / wgs;
+  if (n > nchunks / 4) n = nchunks / 4;
+  if (n < 1) n = 1;
+  DecayPlan p;
+  const int per = (nchunks + (int)n - 1) / (int)n;
+  p.seglen = (per < 1 ? 1 : per) * C;
+  p.nseg = nchunks ? (nchunks + per - 1) / per : 1;
+  return p;
+}
+
+size_t decay_states_bytes(int B, int H, int K, int V, const DecayPlan& p) {
+  return p.nseg > 1 ? (size_t)B * H * p.nseg * K * V * sizeof(float) : 0;
+}
+
+// Local end states -> states at the segments' starts, in place and in walking order:
+// x[s] <- S, S <- a^{n_s} S + (old x[s]).  One thread per state element; the locals of eight
+// segments are fetched before they are used, so the latency of memory is paid once in eight.
+template <bool REV>
+__global__ void __launch_bounds__(256) decay_join_kernel(float* __restrict__ x, const float* __restrict__ state_in,
+                                                         const float* __restrict__ log_decay,
+                                                         const int* __restrict__ lengths, int H, int T, int nseg,
+                                                         int seglen, int KV, int per_head) {
+  constexpr int BATCH = 8;
+  const int bh = blockIdx.x / per_head, e = (blockIdx.x - bh * per_head) * 256 + threadIdx.x;
+  if (e >= KV) return;
+  int len = T;
+  if (lengths) len = min(max(lengths[bh / H], 0), T);
+  const float g = log_decay[bh % H];
+  float* p = x + (size_t)bh * nseg * KV + e;
+  float S = state_in ? state_in[(size_t)bh * KV + e] : 0.0f;
+  const Decay2 whole = decay_pow2(g, seglen);
+  for (int s0 = 0; s0 < nseg; s0 += BATCH) {
+    float loc[BATCH];
+#pragma unroll
+    for (int b = 0; b < BATCH; ++b) {
+      const int s = s0 + b, seg = REV ? nseg - 1 - s : s;
+      loc[b] = s < nseg - 1 ? p[(size_t)seg * KV] : 0.0f;    // the last one has no local state
+    }
+#pragma unroll
+    for (int b = 0; b < BATCH; ++b) {
+      const int s = s0 + b, seg = REV ? nseg - 1 - s : s;
+      if (s < nseg) {
+        p[(size_t)seg * KV] = S;
+        const long long left = (long long)len - (long long)seg * seglen;
+        const int n = left < 0 ? 0 : (left < seglen ? (int)left : seglen);
+        const Decay2 d = n == seglen ? whole : decay_pow2(g, n);
+        S = fmaf(S, d.hi, fmaf(S, d.lo, loc[b]));
+      }
+    }
+  }
+}
+
+static hipError_t join(bool rev, float* x, const float* state_in, const float* log_decay, const int* lengths, int B,
+                       int H, int T, int KV, const DecayPlan& p, hipStream_t s) {
+  const int per_head = (KV + 255) / 256;
+  const dim3 grid((unsigned)(B * H * per_head));
+  if (rev)
+    hipLaunchKernelGGL(decay_join_kernel<true>, grid, dim3(256), 0, s, x, state_in, log_decay, lengths, H, T, p.nseg,
+                       p.seglen, KV, per_head);
+  else
+    hipLaunchKernelGGL(decay_join_kernel<false>, grid, dim3(256), 0, s, x, state_in, log_decay, lengths, H, T, p.nseg,
+                       p.seglen, KV, per_head);
+  return hipGetLastError();
+}
+
+template <typename T> static hipError_t walk(const WalkArgs& a, bool rev, hipStream_t s) {
+  const bool pk = a.q_sc || a.k_sc || a.v_sc;
+  if (a.K <= 32) return pk ? launch_walk_kd<T, 32, true>(a, rev, s) : launch_walk_kd<T, 32, false>(a, rev, s);
+  if (a.K <= 64) return pk ? launch_walk_kd<T, 64, true>(a, rev, s) : launch_walk_kd<T, 64, false>(a, rev, s);
+  return pk ? launch_walk_kd<T, 128, true>(a, rev, s) : launch_walk_kd<T, 128, false>(a, rev, s);
+}
+template <typename T> static hipError_t segments(const SegArgs& a, bool rev, hipStream_t s) {
+  const bool pk = a.k_sc || a.v_sc;
+  if (a.K <= 32) return pk ? launch_segments_kd<T, 32, true>(a, rev, s) : launch_segments_kd<T, 32, false>(a, rev, s);
+  if (a.K <= 64) return pk ? launch_segments_kd<T, 64, true>(a, rev, s) : launch_segments_kd<T, 64, false>(a, rev, s);
+  return pk ? launch_segments_kd<T, 128, true>(a, rev, s) : launch_segments_kd<T, 128, false>(a, rev, s);
+}
+
+template <typename T>
+hipError_t launch_decay_fwd(const void* q, const void* k, const void* v, const float* log_decay, const int* lengths,
+                            const float* state_in, float scale, void* o, float* state_out, void* workspace, int B,
+                            int H, int T_, int K, int V, hipStream_t s) {
+  const DecayPlan p = decay_plan(B, H, T_, K, V, sizeof(T) == 2);
+  float* ws = reinterpret_cast<float*>(workspace);
+  if (p.nseg > 1) {
+    const SegArgs g{k, v, nullptr, nullptr, log_decay, lengths, ws, 1.0f, B * H, H, T_, K, V, p.nseg, p.seglen};
+    hipError_t e = segments<T>(g, false, s);
+    if (e == hipSuccess) e = join(false, ws, state_in, log_decay, lengths, B, H, T_, K * V, p, s);
+    if (e != hipSuccess) return e;
+  }
+  WalkArgs a{};
+  a.q = q, a.k = k, a.v = v;
+  a.log_decay = log_decay, a.lengths = lengths, a.state_in = state_in, a.seg_state = ws, a.state_out = state_out;
+  a.o = o;
+  a.c = a.r = scale, a.u = 1.0f;
+  a.si_k = V, a.si_v = 1;
+  a.BH = B * H, a.H = H, a.T = T_, a.K = K, a.V = V, a.nseg = p.nseg, a.seglen = p.seglen;
+  return walk<T>(a, false, s);
+}
+
+// Segment boundaries and states are those of the K x V state in all three walks: S for dq, R = dL/dS
+// for dk and dv, each computed and joined once.
+template <typename T>
+hipError_t launch_decay_bwd(const void* q, const void* k, const void* v, const uint8_t* q_sc, const uint8_t* k_sc,
+                            const uint8_t* v_sc, const float* log_decay, const int* lengths, const float* state_in,
+                            float scale, const void* d_o, const float* d_state_out, void* dq, void* dk, void* dv,
+                            float* dstate_in, void* workspace, int B, int H, int T_, int K, int V, hipStream_t s) {
+  const DecayPlan p = decay_plan(B, H, T_, K, V, sizeof(T) == 2);
+  float* wS = reinterpret_cast<float*>(workspace);
+  float* wR = wS + decay_states_bytes(B, H, K, V, p) / sizeof(float);
+  hipError_t e = hipSuccess;
+  if (p.nseg > 1) {
+    SegArgs g{k, v, k_sc, v_sc, log_decay, lengths, wS, 1.0f, B * H, H, T_, K, V, p.nseg, p.seglen};
+    e = segments<T>(g, false, s);
+    if (e == hipSuccess) e = join(false, wS, state_in, log_decay, lengths, B, H, T_, K * V, p, s);
+    g = SegArgs{q, d_o, q_sc, nullptr, log_decay, lengths, wR, scale, B * H, H, T_, K, V, p.nseg, p.seglen};
+    if (e == hipSuccess) e = segments<T>(g, true, s);
+    if (e == hipSuccess) e = join(true, wR, d_state_out, log_decay, lengths, B, H, T_, K * V, p, s);
+  }
+  WalkArgs a{};
+  a.log_decay = log_decay, a.lengths = lengths;
+  a.BH = B * H, a.H = H, a.T = T_, a.nseg = p.nseg, a.seglen = p.seglen, a.zero_tail = lengths != nullptr;
+  // dq: width V keys, width K values, the state read as its transpose
+  a.q = d_o, a.k = v, a.v = k, a.q_sc = nullptr, a.k_sc = v_sc, a.v_sc = k_sc;
+  a.state_in = state_in, a.seg_state = wS, a.state_out = nullptr, a.o = dq;
+  a.c = a.r = scale, a.u = 1.0f;
+  a.si_k = 1, a.si_v = V, a.K = V, a.V = K;
+  if (e == hipSuccess) e = walk<T>(a, false, s);
+  // dk
+  a.q = v, a.k = d_o, a.v = q, a.q_sc = v_sc, a.k_sc = nullptr, a.v_sc = q_sc;
+  a.state_in = d_state_out, a.seg_state = wR, a.o = dk;
+  a.c = a.u = scale, a.r = 1.0f;
+  if (e == hipSuccess) e = walk<T>(a, true, s);
+  // dv, and the state's gradient
+  a.q = k, a.k = q, a.v = d_o, a.q_sc = k_sc, a.k_sc = q_sc, a.v_sc = nullptr;
+  a.state_out = dstate_in, a.o = dv;
+  a.si_k = V, a.si_v = 1, a.K = K, a.V = V;
+  if (e == hipSuccess) e = walk<T>(a, true, s);
+  return e;
+}
+
+// ------------------------------------------------------------------ one token
+// S <- a S + k v^T and o = scale S^T q for one token per head.  Bound by the state's traffic (2 K V
+// fp32 per head): a thread holds four columns (one 16-byte access) of K / RG rows, all loaded before
+// the first is used; the RG partial sums of a column meet in LDS.  VS columns per workgroup.
+template <typename T, int VS>
+__global__ void __launch_bounds__(256) decay_step_kernel(const T* __restrict__ q, const T* __restrict__ k,
+                                                         const T* __restrict__ v,
+                                                         const float* __restrict__ log_decay,
+                                                         float* __restrict__ state, float scale, T* __restrict__ o,
+                                                         int H, int K, int V) {
+  constexpr int LC = VS / 4, RG = 256 / LC, MAXR = (128 + RG - 1) / RG;
+  __shared__ float sq[128], sk[128];
+  __shared__ __align__(16) float red[RG * VS];
+  const int ntile = V / VS;
+  const int bh = blockIdx.x / ntile, v0 = (blockIdx.x - bh * ntile) * VS;
+  const int tid = threadIdx.x, c = tid % LC, rg = tid / LC;
+  float* S = state + (size_t)bh * K * V + v0 + 4 * c;
+  floatx4 s[MAXR];
+#pragma unroll
+  for (int i = 0; i < MAXR; ++i) {
+    const int row = rg + i * RG;
+    if (row < K) s[i] = *reinterpret_cast<const floatx4*>(S + (size_t)row * V);
+  }
+  if (tid < K) {
+    sq[tid] = to_f<T>(q[(size_t)bh * K + tid]);
+    sk[tid] = to_f<T>(k[(size_t)bh * K + tid]);
+  }
+  const float a = expf(log_decay[bh % H]);
+  const T* vp = v + (size_t)bh * V + v0 + 4 * c;
+  const floatx4 vv = {to_f<T>(vp[0]), to_f<T>(vp[1]), to_f<T>(vp[2]), to_f<T>(vp[3])};
+  lds_barrier();
+  floatx4 sum = zero4();
+#pragma unroll
+  for (int i = 0; i < MAXR; ++i) {
+    const int row = rg + i * RG;
+    if (row < K) {
+      const float kr = sk[row], qr = sq[row];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s[i][e] = fmaf(a, s[i][e], kr * vv[e]);
+        sum[e] = fmaf(qr, s[i][e], sum[e]);
+      }
+      *reinterpret_cast<floatx4*>(S + (size_t)row * V) = s[i];
+    }
+  }
+  *reinterpret_cast<floatx4*>(red + rg * VS + 4 * c) = sum;
+  lds_barrier();
+  if (tid < VS) {
+    float x = 0.0f;
+#pragma unroll
+    for (int r = 0; r < RG; ++r) x += red[r * VS + tid];
+    o[(size_t)bh * V + v0 + tid] = from_f<T>(scale * x);
+  }
+}
+
+template <typename T>
+hipError_t launch_decay_step(const void* q, const void* k, const void* v, const float* log_decay, float* state,
+                             float scale, void* o, int B, int H, int K, int V, hipStream_t s) {
+#define KDA_DECAY_STEP(VS)                                                                                          \
+  hipLaunchKernelGGL((decay_step_kernel<T, VS>), dim3((unsigned)(B * H * (V / VS))), dim3(256), 0, s, (const T*)q,  \
+                     (const T*)k, (const T*)v, log_decay, state, scale, (T*)o, H, K, V)
+  if (V >= 32) KDA_DECAY_STEP(32);
+  else if (V == 16) KDA_DECAY_STEP(16);
+  else KDA_DECAY_STEP(8);
+#undef KDA_DECAY_STEP
+  return hipGetLastError();
+}
+
+#define KDA_INST(T)                                                                                                  \
+  template hipError_t launch_decay_fwd<T>(const void*, const void*, const void*, const float*, const int*,           \
+                                          const float*, float, void*, float*, void*, int, int, int, int, int,        \
+                                          hipStream_t);                                                              \
+  template hipError_t launch_decay_bwd<T>(const void*, const void*, const void*, const uint8_t*, const uint8_t*,     \
+                                          const uint8_t*, const float*, const int*, const float*, float,             \
+                                          const void*, const float*, void*, void*, void*, float*, void*, int, int,   \
+                                          int, int, int, hipStream_t);                                               \
+  template hipError_t launch_decay_step<T>(const void*, const void*, const void*, const float*, float*, float,       \
+                                           void*, int, int, int, int, hipStream_t);
+KDA_INST(float)
+KDA_INST(bf16_t)
+#undef KDA_INST
+
+}  // namespace kda

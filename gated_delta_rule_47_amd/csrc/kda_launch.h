@@ -79,5 +79,45 @@ hipError_t launch_chunk_bwd_mfma(const float* q, const float* k, const float* v,
                                  float* dg, float* dbeta, float* dstate_in, void* workspace, int B, int H, int T,
                                  int K, int V, hipStream_t s);
 
+// Linear attention with a constant decay per head (kda_decay_attn.hip).  The tokens are walked in nseg
+// segments of seglen tokens; nseg > 1 needs the segments' states in a workspace (two of them backward).
+struct DecayPlan {
+  int nseg, seglen;
+};
+DecayPlan decay_plan(int B, int H, int T, int K, int V, bool bf16);
+size_t decay_states_bytes(int B, int H, int K, int V, const DecayPlan& p);
+template <typename T>
+hipError_t launch_decay_fwd(const void* q, const void* k, const void* v, const float* log_decay, const int* lengths,
+                            const float* state_in, float scale, void* o, float* state_out, void* workspace, int B,
+                            int H, int T_, int K, int V, hipStream_t s);
+template <typename T>
+hipError_t launch_decay_bwd(const void* q, const void* k, const void* v, const uint8_t* q_sc, const uint8_t* k_sc,
+                            const uint8_t* v_sc, const float* log_decay, const int* lengths, const float* state_in,
+                            float scale, const void* d_o, const float* d_state_out, void* dq, void* dk, void* dv,
+                            float* dstate_in, void* workspace, int B, int H, int T_, int K, int V, hipStream_t s);
+template <typename T>
+hipError_t launch_decay_step(const void* q, const void* k, const void* v, const float* log_decay, float* state,
+                             float scale, void* o, int B, int H, int K, int V, hipStream_t s);
+
+// Layer norm (kda_layer_norm.hip); x_scales non-null: x holds 8-bit codes.
+template <typename T>
+hipError_t launch_norm_fwd(const void* x, const float* w, const float* b, float eps, void* y, float* mean, float* rstd,
+                           int B, int H, int T_, int D, hipStream_t s);
+size_t norm_bwd_workspace_bytes(int B, int H, int T, int D, bool bf16);
+template <typename T>
+hipError_t launch_norm_bwd(const void* x, const uint8_t* x_scales, const float* w, const float* mean,
+                           const float* rstd, const void* dy, void* dx, float* dw, float* db, void* workspace, int B,
+                           int H, int T_, int D, hipStream_t s);
+
+// 8-bit activations (kda_ckpt.hip).
+template <typename T>
+hipError_t launch_ckpt_pack(const void* x, uint8_t* codes, uint8_t* scales, long long rows, int D, hipStream_t s);
+template <typename T>
+hipError_t launch_ckpt_unpack(const uint8_t* codes, const uint8_t* scales, void* x, long long rows, int D,
+                              hipStream_t s);
+
+// Counters of kda_api.hip: a rejected call (returns its status), an accepted one.
+int reject(int status);
+void count_call(int counter);
 
 }  // namespace kda

@@ -280,12 +280,118 @@ int kda_gate_bwd_noalloc(const void* z, const float* A_log, const float* dt_bias
                          float* dz, float* dA_log, float* d_dt_bias,
                          int B, int H, int T, int K, int dtype, void* stream);
 
+/* ---------------------------------------------------------------------------------
+ * Linear attention with a constant decay per head: the same state and read without the
+ * delta rule, for layers whose decay is a fixed slope of the head.  With a = exp(log_decay[h]),
+ *   S_t = a S_{t-1} + k_t v_t^T,   o_t = scale * S_t^T q_t
+ * Layouts, sizes (K, V in {8, 16, 32, 64, 128}; B, H >= 1; T >= 0; B * H <= 2^24), streams and
+ * errors are those of this file's conventions; `dtype` is the type of q, k, v, o, d_o and of the
+ * gradients dq, dk, dv (which the projections' own backward takes in that type); states and their
+ * gradients are float32.
+ *   log_decay (H) float32, <= 0 (not checked: it lives on the device); 0 keeps everything, -inf keeps
+ *             the last token only.  It is a constant of the model: its gradient is not computed
+ *             (kda_chunk_fwd is the operator with a learned decay).
+ *   lengths   (B) int32 on the device, or NULL (every sequence has T tokens): sequence b ends before
+ *             token lengths[b], clamped to 0..T.  Tokens behind it are not read; their rows of o stay
+ *             as they were, their rows of dq, dk and dv become zero, and the final state is the one
+ *             after the last token (state_in for an empty sequence).
+ *   q, k, v, o, d_o, dq, dk, dv must be 16-byte aligned (KDA_ERR_ALIGN), and
+ *             (T + 64) * max(K, V) * element size < 2^31 (KDA_ERR_SHAPE).
+ * KDA_F32 products run on fp32 MFMA.  KDA_BF16 products run on bf16 MFMA with fp32 accumulation: the
+ * scores of a block of 64 tokens and the state as the read sees it are rounded to bf16 once; the
+ * carried state is not (fp32, its products in two bf16 parts).  Results equal the token recurrence up
+ * to those roundings.  A non-finite value in a token can reach every output of its block of tokens. */
+
+/* Bytes of device workspace kda_decay_attn_fwd needs for these sizes: nonzero where B * H heads alone
+ * do not fill the GPU and the tokens are walked in segments; 0 otherwise or on bad sizes. */
+size_t kda_decay_attn_workspace_bytes(int B, int H, int T, int K, int V, int dtype);
+
+/* Prompts (chunked form).
+ *   q, k (B,H,T,K), v (B,H,T,V), o (B,H,T,V); state_in (B,H,K,V) f32 or NULL (= 0)
+ *   state_out (B,H,K,V) f32 or NULL (not written); may equal state_in
+ *   workspace  kda_decay_attn_workspace_bytes() bytes, 256-byte aligned (NULL when that is 0); contents
+ *              on entry ignored; two calls in flight at once must not share one.
+ * o and state_out must not overlap an input, each other or the workspace. */
+int kda_decay_attn_fwd(const void* q, const void* k, const void* v, const float* log_decay, const int* lengths,
+                       const float* state_in, float scale, void* o, float* state_out,
+                       void* workspace, size_t workspace_bytes,
+                       int B, int H, int T, int K, int V, int dtype, void* stream);
+
+/* One token: q, k (B,H,K), v (B,H,V), o (B,H,V), state (B,H,K,V) f32 updated in place.  o must not
+ * overlap an input.  state and v must be 16-byte aligned. */
+int kda_decay_attn_step(const void* q, const void* k, const void* v, const float* log_decay, float* state,
+                        float scale, void* o, int B, int H, int K, int V, int dtype, void* stream);
+
+/* Bytes of device workspace kda_decay_attn_bwd needs for these sizes (may be 0). */
+size_t kda_decay_attn_bwd_workspace_bytes(int B, int H, int T, int K, int V, int dtype);
+
+/* Adjoint of kda_decay_attn_fwd for L = sum(o * d_o) + sum(state_out * d_state_out).  With
+ * R_t = dL/dS_t = a R_{t+1} + scale q_t d_o_t^T:
+ *   dq_t = scale S_t d_o_t,  dk_t = R_t v_t,  dv_t = R_t^T k_t,  dstate_in = a R_0
+ * Inputs as the forward's, d_o (B,H,T,V) in `dtype`, d_state_out (B,H,K,V) f32 or NULL (= 0).
+ *   q_scales, k_scales, v_scales: NULL for tensors in `dtype`; otherwise that tensor is kept in 8 bits
+ *   as kda_ckpt_pack writes it (q holds the codes, 8-byte aligned, q_scales the scale bytes) and is
+ *   read as the values it stands for.
+ * dq, dk, dv in `dtype`, dstate_in f32; no output may overlap an input, another output or the
+ * workspace (256-byte aligned, contents on entry ignored). */
+int kda_decay_attn_bwd(const void* q, const void* k, const void* v, const unsigned char* q_scales,
+                       const unsigned char* k_scales, const unsigned char* v_scales, const float* log_decay,
+                       const int* lengths, const float* state_in, float scale, const void* d_o,
+                       const float* d_state_out, void* dq, void* dk, void* dv, float* dstate_in,
+                       void* workspace, size_t workspace_bytes,
+                       int B, int H, int T, int K, int V, int dtype, void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * Layer norm over the last axis of x (B,H,T,D) with one weight and bias row per head (H = 1: rows of a
+ * whole layer), as the read of a linear-attention layer is normalised:
+ *   y = (x - mean) * rstd * weight[h] + bias[h],   rstd = (mean((x - mean)^2) + eps)^-1/2
+ *   x, y (B,H,T,D) in `dtype`, aligned to an element (rows that are 16-byte aligned run fastest)
+ *   weight, bias (H,D) f32, NULL = ones / zeros;  mean, rstd (B,H,T) f32, NULL = not written
+ *   eps >= 0 and finite (KDA_ERR_SHAPE otherwise);  D >= 1;  T >= 0;  B * H * T < 2^31
+ * Statistics are taken in float32 in two passes over the row.  y must not overlap an input. */
+int kda_layer_norm_fwd(const void* x, const float* weight, const float* bias, float eps, void* y, float* mean,
+                       float* rstd, int B, int H, int T, int D, int dtype, void* stream);
+
+/* Bytes of device workspace kda_layer_norm_bwd needs for these sizes when dweight or dbias is asked for
+ * (0 when T = 0 or on bad sizes). */
+size_t kda_layer_norm_bwd_workspace_bytes(int B, int H, int T, int D, int dtype);
+
+/* Adjoint of kda_layer_norm_fwd for a cotangent dy (B,H,T,D) in `dtype` on y, from the forward's mean
+ * and rstd; with xh = (x - mean) rstd and p = dy weight[h]:
+ *   dx      (B,H,T,D) in `dtype` = rstd (p - mean(p) - xh mean(p xh))   (it is the d_o of the operator
+ *           whose output was normalised)
+ *   dweight (H,D) f32 = sum over b, t of dy xh, dbias (H,D) f32 = sum of dy; NULL = not computed
+ *   x_scales NULL, or x is kept in 8 bits (codes 16-byte aligned for the fast path; D <= 32 or a
+ *           multiple of 32) as kda_ckpt_pack writes it.
+ *   workspace kda_layer_norm_bwd_workspace_bytes() bytes, 16-byte aligned (NULL when that is 0 or
+ *           neither sum is asked for); contents on entry ignored.
+ * The sums over rows run in a fixed order (bitwise repeatable).  No output may overlap an input, another
+ * output or the workspace; dx may be dy itself. */
+int kda_layer_norm_bwd(const void* x, const unsigned char* x_scales, const float* weight, const float* mean,
+                       const float* rstd, const void* dy, void* dx, float* dweight, float* dbias,
+                       void* workspace, size_t workspace_bytes, int B, int H, int T, int D, int dtype, void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * Activations kept in 8 bits between the forward and the backward pass.  A row of D channels is cut
+ * into groups of G = min(D, 32); a group has the scale 2^e, e the smallest exponent >= -127 with
+ * max|x| <= 448 * 2^e over its finite values, stored as the byte e + 127, and each channel is the
+ * nearest-even OCP e4m3 value of x / 2^e.  Infinities and NaN become NaN.  D <= 32 or a multiple of 32
+ * (KDA_ERR_SHAPE).
+ *   x (rows, D) in `dtype`, aligned to an element; codes (rows, D) bytes; scales (rows, D / G) bytes
+ * kda_ckpt_unpack writes the values the codes stand for (for KDA_BF16 exact, except below 2^-133).
+ * Outputs must not overlap inputs or each other. */
+int kda_ckpt_pack(const void* x, unsigned char* codes, unsigned char* scales, long long rows, int D, int dtype,
+                  void* stream);
+int kda_ckpt_unpack(const unsigned char* codes, const unsigned char* scales, void* x, long long rows, int D,
+                    int dtype, void* stream);
+
 /* Static string for a status code ("ok", "null pointer", ...). Never NULL. */
 const char* kda_status_string(int status);
 
 /* Copies up to n counters into out and returns how many exist (KDA_NUM_COUNTERS).
- * Counters are process-wide and monotonic: calls accepted per entry point and
- * calls rejected with an error status (modelled on the page's dispatch counters,
+ * Counters are process-wide and monotonic: calls accepted per entry point (the decay
+ * attention counts with the entry point of its kind: forward, step, adjoint; the layer
+ * norm and the 8-bit activations are not counted) and calls rejected with an error status (modelled on the page's dispatch counters,
  * "The fused KDA adjoint" page, section 6). */
 #define KDA_NUM_COUNTERS 6
 #define KDA_COUNTER_GATE 0

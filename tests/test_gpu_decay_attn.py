@@ -1,0 +1,365 @@
+"""Decay attention on the GPU against the float64 token recurrence: prompts, gradients, single tokens.
+
+Tolerances.  u = 2^-8 is the largest relative error of one rounding to bf16.  A bf16 output is a sum of
+a part with scores rounded once and a part with state entries rounded once, rounded once at the end:
+element by element it is off by at most u (M + |ref|), M the same sum over absolute values, and a 5%
+allowance covers the products of errors and the fp32 sums (at most 1000 terms: 1000 2^-24 M < 0.02 u M).
+In the 2-norm, with independent roundings of RMS u / sqrt(3), that is sqrt(2/3) u; the bar is u.
+fp32 results: chains of at most K + C + 2 T / C roundings of 2^-24 (K <= 128, C = 64, T <= 2100), and
+exp2 of an exponent rounded at 2^-24 relative, at most 20 where the term counts: below 2e-5 of the sum
+over absolute values; the carried state of bf16 walks adds 2^-18 (its operand in two bf16 parts).
+"""
+import numpy as np
+import pytest
+import torch
+
+import gated_delta_rule_47_amd as kda
+from oracle import layer_ref as R
+
+from gpu_helpers import DEV, host, say, to_dev
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -8
+F32 = 2e-5
+BF, FP = torch.bfloat16, torch.float32
+
+
+def norm2(got, ref):
+    n = np.linalg.norm(ref)
+    return np.linalg.norm(got - ref) / n if n else float(np.abs(got).max(initial=0.0))
+
+
+def check(name, got, ref, M, dtype):
+    """got against ref: 2-norm, and element by element against M, the sum over absolute values."""
+    got = host(got)
+    assert got.shape == ref.shape and np.all(np.isfinite(got)), name
+    bar = U if dtype == BF else F32
+    e = norm2(got, ref)
+    lim = 1.05 * U * (M + np.abs(ref)) if dtype == BF else F32 * (M + np.abs(ref))
+    worst = float(((np.abs(got - ref)) / (lim + 1e-300)).max(initial=0.0))
+    say("  %-9s 2-norm %.2e (bar %.1e), worst element at %.2f of its bound" % (name, e, bar, worst))
+    assert e <= bar, (name, e)
+    assert worst <= 1.0, (name, worst)
+
+
+def make(B, H, T, K, V, dtype, seed=0, g=None):
+    rng = np.random.default_rng(seed)
+    x = {n: rng.standard_normal((B, H, T, D)).astype(np.float32)
+         for n, D in (("q", K), ("k", K), ("v", V), ("d_o", V))}
+    x["q"] /= K ** 0.5
+    x["g"] = (-rng.uniform(0.005, 0.7, H)).astype(np.float32) if g is None else np.resize(np.float32(g), H)
+    x["S0"] = (0.3 * rng.standard_normal((B, H, K, V))).astype(np.float32)
+    x["dS"] = (0.3 * rng.standard_normal((B, H, K, V))).astype(np.float32)
+    d = {n: to_dev(x[n], dtype if n in ("q", "k", "v", "d_o") else FP) for n in x}
+    for n in ("q", "k", "v", "d_o"):
+        x[n] = host(d[n])
+    return x, d
+
+
+def lens(lengths):
+    return None if lengths is None else torch.tensor(lengths, dtype=torch.int32, device=DEV)
+
+
+def run_fwd(B, H, T, K, V, dtype, lengths=None, g=None, state=True, seed=0, **kw):
+    say("fwd", B, H, T, K, V, dtype, lengths, g)
+    x, d = make(B, H, T, K, V, dtype, seed, g)
+    out = torch.full((B, H, T, V), 7.0, dtype=dtype, device=DEV)
+    o, S = kda.decay_attn_fwd(d["q"], d["k"], d["v"], d["g"], d["S0"] if state else None, lengths=lens(lengths),
+                              out=out, **kw)
+    torch.cuda.synchronize()
+    S0 = x["S0"] if state else None
+    ro, rS = R.decay_attn(x["q"], x["k"], x["v"], x["g"], S0, lengths)
+    Mo, MS = R.decay_attn(*(np.abs(x[n]) for n in ("q", "k", "v")), x["g"], None if S0 is None else np.abs(S0), lengths)
+    got = host(o)
+    for b, n in enumerate([T] * B if lengths is None else lengths):
+        n = min(max(n, 0), T)
+        assert np.all(got[b, :, n:] == 7.0), "rows behind a sequence were written"
+        got[b, :, n:] = 0.0
+    check("o", torch.from_numpy(got), ro, Mo, dtype)
+    check("state", S, rS, MS, FP)
+
+
+def run_bwd(B, H, T, K, V, dtype, lengths=None, g=None, state=True, packed=(), seed=1, **kw):
+    say("bwd", B, H, T, K, V, dtype, lengths, g, packed)
+    x, d = make(B, H, T, K, V, dtype, seed, g)
+    args = {n: d[n] for n in ("q", "k", "v")}
+    for n in packed:
+        args[n] = kda.ckpt_pack(d[n])
+        x[n] = R.ckpt_unpack(*(t.cpu().numpy() for t in args[n]))
+    got = kda.decay_attn_bwd(args["q"], args["k"], args["v"], d["g"], d["S0"] if state else None, d["d_o"],
+                             d["dS"] if state else None, lengths=lens(lengths), **kw)
+    torch.cuda.synchronize()
+    S0, dS = (x["S0"], x["dS"]) if state else (None, None)
+    ref = R.decay_attn_adjoint(x["q"], x["k"], x["v"], x["g"], S0, x["d_o"], dS, lengths)
+    ab = lambda a: None if a is None else np.abs(a)
+    M = R.decay_attn_adjoint(ab(x["q"]), ab(x["k"]), ab(x["v"]), x["g"], ab(S0), ab(x["d_o"]), ab(dS), lengths)
+    for n in ("dq", "dk", "dv", "dstate_in"):
+        check(n, got[n], ref[n], M[n], FP if n == "dstate_in" else dtype)
+    if lengths is not None:
+        for b, n in enumerate(lengths):
+            for name in ("dq", "dk", "dv"):
+                assert torch.all(got[name][b, :, min(max(n, 0), T):] == 0)
+
+
+DTYPES = [BF, FP]
+SIZES = [8, 16, 32, 64, 128]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T", [1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 200])
+def test_fwd_lengths(T, dtype):
+    run_fwd(2, 2, T, 64, 64, dtype, seed=T)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("K", SIZES)
+@pytest.mark.parametrize("V", SIZES)
+def test_fwd_widths(K, V, dtype):
+    run_fwd(1, 3, 150, K, V, dtype, seed=K + V)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("B,H,T,K,V", [(1, 1, 1000, 64, 64), (1, 2, 2049, 16, 128), (2, 1, 777, 128, 32),
+                                       (1, 1, 2100, 128, 128)])
+def test_fwd_segments(B, H, T, K, V, dtype):
+    assert kda.decay_attn_workspace_bytes(B, H, T, K, V, dtype) > 0
+    run_fwd(B, H, T, K, V, dtype)
+    run_fwd(B, H, T, K, V, dtype, g=[-1e-4])
+    run_bwd(B, H, T, K, V, dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T", [70, 600])
+def test_padded_batch(T, dtype):
+    lengths = [T, 0, 1, T // 2, T - 1, 64, 65, T + 100, -3]
+    run_fwd(9, 2, T, 32, 64, dtype, lengths=lengths)
+    run_bwd(9, 2, T, 32, 64, dtype, lengths=lengths)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_padding_may_hold_anything(dtype):
+    """Tokens behind a sequence are not read: NaN and infinity there reach nothing."""
+    B, H, T, K, V, n = 2, 2, 200, 32, 32, [77, 128]
+    x, d = make(B, H, T, K, V, dtype, 5)
+    ref = kda.decay_attn_fwd(d["q"], d["k"], d["v"], d["g"], d["S0"], lengths=lens(n))
+    gref = kda.decay_attn_bwd(d["q"], d["k"], d["v"], d["g"], d["S0"], d["d_o"], d["dS"], lengths=lens(n))
+    for b in range(B):
+        for name, bad in (("q", float("nan")), ("k", float("inf")), ("v", -float("inf")), ("d_o", float("nan"))):
+            d[name][b, :, n[b]:] = bad
+    got = kda.decay_attn_fwd(d["q"], d["k"], d["v"], d["g"], d["S0"], lengths=lens(n))
+    ggot = kda.decay_attn_bwd(d["q"], d["k"], d["v"], d["g"], d["S0"], d["d_o"], d["dS"], lengths=lens(n))
+    torch.cuda.synchronize()
+    for b in range(B):
+        assert torch.equal(got[0][b, :, :n[b]], ref[0][b, :, :n[b]])
+    assert torch.equal(got[1], ref[1])
+    for name in gref:
+        assert torch.equal(ggot[name], gref[name]), name
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("g", [0.0, -float("inf"), -30.0, -1e-5, -2.0])
+def test_decays(g, dtype):
+    with np.errstate(over="ignore", invalid="ignore"):
+        run_fwd(1, 2, 600, 32, 32, dtype, g=[g])
+        run_bwd(1, 2, 600, 32, 32, dtype, g=[g])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("K,V", [(8, 8), (8, 128), (16, 32), (32, 16), (64, 64), (64, 128), (128, 64), (128, 128)])
+@pytest.mark.parametrize("T", [1, 130])
+def test_bwd_widths(T, K, V, dtype):
+    run_bwd(1, 2, T, K, V, dtype, seed=K + V + T)
+    run_bwd(1, 2, T, K, V, dtype, state=False, seed=K + V + T)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("packed", [("q", "k", "v"), ("q",), ("k",), ("v",)])
+@pytest.mark.parametrize("K,V", [(8, 16), (64, 128), (128, 64)])
+def test_bwd_from_8_bits(K, V, packed, dtype):
+    run_bwd(2, 2, 100, K, V, dtype, packed=packed, lengths=[100, 37])
+    run_bwd(1, 1, 600, K, V, dtype, packed=packed)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_no_tokens(dtype):
+    x, d = make(2, 3, 0, 16, 8, dtype)
+    o, S = kda.decay_attn_fwd(d["q"], d["k"], d["v"], d["g"], d["S0"])
+    assert o.shape == (2, 3, 0, 8) and torch.equal(S, d["S0"])
+    assert torch.all(kda.decay_attn_fwd(d["q"], d["k"], d["v"], d["g"])[1] == 0)
+    got = kda.decay_attn_bwd(d["q"], d["k"], d["v"], d["g"], d["S0"], d["d_o"], d["dS"])
+    assert torch.equal(got["dstate_in"], d["dS"])
+
+
+def test_state_in_place_scale_and_caller_buffers():
+    for T in (100, 1000):                                          # one segment, several
+        x, d = make(1, 2, T, 32, 64, BF)
+        o, S = kda.decay_attn_fwd(d["q"], d["k"], d["v"], d["g"], d["S0"], scale=0.25)
+        need = kda.decay_attn_workspace_bytes(1, 2, T, 32, 64)
+        assert (need > 0) == (T == 1000)
+        ws = torch.full((max(need, 1),), 255, dtype=torch.uint8, device=DEV)      # contents are ignored
+        state, out = d["S0"].clone(), torch.empty_like(o)
+        o2, S2 = kda.decay_attn_fwd(d["q"], d["k"], d["v"], d["g"], state, scale=0.25, out=out, state_out=state,
+                                    workspace=ws)
+        assert o2 is out and S2 is state and torch.equal(o, o2) and torch.equal(S, state)
+        o0, none = kda.decay_attn_fwd(d["q"], d["k"], d["v"], d["g"], d["S0"], scale=0.0, output_state=False)
+        assert none is None and torch.all(o0 == 0)
+        ref, _ = R.decay_attn(x["q"], x["k"], x["v"], x["g"], x["S0"], scale=0.25)
+        assert norm2(host(o), ref) <= U
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("K", SIZES)
+@pytest.mark.parametrize("V", SIZES)
+def test_step(K, V, dtype):
+    B, H = 3, 5
+    x, d = make(B, H, 1, K, V, dtype, seed=K * V, g=[-0.3, 0.0, -float("inf"), -1e-3, -9.0])
+    q, k, v = (d[n][:, :, 0].contiguous() for n in ("q", "k", "v"))
+    S = d["S0"].clone()
+    with np.errstate(over="ignore"):
+        ro, rS = R.decay_attn(x["q"], x["k"], x["v"], x["g"], x["S0"])
+        Mo, MS = R.decay_attn(*(np.abs(x[n]) for n in ("q", "k", "v")), x["g"], np.abs(x["S0"]))
+    o = kda.decay_attn_step(q, k, v, d["g"], S)
+    torch.cuda.synchronize()
+    check("o", o.unsqueeze(2), ro, Mo, dtype)
+    check("state", S, rS, MS, FP)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_prompt_then_tokens(dtype):
+    """A prompt of 150 tokens and 20 single tokens give what 170 tokens at once give."""
+    x, d = make(2, 2, 170, 64, 32, dtype)
+    cut = lambda n, a, b: d[n][:, :, a:b].contiguous()
+    _, S = kda.decay_attn_fwd(cut("q", 0, 150), cut("k", 0, 150), cut("v", 0, 150), d["g"], d["S0"])
+    ro, rS = R.decay_attn(x["q"], x["k"], x["v"], x["g"], x["S0"])
+    Mo, MS = R.decay_attn(*(np.abs(x[n]) for n in ("q", "k", "v")), x["g"], np.abs(x["S0"]))
+    os_ = [kda.decay_attn_step(*(d[n][:, :, t].contiguous() for n in ("q", "k", "v")), d["g"], S)
+           for t in range(150, 170)]
+    torch.cuda.synchronize()
+    check("o", torch.stack(os_, 2), ro[:, :, 150:], Mo[:, :, 150:], dtype)
+    check("state", S, rS, MS, FP)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_gradient_against_differences_of_the_forward(dtype):
+    """The loss moves along a direction as the gradients say.  Differences of the float64 definition;
+    the gradients' own error is the one checked above."""
+    x, d = make(1, 2, 90, 16, 16, dtype)
+    got = kda.decay_attn_bwd(d["q"], d["k"], d["v"], d["g"], d["S0"], d["d_o"], d["dS"])
+    rng = np.random.default_rng(8)
+
+    def loss(q, k, v, S0):
+        o, S = R.decay_attn(q, k, v, x["g"], S0)
+        return (o * x["d_o"]).sum() + (S * x["dS"]).sum()
+
+    base = [x["q"], x["k"], x["v"], x["S0"].astype(np.float64)]
+    for i, n in enumerate(("dq", "dk", "dv", "dstate_in")):
+        dirn = rng.standard_normal(base[i].shape)
+        h = 1e-4
+        up = [b + (h * dirn if j == i else 0) for j, b in enumerate(base)]
+        dn = [b - (h * dirn if j == i else 0) for j, b in enumerate(base)]
+        fd = (loss(*up) - loss(*dn)) / (2 * h)
+        g = host(got[n])
+        # each element is off by at most about its bound's share: u |g| in the 2-norm times the direction's norm
+        tol = (U if dtype == BF and n != "dstate_in" else F32) * np.linalg.norm(g) * np.linalg.norm(dirn)
+        assert abs((g * dirn).sum() - fd) <= tol + 1e-6 * abs(fd), n
+
+
+def test_another_stream_and_graph_replays():
+    """Calls on a side stream; a captured forward and backward replayed with other work in between, on
+    changed inputs, give the eager results bit for bit."""
+    B, H, T, K, V = 1, 2, 700, 64, 64
+    x, d = make(B, H, T, K, V, BF, 1)
+    _, e = make(B, H, T, K, V, BF, 2)
+    assert kda.decay_attn_workspace_bytes(B, H, T, K, V) > 0
+
+    def step(a):
+        o, S = kda.decay_attn_fwd(a["q"], a["k"], a["v"], a["g"], a["S0"])
+        y, mean, rstd = kda.layer_norm_fwd(o)
+        dx, dw, db = kda.layer_norm_bwd(o, None, mean, rstd, a["d_o"])
+        pk = [kda.ckpt_pack(a[n]) for n in ("q", "k", "v")]
+        g = kda.decay_attn_bwd(*pk, a["g"], a["S0"], dx, a["dS"])
+        one = kda.decay_attn_step(a["q"][:, :, 0].contiguous(), a["k"][:, :, 0].contiguous(),
+                                  a["v"][:, :, 0].contiguous(), a["g"], S.clone())
+        return [o, S, y, dx, dw, db, one] + [g[n] for n in sorted(g)]
+
+    want = [[t.clone() for t in step(a)] for a in (d, e)]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        side = step(d)
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    for a, b in zip(side, want[0]):
+        assert torch.equal(a, b)
+    static = {n: t.clone() for n, t in d.items()}
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(s):
+        step(static)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        out = step(static)
+    for it in range(4):
+        src = (d, e)[it % 2]
+        for n in static:
+            static[n].copy_(src[n])
+        graph.replay()
+        eager = step(src)
+        torch.cuda.synchronize()
+        for i, (a, b, c) in enumerate(zip(out, want[it % 2], eager)):
+            assert torch.equal(a, b) and torch.equal(c, b), (it, i)
+
+
+def test_same_results_every_time():
+    x, d = make(2, 3, 900, 64, 128, BF)
+    f = lambda: [*kda.decay_attn_fwd(d["q"], d["k"], d["v"], d["g"], d["S0"]),
+                 *kda.decay_attn_bwd(d["q"], d["k"], d["v"], d["g"], d["S0"], d["d_o"], d["dS"]).values()]
+    a = f()
+    for _ in range(3):
+        for p, q in zip(a, f()):
+            assert torch.equal(p, q)
+
+
+def test_training_step_as_a_layer_runs_it():
+    """attention -> norm, activations kept in 8 bits, norm's and attention's backward from them, against
+    the same chain of definitions in float64 on the values the codes stand for."""
+    B, H, T, K, V = 2, 3, 300, 64, 64
+    n = [300, 130]
+    x, d = make(B, H, T, K, V, BF, 4)
+    rng = np.random.default_rng(9)
+    w = (1 + 0.1 * rng.standard_normal((H, V))).astype(np.float32)
+    b = (0.1 * rng.standard_normal((H, V))).astype(np.float32)
+    wd, bd = to_dev(w, FP), to_dev(b, FP)
+    out = torch.zeros((B, H, T, V), dtype=BF, device=DEV)
+    o, S = kda.decay_attn_fwd(d["q"], d["k"], d["v"], d["g"], d["S0"], lengths=lens(n), out=out)
+    y, mean, rstd = kda.layer_norm_fwd(o, wd, bd)
+    kept = {m: kda.ckpt_pack(t) for m, t in (("q", d["q"]), ("k", d["k"]), ("v", d["v"]), ("o", o))}
+    dx, dw, db = kda.layer_norm_bwd(kept["o"], wd, mean, rstd, d["d_o"])
+    g = kda.decay_attn_bwd(kept["q"], kept["k"], kept["v"], d["g"], d["S0"], dx, d["dS"], lengths=lens(n))
+    torch.cuda.synchronize()
+    ry, rm, rr = R.layer_norm(host(o), w, b)
+    assert norm2(host(y), ry) <= U and norm2(host(mean), rm) <= F32 and norm2(host(rstd), rr) <= F32
+    val = {m: R.ckpt_unpack(*(t.cpu().numpy() for t in c)) for m, c in kept.items()}
+    rdx, rdw, rdb = R.layer_norm_adjoint(val["o"], w, host(mean), host(rstd), x["d_o"])
+    assert norm2(host(dx), rdx) <= U and norm2(host(dw), rdw) <= F32 and norm2(host(db), rdb) <= F32
+    ref = R.decay_attn_adjoint(val["q"], val["k"], val["v"], x["g"], x["S0"], host(dx), x["dS"], n)
+    for m in ref:
+        e = norm2(host(g[m]), ref[m])
+        assert e <= (F32 if m == "dstate_in" else U), (m, e)
+
+
+def test_long_offsets():
+    """A tensor of more than 2^31 elements: the last head's rows are addressed past 32 bits."""
+    B, H, T, K, V = 1, 40, 430000, 128, 8
+    g = torch.full((H,), -0.05, device=DEV)
+    q = torch.zeros((B, H, T, K), dtype=BF, device=DEV)
+    assert q.numel() > 2 ** 31
+    k = torch.zeros_like(q)
+    v = torch.zeros((B, H, T, V), dtype=BF, device=DEV)
+    x, d = make(1, 1, 64, K, V, BF, 3, g=[-0.05])
+    for n, t in (("q", q), ("k", k), ("v", v)):
+        t[0, -1, -64:] = d[n][0, 0]
+    o, S = kda.decay_attn_fwd(q, k, v, g)
+    ro, rS = R.decay_attn(x["q"], x["k"], x["v"], x["g"])
+    assert norm2(host(o[0, -1, -64:]), ro[0, 0]) <= U and norm2(host(S[0, -1]), rS[0, 0]) <= F32
+    assert torch.all(o[0, 0] == 0) and torch.all(S[0, 0] == 0)
