@@ -61,27 +61,45 @@ typedef short short4v_t __attribute__((ext_vector_type(4)));
 // index 16 n + 4 g + r of tile n).  `tr` reads the transpose of a [index][column] tile in the
 // accumulator order.  Tile `ct` of 16 rows covers the rows row_of(ct, m), m = 0..15, which give a
 // lane's accumulator registers of NACC adjacent tiles DG / 4 consecutive rows.
+//
+// bf16 LDS tiles are [row][W elements] without padding; the 16-byte pieces of row t are stored in the
+// order piece ^ swz(t).  64 banks hold 16 pieces, so W's pieces per row leave some low bits of t to the address
+// and the rest, permuted, to swz: the 16 rows of a natural read, the 4 rows x 4 column blocks of each
+// transposing read and the 16 columns of the state image's writes all fall on different banks.  (With
+// rows padded by 16 bytes instead, over half of the LDS cycles were conflicts of the transposing reads.)
+// fp32 tiles have no transposing reads and rows padded by 16 bytes are free of conflicts.
 template <typename T> struct Lin;
 
 template <> struct Lin<bf16_t> {                 // v_mfma_f32_16x16x32_bf16
-  static constexpr int DG = 32, NACC = 2, EPP = 8, PAD = 8, SPLIT = 2;
+  static constexpr int DG = 32, NACC = 2, EPP = 8, PAD = 0, SPLIT = 3;
   typedef short8 frag;
   static __device__ __forceinline__ int row_of(int ct, int m) {
     return 32 * (ct >> 1) + 8 * (m >> 2) + 4 * (ct & 1) + (m & 3);
   }
-  static __device__ __forceinline__ frag nat(const bf16_t* row, int d0, int lane) {
-    return *reinterpret_cast<const short8*>(row + d0 + 8 * (lane >> 4));
+  // IMG: the state image, whose natural reads take the rows row_of() of a tile
+  template <int W, bool IMG> static __device__ __forceinline__ int swz(int t) {
+    const int lo = IMG ? ((t >> 4 ^ t >> 2) & 1) << 1 | (t >> 3 & 1) : t >> 2 & 3;
+    if constexpr (W == 128) return (t & 3) << 2 | lo;
+    else if constexpr (W == 64) return (t & 2) << 1 | lo;
+    else return lo;
+  }
+  template <int W, bool IMG> static __device__ __forceinline__ int at(int t, int e) {
+    return t * W + ((e >> 3) ^ swz<W, IMG>(t)) * 8 + (e & 7);
+  }
+  template <int W, bool IMG>
+  static __device__ __forceinline__ frag nat(const bf16_t* base, int t, int d0, int lane) {
+    return *reinterpret_cast<const short8*>(base + at<W, IMG>(t, d0 + 8 * (lane >> 4)));
   }
   // two transposing reads: lane 4r + m of a group of 16 addresses row 4g + r (then 16 + 4g + r) at
   // four columns and lane j receives column j of the group's 16
-  template <bool PERM> static __device__ __forceinline__ frag tr(const bf16_t* base, int ld, int ct, int d0, int lane) {
+  template <int W, bool PERM> static __device__ __forceinline__ frag tr(const bf16_t* base, int ct, int d0, int lane) {
     const int g = lane >> 4, r = (lane >> 2) & 3, m = lane & 3;
     const int col = PERM ? 32 * (ct >> 1) + 8 * m + 4 * (ct & 1) : 16 * ct + 4 * m;
-    const bf16_t* p = base + (d0 + 4 * g + r) * ld + col;
+    const bf16_t* p = base + at<W, false>(d0 + 4 * g + r, col);     // (swz is the same 16 rows on)
     const short4v_t a = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
         (__attribute__((address_space(3))) short4v_t*)(__attribute__((address_space(3))) const void*)p);
     const short4v_t b = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-        (__attribute__((address_space(3))) short4v_t*)(__attribute__((address_space(3))) const void*)(p + 16 * ld));
+        (__attribute__((address_space(3))) short4v_t*)(__attribute__((address_space(3))) const void*)(p + 16 * W));
     return short8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
   }
   static __device__ __forceinline__ floatx4 mma(frag a, frag b, floatx4 c) {
@@ -92,18 +110,23 @@ template <> struct Lin<bf16_t> {                 // v_mfma_f32_16x16x32_bf16
     return __builtin_bit_cast(short8, u32x4_t{pack_bf16x2(x[0][0], x[0][1]), pack_bf16x2(x[0][2], x[0][3]),
                                               pack_bf16x2(x[1][0], x[1][1]), pack_bf16x2(x[1][2], x[1][3])});
   }
-  // x f as bf16 parts hi + lo, off by at most 2^-18 of the product: the state is returned in fp32, and
-  // one bf16 rounding of the decayed operand (2^-9) would show in it
+  // x f as the sum of SPLIT bf16 parts, off by 2^-26 of it: the state is returned in fp32, and the
+  // rounding of two parts (2^-17) would show in it
   static __device__ __forceinline__ void scaled(frag x, const float* f, frag* out) {
-    uint32_t hi[4], lo[4];
+    u32x4_t part[SPLIT];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float a = bf2f((bf16_t)x[2 * e]) * f[2 * e], b = bf2f((bf16_t)x[2 * e + 1]) * f[2 * e + 1];
-      hi[e] = pack_bf16x2(a, b);
-      lo[e] = pack_bf16x2(a - __uint_as_float(hi[e] << 16), b - __uint_as_float(hi[e] & 0xffff0000u));
+      float a = bf2f((bf16_t)x[2 * e]) * f[2 * e], b = bf2f((bf16_t)x[2 * e + 1]) * f[2 * e + 1];
+#pragma unroll
+      for (int s = 0; s < SPLIT; ++s) {
+        const uint32_t w = pack_bf16x2(a, b);
+        part[s][e] = w;
+        a -= __uint_as_float(w << 16);
+        b -= __uint_as_float(w & 0xffff0000u);
+      }
     }
-    out[0] = __builtin_bit_cast(short8, u32x4_t{hi[0], hi[1], hi[2], hi[3]});
-    out[1] = __builtin_bit_cast(short8, u32x4_t{lo[0], lo[1], lo[2], lo[3]});
+#pragma unroll
+    for (int s = 0; s < SPLIT; ++s) out[s] = __builtin_bit_cast(short8, part[s]);
   }
   // token (within a group of DG) of fragment element e in the accumulator order
   static __device__ __forceinline__ int tok_of(int e, int g) { return 16 * (e >> 2) + 4 * g + (e & 3); }
@@ -116,12 +139,15 @@ template <> struct Lin<float> {                  // four v_mfma_f32_16x16x4_f32
   static constexpr int DG = 16, NACC = 1, EPP = 4, PAD = 4, SPLIT = 1;
   typedef floatx4 frag;
   static __device__ __forceinline__ int row_of(int ct, int m) { return 16 * ct + m; }
-  static __device__ __forceinline__ frag nat(const float* row, int d0, int lane) {
-    return *reinterpret_cast<const floatx4*>(row + d0 + 4 * (lane >> 4));
+  template <int W, bool IMG> static __device__ __forceinline__ int at(int t, int e) { return t * (W + PAD) + e; }
+  template <int W, bool IMG>
+  static __device__ __forceinline__ frag nat(const float* base, int t, int d0, int lane) {
+    return *reinterpret_cast<const floatx4*>(base + at<W, IMG>(t, d0 + 4 * (lane >> 4)));
   }
-  template <bool PERM> static __device__ __forceinline__ frag tr(const float* base, int ld, int ct, int d0, int lane) {
-    const float* p = base + (d0 + 4 * (lane >> 4)) * ld + 16 * ct + (lane & 15);
-    return floatx4{p[0], p[ld], p[2 * ld], p[3 * ld]};
+  template <int W, bool PERM> static __device__ __forceinline__ frag tr(const float* base, int ct, int d0, int lane) {
+    const int t = d0 + 4 * (lane >> 4), e = 16 * ct + (lane & 15);
+    return floatx4{base[at<W, false>(t, e)], base[at<W, false>(t + 1, e)], base[at<W, false>(t + 2, e)],
+                   base[at<W, false>(t + 3, e)]};
   }
   static __device__ __forceinline__ floatx4 mma(frag a, frag b, floatx4 c) {
 #pragma unroll
@@ -140,73 +166,94 @@ template <> struct Lin<float> {                  // four v_mfma_f32_16x16x4_f32
 // 2^(b - 127) for a scale byte b (b = 0: 2^-127, a subnormal).
 __device__ __forceinline__ float ckpt_scale(uint32_t b) { return __uint_as_float(b ? b << 23 : 0x00400000u); }
 
-// One piece of EPP consecutive channels of a row on its way from memory: 16 bytes of elements, or
+// One piece of EPP consecutive channels of a row on its way from memory: 16 bytes of elements, or (PK)
 // EPP codes and their group's scale byte.
-template <typename T> struct Piece {
-  u32x4_t raw;
+template <typename T, bool PK> struct Piece {
+  static constexpr int W = PK ? Lin<T>::EPP / 4 : 4;
+  uint32_t raw[W];
   uint32_t sc;
-  __device__ __forceinline__ u32x4_t elems(bool packed) const {
-    if (!packed) return raw;
-    const float s = ckpt_scale(sc);
-    float f[8];
+  __device__ __forceinline__ u32x4_t elems() const {
+    if constexpr (!PK) {
+      return u32x4_t{raw[0], raw[1], raw[2], raw[3]};
+    } else {
+      const float s = ckpt_scale(sc);
+      float f[4 * W];
 #pragma unroll
-    for (int i = 0; i < Lin<T>::EPP / 4; ++i) {
-      const floatx2 a = __builtin_amdgcn_cvt_pk_f32_fp8((int)raw[i], false);
-      const floatx2 b = __builtin_amdgcn_cvt_pk_f32_fp8((int)raw[i], true);
-      f[4 * i] = a[0] * s;
-      f[4 * i + 1] = a[1] * s;
-      f[4 * i + 2] = b[0] * s;
-      f[4 * i + 3] = b[1] * s;
+      for (int i = 0; i < W; ++i) {
+        const floatx2 a = __builtin_amdgcn_cvt_pk_f32_fp8((int)raw[i], false);
+        const floatx2 b = __builtin_amdgcn_cvt_pk_f32_fp8((int)raw[i], true);
+        f[4 * i] = a[0] * s;
+        f[4 * i + 1] = a[1] * s;
+        f[4 * i + 2] = b[0] * s;
+        f[4 * i + 3] = b[1] * s;
+      }
+      if constexpr (std::is_same<T, float>::value)
+        return u32x4_t{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])};
+      else
+        return u32x4_t{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                       pack_bf16x2(f[6], f[7])};
     }
-    if constexpr (std::is_same<T, float>::value)
-      return u32x4_t{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])};
-    else
-      return u32x4_t{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                     pack_bf16x2(f[6], f[7])};
   }
 };
 
+// Words of a raw buffer resource, for the copies below.
+__device__ __forceinline__ u32x4_t buffer_words(const void* base, unsigned bytes) {
+  const uintptr_t p = (uintptr_t)base;
+  return u32x4_t{(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)p),
+                 (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(p >> 32)) & 0xffffu,
+                 (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes), 0x00020000u};
+}
 // One head of a tensor (rows tokens x D channels) behind a range-checked buffer: rows from `len` on
 // and channels from D on read as zero.
 template <typename T, bool PK> struct HeadRows {
   __amdgpu_buffer_rsrc_t r, rs;
+  u32x4_t words;                                 // of r, for the copies
   int D, nsc;
-  bool packed;
   __device__ __forceinline__ HeadRows(const void* base, const uint8_t* sc, int bh, int T_, int D_, int len) {
     D = D_;
-    packed = PK && sc != nullptr;
-    const int es = packed ? 1 : (int)sizeof(T);
-    r = make_rsrc((const char*)base + (size_t)bh * T_ * D * es, (unsigned)len * (unsigned)(D * es));
+    constexpr int es = PK ? 1 : (int)sizeof(T);
+    const char* head = (const char*)base + (size_t)bh * T_ * D * es;
+    r = make_rsrc(head, (unsigned)len * (unsigned)(D * es));
+    words = buffer_words(head, (unsigned)len * (unsigned)(D * es));
     nsc = D < 32 ? 1 : D / 32;
-    if (PK) rs = make_rsrc(sc + (packed ? (size_t)bh * T_ * nsc : 0), packed ? (unsigned)len * (unsigned)nsc : 0u);
+    if constexpr (PK) rs = make_rsrc(sc + (size_t)bh * T_ * nsc, (unsigned)len * (unsigned)nsc);
   }
-  __device__ __forceinline__ Piece<T> load(int t, int ch) const {
-    Piece<T> p;
+  __device__ __forceinline__ Piece<T, PK> load(int t, int ch) const {
+    Piece<T, PK> p;
+    constexpr unsigned kOut = 0xfffffff0u;                     // past any buffer's range
     const unsigned at = (unsigned)t * (unsigned)D + (unsigned)ch;
     const bool in = ch < D;
-    if (PK && packed) {
-      const unsigned off = in ? at : 0xfffffff0u;
-      if constexpr (std::is_same<T, float>::value) {
-        p.raw[0] = __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0);
+    if constexpr (!PK) {
+      const u32x4_t x = __builtin_bit_cast(
+          u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, in ? at * (unsigned)sizeof(T) : kOut, 0, 0));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) p.raw[i] = x[i];
+    } else {
+      if constexpr (Piece<T, PK>::W == 1) {
+        p.raw[0] = __builtin_amdgcn_raw_buffer_load_b32(r, in ? at : kOut, 0, 0);
       } else {
-        const u32x2_t x = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0));
+        const u32x2_t x =
+            __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(r, in ? at : kOut, 0, 0));
         p.raw[0] = x[0];
         p.raw[1] = x[1];
       }
-      p.sc = __builtin_amdgcn_raw_buffer_load_b8(rs, in ? (unsigned)t * (unsigned)nsc + (unsigned)(ch >> 5) : 0xfffffff0u,
-                                                 0, 0);
-    } else {
-      p.raw = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
-                                              r, in ? at * (unsigned)sizeof(T) : 0xfffffff0u, 0, 0));
+      p.sc = __builtin_amdgcn_raw_buffer_load_b8(
+          rs, in ? (unsigned)t * (unsigned)nsc + (unsigned)(ch >> 5) : kOut, 0, 0);
     }
     return p;
   }
 };
 
-// A chunk of C rows x D channels (padded to DP) held by the NT threads between memory and LDS.
+// LDS image of C rows x DP channels: row pitch and size in 16-byte pieces (a size that whole waves fill).
+template <typename T, int C, int DP> struct Tile {
+  static constexpr int PPR = (DP + Lin<T>::PAD) / Lin<T>::EPP, NP = round_up(C * PPR, 64), ELEMS = NP * Lin<T>::EPP;
+};
+
+// A chunk of C rows x DP channels (from ch0) held by the NT threads between memory and LDS (8-bit
+// operands, whose codes become elements on the way).
 template <typename T, bool PK, int C, int DP, int NT> struct Stage {
   static constexpr int PPR = DP / Lin<T>::EPP, N = C * PPR, PER = (N + NT - 1) / NT;
-  Piece<T> p[PER];
+  Piece<T, PK> p[PER];
   __device__ __forceinline__ void load(const HeadRows<T, PK>& h, int t0, int ch0, int tid) {
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
@@ -214,15 +261,81 @@ template <typename T, bool PK, int C, int DP, int NT> struct Stage {
       if (N % NT == 0 || x < N) p[i] = h.load(t0 + x / PPR, ch0 + (x % PPR) * Lin<T>::EPP);
     }
   }
-  __device__ __forceinline__ void store(const HeadRows<T, PK>& h, T* lds, int ld, int tid) const {
+  __device__ __forceinline__ void store(T* lds, int tid) const {
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int x = tid + i * NT;
       if (N % NT == 0 || x < N)
-        *reinterpret_cast<u32x4_t*>(lds + (x / PPR) * ld + (x % PPR) * Lin<T>::EPP) = p[i].elems(h.packed);
+        *reinterpret_cast<u32x4_t*>(lds + Lin<T>::template at<DP, false>(x / PPR, (x % PPR) * Lin<T>::EPP)) =
+            p[i].elems();
     }
   }
 };
+
+// 16 bytes per lane from byte `lane_off` + `off` of the buffer into LDS at lds + 16 * lane (lds and off are
+// the wave's).  Past the buffer's range: zeros.  Written in asm, with no register as its output, because
+// the compiler would wait for every copy in flight before each transposing LDS read; the waits are
+// wait_vm_but()'s (the compiler's own waits for its loads and stores only grow stricter by operations that
+// it does not count).
+__device__ __forceinline__ void copy_to_lds(u32x4_t r, const void* lds, unsigned lane_off, unsigned off) {
+  const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)lds;
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(
+                   __builtin_amdgcn_readfirstlane((int)at)),
+               "v"(lane_off), "s"(r), "s"(off)
+               : "memory", "m0");
+}
+
+// The tiles of one chunk, copied from memory straight into LDS: each wave instruction fills 64
+// consecutive pieces, so the order of the pieces within a row is made by the address each lane reads.
+// A wave issues MIN or MIN + 1 instructions per chunk.  Rows behind the range read as zeros.
+template <typename T, int C, int DK, int DV, int DQ, int NW> struct Copy {
+  typedef Tile<T, C, DK> TK;
+  typedef Tile<T, C, DV> TV;
+  typedef Tile<T, C, (DQ ? DQ : 32)> TQ;
+  static constexpr int IK = TK::NP / 64, IV = TV::NP / 64, IQ = DQ ? TQ::NP / 64 : 0, NI = IK + IV + IQ;
+  static constexpr int PER = (NI + NW - 1) / NW, MIN = NI / NW;
+  unsigned off[PER];                             // byte offset of this lane's piece from the chunk's first row
+
+  template <int DP> static __device__ __forceinline__ unsigned piece(int slot, int D, int ch0) {
+    typedef Tile<T, C, DP> TL;
+    constexpr int E = Lin<T>::EPP, W = DP / E;
+    const int row = slot / TL::PPR, pos = slot % TL::PPR;
+    int pc = pos;
+    if constexpr (Lin<T>::PAD == 0) pc = pos ^ (Lin<T>::template at<DP, false>(row, 0) - row * DP) / E;
+    const int ch = ch0 + pc * E;
+    return row < C && pc < W && ch < D ? (unsigned)(row * D + ch) * (unsigned)sizeof(T) : 0xfffffff0u;
+  }
+  __device__ __forceinline__ Copy(int wave, int lane, int K, int V, int v0) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int x = wave + i * NW;
+      off[i] = x < IK ? piece<DK>(64 * x + lane, K, 0)
+                      : x < IK + IV ? piece<DV>(64 * (x - IK) + lane, V, v0)
+                                    : piece<TQ::PPR * Lin<T>::EPP - Lin<T>::PAD>(64 * (x - IK - IV) + lane, K, 0);
+    }
+  }
+  // tokens from t0 into the tiles at lds (K, V and Q one behind the other)
+  __device__ __forceinline__ void issue(u32x4_t rk, u32x4_t rv, u32x4_t rq, int t0, int K, int V, const T* lds,
+                                        int wave) const {
+    const unsigned sk = (unsigned)t0 * (unsigned)(K * sizeof(T)), sv = (unsigned)t0 * (unsigned)(V * sizeof(T));
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int x = wave + i * NW;
+      if (x < NI) {
+        const bool isv = x >= IK && x < IK + IV;
+        copy_to_lds(isv ? rv : (x < IK ? rk : rq), lds + x * 64 * Lin<T>::EPP, off[i], isv ? sv : sk);
+      }
+    }
+  }
+};
+// Until at most N of this wave's latest vector-memory operations are outstanding.
+template <int N> __device__ __forceinline__ void wait_vm_but() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
+// Until none is, known to the compiler too: before a loop with copies in flight, so that it does not wait in
+// the loop for loads from before it.
+__device__ __forceinline__ void wait_vm_all() { __builtin_amdgcn_s_waitcnt(0x0F70); }
+// Barrier for LDS that leaves copies into LDS in flight: each wave waits for its own reads and writes, and
+// before it for the copies that the next chunk needs.
+__device__ __forceinline__ void chunk_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
 // ------------------------------------------------------------------ decay
 // a^n for n >= 0 as hi + lo: the chunk factor multiplies the state once per chunk, and a bias of one
@@ -240,10 +353,15 @@ __device__ __forceinline__ Decay2 decay_pow2(float g, int n) {
 // a^n, g2 = log2(a); n = 0 gives 1 also for a = 0 (g2 = -inf)
 __device__ __forceinline__ float decay_pow(float g2, int n) { return n == 0 ? 1.0f : fast_exp2(g2 * (float)n); }
 
+// A value that is the same in all lanes, kept in a scalar register.
+__device__ __forceinline__ float uniform(float x) {
+  return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(x)));
+}
+
 // ------------------------------------------------------------------ state part of a chunk
 // The accumulators of one state wave: rows of the channel tiles ct0 .. ct0 + NK - 1, columns of
 // the NV value tiles from vt0.
-template <typename T, int C, int NK, int NV, bool REV> struct StateTile {
+template <typename T, int KD, int VT, int C, int NK, int NV, bool REV> struct StateTile {
   typedef Lin<T> L;
   floatx4 acc[NK][NV];
   float f[C / L::DG][L::DG / 4];                 // u a^(...) of this lane's tokens
@@ -260,10 +378,15 @@ template <typename T, int C, int NK, int NV, bool REV> struct StateTile {
     for (int i = 0; i < NK; ++i)
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
+        // (rows and columns of the padding: some element of the state, then zero)
         const int row = L::row_of(ct0 + i, 4 * (lane >> 4)), col = col0 + 16 * j + (lane & 15);
+        const bool in = row < K && col < V;                  // K is a multiple of 4
+        const float* p = S + (in ? row * sk + col * sv : 0);
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          acc[i][j][r] = (row + r < K && col < V) ? S[(size_t)(row + r) * sk + (size_t)col * sv] : 0.0f;
+        for (int r = 0; r < 4; ++r) {
+          const float x = p[r * sk];
+          acc[i][j][r] = in ? x : 0.0f;
+        }
       }
   }
   __device__ __forceinline__ void save(float* S, int sk, int sv, int ct0, int col0, int K, int V, int lane) const {
@@ -272,18 +395,21 @@ template <typename T, int C, int NK, int NV, bool REV> struct StateTile {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         const int row = L::row_of(ct0 + i, 4 * (lane >> 4)), col = col0 + 16 * j + (lane & 15);
+        if (row < K && col < V) {
+          float* p = S + row * sk + col * sv;
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (row + r < K && col < V) S[(size_t)(row + r) * sk + (size_t)col * sv] = acc[i][j][r];
+          for (int r = 0; r < 4; ++r) p[r * sk] = acc[i][j][r];
+        }
       }
   }
   // [column][channel] image in LDS
-  __device__ __forceinline__ void image(T* dst, int ld, int ct0, int col0, int lane) const {
+  __device__ __forceinline__ void image(T* dst, int ct0, int col0, int lane) const {
 #pragma unroll
     for (int i = 0; i < NK; ++i)
 #pragma unroll
       for (int j = 0; j < NV; ++j)
-        L::store4(dst + (col0 + 16 * j + (lane & 15)) * ld + L::row_of(ct0 + i, 4 * (lane >> 4)), acc[i][j]);
+        L::store4(dst + L::template at<KD, true>(col0 + 16 * j + (lane & 15), L::row_of(ct0 + i, 4 * (lane >> 4))),
+                  acc[i][j]);
   }
   // factors of a chunk of n tokens; tokens behind it get 0
   __device__ __forceinline__ void factors(float g2, float u, int n, int lane) {
@@ -297,37 +423,57 @@ template <typename T, int C, int NK, int NV, bool REV> struct StateTile {
         f[d][e] = i < n ? u * decay_pow(g2, REV ? i + 1 : n - 1 - i) : 0.0f;
       }
   }
-  __device__ __forceinline__ void update(const T* sK, int ldk, const T* sV, int ldv, int ct0, int vt0, Decay2 an,
-                                         int lane) {
+  __device__ __forceinline__ void update(const T* sK, const T* sV, int ct0, int vt0, Decay2 an, int lane) {
 #pragma unroll
     for (int i = 0; i < NK; ++i)
 #pragma unroll
       for (int j = 0; j < NV; ++j)
 #pragma unroll
         for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(acc[i][j][r], an.hi, acc[i][j][r] * an.lo);
+    constexpr int ND = C / L::DG;
 #pragma unroll
-    for (int d = 0; d < C / L::DG; ++d) {
-      typename L::frag vf[NV][L::SPLIT];
+    for (int d = 0; d < ND; ++d) {
+      typename L::frag kf[NK], vf[NV][L::SPLIT];
 #pragma unroll
       for (int j = 0; j < NV; ++j)
-        L::scaled(L::template tr<false>(sV, ldv, vt0 + j, d * L::DG, lane), f[d], vf[j]);
+        L::scaled(L::template tr<VT, false>(sV, vt0 + j, d * L::DG, lane), f[d], vf[j]);
 #pragma unroll
-      for (int i = 0; i < NK; ++i) {
-        const typename L::frag kf = L::template tr<true>(sK, ldk, ct0 + i, d * L::DG, lane);
+      for (int i = 0; i < NK; ++i) kf[i] = L::template tr<KD, true>(sK, ct0 + i, d * L::DG, lane);
 #pragma unroll
-        for (int s = 0; s < L::SPLIT; ++s)
+      for (int s = 0; s < L::SPLIT; ++s)
 #pragma unroll
-          for (int j = 0; j < NV; ++j) acc[i][j] = L::mma(kf, vf[j][s], acc[i][j]);
-      }
+        for (int i = 0; i < NK; ++i)
+#pragma unroll
+          for (int j = 0; j < NV; ++j) acc[i][j] = L::mma(kf[i], vf[j][s], acc[i][j]);
     }
   }
 };
 
 // ------------------------------------------------------------------ the walk
-template <typename T, int KD, int VT, int C> struct WalkShape {
+// How NW state waves share the KD x VT state: one 16-column value tile and a part of the channels each.
+template <int KD, int VT, int NW> struct StateShape {
+  static constexpr int WV = cmin(VT / 16, NW), WK = NW / WV;
+  static constexpr int NK = KD / 16 / WK, NV = VT / 16 / WV;          // tiles of a wave
+  static_assert(NK >= 1 && NV >= 1, "tile too small for the waves");
+};
+
+// Four output waves: one per 16 tokens (and, in fp32's shorter chunks, per half of the value tile); four
+// state waves, of about the same length.
+template <typename T, int KD, int VT> struct WalkShape {
   typedef Lin<T> L;
-  static constexpr int LDK = KD + L::PAD, LDV = VT + L::PAD;
-  static constexpr int kK = C * LDK, kV = C * LDV, kS = VT * LDK;     // elements
+  static constexpr int C = sizeof(T) == 4 ? 32 : 64;
+  static constexpr int NTT = C / 16, NVP = 4 / NTT;                   // output waves: token tiles x value parts
+  static constexpr int NO = VT / 16 / NVP;                            // value tiles of an output wave
+  typedef StateShape<KD, VT, 4> S;
+  static_assert(NO >= L::NACC, "tile too small for the waves");
+  // waves per SIMD that the registers are cut to.  A workgroup of 8 waves at up to 256 registers holds
+  // both roles' pipelines without spilling; narrower keys leave room for two workgroups per CU.
+  static constexpr int EU = KD == 128 ? 2 : 4;
+  static constexpr int kK = Tile<T, C, KD>::ELEMS, kV = Tile<T, C, VT>::ELEMS, kS = VT * (KD + L::PAD);
+  static constexpr int kC = 2 * kK + kV;                              // a chunk's k, v and q
+  // chunks in LDS: three (a copy has two chunks' time to arrive) where one workgroup has the CU for
+  // itself anyway and they fit
+  static constexpr int NS = sizeof(T) * (3 * kC + 2 * kS) <= 160 * 1024 && EU == 2 ? 3 : 2;
 };
 
 // Workgroup -> (head and segment, value tile): the value tiles of one head and segment read the same
@@ -343,20 +489,24 @@ __device__ __forceinline__ void walk_block(int b, int m, int ntile, int* idx, in
   }
 }
 
-template <typename T, int KD, int VT, int C, bool REV, bool PK>
-__global__ void __launch_bounds__(512) decay_walk_kernel(WalkArgs a) {
+// PQ, PK, PV: the operand is kept in 8 bits.
+template <typename T, int KD, int VT, bool REV, bool PQ, bool PK, bool PV>
+__global__ void __launch_bounds__(512, (WalkShape<T, KD, VT>::EU)) decay_walk_kernel(WalkArgs a) {
   typedef Lin<T> L;
-  typedef WalkShape<T, KD, VT, C> W;
-  constexpr int NT = 512;
-  constexpr int NTT = C / 16, NVP = 4 / NTT;                 // token tiles; value parts of the output waves
-  constexpr int NO = VT / 16 / NVP;                          // value tiles of an output wave
-  constexpr int NKS = KD / 32, NVS = VT / 32;                // tiles of a state wave (2 x 2 waves)
-  constexpr int NQ = KD / L::DG;
-  __shared__ __align__(16) T smem[2 * (W::kK + W::kV + W::kS)];
+  typedef typename L::frag frag;
+  typedef WalkShape<T, KD, VT> W;
+  constexpr int C = W::C, NT = 512, NTT = W::NTT, NO = W::NO, NKS = W::S::NK, NVS = W::S::NV;
+  constexpr int NQ = KD / L::DG, ND = C / L::DG;
+  constexpr int NH = NQ > 1 ? 2 : 1, HQ = NQ / NH;             // the read's contraction in NH steps
+  static_assert(ND == 2, "two groups of tokens per chunk");
+  constexpr bool DMA = !(PQ || PK || PV);                      // 8-bit operands go through registers
+  constexpr int NS = DMA ? W::NS : 2;
+  __shared__ __align__(16) T smem[NS * W::kC + 2 * W::kS];
   static_assert(sizeof(smem) <= 160 * 1024, "LDS of one gfx950 workgroup exceeded");
-  T* const sK = smem;
-  T* const sV = sK + 2 * W::kK;
-  T* const sS = sV + 2 * W::kV;
+  T* const sS = smem + NS * W::kC;
+  const auto tile_k = [&](int ci) { return smem + ci % NS * W::kC; };
+  const auto tile_v = [&](int ci) { return smem + ci % NS * W::kC + W::kK; };
+  const auto tile_q = [&](int ci) { return smem + ci % NS * W::kC + W::kK + W::kV; };
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int ntile = (a.V + VT - 1) / VT;
@@ -370,136 +520,209 @@ __global__ void __launch_bounds__(512) decay_walk_kernel(WalkArgs a) {
   const int nch = (t_end - t_beg + C - 1) / C;
   const int n_last = t_end - t_beg - (nch - 1) * C;          // tokens of the chunk that may be short
   const float g = a.log_decay[h], g2 = g * kLog2e;
+  const size_t hs = (size_t)a.K * a.V;
+  T* const oh = reinterpret_cast<T*>(a.o) + (size_t)bh * a.T * a.V;
 
-  const HeadRows<T, PK> hq(a.q, a.q_sc, bh, a.T, a.K, t_end), hk(a.k, a.k_sc, bh, a.T, a.K, t_end),
-      hv(a.v, a.v_sc, bh, a.T, a.V, t_end);
+  const HeadRows<T, PK> hk(a.k, a.k_sc, bh, a.T, a.K, t_end);
+  const HeadRows<T, PV> hv(a.v, a.v_sc, bh, a.T, a.V, t_end);
   const auto chunk_t0 = [&](int ci) { return t_beg + (REV ? nch - 1 - ci : ci) * C; };
   const auto chunk_n = [&](int ci) { return (REV ? ci == 0 : ci == nch - 1) ? n_last : C; };
 
-  const bool is_state = wave >= 4;
-  // state waves
-  const int sw = wave & 3, ct0 = (sw & 1) * NKS, sv0 = (sw >> 1) * NVS;
-  StateTile<T, C, NKS, NVS, REV> st;
-  // output waves
-  const int ti = wave % NTT, ov0 = (wave & 3) / NTT * NO;
-  Piece<T> qn[NQ];
-  typename L::frag qf[NQ];
-  float pf[NTT][4];
-  Decay2 an{0.f, 0.f}, an_short{0.f, 0.f};
-  const int tl = 16 * ti + (lane & 15);
+  const HeadRows<T, PQ> hq(a.q, a.q_sc, bh, a.T, a.K, t_end);
 
-  const size_t hs = (size_t)a.K * a.V;
-  if (is_state) {
+  // Both roles bring in the chunks.  Copies: chunk ci + NS - 1 is requested when chunk ci begins (its place
+  // was last read in chunk ci - 1) and has arrived before chunk ci + NS - 2 ends.  Through registers: chunk
+  // ci + 1 is written to LDS when chunk ci ends, and chunk ci + 2 requested.
+  const Copy<T, C, KD, VT, KD, 8> copy(wave, lane, a.K, a.V, v0);
+  Stage<T, PK, C, KD, NT> pk;
+  Stage<T, PV, C, VT, NT> pv;
+  Stage<T, PQ, C, KD, NT> pq;
+  const auto request = [&](int ci) {
+    if (ci < nch) {
+      const int t0 = chunk_t0(ci);
+      if constexpr (DMA) {
+        copy.issue(hk.words, hv.words, hq.words, t0, a.K, a.V, tile_k(ci), wave);
+      } else {
+        pk.load(hk, t0, 0, tid);
+        pv.load(hv, t0, v0, tid);
+        pq.load(hq, t0, 0, tid);
+      }
+    }
+  };
+  const auto begin = [&](int ci) {
+    if constexpr (DMA) request(ci + NS - 1);
+  };
+  const auto stage = [&](int ci) {
+    if (ci < nch) {
+      pk.store(tile_k(ci), tid);
+      pv.store(tile_v(ci), tid);
+      pq.store(tile_q(ci), tid);
+    }
+    request(ci + 1);
+  };
+  // end of chunk ci; an output wave's stores of the chunk (STORES) are behind the copies that it waits for
+  constexpr int COPIES = Copy<T, C, KD, VT, KD, 8>::MIN, STORES = NO / L::NACC;
+  const auto end = [&](int ci) {
+    if constexpr (DMA) {
+      const bool more = NS == 3 && ci + 2 < nch;
+      if (wave >= 4) {
+        if (more) wait_vm_but<COPIES>();
+        else wait_vm_but<0>();
+      } else {
+        if (more) wait_vm_but<COPIES + STORES>();
+        else wait_vm_but<STORES>();
+      }
+    } else {
+      stage(ci + 1);
+    }
+    chunk_barrier();
+  };
+  request(0);
+  if constexpr (DMA && NS == 3) request(1);
+
+  if (wave >= 4) {
+    const int rw = wave - 4;
+    const int ct0 = rw / W::S::WV * NKS, sv0 = rw % W::S::WV * NVS;
+    StateTile<T, KD, VT, C, NKS, NVS, REV> st;
     const float* S0 = a.nseg > 1 ? a.seg_state + ((size_t)bh * a.nseg + seg) * hs
                                  : (a.state_in ? a.state_in + (size_t)bh * hs : nullptr);
     if (S0) st.load(S0, a.si_k, a.si_v, ct0, v0 + 16 * sv0, a.K, a.V, lane);
     else st.zero();
-    an = decay_pow2(g, C);
-    an_short = decay_pow2(g, nch > 0 ? n_last : 0);
-    if (nch > 0) st.image(sS, W::LDK, ct0, 16 * sv0, lane);
-  } else {
-#pragma unroll
-    for (int s = 0; s < NTT; ++s)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int j = 16 * s + 4 * (lane >> 4) + r, d = REV ? j - tl : tl - j;
-        pf[s][r] = d < 0 ? 0.0f : a.c * decay_pow(g2, d);
-      }
-    if (nch > 0) {
-#pragma unroll
-      for (int x = 0; x < NQ; ++x) qn[x] = hq.load(chunk_t0(0) + tl, x * L::DG + (L::DG / 4) * (lane >> 4));
-    }
-  }
-  Stage<T, PK, C, KD, NT> pk;
-  Stage<T, PK, C, VT, NT> pv;
-  if (nch > 0) {
-    pk.load(hk, chunk_t0(0), 0, tid);
-    pv.load(hv, chunk_t0(0), v0, tid);
-    pk.store(hk, sK, W::LDK, tid);
-    pv.store(hv, sV, W::LDV, tid);
-    if (nch > 1) {
-      pk.load(hk, chunk_t0(1), 0, tid);
-      pv.load(hv, chunk_t0(1), v0, tid);
-    }
-  }
-  lds_barrier();
-
-  T* const oh = reinterpret_cast<T*>(a.o) + (size_t)bh * a.T * a.V;
-  const __amdgpu_buffer_rsrc_t ro = make_rsrc(oh, (unsigned)t_end * (unsigned)(a.V * sizeof(T)));
-
-  for (int ci = 0; ci < nch; ++ci) {
-    const int cur = ci & 1, n = chunk_n(ci), t0 = chunk_t0(ci);
-    const T* cK = sK + cur * W::kK;
-    const T* cV = sV + cur * W::kV;
-    if (is_state) {
+    const Decay2 an = decay_pow2(g, C), an_short = decay_pow2(g, nch > 0 ? n_last : 0);
+    if (nch > 0) st.image(sS, ct0, 16 * sv0, lane);
+    if constexpr (!DMA) stage(0);
+    wait_vm_all();
+    chunk_barrier();
+    for (int ci = 0; ci < nch; ++ci) {
+      const int n = chunk_n(ci);
+      begin(ci);
       st.factors(g2, a.u, n, lane);
-      st.update(cK, W::LDK, cV, W::LDV, ct0, sv0, n == C ? an : an_short, lane);
-      if (ci + 1 < nch) st.image(sS + (cur ^ 1) * W::kS, W::LDK, ct0, 16 * sv0, lane);
-    } else {
-#pragma unroll
-      for (int x = 0; x < NQ; ++x) qf[x] = __builtin_bit_cast(typename L::frag, qn[x].elems(hq.packed));
+      st.update(tile_k(ci), tile_v(ci), ct0, sv0, n == C ? an : an_short, lane);
       if (ci + 1 < nch) {
-#pragma unroll
-        for (int x = 0; x < NQ; ++x) qn[x] = hq.load(chunk_t0(ci + 1) + tl, x * L::DG + (L::DG / 4) * (lane >> 4));
+        st.image(sS + (ci + 1 & 1) * W::kS, ct0, 16 * sv0, lane);
+        end(ci);
       }
-      const T* cS = sS + cur * W::kS;
-      floatx4 acc[NO];
+    }
+    if (a.state_out && seg == (REV ? 0 : a.nseg - 1))
+      st.save(a.state_out + (size_t)bh * hs, a.si_k, a.si_v, ct0, v0 + 16 * sv0, a.K, a.V, lane);
+  } else {
+    const int ti = wave % NTT, ov0 = wave / NTT * NO;
+    const int tl = 16 * ti + (lane & 15);
+    const __amdgpu_buffer_rsrc_t ro = make_rsrc(oh, (unsigned)t_end * (unsigned)(a.V * sizeof(T)));
+    // c a^{|i - j|} of a score: on the diagonal tile pd (0 where the mask cuts it off), k tiles off it
+    // po a^{16 (k - 1)}
+    float pd[4], po[4], far[NTT];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int j = 4 * (lane >> 4) + r, d = REV ? j - (lane & 15) : (lane & 15) - j;
+      pd[r] = d < 0 ? 0.0f : a.c * decay_pow(g2, d);
+      po[r] = a.c * decay_pow(g2, 16 + d);
+    }
+#pragma unroll
+    for (int s = 0; s < NTT; ++s) {
+      const int k = REV ? s - ti : ti - s;
+      far[s] = k < 1 ? 0.0f : uniform(decay_pow(g2, 16 * (k - 1)));
+    }
+    if constexpr (!DMA) stage(0);
+    wait_vm_all();
+    chunk_barrier();
+    for (int ci = 0; ci < nch; ++ci) {
+      const int n = chunk_n(ci);
+      const T* cK = tile_k(ci);
+      const T* cV = tile_v(ci);
+      const T* cS = sS + (ci & 1) * W::kS;
+      begin(ci);
+      frag qf[NQ];
+#pragma unroll
+      for (int x = 0; x < NQ; ++x) qf[x] = L::template nat<KD, false>(tile_q(ci), tl, x * L::DG, lane);
+      frag kf[L::NACC][NQ], sf[HQ][NO], vf[NO];
+      floatx4 p[L::NACC], acc[NO];
+      const auto read_k = [&](int d) {
+#pragma unroll
+        for (int x = 0; x < NQ; ++x)
+#pragma unroll
+          for (int s = 0; s < L::NACC; ++s)
+            kf[s][x] = L::template nat<KD, false>(cK, d * L::DG + 16 * s + (lane & 15), x * L::DG, lane);
+      };
+      // scores (keys x tokens) of token group d; the tiles that the mask cuts off come out as zeros.
+      // They are rounded to bf16 for the product with V (fp32 walks keep them): one rounding, 2^-8.
+      const auto scores = [&](int d) {
+#pragma unroll
+        for (int s = 0; s < L::NACC; ++s) p[s] = zero4();
+#pragma unroll
+        for (int x = 0; x < NQ; ++x)
+#pragma unroll
+          for (int s = 0; s < L::NACC; ++s) p[s] = L::mma(kf[s][x], qf[x], p[s]);
+      };
+      const auto masked = [&](int d) {
+#pragma unroll
+        for (int s = 0; s < L::NACC; ++s)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int st = d * L::NACC + s;
+            p[s][r] *= st == ti ? pd[r] : po[r] * far[st];
+          }
+        return L::from_acc(p);
+      };
+      const auto read_s = [&](int hx) {
+#pragma unroll
+        for (int x = 0; x < HQ; ++x)
+#pragma unroll
+          for (int j = 0; j < NO; ++j)
+            sf[x][j] = L::template nat<KD, true>(cS, L::row_of(ov0 + j, lane & 15), (hx * HQ + x) * L::DG, lane);
+      };
+      const auto read_out = [&](int hx) {
+#pragma unroll
+        for (int x = 0; x < HQ; ++x)
+#pragma unroll
+          for (int j = 0; j < NO; ++j) acc[j] = L::mma(sf[x][j], qf[hx * HQ + x], acc[j]);
+      };
+      const auto read_v = [&](int d) {
+#pragma unroll
+        for (int j = 0; j < NO; ++j) vf[j] = L::template tr<VT, true>(cV, ov0 + j, d * L::DG, lane);
+      };
+      const auto value_out = [&](frag b) {
+#pragma unroll
+        for (int j = 0; j < NO; ++j) acc[j] = L::mma(vf[j], b, acc[j]);
+      };
+      // O^T = r a^e S^T Q + V^T scores: token groups 0 and 1 reach this wave's tokens, or only the one
+      // that holds them (REV: 1, else 0)
+      const bool both = REV ? ti < L::NACC : ti >= L::NACC;
+      constexpr int D0 = REV ? 1 : 0, D1 = 1 - D0;
 #pragma unroll
       for (int j = 0; j < NO; ++j) acc[j] = zero4();
-      // O^T = S^T Q, scaled by the token's read factor (the token is the lane's column)
-#pragma unroll
-      for (int x = 0; x < NQ; ++x)
-#pragma unroll
-        for (int j = 0; j < NO; ++j)
-          acc[j] = L::mma(L::nat(cS + L::row_of(ov0 + j, lane & 15) * W::LDK, x * L::DG, lane), qf[x], acc[j]);
+      read_k(D0);
+      read_s(0);
+      scores(D0);
+      frag b0 = masked(D0), b1;
+      if (both) read_k(D1);
+      read_out(0);
+      if (NH > 1) read_s(1);
+      if (both) {
+        scores(D1);
+        b1 = masked(D1);
+      }
+      read_v(D0);
+      if (NH > 1) read_out(1);
       const int e = REV ? n - 1 - tl : tl + 1;
       const float rf = a.r * decay_pow(g2, e < 0 ? 0 : e);
 #pragma unroll
       for (int j = 0; j < NO; ++j) acc[j] *= rf;
-      // scores (keys x tokens) of the tiles the mask reaches, then O^T += V^T scores
-#pragma unroll
-      for (int d = 0; d < C / L::DG; ++d) {
-        const int s0 = d * L::NACC;
-        if (REV ? s0 + L::NACC - 1 >= ti : s0 <= ti) {
-          floatx4 p[L::NACC];
-#pragma unroll
-          for (int s = 0; s < L::NACC; ++s) {
-            p[s] = zero4();
-            if (REV ? s0 + s >= ti : s0 + s <= ti) {
-#pragma unroll
-              for (int x = 0; x < NQ; ++x)
-                p[s] = L::mma(L::nat(cK + (16 * (s0 + s) + (lane & 15)) * W::LDK, x * L::DG, lane), qf[x], p[s]);
-#pragma unroll
-              for (int r = 0; r < 4; ++r) p[s][r] *= pf[s0 + s][r];
-            }
-          }
-          // scores are rounded to bf16 for the product (fp32 walks keep them): one rounding, 2^-9
-          const typename L::frag b = L::from_acc(p);
-#pragma unroll
-          for (int j = 0; j < NO; ++j)
-            acc[j] = L::mma(L::template tr<true>(cV, W::LDV, ov0 + j, d * L::DG, lane), b, acc[j]);
-        }
+      value_out(b0);
+      if (both) {
+        read_v(D1);
+        value_out(b1);
       }
-      const unsigned row = (unsigned)(t0 + tl) * (unsigned)(a.V * sizeof(T));
+      const unsigned row = (unsigned)(chunk_t0(ci) + tl) * (unsigned)(a.V * sizeof(T));
 #pragma unroll
       for (int j = 0; j < NO; j += L::NACC) {
         const int col = v0 + L::row_of(ov0 + j, 4 * (lane >> 4));
         const unsigned off = col < a.V ? row + (unsigned)(col * sizeof(T)) : 0xfffffff0u;
         __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, L::from_acc(acc + j)), ro, off, 0, 0);
       }
-    }
-    if (ci + 1 < nch) {
-      pk.store(hk, sK + (cur ^ 1) * W::kK, W::LDK, tid);
-      pv.store(hv, sV + (cur ^ 1) * W::kV, W::LDV, tid);
-      if (ci + 2 < nch) {
-        pk.load(hk, chunk_t0(ci + 2), 0, tid);
-        pv.load(hv, chunk_t0(ci + 2), v0, tid);
-      }
-      lds_barrier();
+      if (ci + 1 < nch) end(ci);
     }
   }
-  if (is_state && a.state_out && seg == (REV ? 0 : a.nseg - 1))
-    st.save(a.state_out + (size_t)bh * hs, a.si_k, a.si_v, ct0, v0 + 16 * sv0, a.K, a.V, lane);
   if (a.zero_tail) {
     const int e_end = (int)min((long long)seg * a.seglen + a.seglen, (long long)a.T);
     const int e_beg = max(len, seg * a.seglen);
@@ -509,18 +732,21 @@ __global__ void __launch_bounds__(512) decay_walk_kernel(WalkArgs a) {
   }
 }
 
-// Local end state of every segment but the last in walking order.
-template <typename T, int KD, int VT, int C, bool REV, bool PK>
-__global__ void __launch_bounds__(256) decay_segment_kernel(SegArgs a) {
-  typedef WalkShape<T, KD, VT, C> W;
-  constexpr int NT = 256, NKS = KD / 32, NVS = VT / 32;
-  __shared__ __align__(16) T smem[2 * (W::kK + W::kV)];
-  T* const sK = smem;
-  T* const sV = sK + 2 * W::kK;
+constexpr int kSegChunks = 3;                    // chunks in LDS
+
+// Local end state of one segment (not the last in walking order) for one value tile.
+template <typename T, int KD, int VT, int NW, bool REV, bool PK, bool PV>
+__device__ __forceinline__ void segment_state(const SegArgs& a, int block, T* smem) {
+  typedef WalkShape<T, KD, VT> W;
+  typedef StateShape<KD, VT, NW> S;
+  constexpr int C = W::C, NT = 64 * NW, NS = kSegChunks;
+  constexpr bool DMA = !(PK || PV);
+  const auto tile_k = [&](int ci) { return smem + ci % NS * (W::kK + W::kV); };
+  const auto tile_v = [&](int ci) { return smem + ci % NS * (W::kK + W::kV) + W::kK; };
   const int tid = threadIdx.x, lane = tid & 63, sw = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int ntile = (a.V + VT - 1) / VT;
   int idx, tile;
-  walk_block(blockIdx.x, a.BH * (a.nseg - 1), ntile, &idx, &tile);
+  walk_block(block, a.BH * (a.nseg - 1), ntile, &idx, &tile);
   const int bh = idx / (a.nseg - 1), seg = idx - bh * (a.nseg - 1) + (REV ? 1 : 0), v0 = tile * VT;
   int len = a.T;
   if (a.lengths) len = min(max(a.lengths[bh / a.H], 0), a.T);
@@ -528,67 +754,115 @@ __global__ void __launch_bounds__(256) decay_segment_kernel(SegArgs a) {
   const int nch = (t_end - t_beg + C - 1) / C;
   const int n_last = t_end - t_beg - (nch - 1) * C;
   const float g = a.log_decay[bh % a.H], g2 = g * kLog2e;
-  const HeadRows<T, PK> hk(a.k, a.k_sc, bh, a.T, a.K, t_end), hv(a.v, a.v_sc, bh, a.T, a.V, t_end);
+  const HeadRows<T, PK> hk(a.k, a.k_sc, bh, a.T, a.K, t_end);
+  const HeadRows<T, PV> hv(a.v, a.v_sc, bh, a.T, a.V, t_end);
   const auto chunk_t0 = [&](int ci) { return t_beg + (REV ? nch - 1 - ci : ci) * C; };
   const auto chunk_n = [&](int ci) { return (REV ? ci == 0 : ci == nch - 1) ? n_last : C; };
-  const int ct0 = (sw & 1) * NKS, sv0 = (sw >> 1) * NVS;
-  StateTile<T, C, NKS, NVS, REV> st;
+  const int ct0 = sw / S::WV * S::NK, sv0 = sw % S::WV * S::NV;
+  StateTile<T, KD, VT, C, S::NK, S::NV, REV> st;
   st.zero();
-  const Decay2 an = decay_pow2(g, C), an_short = decay_pow2(g, nch > 0 ? n_last : 0);
+  const Copy<T, C, KD, VT, 0, NW> copy(sw, lane, a.K, a.V, v0);
   Stage<T, PK, C, KD, NT> pk;
-  Stage<T, PK, C, VT, NT> pv;
-  if (nch > 0) {
-    pk.load(hk, chunk_t0(0), 0, tid);
-    pv.load(hv, chunk_t0(0), v0, tid);
-  }
-  for (int ci = 0; ci < nch; ++ci) {
-    const int cur = ci & 1, n = chunk_n(ci);
-    // the buffer written here was last read two chunks ago, before the previous barrier
-    pk.store(hk, sK + cur * W::kK, W::LDK, tid);
-    pv.store(hv, sV + cur * W::kV, W::LDV, tid);
-    if (ci + 1 < nch) {
-      pk.load(hk, chunk_t0(ci + 1), 0, tid);
-      pv.load(hv, chunk_t0(ci + 1), v0, tid);
+  Stage<T, PV, C, VT, NT> pv;
+  const auto request = [&](int ci) {
+    if (ci < nch) {
+      const int t0 = chunk_t0(ci);
+      if constexpr (DMA) {
+        copy.issue(hk.words, hv.words, hk.words, t0, a.K, a.V, tile_k(ci), sw);
+      } else {
+        pk.load(hk, t0, 0, tid);
+        pv.load(hv, t0, v0, tid);
+      }
     }
-    lds_barrier();
+  };
+  request(0);
+  if constexpr (DMA) request(1);
+  const Decay2 an = decay_pow2(g, C), an_short = decay_pow2(g, nch > 0 ? n_last : 0);
+  for (int ci = 0; ci < nch; ++ci) {
+    const int n = chunk_n(ci);
+    if constexpr (DMA) {
+      // chunk ci has arrived; the one after it, requested a chunk later, may not have
+      if (ci + 1 < nch) wait_vm_but<Copy<T, C, KD, VT, 0, NW>::MIN>();
+      else wait_vm_but<0>();
+      chunk_barrier();
+      request(ci + 2);                           // its place was last read in chunk ci - 1
+    } else {
+      pk.store(tile_k(ci), tid);
+      pv.store(tile_v(ci), tid);
+      request(ci + 1);
+      chunk_barrier();
+    }
     st.factors(g2, a.u, n, lane);
-    st.update(sK + cur * W::kK, W::LDK, sV + cur * W::kV, W::LDV, ct0, sv0, n == C ? an : an_short, lane);
+    st.update(tile_k(ci), tile_v(ci), ct0, sv0, n == C ? an : an_short, lane);
   }
   st.save(a.seg_state + ((size_t)bh * a.nseg + seg) * a.K * a.V, a.V, 1, ct0, v0 + 16 * sv0, a.K, a.V, lane);
 }
 
-// ------------------------------------------------------------------ launchers
-template <typename T> constexpr int walk_chunk() { return std::is_same<T, float>::value ? 32 : 64; }
+// The segments of S (first `nblock` workgroups) and, in a backward pass, those of dL/dS behind them: one
+// launch, as either alone may leave half of the chip idle.  PACK: q, k and v are kept in 8 bits.
+template <int KD, int VT> constexpr int seg_waves() { return KD == 128 && VT == 64 ? 8 : 4; }
+template <typename T, int KD, int VT, bool PACK>
+__global__ void __launch_bounds__((64 * seg_waves<KD, VT>())) decay_segment_kernel(SegArgs s, SegArgs r, int nblock) {
+  typedef WalkShape<T, KD, VT> W;
+  __shared__ __align__(16) T smem[kSegChunks * (W::kK + W::kV)];
+  constexpr int NW = seg_waves<KD, VT>();
+  if ((int)blockIdx.x < nblock) segment_state<T, KD, VT, NW, false, PACK, PACK>(s, blockIdx.x, smem);
+  else segment_state<T, KD, VT, NW, true, PACK, false>(r, blockIdx.x - nblock, smem);
+}
 
-template <typename T, int KD, int VT, bool REV, bool PK>
+// ------------------------------------------------------------------ launchers
+// Which operands of a walk are kept in 8 bits: none, or those of a gradient whose q, k, v are.
+enum WalkKind { kFwd, kRev, kFwdDq8, kRevDk8, kRevDv8 };
+
+template <typename T, int KD, int VT, bool REV, bool PQ, bool PK, bool PV>
 hipError_t launch_walk_inst(const WalkArgs& a, hipStream_t s) {
-  constexpr int C = walk_chunk<T>();
-  const auto kern = decay_walk_kernel<T, KD, VT, C, REV, PK>;
   const int blocks = a.BH * a.nseg * ((a.V + VT - 1) / VT);
-  hipLaunchKernelGGL(kern, dim3(blocks), dim3(512), 0, s, a);
+  hipLaunchKernelGGL((decay_walk_kernel<T, KD, VT, REV, PQ, PK, PV>), dim3(blocks), dim3(512), 0, s, a);
   return hipGetLastError();
 }
 
-template <typename T, int KD, int VT, bool REV, bool PK>
-hipError_t launch_segments_inst(const SegArgs& a, hipStream_t s) {
-  constexpr int C = walk_chunk<T>();
-  const auto kern = decay_segment_kernel<T, KD, VT, C, REV, PK>;
-  const int blocks = a.BH * (a.nseg - 1) * ((a.V + VT - 1) / VT);
-  hipLaunchKernelGGL(kern, dim3(blocks), dim3(256), 0, s, a);
+template <typename T, int KD, int VT, bool PACK>
+hipError_t launch_segments_inst(const SegArgs& st, const SegArgs* r, hipStream_t s) {
+  const int blocks = st.BH * (st.nseg - 1) * ((st.V + VT - 1) / VT);
+  hipLaunchKernelGGL((decay_segment_kernel<T, KD, VT, PACK>), dim3(r ? 2 * blocks : blocks),
+                     dim3(64 * seg_waves<KD, VT>()), 0, s, st, r ? *r : st, blocks);
   return hipGetLastError();
 }
 
 // Instances by padded key width KD; the value tile is 64 columns, or 32 where V <= 32.
-template <typename T, int KD, bool PK>
-hipError_t launch_walk_kd(const WalkArgs& a, bool rev, hipStream_t s) {
-  if (a.V <= 32) return rev ? launch_walk_inst<T, KD, 32, true, PK>(a, s) : launch_walk_inst<T, KD, 32, false, PK>(a, s);
-  return rev ? launch_walk_inst<T, KD, 64, true, PK>(a, s) : launch_walk_inst<T, KD, 64, false, PK>(a, s);
+template <typename T, int KD, int VT> hipError_t launch_walk_vt(const WalkArgs& a, WalkKind kind, hipStream_t s) {
+  switch (kind) {
+    case kFwd: return launch_walk_inst<T, KD, VT, false, false, false, false>(a, s);
+    case kRev: return launch_walk_inst<T, KD, VT, true, false, false, false>(a, s);
+    case kFwdDq8: return launch_walk_inst<T, KD, VT, false, false, true, true>(a, s);
+    case kRevDk8: return launch_walk_inst<T, KD, VT, true, true, false, true>(a, s);
+    case kRevDv8: return launch_walk_inst<T, KD, VT, true, true, true, false>(a, s);
+  }
+  return hipErrorInvalidValue;
 }
-template <typename T, int KD, bool PK>
-hipError_t launch_segments_kd(const SegArgs& a, bool rev, hipStream_t s) {
-  if (a.V <= 32)
-    return rev ? launch_segments_inst<T, KD, 32, true, PK>(a, s) : launch_segments_inst<T, KD, 32, false, PK>(a, s);
-  return rev ? launch_segments_inst<T, KD, 64, true, PK>(a, s) : launch_segments_inst<T, KD, 64, false, PK>(a, s);
+template <typename T, int KD> hipError_t launch_walk_kd(const WalkArgs& a, WalkKind kind, hipStream_t s) {
+  return a.V <= 32 ? launch_walk_vt<T, KD, 32>(a, kind, s) : launch_walk_vt<T, KD, 64>(a, kind, s);
 }
+
+// Local states of S (from k, v) and, r non-null, of dL/dS (from q, d_o); packed: q, k, v are in 8 bits.
+template <typename T, int KD>
+hipError_t launch_segments_kd(const SegArgs& st, const SegArgs* r, bool packed, hipStream_t s) {
+  if (st.V <= 32)
+    return packed ? launch_segments_inst<T, KD, 32, true>(st, r, s) : launch_segments_inst<T, KD, 32, false>(st, r, s);
+  return packed ? launch_segments_inst<T, KD, 64, true>(st, r, s) : launch_segments_inst<T, KD, 64, false>(st, r, s);
+}
+
+#ifndef KDA_DECAY_INSTANCES                       // defined where the instances are compiled
+#define KDA_DECAY_EXTERN(T, KD)                                                              \
+  extern template hipError_t launch_walk_kd<T, KD>(const WalkArgs&, WalkKind, hipStream_t); \
+  extern template hipError_t launch_segments_kd<T, KD>(const SegArgs&, const SegArgs*, bool, hipStream_t);
+KDA_DECAY_EXTERN(float, 32)
+KDA_DECAY_EXTERN(float, 64)
+KDA_DECAY_EXTERN(float, 128)
+KDA_DECAY_EXTERN(bf16_t, 32)
+KDA_DECAY_EXTERN(bf16_t, 64)
+KDA_DECAY_EXTERN(bf16_t, 128)
+#undef KDA_DECAY_EXTERN
+#endif
 
 }  // namespace kda

@@ -29,33 +29,40 @@ size_t decay_states_bytes(int B, int H, int K, int V, const DecayPlan& p) {
 }
 
 // Local end states -> states at the segments' starts, in place and in walking order:
-// x[s] <- S, S <- a^{n_s} S + (old x[s]).  One thread per state element; the locals of eight
-// segments are fetched before they are used, so the latency of memory is paid once in eight.
-template <bool REV>
-__global__ void __launch_bounds__(256) decay_join_kernel(float* __restrict__ x, const float* __restrict__ state_in,
+// x[s] <- S, S <- a^{n_s} S + (old x[s]).  One thread per state element; the locals of 16 segments are
+// fetched before the first is used, so the latency of memory is paid once in 16.  The first `nblock`
+// workgroups join S, those behind them (a backward pass) dL/dS from the last segment on.
+struct JoinArgs {
+  float* x;
+  const float* start;
+};
+__global__ void __launch_bounds__(256) decay_join_kernel(JoinArgs s, JoinArgs r, int nblock,
                                                          const float* __restrict__ log_decay,
                                                          const int* __restrict__ lengths, int H, int T, int nseg,
                                                          int seglen, int KV, int per_head) {
-  constexpr int BATCH = 8;
-  const int bh = blockIdx.x / per_head, e = (blockIdx.x - bh * per_head) * 256 + threadIdx.x;
+  constexpr int BATCH = 16;
+  const bool rev = (int)blockIdx.x >= nblock;
+  const int block = rev ? blockIdx.x - nblock : blockIdx.x;
+  const JoinArgs a = rev ? r : s;
+  const int bh = block / per_head, e = (block - bh * per_head) * 256 + threadIdx.x;
   if (e >= KV) return;
   int len = T;
   if (lengths) len = min(max(lengths[bh / H], 0), T);
   const float g = log_decay[bh % H];
-  float* p = x + (size_t)bh * nseg * KV + e;
-  float S = state_in ? state_in[(size_t)bh * KV + e] : 0.0f;
+  float* p = a.x + (size_t)bh * nseg * KV + e;
+  float S = a.start ? a.start[(size_t)bh * KV + e] : 0.0f;
   const Decay2 whole = decay_pow2(g, seglen);
   for (int s0 = 0; s0 < nseg; s0 += BATCH) {
     float loc[BATCH];
 #pragma unroll
     for (int b = 0; b < BATCH; ++b) {
-      const int s = s0 + b, seg = REV ? nseg - 1 - s : s;
-      loc[b] = s < nseg - 1 ? p[(size_t)seg * KV] : 0.0f;    // the last one has no local state
+      const int i = s0 + b, seg = rev ? nseg - 1 - i : i;
+      loc[b] = i < nseg - 1 ? p[(size_t)seg * KV] : 0.0f;    // the last one has no local state
     }
 #pragma unroll
     for (int b = 0; b < BATCH; ++b) {
-      const int s = s0 + b, seg = REV ? nseg - 1 - s : s;
-      if (s < nseg) {
+      const int i = s0 + b, seg = rev ? nseg - 1 - i : i;
+      if (i < nseg) {
         p[(size_t)seg * KV] = S;
         const long long left = (long long)len - (long long)seg * seglen;
         const int n = left < 0 ? 0 : (left < seglen ? (int)left : seglen);
@@ -66,30 +73,23 @@ __global__ void __launch_bounds__(256) decay_join_kernel(float* __restrict__ x, 
   }
 }
 
-static hipError_t join(bool rev, float* x, const float* state_in, const float* log_decay, const int* lengths, int B,
-                       int H, int T, int KV, const DecayPlan& p, hipStream_t s) {
-  const int per_head = (KV + 255) / 256;
-  const dim3 grid((unsigned)(B * H * per_head));
-  if (rev)
-    hipLaunchKernelGGL(decay_join_kernel<true>, grid, dim3(256), 0, s, x, state_in, log_decay, lengths, H, T, p.nseg,
-                       p.seglen, KV, per_head);
-  else
-    hipLaunchKernelGGL(decay_join_kernel<false>, grid, dim3(256), 0, s, x, state_in, log_decay, lengths, H, T, p.nseg,
-                       p.seglen, KV, per_head);
+static hipError_t join(JoinArgs st, const JoinArgs* r, const float* log_decay, const int* lengths, int B, int H, int T,
+                       int KV, const DecayPlan& p, hipStream_t s) {
+  const int per_head = (KV + 255) / 256, n = B * H * per_head;
+  hipLaunchKernelGGL(decay_join_kernel, dim3((unsigned)(r ? 2 * n : n)), dim3(256), 0, s, st, r ? *r : st, n, log_decay,
+                     lengths, H, T, p.nseg, p.seglen, KV, per_head);
   return hipGetLastError();
 }
 
-template <typename T> static hipError_t walk(const WalkArgs& a, bool rev, hipStream_t s) {
-  const bool pk = a.q_sc || a.k_sc || a.v_sc;
-  if (a.K <= 32) return pk ? launch_walk_kd<T, 32, true>(a, rev, s) : launch_walk_kd<T, 32, false>(a, rev, s);
-  if (a.K <= 64) return pk ? launch_walk_kd<T, 64, true>(a, rev, s) : launch_walk_kd<T, 64, false>(a, rev, s);
-  return pk ? launch_walk_kd<T, 128, true>(a, rev, s) : launch_walk_kd<T, 128, false>(a, rev, s);
+template <typename T> static hipError_t walk(const WalkArgs& a, WalkKind kind, hipStream_t s) {
+  if (a.K <= 32) return launch_walk_kd<T, 32>(a, kind, s);
+  if (a.K <= 64) return launch_walk_kd<T, 64>(a, kind, s);
+  return launch_walk_kd<T, 128>(a, kind, s);
 }
-template <typename T> static hipError_t segments(const SegArgs& a, bool rev, hipStream_t s) {
-  const bool pk = a.k_sc || a.v_sc;
-  if (a.K <= 32) return pk ? launch_segments_kd<T, 32, true>(a, rev, s) : launch_segments_kd<T, 32, false>(a, rev, s);
-  if (a.K <= 64) return pk ? launch_segments_kd<T, 64, true>(a, rev, s) : launch_segments_kd<T, 64, false>(a, rev, s);
-  return pk ? launch_segments_kd<T, 128, true>(a, rev, s) : launch_segments_kd<T, 128, false>(a, rev, s);
+template <typename T> static hipError_t segments(const SegArgs& st, const SegArgs* r, bool packed, hipStream_t s) {
+  if (st.K <= 32) return launch_segments_kd<T, 32>(st, r, packed, s);
+  if (st.K <= 64) return launch_segments_kd<T, 64>(st, r, packed, s);
+  return launch_segments_kd<T, 128>(st, r, packed, s);
 }
 
 template <typename T>
@@ -100,8 +100,8 @@ hipError_t launch_decay_fwd(const void* q, const void* k, const void* v, const f
   float* ws = reinterpret_cast<float*>(workspace);
   if (p.nseg > 1) {
     const SegArgs g{k, v, nullptr, nullptr, log_decay, lengths, ws, 1.0f, B * H, H, T_, K, V, p.nseg, p.seglen};
-    hipError_t e = segments<T>(g, false, s);
-    if (e == hipSuccess) e = join(false, ws, state_in, log_decay, lengths, B, H, T_, K * V, p, s);
+    hipError_t e = segments<T>(g, nullptr, false, s);
+    if (e == hipSuccess) e = join(JoinArgs{ws, state_in}, nullptr, log_decay, lengths, B, H, T_, K * V, p, s);
     if (e != hipSuccess) return e;
   }
   WalkArgs a{};
@@ -111,7 +111,7 @@ hipError_t launch_decay_fwd(const void* q, const void* k, const void* v, const f
   a.c = a.r = scale, a.u = 1.0f;
   a.si_k = V, a.si_v = 1;
   a.BH = B * H, a.H = H, a.T = T_, a.K = K, a.V = V, a.nseg = p.nseg, a.seglen = p.seglen;
-  return walk<T>(a, false, s);
+  return walk<T>(a, kFwd, s);
 }
 
 // Segment boundaries and states are those of the K x V state in all three walks: S for dq, R = dL/dS
@@ -124,14 +124,14 @@ hipError_t launch_decay_bwd(const void* q, const void* k, const void* v, const u
   const DecayPlan p = decay_plan(B, H, T_, K, V, sizeof(T) == 2);
   float* wS = reinterpret_cast<float*>(workspace);
   float* wR = wS + decay_states_bytes(B, H, K, V, p) / sizeof(float);
+  const bool packed = q_sc != nullptr;                      // q, k and v, all or none
   hipError_t e = hipSuccess;
   if (p.nseg > 1) {
-    SegArgs g{k, v, k_sc, v_sc, log_decay, lengths, wS, 1.0f, B * H, H, T_, K, V, p.nseg, p.seglen};
-    e = segments<T>(g, false, s);
-    if (e == hipSuccess) e = join(false, wS, state_in, log_decay, lengths, B, H, T_, K * V, p, s);
-    g = SegArgs{q, d_o, q_sc, nullptr, log_decay, lengths, wR, scale, B * H, H, T_, K, V, p.nseg, p.seglen};
-    if (e == hipSuccess) e = segments<T>(g, true, s);
-    if (e == hipSuccess) e = join(true, wR, d_state_out, log_decay, lengths, B, H, T_, K * V, p, s);
+    const SegArgs gs{k, v, k_sc, v_sc, log_decay, lengths, wS, 1.0f, B * H, H, T_, K, V, p.nseg, p.seglen};
+    const SegArgs gr{q, d_o, q_sc, nullptr, log_decay, lengths, wR, scale, B * H, H, T_, K, V, p.nseg, p.seglen};
+    e = segments<T>(gs, &gr, packed, s);
+    const JoinArgs jr{wR, d_state_out};
+    if (e == hipSuccess) e = join(JoinArgs{wS, state_in}, &jr, log_decay, lengths, B, H, T_, K * V, p, s);
   }
   WalkArgs a{};
   a.log_decay = log_decay, a.lengths = lengths;
@@ -141,17 +141,17 @@ hipError_t launch_decay_bwd(const void* q, const void* k, const void* v, const u
   a.state_in = state_in, a.seg_state = wS, a.state_out = nullptr, a.o = dq;
   a.c = a.r = scale, a.u = 1.0f;
   a.si_k = 1, a.si_v = V, a.K = V, a.V = K;
-  if (e == hipSuccess) e = walk<T>(a, false, s);
+  if (e == hipSuccess) e = walk<T>(a, packed ? kFwdDq8 : kFwd, s);
   // dk
   a.q = v, a.k = d_o, a.v = q, a.q_sc = v_sc, a.k_sc = nullptr, a.v_sc = q_sc;
   a.state_in = d_state_out, a.seg_state = wR, a.o = dk;
   a.c = a.u = scale, a.r = 1.0f;
-  if (e == hipSuccess) e = walk<T>(a, true, s);
+  if (e == hipSuccess) e = walk<T>(a, packed ? kRevDk8 : kRev, s);
   // dv, and the state's gradient
   a.q = k, a.k = q, a.v = d_o, a.q_sc = k_sc, a.k_sc = q_sc, a.v_sc = nullptr;
   a.state_out = dstate_in, a.o = dv;
   a.si_k = V, a.si_v = 1, a.K = K, a.V = V;
-  if (e == hipSuccess) e = walk<T>(a, true, s);
+  if (e == hipSuccess) e = walk<T>(a, packed ? kRevDv8 : kRev, s);
   return e;
 }
 

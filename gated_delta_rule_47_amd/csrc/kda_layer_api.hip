@@ -115,6 +115,8 @@ int kda_decay_attn_bwd(const void* q, const void* k, const void* v, const unsign
                        size_t workspace_bytes, int B, int H, int T, int K, int V, int dtype, void* stream) {
   if (!log_decay || !dstate_in || (T != 0 && (!q || !k || !v || !d_o || !dq || !dk || !dv)))
     return reject(KDA_ERR_NULL);
+  if (T != 0 && ((q_scales != nullptr) != (k_scales != nullptr) || (q_scales != nullptr) != (v_scales != nullptr)))
+    return reject(KDA_ERR_NULL);
   if (!valid_dtype(dtype)) return reject(KDA_ERR_DTYPE);
   if (!attn_sizes(B, H, T, K, V, dtype)) return reject(KDA_ERR_SHAPE);
   if (!aligned(q, q_scales ? 8 : 16) || !aligned(k, k_scales ? 8 : 16) || !aligned(v, v_scales ? 8 : 16) ||

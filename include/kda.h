@@ -329,9 +329,9 @@ size_t kda_decay_attn_bwd_workspace_bytes(int B, int H, int T, int K, int V, int
  * R_t = dL/dS_t = a R_{t+1} + scale q_t d_o_t^T:
  *   dq_t = scale S_t d_o_t,  dk_t = R_t v_t,  dv_t = R_t^T k_t,  dstate_in = a R_0
  * Inputs as the forward's, d_o (B,H,T,V) in `dtype`, d_state_out (B,H,K,V) f32 or NULL (= 0).
- *   q_scales, k_scales, v_scales: NULL for tensors in `dtype`; otherwise that tensor is kept in 8 bits
- *   as kda_ckpt_pack writes it (q holds the codes, 8-byte aligned, q_scales the scale bytes) and is
- *   read as the values it stands for.
+ *   q_scales, k_scales, v_scales: all NULL for tensors in `dtype`; all given (KDA_ERR_NULL otherwise)
+ *   where q, k and v are kept in 8 bits as kda_ckpt_pack writes them (q holds the codes, 8-byte aligned,
+ *   q_scales the scale bytes): they are read as the values they stand for.
  * dq, dk, dv in `dtype`, dstate_in f32; no output may overlap an input, another output or the
  * workspace (256-byte aligned, contents on entry ignored). */
 int kda_decay_attn_bwd(const void* q, const void* k, const void* v, const unsigned char* q_scales,

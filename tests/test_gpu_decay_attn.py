@@ -174,9 +174,9 @@ def test_bwd_widths(T, K, V, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("packed", [("q", "k", "v"), ("q",), ("k",), ("v",)])
-@pytest.mark.parametrize("K,V", [(8, 16), (64, 128), (128, 64)])
-def test_bwd_from_8_bits(K, V, packed, dtype):
+@pytest.mark.parametrize("K,V", [(8, 16), (16, 8), (32, 32), (64, 64), (64, 128), (128, 64), (128, 128)])
+def test_bwd_from_8_bits(K, V, dtype):
+    packed = ("q", "k", "v")
     run_bwd(2, 2, 100, K, V, dtype, packed=packed, lengths=[100, 37])
     run_bwd(1, 1, 600, K, V, dtype, packed=packed)
 

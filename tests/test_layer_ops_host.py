@@ -106,10 +106,11 @@ def test_decay_attn_bwd_refusals():
     for name in ("q", "k", "v", "g", "do", "dq", "dk", "dv", "d0"):
         assert call(**{name: None}) == NULL, name
     for kw, status in ((dict(dt=-1), DTYPE), (dict(V=7), SHAPE), (dict(q=P(q.value + 8)), ALIGN),
-                       (dict(q=P(q.value + 4), qs=qs), ALIGN), (dict(do=P(do.value + 2)), ALIGN),
+                       (dict(q=P(q.value + 4), qs=qs, ks=ks, vs=vs), ALIGN), (dict(qs=qs), NULL),
+                       (dict(ks=ks, vs=vs), NULL), (dict(do=P(do.value + 2)), ALIGN),
                        (dict(ws=None), WORKSPACE), (dict(nws=64), WORKSPACE), (dict(dq=q), ALIAS), (dict(dk=do), ALIAS),
-                       (dict(dv=dk), ALIAS), (dict(d0=ds), ALIAS), (dict(d0=s0), ALIAS), (dict(dq=qs, qs=qs), ALIAS),
-                       (dict(ws=dq), ALIAS), (dict(ws=vs, vs=vs), ALIAS), (dict(dk=g), ALIAS)):
+                       (dict(dv=dk), ALIAS), (dict(d0=ds), ALIAS), (dict(d0=s0), ALIAS), (dict(dq=qs, qs=qs, ks=ks, vs=vs), ALIAS),
+                       (dict(ws=dq), ALIAS), (dict(ws=vs, qs=qs, ks=ks, vs=vs), ALIAS), (dict(dk=g), ALIAS)):
         assert call(**kw) == status, kw
 
 
@@ -170,7 +171,7 @@ def test_binding_refuses_before_the_library():
         with pytest.raises(err):
             kda.decay_attn_fwd(**a)
     codes, scales = torch.zeros(1, 2, 4, 8, dtype=torch.uint8), torch.zeros(1, 2, 4, 1, dtype=torch.uint8)
-    for bad in ((codes, scales[..., 0]), (codes.to(f32), scales), (codes[:, :1], scales)):
+    for bad in ((codes, scales[..., 0]), (codes.to(f32), scales), (codes[:, :1], scales), (codes, scales)):
         with pytest.raises((ValueError, TypeError)):
             kda.decay_attn_bwd(q, bad, v, g, None, v)
     with pytest.raises(TypeError):
