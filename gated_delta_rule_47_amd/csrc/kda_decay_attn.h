@@ -54,6 +54,9 @@ typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
 typedef unsigned int u32x2_t __attribute__((ext_vector_type(2)));
 typedef short short4v_t __attribute__((ext_vector_type(4)));
 
+// Pointers into LDS keep their address space (a generic one would be tested for null at every cast).
+template <typename U> using Lds = __attribute__((address_space(3))) U;
+
 // ------------------------------------------------------------------ operand layouts
 // A product's contraction runs in groups of DG indices.  A fragment holds, for row (or column)
 // lane % 16 and lane group g = lane / 16, DG / 4 of the group's indices: DG / 4 consecutive ones
@@ -87,19 +90,17 @@ template <> struct Lin<bf16_t> {                 // v_mfma_f32_16x16x32_bf16
     return t * W + ((e >> 3) ^ swz<W, IMG>(t)) * 8 + (e & 7);
   }
   template <int W, bool IMG>
-  static __device__ __forceinline__ frag nat(const bf16_t* base, int t, int d0, int lane) {
-    return *reinterpret_cast<const short8*>(base + at<W, IMG>(t, d0 + 8 * (lane >> 4)));
+  static __device__ __forceinline__ frag nat(const Lds<bf16_t>* base, int t, int d0, int lane) {
+    return *(const Lds<short8>*)(base + at<W, IMG>(t, d0 + 8 * (lane >> 4)));
   }
   // two transposing reads: lane 4r + m of a group of 16 addresses row 4g + r (then 16 + 4g + r) at
   // four columns and lane j receives column j of the group's 16
-  template <int W, bool PERM> static __device__ __forceinline__ frag tr(const bf16_t* base, int ct, int d0, int lane) {
+  template <int W, bool PERM> static __device__ __forceinline__ frag tr(const Lds<bf16_t>* base, int ct, int d0, int lane) {
     const int g = lane >> 4, r = (lane >> 2) & 3, m = lane & 3;
     const int col = PERM ? 32 * (ct >> 1) + 8 * m + 4 * (ct & 1) : 16 * ct + 4 * m;
-    const bf16_t* p = base + at<W, false>(d0 + 4 * g + r, col);     // (swz is the same 16 rows on)
-    const short4v_t a = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-        (__attribute__((address_space(3))) short4v_t*)(__attribute__((address_space(3))) const void*)p);
-    const short4v_t b = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-        (__attribute__((address_space(3))) short4v_t*)(__attribute__((address_space(3))) const void*)(p + 16 * W));
+    const Lds<bf16_t>* p = base + at<W, false>(d0 + 4 * g + r, col);     // (swz is the same 16 rows on)
+    const short4v_t a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds<short4v_t>*)p);
+    const short4v_t b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds<short4v_t>*)(p + 16 * W));
     return short8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
   }
   static __device__ __forceinline__ floatx4 mma(frag a, frag b, floatx4 c) {
@@ -130,8 +131,8 @@ template <> struct Lin<bf16_t> {                 // v_mfma_f32_16x16x32_bf16
   }
   // token (within a group of DG) of fragment element e in the accumulator order
   static __device__ __forceinline__ int tok_of(int e, int g) { return 16 * (e >> 2) + 4 * g + (e & 3); }
-  static __device__ __forceinline__ void store4(bf16_t* p, floatx4 x) {
-    *reinterpret_cast<u32x2_t*>(p) = u32x2_t{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
+  static __device__ __forceinline__ void store4(Lds<bf16_t>* p, floatx4 x) {
+    *(Lds<u32x2_t>*)p = u32x2_t{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
   }
 };
 
@@ -141,10 +142,10 @@ template <> struct Lin<float> {                  // four v_mfma_f32_16x16x4_f32
   static __device__ __forceinline__ int row_of(int ct, int m) { return 16 * ct + m; }
   template <int W, bool IMG> static __device__ __forceinline__ int at(int t, int e) { return t * (W + PAD) + e; }
   template <int W, bool IMG>
-  static __device__ __forceinline__ frag nat(const float* base, int t, int d0, int lane) {
-    return *reinterpret_cast<const floatx4*>(base + at<W, IMG>(t, d0 + 4 * (lane >> 4)));
+  static __device__ __forceinline__ frag nat(const Lds<float>* base, int t, int d0, int lane) {
+    return *(const Lds<floatx4>*)(base + at<W, IMG>(t, d0 + 4 * (lane >> 4)));
   }
-  template <int W, bool PERM> static __device__ __forceinline__ frag tr(const float* base, int ct, int d0, int lane) {
+  template <int W, bool PERM> static __device__ __forceinline__ frag tr(const Lds<float>* base, int ct, int d0, int lane) {
     const int t = d0 + 4 * (lane >> 4), e = 16 * ct + (lane & 15);
     return floatx4{base[at<W, false>(t, e)], base[at<W, false>(t + 1, e)], base[at<W, false>(t + 2, e)],
                    base[at<W, false>(t + 3, e)]};
@@ -159,7 +160,7 @@ template <> struct Lin<float> {                  // four v_mfma_f32_16x16x4_f32
     out[0] = floatx4{x[0] * f[0], x[1] * f[1], x[2] * f[2], x[3] * f[3]};
   }
   static __device__ __forceinline__ int tok_of(int e, int g) { return 4 * g + e; }
-  static __device__ __forceinline__ void store4(float* p, floatx4 x) { *reinterpret_cast<floatx4*>(p) = x; }
+  static __device__ __forceinline__ void store4(Lds<float>* p, floatx4 x) { *(Lds<floatx4>*)p = x; }
 };
 
 // ------------------------------------------------------------------ loads
@@ -261,12 +262,12 @@ template <typename T, bool PK, int C, int DP, int NT> struct Stage {
       if (N % NT == 0 || x < N) p[i] = h.load(t0 + x / PPR, ch0 + (x % PPR) * Lin<T>::EPP);
     }
   }
-  __device__ __forceinline__ void store(T* lds, int tid) const {
+  __device__ __forceinline__ void store(Lds<T>* lds, int tid) const {
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int x = tid + i * NT;
       if (N % NT == 0 || x < N)
-        *reinterpret_cast<u32x4_t*>(lds + Lin<T>::template at<DP, false>(x / PPR, (x % PPR) * Lin<T>::EPP)) =
+        *(Lds<u32x4_t>*)(lds + Lin<T>::template at<DP, false>(x / PPR, (x % PPR) * Lin<T>::EPP)) =
             p[i].elems();
     }
   }
@@ -276,13 +277,13 @@ template <typename T, bool PK, int C, int DP, int NT> struct Stage {
 // the wave's).  Past the buffer's range: zeros.  Written in asm, with no register as its output, because
 // the compiler would wait for every copy in flight before each transposing LDS read; the waits are
 // wait_vm_but()'s (the compiler's own waits for its loads and stores only grow stricter by operations that
-// it does not count).
-__device__ __forceinline__ void copy_to_lds(u32x4_t r, const void* lds, unsigned lane_off, unsigned off) {
-  const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)lds;
+// it does not count).  m0, the copies' LDS address, is read by no other instruction of these kernels.
+__device__ __forceinline__ void copy_to_lds(u32x4_t r, const Lds<void>* lds, unsigned lane_off, unsigned off) {
+  const uint32_t at = (uint32_t)(uintptr_t)lds;
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(
                    __builtin_amdgcn_readfirstlane((int)at)),
                "v"(lane_off), "s"(r), "s"(off)
-               : "memory", "m0");
+               : "memory");
 }
 
 // The tiles of one chunk, copied from memory straight into LDS: each wave instruction fills 64
@@ -315,7 +316,7 @@ template <typename T, int C, int DK, int DV, int DQ, int NW> struct Copy {
     }
   }
   // tokens from t0 into the tiles at lds (K, V and Q one behind the other)
-  __device__ __forceinline__ void issue(u32x4_t rk, u32x4_t rv, u32x4_t rq, int t0, int K, int V, const T* lds,
+  __device__ __forceinline__ void issue(u32x4_t rk, u32x4_t rv, u32x4_t rq, int t0, int K, int V, const Lds<T>* lds,
                                         int wave) const {
     const unsigned sk = (unsigned)t0 * (unsigned)(K * sizeof(T)), sv = (unsigned)t0 * (unsigned)(V * sizeof(T));
 #pragma unroll
@@ -403,7 +404,7 @@ template <typename T, int KD, int VT, int C, int NK, int NV, bool REV> struct St
       }
   }
   // [column][channel] image in LDS
-  __device__ __forceinline__ void image(T* dst, int ct0, int col0, int lane) const {
+  __device__ __forceinline__ void image(Lds<T>* dst, int ct0, int col0, int lane) const {
 #pragma unroll
     for (int i = 0; i < NK; ++i)
 #pragma unroll
@@ -423,7 +424,7 @@ template <typename T, int KD, int VT, int C, int NK, int NV, bool REV> struct St
         f[d][e] = i < n ? u * decay_pow(g2, REV ? i + 1 : n - 1 - i) : 0.0f;
       }
   }
-  __device__ __forceinline__ void update(const T* sK, const T* sV, int ct0, int vt0, Decay2 an, int lane) {
+  __device__ __forceinline__ void update(const Lds<T>* sK, const Lds<T>* sV, int ct0, int vt0, Decay2 an, int lane) {
 #pragma unroll
     for (int i = 0; i < NK; ++i)
 #pragma unroll
@@ -489,9 +490,15 @@ __device__ __forceinline__ void walk_block(int b, int m, int ntile, int* idx, in
   }
 }
 
+// LDS elements of a walk; 8-bit operands go through registers and need two chunks only.
+template <typename T, int KD, int VT, bool PACK> constexpr int walk_lds() {
+  typedef WalkShape<T, KD, VT> W;
+  return (PACK ? 2 : W::NS) * W::kC + 2 * W::kS;
+}
+
 // PQ, PK, PV: the operand is kept in 8 bits.
 template <typename T, int KD, int VT, bool REV, bool PQ, bool PK, bool PV>
-__global__ void __launch_bounds__(512, (WalkShape<T, KD, VT>::EU)) decay_walk_kernel(WalkArgs a) {
+__device__ __forceinline__ void walk(const WalkArgs& a, int block, Lds<T>* smem) {
   typedef Lin<T> L;
   typedef typename L::frag frag;
   typedef WalkShape<T, KD, VT> W;
@@ -499,11 +506,9 @@ __global__ void __launch_bounds__(512, (WalkShape<T, KD, VT>::EU)) decay_walk_ke
   constexpr int NQ = KD / L::DG, ND = C / L::DG;
   constexpr int NH = NQ > 1 ? 2 : 1, HQ = NQ / NH;             // the read's contraction in NH steps
   static_assert(ND == 2, "two groups of tokens per chunk");
-  constexpr bool DMA = !(PQ || PK || PV);                      // 8-bit operands go through registers
+  constexpr bool DMA = !(PQ || PK || PV);
   constexpr int NS = DMA ? W::NS : 2;
-  __shared__ __align__(16) T smem[NS * W::kC + 2 * W::kS];
-  static_assert(sizeof(smem) <= 160 * 1024, "LDS of one gfx950 workgroup exceeded");
-  T* const sS = smem + NS * W::kC;
+  Lds<T>* const sS = smem + NS * W::kC;
   const auto tile_k = [&](int ci) { return smem + ci % NS * W::kC; };
   const auto tile_v = [&](int ci) { return smem + ci % NS * W::kC + W::kK; };
   const auto tile_q = [&](int ci) { return smem + ci % NS * W::kC + W::kK + W::kV; };
@@ -511,7 +516,7 @@ __global__ void __launch_bounds__(512, (WalkShape<T, KD, VT>::EU)) decay_walk_ke
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int ntile = (a.V + VT - 1) / VT;
   int idx, tile;
-  walk_block(blockIdx.x, a.BH * a.nseg, ntile, &idx, &tile);
+  walk_block(block, a.BH * a.nseg, ntile, &idx, &tile);
   const int bh = idx / a.nseg, seg = idx - bh * a.nseg, v0 = tile * VT;
   const int h = bh % a.H;
   int len = a.T;
@@ -628,9 +633,9 @@ __global__ void __launch_bounds__(512, (WalkShape<T, KD, VT>::EU)) decay_walk_ke
     chunk_barrier();
     for (int ci = 0; ci < nch; ++ci) {
       const int n = chunk_n(ci);
-      const T* cK = tile_k(ci);
-      const T* cV = tile_v(ci);
-      const T* cS = sS + (ci & 1) * W::kS;
+      const Lds<T>* cK = tile_k(ci);
+      const Lds<T>* cV = tile_v(ci);
+      const Lds<T>* cS = sS + (ci & 1) * W::kS;
       begin(ci);
       frag qf[NQ];
 #pragma unroll
@@ -732,11 +737,47 @@ __global__ void __launch_bounds__(512, (WalkShape<T, KD, VT>::EU)) decay_walk_ke
   }
 }
 
+// Workgroups of one walk.
+__host__ __device__ inline int walk_blocks(const WalkArgs& a, int VT) { return a.BH * a.nseg * ((a.V + VT - 1) / VT); }
+
+template <typename T, int KD, int VT>
+__global__ void __launch_bounds__(512, (WalkShape<T, KD, VT>::EU)) decay_fwd_kernel(WalkArgs a) {
+  __shared__ __align__(1024) T smem[walk_lds<T, KD, VT, false>()];
+  static_assert(sizeof(smem) <= 160 * 1024, "LDS of one gfx950 workgroup exceeded");
+  walk<T, KD, VT, false, false, false, false>(a, blockIdx.x, (Lds<T>*)smem);
+}
+
+// The three walks of a backward pass in one launch: dq (keys V, values K wide), dk (the same), dv (keys K,
+// values V wide).  Each has as many workgroups as the forward has, so that where those fill the chip once
+// the other walks' workgroups take the places of the first ones to end, and a small pass costs one launch.
+// PACK: q, k and v are kept in 8 bits.
+template <typename T, int KD, int VD, bool PACK> struct BwdShape {
+  static constexpr int VTK = KD <= 32 ? 32 : 64, VTV = VD <= 32 ? 32 : 64;        // value tiles over K and over V
+  static constexpr int LDS = cmax(walk_lds<T, VD, VTK, PACK>(), walk_lds<T, KD, VTV, PACK>());
+  static constexpr int EU = PACK ? 2 : cmin(WalkShape<T, VD, VTK>::EU, WalkShape<T, KD, VTV>::EU);
+};
+template <typename T, int KD, int VD, bool PACK>
+__global__ void __launch_bounds__(512, (BwdShape<T, KD, VD, PACK>::EU))
+    decay_bwd_kernel(WalkArgs dq, WalkArgs dk, WalkArgs dv) {
+  typedef BwdShape<T, KD, VD, PACK> S;
+  __shared__ __align__(1024) T smem[S::LDS];
+  static_assert(sizeof(smem) <= 160 * 1024, "LDS of one gfx950 workgroup exceeded");
+  const int n = walk_blocks(dq, S::VTK);
+  int b = blockIdx.x;
+  if (b < n) {
+    walk<T, VD, S::VTK, false, false, PACK, PACK>(dq, b, (Lds<T>*)smem);
+  } else if ((b -= n) < n) {
+    walk<T, VD, S::VTK, true, PACK, false, PACK>(dk, b, (Lds<T>*)smem);
+  } else {
+    walk<T, KD, S::VTV, true, PACK, PACK, false>(dv, b - n, (Lds<T>*)smem);
+  }
+}
+
 constexpr int kSegChunks = 3;                    // chunks in LDS
 
 // Local end state of one segment (not the last in walking order) for one value tile.
 template <typename T, int KD, int VT, int NW, bool REV, bool PK, bool PV>
-__device__ __forceinline__ void segment_state(const SegArgs& a, int block, T* smem) {
+__device__ __forceinline__ void segment_state(const SegArgs& a, int block, Lds<T>* smem) {
   typedef WalkShape<T, KD, VT> W;
   typedef StateShape<KD, VT, NW> S;
   constexpr int C = W::C, NT = 64 * NW, NS = kSegChunks;
@@ -806,18 +847,26 @@ __global__ void __launch_bounds__((64 * seg_waves<KD, VT>())) decay_segment_kern
   typedef WalkShape<T, KD, VT> W;
   __shared__ __align__(16) T smem[kSegChunks * (W::kK + W::kV)];
   constexpr int NW = seg_waves<KD, VT>();
-  if ((int)blockIdx.x < nblock) segment_state<T, KD, VT, NW, false, PACK, PACK>(s, blockIdx.x, smem);
-  else segment_state<T, KD, VT, NW, true, PACK, false>(r, blockIdx.x - nblock, smem);
+  if ((int)blockIdx.x < nblock) segment_state<T, KD, VT, NW, false, PACK, PACK>(s, blockIdx.x, (Lds<T>*)smem);
+  else segment_state<T, KD, VT, NW, true, PACK, false>(r, blockIdx.x - nblock, (Lds<T>*)smem);
 }
 
 // ------------------------------------------------------------------ launchers
-// Which operands of a walk are kept in 8 bits: none, or those of a gradient whose q, k, v are.
-enum WalkKind { kFwd, kRev, kFwdDq8, kRevDk8, kRevDv8 };
+// Instances by key and value widths padded to 32, 64 or 128; value tiles are 64 columns wide, or 32 for
+// widths up to 32.
+template <typename T, int KD> hipError_t launch_walk_fwd(const WalkArgs& a, hipStream_t s) {
+  if (a.V <= 32)
+    hipLaunchKernelGGL((decay_fwd_kernel<T, KD, 32>), dim3(walk_blocks(a, 32)), dim3(512), 0, s, a);
+  else
+    hipLaunchKernelGGL((decay_fwd_kernel<T, KD, 64>), dim3(walk_blocks(a, 64)), dim3(512), 0, s, a);
+  return hipGetLastError();
+}
 
-template <typename T, int KD, int VT, bool REV, bool PQ, bool PK, bool PV>
-hipError_t launch_walk_inst(const WalkArgs& a, hipStream_t s) {
-  const int blocks = a.BH * a.nseg * ((a.V + VT - 1) / VT);
-  hipLaunchKernelGGL((decay_walk_kernel<T, KD, VT, REV, PQ, PK, PV>), dim3(blocks), dim3(512), 0, s, a);
+template <typename T, int KD, int VD, bool PACK>
+hipError_t launch_walk_bwd(const WalkArgs& dq, const WalkArgs& dk, const WalkArgs& dv, hipStream_t s) {
+  typedef BwdShape<T, KD, VD, PACK> S;
+  const int n = 2 * walk_blocks(dq, S::VTK) + walk_blocks(dv, S::VTV);
+  hipLaunchKernelGGL((decay_bwd_kernel<T, KD, VD, PACK>), dim3(n), dim3(512), 0, s, dq, dk, dv);
   return hipGetLastError();
 }
 
@@ -829,21 +878,6 @@ hipError_t launch_segments_inst(const SegArgs& st, const SegArgs* r, hipStream_t
   return hipGetLastError();
 }
 
-// Instances by padded key width KD; the value tile is 64 columns, or 32 where V <= 32.
-template <typename T, int KD, int VT> hipError_t launch_walk_vt(const WalkArgs& a, WalkKind kind, hipStream_t s) {
-  switch (kind) {
-    case kFwd: return launch_walk_inst<T, KD, VT, false, false, false, false>(a, s);
-    case kRev: return launch_walk_inst<T, KD, VT, true, false, false, false>(a, s);
-    case kFwdDq8: return launch_walk_inst<T, KD, VT, false, false, true, true>(a, s);
-    case kRevDk8: return launch_walk_inst<T, KD, VT, true, true, false, true>(a, s);
-    case kRevDv8: return launch_walk_inst<T, KD, VT, true, true, true, false>(a, s);
-  }
-  return hipErrorInvalidValue;
-}
-template <typename T, int KD> hipError_t launch_walk_kd(const WalkArgs& a, WalkKind kind, hipStream_t s) {
-  return a.V <= 32 ? launch_walk_vt<T, KD, 32>(a, kind, s) : launch_walk_vt<T, KD, 64>(a, kind, s);
-}
-
 // Local states of S (from k, v) and, r non-null, of dL/dS (from q, d_o); packed: q, k, v are in 8 bits.
 template <typename T, int KD>
 hipError_t launch_segments_kd(const SegArgs& st, const SegArgs* r, bool packed, hipStream_t s) {
@@ -852,17 +886,14 @@ hipError_t launch_segments_kd(const SegArgs& st, const SegArgs* r, bool packed, 
   return packed ? launch_segments_inst<T, KD, 64, true>(st, r, s) : launch_segments_inst<T, KD, 64, false>(st, r, s);
 }
 
-#ifndef KDA_DECAY_INSTANCES                       // defined where the instances are compiled
-#define KDA_DECAY_EXTERN(T, KD)                                                              \
-  extern template hipError_t launch_walk_kd<T, KD>(const WalkArgs&, WalkKind, hipStream_t); \
-  extern template hipError_t launch_segments_kd<T, KD>(const SegArgs&, const SegArgs*, bool, hipStream_t);
-KDA_DECAY_EXTERN(float, 32)
-KDA_DECAY_EXTERN(float, 64)
-KDA_DECAY_EXTERN(float, 128)
-KDA_DECAY_EXTERN(bf16_t, 32)
-KDA_DECAY_EXTERN(bf16_t, 64)
-KDA_DECAY_EXTERN(bf16_t, 128)
-#undef KDA_DECAY_EXTERN
-#endif
+#define KDA_DECAY_FWD_INSTANCES(EXT, T, KD)                                 \
+  EXT template hipError_t launch_walk_fwd<T, KD>(const WalkArgs&, hipStream_t); \
+  EXT template hipError_t launch_segments_kd<T, KD>(const SegArgs&, const SegArgs*, bool, hipStream_t);
+#define KDA_DECAY_BWD_INSTANCE(EXT, T, KD, VD, PACK) \
+  EXT template hipError_t launch_walk_bwd<T, KD, VD, PACK>(const WalkArgs&, const WalkArgs&, const WalkArgs&, hipStream_t);
+#define KDA_DECAY_BWD_INSTANCES(EXT, T, KD) \
+  KDA_DECAY_BWD_INSTANCE(EXT, T, KD, 32, false) KDA_DECAY_BWD_INSTANCE(EXT, T, KD, 32, true)   \
+  KDA_DECAY_BWD_INSTANCE(EXT, T, KD, 64, false) KDA_DECAY_BWD_INSTANCE(EXT, T, KD, 64, true)   \
+  KDA_DECAY_BWD_INSTANCE(EXT, T, KD, 128, false) KDA_DECAY_BWD_INSTANCE(EXT, T, KD, 128, true)
 
 }  // namespace kda

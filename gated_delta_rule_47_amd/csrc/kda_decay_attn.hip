@@ -5,18 +5,32 @@
 
 namespace kda {
 
+#define KDA_DECAY_EXTERN(T, KD)                \
+  KDA_DECAY_FWD_INSTANCES(extern, T, KD)       \
+  KDA_DECAY_BWD_INSTANCES(extern, T, KD)
+KDA_DECAY_EXTERN(float, 32)
+KDA_DECAY_EXTERN(float, 64)
+KDA_DECAY_EXTERN(float, 128)
+KDA_DECAY_EXTERN(bf16_t, 32)
+KDA_DECAY_EXTERN(bf16_t, 64)
+KDA_DECAY_EXTERN(bf16_t, 128)
+#undef KDA_DECAY_EXTERN
+
 // ------------------------------------------------------------------ segments
 // A walk is sequential over its chunks, so heads x value tiles alone may leave most of the 256 CUs
-// idle; then the tokens are cut into segments.  The price is a second read of k and v (the segments'
-// local states), so no more segments are taken than fill the chip once, and none under 4 chunks.
-DecayPlan decay_plan(int B, int H, int T, int K, int V, bool bf16) {
+// idle; then the tokens are cut into segments.  The price is a second read of k and v (the segments' local
+// states) and two more launches, so: no more segments than fill the chip once, four chunks at least in
+// each, none in sequences of under 16 chunks (which one walk passes in the time of the launches), and in a
+// forward pass not two of them (4 x 16 heads of 4096 tokens, K = V = 128, bf16: 114 us in two segments, 111
+// in one; backward, whose three walks share the segments' states, 268 and 330).
+DecayPlan decay_plan(int B, int H, int T, int K, int V, bool bf16, bool bwd) {
   const int C = bf16 ? 64 : 32;
   const long long wgs = (long long)B * H * ((V + 63) / 64);
   const int nchunks = (T + C - 1) / C;
   const long long fill = 256;
   long long n = (fill + wgs - 1) / wgs;
   if (n > nchunks / 4) n = nchunks / 4;
-  if (n < 1) n = 1;
+  if (nchunks < 16 || n < (bwd ? 2 : 3)) n = 1;
   DecayPlan p;
   const int per = (nchunks + (int)n - 1) / (int)n;
   p.seglen = (per < 1 ? 1 : per) * C;
@@ -81,10 +95,22 @@ static hipError_t join(JoinArgs st, const JoinArgs* r, const float* log_decay, c
   return hipGetLastError();
 }
 
-template <typename T> static hipError_t walk(const WalkArgs& a, WalkKind kind, hipStream_t s) {
-  if (a.K <= 32) return launch_walk_kd<T, 32>(a, kind, s);
-  if (a.K <= 64) return launch_walk_kd<T, 64>(a, kind, s);
-  return launch_walk_kd<T, 128>(a, kind, s);
+template <typename T> static hipError_t walk_fwd(const WalkArgs& a, hipStream_t s) {
+  if (a.K <= 32) return launch_walk_fwd<T, 32>(a, s);
+  if (a.K <= 64) return launch_walk_fwd<T, 64>(a, s);
+  return launch_walk_fwd<T, 128>(a, s);
+}
+template <typename T, int KD, bool PACK>
+static hipError_t walk_bwd_v(const WalkArgs& dq, const WalkArgs& dk, const WalkArgs& dv, hipStream_t s) {
+  if (dv.V <= 32) return launch_walk_bwd<T, KD, 32, PACK>(dq, dk, dv, s);
+  if (dv.V <= 64) return launch_walk_bwd<T, KD, 64, PACK>(dq, dk, dv, s);
+  return launch_walk_bwd<T, KD, 128, PACK>(dq, dk, dv, s);
+}
+template <typename T, bool PACK>
+static hipError_t walk_bwd(const WalkArgs& dq, const WalkArgs& dk, const WalkArgs& dv, hipStream_t s) {
+  if (dv.K <= 32) return walk_bwd_v<T, 32, PACK>(dq, dk, dv, s);
+  if (dv.K <= 64) return walk_bwd_v<T, 64, PACK>(dq, dk, dv, s);
+  return walk_bwd_v<T, 128, PACK>(dq, dk, dv, s);
 }
 template <typename T> static hipError_t segments(const SegArgs& st, const SegArgs* r, bool packed, hipStream_t s) {
   if (st.K <= 32) return launch_segments_kd<T, 32>(st, r, packed, s);
@@ -96,7 +122,7 @@ template <typename T>
 hipError_t launch_decay_fwd(const void* q, const void* k, const void* v, const float* log_decay, const int* lengths,
                             const float* state_in, float scale, void* o, float* state_out, void* workspace, int B,
                             int H, int T_, int K, int V, hipStream_t s) {
-  const DecayPlan p = decay_plan(B, H, T_, K, V, sizeof(T) == 2);
+  const DecayPlan p = decay_plan(B, H, T_, K, V, sizeof(T) == 2, false);
   float* ws = reinterpret_cast<float*>(workspace);
   if (p.nseg > 1) {
     const SegArgs g{k, v, nullptr, nullptr, log_decay, lengths, ws, 1.0f, B * H, H, T_, K, V, p.nseg, p.seglen};
@@ -111,7 +137,7 @@ hipError_t launch_decay_fwd(const void* q, const void* k, const void* v, const f
   a.c = a.r = scale, a.u = 1.0f;
   a.si_k = V, a.si_v = 1;
   a.BH = B * H, a.H = H, a.T = T_, a.K = K, a.V = V, a.nseg = p.nseg, a.seglen = p.seglen;
-  return walk<T>(a, kFwd, s);
+  return walk_fwd<T>(a, s);
 }
 
 // Segment boundaries and states are those of the K x V state in all three walks: S for dq, R = dL/dS
@@ -121,7 +147,7 @@ hipError_t launch_decay_bwd(const void* q, const void* k, const void* v, const u
                             const uint8_t* v_sc, const float* log_decay, const int* lengths, const float* state_in,
                             float scale, const void* d_o, const float* d_state_out, void* dq, void* dk, void* dv,
                             float* dstate_in, void* workspace, int B, int H, int T_, int K, int V, hipStream_t s) {
-  const DecayPlan p = decay_plan(B, H, T_, K, V, sizeof(T) == 2);
+  const DecayPlan p = decay_plan(B, H, T_, K, V, sizeof(T) == 2, true);
   float* wS = reinterpret_cast<float*>(workspace);
   float* wR = wS + decay_states_bytes(B, H, K, V, p) / sizeof(float);
   const bool packed = q_sc != nullptr;                      // q, k and v, all or none
@@ -133,26 +159,28 @@ hipError_t launch_decay_bwd(const void* q, const void* k, const void* v, const u
     const JoinArgs jr{wR, d_state_out};
     if (e == hipSuccess) e = join(JoinArgs{wS, state_in}, &jr, log_decay, lengths, B, H, T_, K * V, p, s);
   }
+  if (e != hipSuccess) return e;
   WalkArgs a{};
   a.log_decay = log_decay, a.lengths = lengths;
   a.BH = B * H, a.H = H, a.T = T_, a.nseg = p.nseg, a.seglen = p.seglen, a.zero_tail = lengths != nullptr;
-  // dq: width V keys, width K values, the state read as its transpose
-  a.q = d_o, a.k = v, a.v = k, a.q_sc = nullptr, a.k_sc = v_sc, a.v_sc = k_sc;
-  a.state_in = state_in, a.seg_state = wS, a.state_out = nullptr, a.o = dq;
-  a.c = a.r = scale, a.u = 1.0f;
-  a.si_k = 1, a.si_v = V, a.K = V, a.V = K;
-  if (e == hipSuccess) e = walk<T>(a, packed ? kFwdDq8 : kFwd, s);
-  // dk
-  a.q = v, a.k = d_o, a.v = q, a.q_sc = v_sc, a.k_sc = nullptr, a.v_sc = q_sc;
-  a.state_in = d_state_out, a.seg_state = wR, a.o = dk;
-  a.c = a.u = scale, a.r = 1.0f;
-  if (e == hipSuccess) e = walk<T>(a, packed ? kRevDk8 : kRev, s);
+  // dq: keys V, values K wide, the state read as its transpose
+  WalkArgs dq_ = a;
+  dq_.q = d_o, dq_.k = v, dq_.v = k, dq_.k_sc = v_sc, dq_.v_sc = k_sc;
+  dq_.state_in = state_in, dq_.seg_state = wS, dq_.o = dq;
+  dq_.c = dq_.r = scale, dq_.u = 1.0f;
+  dq_.si_k = 1, dq_.si_v = V, dq_.K = V, dq_.V = K;
+  WalkArgs dk_ = a;
+  dk_.q = v, dk_.k = d_o, dk_.v = q, dk_.q_sc = v_sc, dk_.v_sc = q_sc;
+  dk_.state_in = d_state_out, dk_.seg_state = wR, dk_.o = dk;
+  dk_.c = dk_.u = scale, dk_.r = 1.0f;
+  dk_.si_k = 1, dk_.si_v = V, dk_.K = V, dk_.V = K;
   // dv, and the state's gradient
-  a.q = k, a.k = q, a.v = d_o, a.q_sc = k_sc, a.k_sc = q_sc, a.v_sc = nullptr;
-  a.state_out = dstate_in, a.o = dv;
-  a.si_k = V, a.si_v = 1, a.K = K, a.V = V;
-  if (e == hipSuccess) e = walk<T>(a, packed ? kRevDv8 : kRev, s);
-  return e;
+  WalkArgs dv_ = a;
+  dv_.q = k, dv_.k = q, dv_.v = d_o, dv_.q_sc = k_sc, dv_.k_sc = q_sc;
+  dv_.state_in = d_state_out, dv_.seg_state = wR, dv_.state_out = dstate_in, dv_.o = dv;
+  dv_.c = dv_.u = scale, dv_.r = 1.0f;
+  dv_.si_k = V, dv_.si_v = 1, dv_.K = K, dv_.V = V;
+  return packed ? walk_bwd<T, true>(dq_, dk_, dv_, s) : walk_bwd<T, false>(dq_, dk_, dv_, s);
 }
 
 // ------------------------------------------------------------------ one token

@@ -84,7 +84,7 @@ hipError_t launch_chunk_bwd_mfma(const float* q, const float* k, const float* v,
 struct DecayPlan {
   int nseg, seglen;
 };
-DecayPlan decay_plan(int B, int H, int T, int K, int V, bool bf16);
+DecayPlan decay_plan(int B, int H, int T, int K, int V, bool bf16, bool bwd);
 size_t decay_states_bytes(int B, int H, int K, int V, const DecayPlan& p);
 template <typename T>
 hipError_t launch_decay_fwd(const void* q, const void* k, const void* v, const float* log_decay, const int* lengths,

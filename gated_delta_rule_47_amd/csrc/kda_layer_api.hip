@@ -37,9 +37,10 @@ bool attn_sizes(int B, int H, int T, int K, int V, int dtype) {
   return B >= 1 && H >= 1 && T >= 0 && valid_dim(K) && valid_dim(V) && (long long)B * H <= (1 << 24) &&
          ((size_t)T + 64) * (size_t)(K > V ? K : V) * esize(dtype) <= 0x7fffffffu;
 }
-size_t attn_states(int B, int H, int T, int K, int V, int dtype, int count) {
+// S forward, S and its gradient backward
+size_t attn_states(int B, int H, int T, int K, int V, int dtype, bool bwd) {
   if (!valid_dtype(dtype) || !attn_sizes(B, H, T, K, V, dtype)) return 0;
-  return count * decay_states_bytes(B, H, K, V, decay_plan(B, H, T, K, V, dtype == KDA_BF16));
+  return (bwd ? 2 : 1) * decay_states_bytes(B, H, K, V, decay_plan(B, H, T, K, V, dtype == KDA_BF16, bwd));
 }
 bool norm_sizes(int B, int H, int T, int D) {
   return B >= 1 && H >= 1 && T >= 0 && D >= 1 && D <= (1 << 24) && (long long)B * H <= (1 << 24) &&
@@ -55,7 +56,7 @@ using namespace kda;
 extern "C" {
 
 size_t kda_decay_attn_workspace_bytes(int B, int H, int T, int K, int V, int dtype) {
-  return attn_states(B, H, T, K, V, dtype, 1);
+  return attn_states(B, H, T, K, V, dtype, false);
 }
 
 int kda_decay_attn_fwd(const void* q, const void* k, const void* v, const float* log_decay, const int* lengths,
@@ -65,7 +66,7 @@ int kda_decay_attn_fwd(const void* q, const void* k, const void* v, const float*
   if (!valid_dtype(dtype)) return reject(KDA_ERR_DTYPE);
   if (!attn_sizes(B, H, T, K, V, dtype)) return reject(KDA_ERR_SHAPE);
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16)) return reject(KDA_ERR_ALIGN);
-  const size_t need = attn_states(B, H, T, K, V, dtype, 1);
+  const size_t need = attn_states(B, H, T, K, V, dtype, false);
   if (need && (!workspace || workspace_bytes < need)) return reject(KDA_ERR_WORKSPACE);
   if (need && !aligned(workspace, 256)) return reject(KDA_ERR_ALIGN);
   const size_t es = esize(dtype), bh = (size_t)B * H, ns = bh * K * V * 4;
@@ -105,7 +106,7 @@ int kda_decay_attn_step(const void* q, const void* k, const void* v, const float
 }
 
 size_t kda_decay_attn_bwd_workspace_bytes(int B, int H, int T, int K, int V, int dtype) {
-  return attn_states(B, H, T, K, V, dtype, 2);
+  return attn_states(B, H, T, K, V, dtype, true);
 }
 
 int kda_decay_attn_bwd(const void* q, const void* k, const void* v, const unsigned char* q_scales,
@@ -122,7 +123,7 @@ int kda_decay_attn_bwd(const void* q, const void* k, const void* v, const unsign
   if (!aligned(q, q_scales ? 8 : 16) || !aligned(k, k_scales ? 8 : 16) || !aligned(v, v_scales ? 8 : 16) ||
       !aligned(d_o, 16) || !aligned(dq, 16) || !aligned(dk, 16) || !aligned(dv, 16))
     return reject(KDA_ERR_ALIGN);
-  const size_t need = attn_states(B, H, T, K, V, dtype, 2);
+  const size_t need = attn_states(B, H, T, K, V, dtype, true);
   if (need && (!workspace || workspace_bytes < need)) return reject(KDA_ERR_WORKSPACE);
   if (need && !aligned(workspace, 256)) return reject(KDA_ERR_ALIGN);
   const size_t es = esize(dtype), bh = (size_t)B * H, ns = bh * K * V * 4;
