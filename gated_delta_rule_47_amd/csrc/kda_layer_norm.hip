@@ -21,9 +21,23 @@ constexpr int kNormThreads = 256;
 
 // Sum over the L lanes of a row: a power of two up to 64, or the whole workgroup (whose four waves add
 // in a fixed order through `red`); every lane of the row gets it.
+// Lanes exchange within the register file (DPP within 16 lanes, lane swaps beyond), not through LDS.
+template <int CTRL> __device__ __forceinline__ float dpp(float x) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(x), CTRL, 0xf, 0xf, true));
+}
 template <int L> __device__ __forceinline__ float row_sum(float x, float* red) {
-#pragma unroll
-  for (int m = 1; m < (L < 64 ? L : 64); m <<= 1) x += __shfl_xor(x, m, 64);
+  if constexpr (L >= 2) x += dpp<0xB1>(x);       // lane ^ 1
+  if constexpr (L >= 4) x += dpp<0x4E>(x);       // lane ^ 2
+  if constexpr (L >= 8) x += dpp<0x141>(x);      // mirrored in 8: the other four's sum
+  if constexpr (L >= 16) x += dpp<0x140>(x);     // mirrored in 16: the other eight's
+  if constexpr (L >= 32) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+  if constexpr (L >= 64) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
   if constexpr (L > 64) {
     static_assert(L == kNormThreads, "rows of a wave or of the workgroup");
     __syncthreads();
@@ -34,16 +48,35 @@ template <int L> __device__ __forceinline__ float row_sum(float x, float* red) {
   return x;
 }
 
-// E consecutive elements of a row in fp32: 16 bytes of T (Wide<T>::E of them), or one element where the
-// width or an address keeps rows from being 16-byte aligned.
+// E consecutive elements of a row, 16 bytes: rows may start at any element, and global memory takes a
+// 16-byte access at any address.  n < E: the last vector of a row, whose elements are taken one by one.
 template <typename T> struct Wide {
   static constexpr int E = 16 / (int)sizeof(T);
 };
-template <typename T, int E> __device__ __forceinline__ void vec_get(const T* p, float* f) {
-  if constexpr (E == 1) {
-    f[0] = to_f<T>(*p);
-  } else {
-    const u32x4_t u = *reinterpret_cast<const u32x4_t*>(p);
+template <int N, int A> struct __attribute__((packed, aligned(A))) Words {
+  uint32_t u[N];
+};
+template <typename T> struct Raw {                // as loaded
+  static constexpr int E = Wide<T>::E;
+  uint32_t u[4];
+  __device__ __forceinline__ void load(const T* p, int n) {
+    if (n == E) {
+      const Words<4, sizeof(T)> x = *reinterpret_cast<const Words<4, sizeof(T)>*>(p);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u[i] = x.u[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (E == 4) {
+          u[i] = i < n ? __float_as_uint(p[i]) : 0u;
+        } else {
+          const uint32_t lo = 2 * i < n ? p[2 * i] : 0u, hi = 2 * i + 1 < n ? p[2 * i + 1] : 0u;
+          u[i] = hi << 16 | lo;
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void get(float* f) const {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if constexpr (E == 4) {
@@ -54,37 +87,66 @@ template <typename T, int E> __device__ __forceinline__ void vec_get(const T* p,
       }
     }
   }
-}
-template <typename T, int E> __device__ __forceinline__ void vec_put(T* p, const float* f) {
-  if constexpr (E == 1) {
-    *p = from_f<T>(f[0]);
-  } else {
-    u32x4_t u;
+};
+// E entries of a head's parameter row (n of them in the row), or the same value for a row that is not there
+template <int E> __device__ __forceinline__ void params(const float* p, int n, float none, float* f) {
+  if (p && n == E) {
+    const Words<E, 4> x = *reinterpret_cast<const Words<E, 4>*>(p);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (E == 4) u[i] = __float_as_uint(f[i]);
-      else u[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
-    }
-    *reinterpret_cast<u32x4_t*>(p) = u;
+    for (int e = 0; e < E; ++e) f[e] = __uint_as_float(x.u[e]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; ++e) f[e] = p && e < n ? p[e] : none;
   }
 }
-// E codes of an 8-bit tensor with the scale s
-template <int E> __device__ __forceinline__ void vec_codes(const uint8_t* p, float s, float* f) {
-  if constexpr (E == 1) {
-    f[0] = __builtin_amdgcn_cvt_pk_f32_fp8((int)*p, false)[0] * s;
+template <typename T> __device__ __forceinline__ void vec_put(T* p, const float* f, int n) {
+  constexpr int E = Wide<T>::E;
+  if (n == E) {
+    Words<4, sizeof(T)> x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (E == 4) x.u[i] = __float_as_uint(f[i]);
+      else x.u[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+    }
+    *reinterpret_cast<Words<4, sizeof(T)>*>(p) = x;
   } else {
 #pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (e < n) p[e] = from_f<T>(f[e]);
+  }
+}
+template <typename T> struct RawCodes {           // E codes of an 8-bit tensor and their scale byte
+  static constexpr int E = Wide<T>::E;
+  uint32_t u[E / 4], sc;
+  __device__ __forceinline__ void load(const uint8_t* p, const uint8_t* s, int n) {
+    sc = *s;
+    if (n == E) {
+      const Words<E / 4, 1> x = *reinterpret_cast<const Words<E / 4, 1>*>(p);
+#pragma unroll
+      for (int i = 0; i < E / 4; ++i) u[i] = x.u[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < E / 4; ++i) {
+        u[i] = 0;
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          if (4 * i + b < n) u[i] |= (uint32_t)p[4 * i + b] << 8 * b;
+      }
+    }
+  }
+  __device__ __forceinline__ void get(float* f) const {
+    const float s = ckpt_scale(sc);
+#pragma unroll
     for (int i = 0; i < E / 4; ++i) {
-      const uint32_t u = reinterpret_cast<const uint32_t*>(p)[i];
-      const floatx2 a = __builtin_amdgcn_cvt_pk_f32_fp8((int)u, false);
-      const floatx2 b = __builtin_amdgcn_cvt_pk_f32_fp8((int)u, true);
+      const floatx2 a = __builtin_amdgcn_cvt_pk_f32_fp8((int)u[i], false);
+      const floatx2 b = __builtin_amdgcn_cvt_pk_f32_fp8((int)u[i], true);
       f[4 * i] = a[0] * s;
       f[4 * i + 1] = a[1] * s;
       f[4 * i + 2] = b[0] * s;
       f[4 * i + 3] = b[1] * s;
     }
   }
-}
+};
 
 // Value i of an 8-bit tensor with D channels, one scale byte per `grp` channels.
 __device__ __forceinline__ float ckpt_value(const uint8_t* codes, const uint8_t* sc, size_t row, int i, int D,
@@ -97,49 +159,59 @@ __device__ __forceinline__ float ckpt_value(const uint8_t* codes, const uint8_t*
 __device__ __forceinline__ float rstd_of(float var, float eps) { return 1.0f / sqrtf((var < 0.0f ? 0.0f : var) + eps); }
 
 // ------------------------------------------------------------------ forward
-template <typename T, int E, int L, int NV>
+// TAIL: D is not a multiple of E, so a row's last vector holds fewer elements.
+template <typename T, int L, int NV, bool TAIL>
 __global__ void __launch_bounds__(kNormThreads) norm_fwd_kernel(const T* __restrict__ x, const float* __restrict__ w,
                                                                 const float* __restrict__ b, float eps,
                                                                 T* __restrict__ y, float* __restrict__ mean,
                                                                 float* __restrict__ rstd, int H, int T_, int D,
                                                                 int ntile, int tile_rows) {
-  constexpr int RPW = kNormThreads / L;
+  constexpr int E = Wide<T>::E, RPW = kNormThreads / L;
   __shared__ float rsum[kNormThreads / 64];
   const int bh = blockIdx.x / ntile, tile = blockIdx.x - bh * ntile;
   const int c = threadIdx.x % L, rr = threadIdx.x / L;
   const float inv = 1.0f / (float)D;
   float wv[NV][E], bv[NV][E];
-  bool in[NV];
+  int n[NV];                                       // elements of this lane's vectors
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int col = (c + i * L) * E;
-    in[i] = col < D;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      wv[i][e] = in[i] && w ? w[(size_t)(bh % H) * D + col + e] : 1.0f;
-      bv[i][e] = in[i] && b ? b[(size_t)(bh % H) * D + col + e] : 0.0f;
-    }
+    n[i] = min(max(D - col, 0), E);
+    const size_t at = (size_t)(bh % H) * D + col;
+    params<E>(w ? w + at : nullptr, n[i], 1.0f, wv[i]);
+    params<E>(b ? b + at : nullptr, n[i], 0.0f, bv[i]);
   }
+  const auto has = [&](int i, int e) { return TAIL ? e < n[i] : n[i] > 0; };
   const int t_end = min(T_, (tile + 1) * tile_rows);
+  Raw<T> next[NV];                                 // the row after this one, requested before this one's sums
+  const auto request = [&](int t) {
+    if (t < t_end) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (n[i] > 0) next[i].load(x + ((size_t)bh * T_ + t) * D + (c + i * L) * E, TAIL ? n[i] : E);
+    }
+  };
+  request(tile * tile_rows + rr);
   for (int t = tile * tile_rows + rr; t < t_end; t += RPW) {
     const size_t row = (size_t)bh * T_ + t;
     float v[NV][E];
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if (in[i]) vec_get<T, E>(x + row * D + (c + i * L) * E, v[i]);
+      next[i].get(v[i]);
 #pragma unroll
-      for (int e = 0; e < E; ++e) s += in[i] ? v[i][e] : 0.0f;
+      for (int e = 0; e < E; ++e) s += has(i, e) ? v[i][e] : 0.0f;
     }
+    request(t + RPW);
     const float m = row_sum<L>(s, rsum) * inv;
     float q = 0.0f, d = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        v[i][e] -= m;
-        q += in[i] ? v[i][e] * v[i][e] : 0.0f;
-        d += in[i] ? v[i][e] : 0.0f;
+        v[i][e] = has(i, e) ? v[i][e] - m : 0.0f;
+        q = fmaf(v[i][e], v[i][e], q);
+        d += v[i][e];
       }
     // m is rounded (by up to 2^-24 |m|, which shows where a row's mean is far above its spread): what is
     // left of the mean in the differences is taken out of them and of their squares
@@ -149,7 +221,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_fwd_kernel(const T* __restr
     for (int i = 0; i < NV; ++i) {
 #pragma unroll
       for (int e = 0; e < E; ++e) v[i][e] = fmaf((v[i][e] - dm) * r, wv[i][e], bv[i][e]);
-      if (in[i]) vec_put<T, E>(y + row * D + (c + i * L) * E, v[i]);
+      if (n[i] > 0) vec_put<T>(y + row * D + (c + i * L) * E, v[i], TAIL ? n[i] : E);
     }
     if (c == 0) {
       if (mean) mean[row] = m + dm;
@@ -158,7 +230,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_fwd_kernel(const T* __restr
   }
 }
 
-// Any width and alignment: a workgroup per row, which is read three times (the second and third time
+// Any width: a workgroup per row, which is read three times (the second and third time
 // from cache for rows that fit it).
 template <typename T>
 __global__ void __launch_bounds__(kNormThreads) norm_fwd_any_kernel(const T* __restrict__ x,
@@ -192,47 +264,65 @@ __global__ void __launch_bounds__(kNormThreads) norm_fwd_any_kernel(const T* __r
 }
 
 // ------------------------------------------------------------------ backward
-template <typename T, int E, int L, int NV, bool PK>
+template <typename T, int L, int NV, bool TAIL, bool PK>
 __global__ void __launch_bounds__(kNormThreads)
     norm_bwd_kernel(const T* __restrict__ x, const uint8_t* __restrict__ xc, const uint8_t* __restrict__ xs,
                     const float* __restrict__ w, const float* __restrict__ mean, const float* __restrict__ rstd,
-                    const T* __restrict__ dy, T* __restrict__ dx, float* __restrict__ part, int H, int T_, int D,
-                    int grp, int ntile, int tile_rows) {
-  constexpr int RPW = kNormThreads / L;
+                    const T* dy, T* dx, float* __restrict__ part, int H, int T_, int D, int grp, int ntile,
+                    int tile_rows) {
+  constexpr int E = Wide<T>::E, RPW = kNormThreads / L;
   __shared__ float rsum[kNormThreads / 64];
   const int bh = blockIdx.x / ntile, tile = blockIdx.x - bh * ntile;
   const int c = threadIdx.x % L, rr = threadIdx.x / L;
   const float inv = 1.0f / (float)D;
   float wv[NV][E], dw[NV][E], db[NV][E];
-  bool in[NV];
+  int n[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int col = (c + i * L) * E;
-    in[i] = col < D;
+    n[i] = min(max(D - col, 0), E);
+    params<E>(w ? w + (size_t)(bh % H) * D + col : nullptr, n[i], 1.0f, wv[i]);
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      wv[i][e] = in[i] && w ? w[(size_t)(bh % H) * D + col + e] : 1.0f;
-      dw[i][e] = db[i][e] = 0.0f;
-    }
+    for (int e = 0; e < E; ++e) dw[i][e] = db[i][e] = 0.0f;
   }
   const int t_end = min(T_, (tile + 1) * tile_rows);
+  typename std::conditional<PK, RawCodes<T>, Raw<T>>::type nx[NV];
+  Raw<T> ndy[NV];
+  float nm = 0.0f, nr = 0.0f;
+  const auto request = [&](int t) {
+    if (t < t_end) {
+      const size_t row = (size_t)bh * T_ + t;
+      nm = mean[row];
+      nr = rstd[row];
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (n[i] > 0) {
+          const int col = (c + i * L) * E, k = TAIL ? n[i] : E;
+          ndy[i].load(dy + row * D + col, k);
+          if constexpr (PK) nx[i].load(xc + row * D + col, xs + row * (D / grp) + col / grp, k);
+          else nx[i].load(x + row * D + col, k);
+        }
+    }
+  };
+  request(tile * tile_rows + rr);
   for (int t = tile * tile_rows + rr; t < t_end; t += RPW) {
     const size_t row = (size_t)bh * T_ + t;
-    const float m = mean[row], r = rstd[row];
+    const float m = nm, r = nr;
     float xh[NV][E], g[NV][E];
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int col = (c + i * L) * E;
-      if (in[i]) {
-        vec_get<T, E>(dy + row * D + col, g[i]);
-        if constexpr (PK)
-          vec_codes<E>(xc + row * D + col, ckpt_scale(xs[row * (D / grp) + col / grp]), xh[i]);
-        else
-          vec_get<T, E>(x + row * D + col, xh[i]);
+      ndy[i].get(g[i]);
+      nx[i].get(xh[i]);
+    }
+    request(t + RPW);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (n[i] > 0) {
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          xh[i][e] = (xh[i][e] - m) * r;
+          // (elements behind the row's end: dy = 0 there, and 0 in place of x's)
+          xh[i][e] = !TAIL || e < n[i] ? (xh[i][e] - m) * r : 0.0f;
           dw[i][e] = fmaf(g[i][e], xh[i][e], dw[i][e]);
           db[i][e] += g[i][e];
           g[i][e] *= wv[i][e];
@@ -244,10 +334,10 @@ __global__ void __launch_bounds__(kNormThreads)
     const float c1 = row_sum<L>(s1, rsum) * inv, c2 = row_sum<L>(s2, rsum) * inv;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      if (in[i]) {
+      if (n[i] > 0) {
 #pragma unroll
         for (int e = 0; e < E; ++e) g[i][e] = r * (g[i][e] - c1 - xh[i][e] * c2);
-        vec_put<T, E>(dx + row * D + (c + i * L) * E, g[i]);
+        vec_put<T>(dx + row * D + (c + i * L) * E, g[i], TAIL ? n[i] : E);
       }
   }
   if (!part) return;
@@ -273,7 +363,7 @@ __global__ void __launch_bounds__(kNormThreads)
     }
 }
 
-// Any width and alignment: a workgroup takes the tile's rows one after another; a thread's columns
+// Any width: a workgroup takes the tile's rows one after another; a thread's columns
 // (threadIdx.x + 256 i) keep their running sums in the workgroup's part of `part`.
 template <typename T, bool PK>
 __global__ void __launch_bounds__(kNormThreads)
@@ -311,25 +401,29 @@ __global__ void __launch_bounds__(kNormThreads)
   }
 }
 
-// dw[h, i], db[h, i]: sums of the parts of head h's workgroups (B * ntile of them), 64 columns per
+// Sums of the parts of a head's workgroups (2 D columns each: dw's, then db's), kRedParts of them into one
+// at a time until one is left: part p of head h is row (p / nt * H + h) * nt + p % nt.  64 columns per
 // workgroup, four threads per column over interleaved parts.
-__global__ void __launch_bounds__(256) norm_bwd_reduce_kernel(const float* __restrict__ part, float* __restrict__ dw,
-                                                              float* __restrict__ db, int B, int H, int D, int ntile,
-                                                              int ncol) {
+constexpr int kRedParts = 64;
+__global__ void __launch_bounds__(256) norm_bwd_reduce_kernel(const float* __restrict__ part, int np, int nt,
+                                                              float* __restrict__ out, float* __restrict__ dw,
+                                                              float* __restrict__ db, int H, int D, int ncol,
+                                                              int nout) {
   __shared__ float red[4][64];
-  const int h = blockIdx.x / ncol, c0 = (blockIdx.x - h * ncol) * 64;
-  const int c = c0 + (threadIdx.x & 63), sl = threadIdx.x >> 6;       // columns of dw, then of db
+  const int cb = blockIdx.x % ncol, hp = blockIdx.x / ncol, h = hp % H, po = hp / H;
+  const int c = cb * 64 + (threadIdx.x & 63), sl = threadIdx.x >> 6;
+  const int p0 = po * kRedParts, p1 = min(np, p0 + kRedParts);
   float s = 0.0f;
-  if (c < 2 * D)
-    for (int p = sl; p < B * ntile; p += 4) {
-      const int b = p / ntile, t = p - b * ntile;
-      s += part[((size_t)(b * H + h) * ntile + t) * 2 * D + c];
-    }
+  if (c < 2 * D) {
+#pragma unroll 8
+    for (int p = p0 + sl; p < p1; p += 4) s += part[((size_t)(p / nt * H + h) * nt + p % nt) * 2 * D + c];
+  }
   red[sl][threadIdx.x & 63] = s;
   __syncthreads();
   if (sl == 0 && c < 2 * D) {
     s = (red[0][threadIdx.x] + red[1][threadIdx.x]) + (red[2][threadIdx.x] + red[3][threadIdx.x]);
-    if (c < D) {
+    if (nout > 1) out[((size_t)h * nout + po) * 2 * D + c] = s;
+    else if (c < D) {
       if (dw) dw[(size_t)h * D + c] = s;
     } else if (db) {
       db[(size_t)h * D + c - D] = s;
@@ -338,15 +432,19 @@ __global__ void __launch_bounds__(256) norm_bwd_reduce_kernel(const float* __res
 }
 
 // ------------------------------------------------------------------ launchers
-// Rows of one workgroup: enough for the weights' read and the partial sums to be a small part of the
-// rows' bytes, few enough for some 2048 workgroups (8 per CU).
+// Rows of one workgroup: 32 where that leaves 512 workgroups (the weights are read, and partial sums
+// written, once per workgroup: 32768 rows of 512 bf16 take 19.6 us in 1024 workgroups, 23 in 2048; 8192
+// rows of 4096 34 us in 512, 44 in 2048), and no more than 1024 workgroups.
 struct NormPlan {
   int ntile, rows;
 };
 static NormPlan norm_plan(int B, int H, int T, int rpw) {
-  const long long bh = (long long)B * H;
-  long long tiles = (2048 + bh - 1) / bh;
-  const long long most = (T + 4LL * rpw - 1) / (4LL * rpw);  // at least four steps of a workgroup's rows
+  const long long bh = (long long)B * H, total = bh * T;
+  long long want = total / 32;
+  if (want < 512) want = 512;
+  if (want > 1024) want = 1024;
+  long long tiles = (want + bh - 1) / bh;
+  const long long most = (T + rpw - 1) / rpw;      // a step of the workgroup's rows at least
   if (tiles > most) tiles = most;
   if (tiles < 1) tiles = 1;
   long long rows = (T + tiles - 1) / tiles;
@@ -355,91 +453,92 @@ static NormPlan norm_plan(int B, int H, int T, int rpw) {
   return NormPlan{(int)((T + rows - 1) / rows), (int)rows};
 }
 
-// How a row of D elements is held: E per access, L lanes, NV accesses per lane.  One element per access
-// (a quarter to an eighth of the bytes per instruction) where a row's start is not 16-byte aligned; the
-// workgroup shares a row once one wave would need more than 64 (128 for 16-byte accesses) fp32
-// registers for it.  NV = 0: wider than that, the any-width kernels run.
+// How a row of D elements is held: L lanes, NV vectors of E elements per lane; the workgroup shares a row
+// once one wave would need more than 32 fp32 registers for it.  NV = 0: wider than 8 vectors for each of
+// 256 lanes, the any-width kernels run.
 struct NormShape {
-  int E, L, NV;
+  int L, NV;
 };
-static NormShape norm_shape(int D, int Ew, bool aligned) {
-  const int E = aligned && D % Ew == 0 ? Ew : 1;
-  const int n = (D + E - 1) / E, wave_nv = E == 1 ? 16 : (E == 4 ? 8 : 4);
-  NormShape p{E, 1, 1};
-  if (E == 1) p.L = 8;
+static NormShape norm_shape(int D, int E) {
+  const int n = (D + E - 1) / E, wave_nv = 32 / E;
+  NormShape p{1, 1};
   while (p.L < n && p.L < 64) p.L <<= 1;
   while (p.NV * p.L < n) p.NV <<= 1;
   if (p.NV > wave_nv) {
     p.L = kNormThreads;
-    p.NV = E == 1 ? 8 : (E == 4 ? 4 : 2);
+    p.NV = wave_nv / 2;
     while (p.NV * p.L < n) p.NV <<= 1;
-    if (p.NV > (E == 1 ? 32 : 8)) p.NV = 0;
+    if (p.NV > 8) p.NV = 0;
   }
   return p;
 }
-static bool aligned16(const void* a, const void* b, const void* c) {
-  return (((uintptr_t)a | (uintptr_t)b | (uintptr_t)c) & 15) == 0;
-}
-// The shapes above as instances: CASE(E, L, NV).
-#define KDA_NORM_SHAPES(W, CASE)                                                                                   \
-  CASE(W, 1, 1) CASE(W, 2, 1) CASE(W, 4, 1) CASE(W, 8, 1) CASE(W, 16, 1) CASE(W, 32, 1) CASE(W, 64, 1)             \
-  CASE(W, 64, 2) CASE(W, 64, 4) CASE(W, 64, 8) CASE(W, 256, 2) CASE(W, 256, 4) CASE(W, 256, 8)                     \
-  CASE(1, 8, 1) CASE(1, 16, 1) CASE(1, 32, 1) CASE(1, 64, 1) CASE(1, 64, 2) CASE(1, 64, 4) CASE(1, 64, 8)          \
-  CASE(1, 64, 16) CASE(1, 256, 8) CASE(1, 256, 16) CASE(1, 256, 32)
+static int norm_rpw(const NormShape& n) { return n.NV ? kNormThreads / n.L : 1; }
+// The shapes above as instances: CASE(L, NV).
+#define KDA_NORM_SHAPES(CASE)                                                                          \
+  CASE(1, 1) CASE(2, 1) CASE(4, 1) CASE(8, 1) CASE(16, 1) CASE(32, 1) CASE(64, 1) CASE(64, 2)          \
+  CASE(64, 4) CASE(64, 8) CASE(256, 2) CASE(256, 4) CASE(256, 8)
 
 template <typename T>
 hipError_t launch_norm_fwd(const void* x, const float* w, const float* b, float eps, void* y, float* mean, float* rstd,
                            int B, int H, int T_, int D, hipStream_t s) {
   if (T_ == 0) return hipSuccess;
-  const NormShape n = norm_shape(D, Wide<T>::E, aligned16(x, y, nullptr));
+  const NormShape n = norm_shape(D, Wide<T>::E);
   if (n.NV == 0) {
     hipLaunchKernelGGL(norm_fwd_any_kernel<T>, dim3((unsigned)((size_t)B * H * T_)), dim3(kNormThreads), 0, s,
                        (const T*)x, w, b, eps, (T*)y, mean, rstd, H, T_, D);
     return hipGetLastError();
   }
-  const NormPlan p = norm_plan(B, H, T_, kNormThreads / n.L);
+  const NormPlan p = norm_plan(B, H, T_, norm_rpw(n));
   const dim3 grid((unsigned)(B * H * p.ntile));
-#define KDA_NORM(E_, L_, NV_)                                                                                         \
-  if (n.E == E_ && n.L == L_ && n.NV == NV_)                                                                          \
-    hipLaunchKernelGGL((norm_fwd_kernel<T, E_, L_, NV_>), grid, dim3(kNormThreads), 0, s, (const T*)x, w, b, eps,     \
-                       (T*)y, mean, rstd, H, T_, D, p.ntile, p.rows);
-  KDA_NORM_SHAPES(Wide<T>::E, KDA_NORM)
+  const bool tail = D % Wide<T>::E != 0;
+#define KDA_NORM(L_, NV_)                                                                                             \
+  if (n.L == L_ && n.NV == NV_) {                                                                                     \
+    if (tail)                                                                                                         \
+      hipLaunchKernelGGL((norm_fwd_kernel<T, L_, NV_, true>), grid, dim3(kNormThreads), 0, s, (const T*)x, w, b, eps, \
+                         (T*)y, mean, rstd, H, T_, D, p.ntile, p.rows);                                               \
+    else                                                                                                              \
+      hipLaunchKernelGGL((norm_fwd_kernel<T, L_, NV_, false>), grid, dim3(kNormThreads), 0, s, (const T*)x, w, b,     \
+                         eps, (T*)y, mean, rstd, H, T_, D, p.ntile, p.rows);                                          \
+  }
+  KDA_NORM_SHAPES(KDA_NORM)
 #undef KDA_NORM
   return hipGetLastError();
 }
 
-// Rows per workgroup for the backward pass.  The plan must not depend on the addresses (the caller sizes
-// the workspace before it has them), so it goes by the aligned shape; any shape can run under it.
-static NormPlan norm_bwd_plan(int B, int H, int T, int D, int Ew) {
-  const NormShape n = norm_shape(D, Ew, true);
-  return norm_plan(B, H, T, n.NV ? kNormThreads / n.L : 1);
-}
-
+// Partial sums of the workgroups, then those of the reduction's steps one behind the other.
 size_t norm_bwd_workspace_bytes(int B, int H, int T, int D, bool bf16) {
   if (T < 1) return 0;
-  const NormPlan p = norm_bwd_plan(B, H, T, D, bf16 ? 8 : 4);
-  return (size_t)B * H * p.ntile * 2 * D * sizeof(float);
+  const NormPlan p = norm_plan(B, H, T, norm_rpw(norm_shape(D, bf16 ? 8 : 4)));
+  size_t rows = 0;
+  for (long long np = (long long)B * p.ntile;; np = (np + kRedParts - 1) / kRedParts) {
+    rows += (size_t)H * np;
+    if (np <= kRedParts) break;
+  }
+  return rows * 2 * D * sizeof(float);
 }
 
 template <typename T, bool PK>
 static hipError_t norm_bwd(const void* x, const uint8_t* xs, const float* w, const float* mean, const float* rstd,
-                           const void* dy, void* dx, float* part, int B, int H, int T_, int D, hipStream_t s) {
+                           const void* dy, void* dx, float* part, int B, int H, int T_, int D, const NormShape& n,
+                           const NormPlan& p, hipStream_t s) {
   const int grp = D < 32 ? D : 32;
-  const NormPlan p = norm_bwd_plan(B, H, T_, D, Wide<T>::E);
   const dim3 grid((unsigned)(B * H * p.ntile));
   const T* xt = PK ? nullptr : (const T*)x;
   const uint8_t* xc = PK ? (const uint8_t*)x : nullptr;
-  const NormShape n = norm_shape(D, Wide<T>::E, aligned16(x, dy, dx));
-  if (n.NV == 0) {
+  const bool tail = D % Wide<T>::E != 0;
+  if (n.NV == 0)
     hipLaunchKernelGGL((norm_bwd_any_kernel<T, PK>), grid, dim3(kNormThreads), 0, s, xt, xc, xs, w, mean, rstd,
                        (const T*)dy, (T*)dx, part, H, T_, D, grp, p.ntile, p.rows);
-    return hipGetLastError();
+#define KDA_NORM(L_, NV_)                                                                                              \
+  if (n.L == L_ && n.NV == NV_) {                                                                                      \
+    if (tail)                                                                                                          \
+      hipLaunchKernelGGL((norm_bwd_kernel<T, L_, NV_, true, PK>), grid, dim3(kNormThreads), 0, s, xt, xc, xs, w, mean, \
+                         rstd, (const T*)dy, (T*)dx, part, H, T_, D, grp, p.ntile, p.rows);                            \
+    else                                                                                                               \
+      hipLaunchKernelGGL((norm_bwd_kernel<T, L_, NV_, false, PK>), grid, dim3(kNormThreads), 0, s, xt, xc, xs, w,      \
+                         mean, rstd, (const T*)dy, (T*)dx, part, H, T_, D, grp, p.ntile, p.rows);                      \
   }
-#define KDA_NORM(E_, L_, NV_)                                                                                         \
-  if (n.E == E_ && n.L == L_ && n.NV == NV_)                                                                          \
-    hipLaunchKernelGGL((norm_bwd_kernel<T, E_, L_, NV_, PK>), grid, dim3(kNormThreads), 0, s, xt, xc, xs, w, mean,    \
-                       rstd, (const T*)dy, (T*)dx, part, H, T_, D, grp, p.ntile, p.rows);
-  KDA_NORM_SHAPES(Wide<T>::E, KDA_NORM)
+  KDA_NORM_SHAPES(KDA_NORM)
 #undef KDA_NORM
   return hipGetLastError();
 }
@@ -449,17 +548,24 @@ hipError_t launch_norm_bwd(const void* x, const uint8_t* x_scales, const float* 
                            const float* rstd, const void* dy, void* dx, float* dw, float* db, void* workspace, int B,
                            int H, int T_, int D, hipStream_t s) {
   float* part = (dw || db) ? reinterpret_cast<float*>(workspace) : nullptr;
-  int ntile = 0;
+  const NormShape n = norm_shape(D, Wide<T>::E);
+  const NormPlan p = norm_plan(B, H, T_, norm_rpw(n));
   if (T_ > 0) {
-    ntile = norm_bwd_plan(B, H, T_, D, Wide<T>::E).ntile;
-    const hipError_t e = x_scales ? norm_bwd<T, true>(x, x_scales, w, mean, rstd, dy, dx, part, B, H, T_, D, s)
-                                  : norm_bwd<T, false>(x, x_scales, w, mean, rstd, dy, dx, part, B, H, T_, D, s);
+    const hipError_t e = x_scales ? norm_bwd<T, true>(x, x_scales, w, mean, rstd, dy, dx, part, B, H, T_, D, n, p, s)
+                                  : norm_bwd<T, false>(x, x_scales, w, mean, rstd, dy, dx, part, B, H, T_, D, n, p, s);
     if (e != hipSuccess) return e;
   }
-  if (dw || db) {                                  // (T = 0: both come out zero)
+  if (dw || db) {                                  // (T = 0: no parts, both come out zero)
     const int ncol = (2 * D + 63) / 64;
-    hipLaunchKernelGGL(norm_bwd_reduce_kernel, dim3((unsigned)(H * ncol)), dim3(256), 0, s, part, dw, db, B, H, D,
-                       ntile, ncol);
+    int np = T_ > 0 ? B * p.ntile : 0, nt = p.ntile > 0 ? p.ntile : 1;
+    for (;;) {
+      const int nout = np > kRedParts ? (np + kRedParts - 1) / kRedParts : 1;
+      float* out = part ? part + (size_t)H * np * 2 * D : nullptr;
+      hipLaunchKernelGGL(norm_bwd_reduce_kernel, dim3((unsigned)((long long)H * ncol * nout)), dim3(256), 0, s, part,
+                         np, nt, out, dw, db, H, D, ncol, nout);
+      if (nout == 1) break;
+      part = out, np = nout, nt = nout;            // part p of head h at row h * nout + p from here on
+    }
   }
   return hipGetLastError();
 }

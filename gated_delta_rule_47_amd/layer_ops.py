@@ -118,7 +118,7 @@ def decay_attn_fwd(q, k, v, log_decay, state_in=None, lengths=None, scale=None, 
     pe = _opt("state_out", state_out, state, _F32, dev)
     _gpu(dev)
     if out is None:
-        out = torch.empty(shape, dtype=dt, device=dev)
+        out = torch.empty_like(v)
         po = out.data_ptr()
     if not output_state:
         state_out = pe = None
@@ -145,7 +145,7 @@ def decay_attn_step(q, k, v, log_decay, state, scale=None, out=None):
     po = _opt("out", out, shape, dt, dev)
     _gpu(dev)
     if out is None:
-        out = torch.empty(shape, dtype=dt, device=dev)
+        out = torch.empty_like(v)
         po = out.data_ptr()
     _run(dev, "kda_decay_attn_step", pq, pk, pv, pg, ps, _scale_of(K) if scale is None else float(scale), po, B, H, K,
          V, code)
@@ -204,7 +204,7 @@ def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, want_stats=True, out=Non
     py = _opt("out", out, shape, dt, dev)
     _gpu(dev)
     if out is None:
-        out = torch.empty(shape, dtype=dt, device=dev)
+        out = torch.empty_like(x)
         py = out.data_ptr()
     mean = rstd = pm = pr = None
     if want_stats:
@@ -233,7 +233,7 @@ def layer_norm_bwd(x, weight, mean, rstd, dy, want_params=True, workspace=None, 
     pdx = _opt("dx_out", dx_out, shape, dt, dev)
     _gpu(dev)
     if dx_out is None:
-        dx_out = torch.empty(shape, dtype=dt, device=dev)
+        dx_out = torch.empty_like(dy)
         pdx = dx_out.data_ptr()
     dw = db = pdw = pdb = None
     need = 0
