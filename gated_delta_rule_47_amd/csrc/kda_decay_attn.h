@@ -48,6 +48,7 @@ struct SegArgs {
   float* seg_state;          // (B*H, nseg, K, V)
   float u;
   int BH, H, T, K, V, nseg, seglen;
+  bool returned;             // the end state that these lead to is returned
 };
 
 typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
@@ -74,7 +75,7 @@ template <typename U> using Lds = __attribute__((address_space(3))) U;
 template <typename T> struct Lin;
 
 template <> struct Lin<bf16_t> {                 // v_mfma_f32_16x16x32_bf16
-  static constexpr int DG = 32, NACC = 2, EPP = 8, PAD = 0, SPLIT = 3;
+  static constexpr int DG = 32, NACC = 2, EPP = 8, PAD = 0, FINE = 3, COARSE = 2;
   typedef short8 frag;
   static __device__ __forceinline__ int row_of(int ct, int m) {
     return 32 * (ct >> 1) + 8 * (m >> 2) + 4 * (ct & 1) + (m & 3);
@@ -111,15 +112,14 @@ template <> struct Lin<bf16_t> {                 // v_mfma_f32_16x16x32_bf16
     return __builtin_bit_cast(short8, u32x4_t{pack_bf16x2(x[0][0], x[0][1]), pack_bf16x2(x[0][2], x[0][3]),
                                               pack_bf16x2(x[1][0], x[1][1]), pack_bf16x2(x[1][2], x[1][3])});
   }
-  // x f as the sum of SPLIT bf16 parts, off by 2^-26 of it: the state is returned in fp32, and the
-  // rounding of two parts (2^-17) would show in it
-  static __device__ __forceinline__ void scaled(frag x, const float* f, frag* out) {
-    u32x4_t part[SPLIT];
+  // x f as the sum of N bf16 parts, off by at most 2^-17 (two) or 2^-26 (three) of it
+  template <int N> static __device__ __forceinline__ void scaled(frag x, const float* f, frag* out) {
+    u32x4_t part[N];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       float a = bf2f((bf16_t)x[2 * e]) * f[2 * e], b = bf2f((bf16_t)x[2 * e + 1]) * f[2 * e + 1];
 #pragma unroll
-      for (int s = 0; s < SPLIT; ++s) {
+      for (int s = 0; s < N; ++s) {
         const uint32_t w = pack_bf16x2(a, b);
         part[s][e] = w;
         a -= __uint_as_float(w << 16);
@@ -127,7 +127,7 @@ template <> struct Lin<bf16_t> {                 // v_mfma_f32_16x16x32_bf16
       }
     }
 #pragma unroll
-    for (int s = 0; s < SPLIT; ++s) out[s] = __builtin_bit_cast(short8, part[s]);
+    for (int s = 0; s < N; ++s) out[s] = __builtin_bit_cast(short8, part[s]);
   }
   // token (within a group of DG) of fragment element e in the accumulator order
   static __device__ __forceinline__ int tok_of(int e, int g) { return 16 * (e >> 2) + 4 * g + (e & 3); }
@@ -137,7 +137,7 @@ template <> struct Lin<bf16_t> {                 // v_mfma_f32_16x16x32_bf16
 };
 
 template <> struct Lin<float> {                  // four v_mfma_f32_16x16x4_f32
-  static constexpr int DG = 16, NACC = 1, EPP = 4, PAD = 4, SPLIT = 1;
+  static constexpr int DG = 16, NACC = 1, EPP = 4, PAD = 4, FINE = 1, COARSE = 1;
   typedef floatx4 frag;
   static __device__ __forceinline__ int row_of(int ct, int m) { return 16 * ct + m; }
   template <int W, bool IMG> static __device__ __forceinline__ int at(int t, int e) { return t * (W + PAD) + e; }
@@ -156,7 +156,7 @@ template <> struct Lin<float> {                  // four v_mfma_f32_16x16x4_f32
     return c;
   }
   static __device__ __forceinline__ frag from_acc(const floatx4* x) { return x[0]; }
-  static __device__ __forceinline__ void scaled(frag x, const float* f, frag* out) {
+  template <int N> static __device__ __forceinline__ void scaled(frag x, const float* f, frag* out) {
     out[0] = floatx4{x[0] * f[0], x[1] * f[1], x[2] * f[2], x[3] * f[3]};
   }
   static __device__ __forceinline__ int tok_of(int e, int g) { return 4 * g + e; }
@@ -424,24 +424,37 @@ template <typename T, int KD, int VT, int C, int NK, int NV, bool REV> struct St
         f[d][e] = i < n ? u * decay_pow(g2, REV ? i + 1 : n - 1 - i) : 0.0f;
       }
   }
-  __device__ __forceinline__ void update(const Lds<T>* sK, const Lds<T>* sV, int ct0, int vt0, Decay2 an, int lane) {
+  // `fine`: as exactly as fp32 holds it (see fine_state)
+  __device__ __forceinline__ void update(const Lds<T>* sK, const Lds<T>* sV, int ct0, int vt0, Decay2 an, bool fine,
+                                         int lane) {
+    if (fine) {
 #pragma unroll
-    for (int i = 0; i < NK; ++i)
+      for (int i = 0; i < NK; ++i)
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(acc[i][j][r], an.hi, acc[i][j][r] * an.lo);
+      add<L::FINE>(sK, sV, ct0, vt0, lane);
+    } else {
+#pragma unroll
+      for (int i = 0; i < NK; ++i)
+#pragma unroll
+        for (int j = 0; j < NV; ++j) acc[i][j] *= an.hi;
+      add<L::COARSE>(sK, sV, ct0, vt0, lane);
+    }
+  }
+  template <int N>
+  __device__ __forceinline__ void add(const Lds<T>* sK, const Lds<T>* sV, int ct0, int vt0, int lane) {
+#pragma unroll
+    for (int d = 0; d < C / L::DG; ++d) {
+      typename L::frag kf[NK], vf[NV][N];
 #pragma unroll
       for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(acc[i][j][r], an.hi, acc[i][j][r] * an.lo);
-    constexpr int ND = C / L::DG;
-#pragma unroll
-    for (int d = 0; d < ND; ++d) {
-      typename L::frag kf[NK], vf[NV][L::SPLIT];
-#pragma unroll
-      for (int j = 0; j < NV; ++j)
-        L::scaled(L::template tr<VT, false>(sV, vt0 + j, d * L::DG, lane), f[d], vf[j]);
+        L::template scaled<N>(L::template tr<VT, false>(sV, vt0 + j, d * L::DG, lane), f[d], vf[j]);
 #pragma unroll
       for (int i = 0; i < NK; ++i) kf[i] = L::template tr<KD, true>(sK, ct0 + i, d * L::DG, lane);
 #pragma unroll
-      for (int s = 0; s < L::SPLIT; ++s)
+      for (int s = 0; s < N; ++s)
 #pragma unroll
         for (int i = 0; i < NK; ++i)
 #pragma unroll
@@ -449,6 +462,18 @@ template <typename T, int KD, int VT, int C, int NK, int NV, bool REV> struct St
     }
   }
 };
+
+// How exactly a chunk's part of the state is computed.  The state serves two ends.  The outputs read its
+// bf16 image: two bf16 parts of the decayed operand (2^-17) and a decay rounded to fp32 are far below that
+// rounding.  The end state is returned in fp32, where both would show (2.8e-6 of the state, and 6e-8 for
+// every chunk of a long sequence), but only from chunks that the decay to the end leaves something of: a
+// chunk counts as fine, three parts (2^-26) and the decay in two floats, while a^{tokens behind it} is over
+// 2^-10, and nothing does where no end state is returned.  At 4 x 32 heads of 16384 tokens, K = V = 128,
+// slopes 1/2 to 1/512, all chunks fine take 535 us, by this rule 495 (the GPU runs these walks at its power
+// limit, so time follows the matrix work).
+__device__ __forceinline__ bool fine_state(bool returned, float g2, int behind) {
+  return returned && g2 * (float)behind > -10.0f;
+}
 
 // ------------------------------------------------------------------ the walk
 // How NW state waves share the KD x VT state: one 16-column value tile and a part of the channels each.
@@ -602,7 +627,8 @@ __device__ __forceinline__ void walk(const WalkArgs& a, int block, Lds<T>* smem)
       const int n = chunk_n(ci);
       begin(ci);
       st.factors(g2, a.u, n, lane);
-      st.update(tile_k(ci), tile_v(ci), ct0, sv0, n == C ? an : an_short, lane);
+      const bool fine = fine_state(a.state_out != nullptr, g2, REV ? chunk_t0(ci) : len - chunk_t0(ci) - n);
+      st.update(tile_k(ci), tile_v(ci), ct0, sv0, n == C ? an : an_short, fine, lane);
       if (ci + 1 < nch) {
         st.image(sS + (ci + 1 & 1) * W::kS, ct0, 16 * sv0, lane);
         end(ci);
@@ -654,10 +680,18 @@ __device__ __forceinline__ void walk(const WalkArgs& a, int block, Lds<T>* smem)
       const auto scores = [&](int d) {
 #pragma unroll
         for (int s = 0; s < L::NACC; ++s) p[s] = zero4();
+        // (the outer tile of the diagonal's group may be cut off whole)
+        constexpr int IN = REV ? L::NACC - 1 : 0, OUT = L::NACC - 1 - IN;
+        const bool outer = REV ? d * L::NACC + OUT >= ti : d * L::NACC + OUT <= ti;
+        if (L::NACC == 1 || outer) {
 #pragma unroll
-        for (int x = 0; x < NQ; ++x)
+          for (int x = 0; x < NQ; ++x)
 #pragma unroll
-          for (int s = 0; s < L::NACC; ++s) p[s] = L::mma(kf[s][x], qf[x], p[s]);
+            for (int s = 0; s < L::NACC; ++s) p[s] = L::mma(kf[s][x], qf[x], p[s]);
+        } else {
+#pragma unroll
+          for (int x = 0; x < NQ; ++x) p[IN] = L::mma(kf[IN][x], qf[x], p[IN]);
+        }
       };
       const auto masked = [&](int d) {
 #pragma unroll
@@ -834,7 +868,8 @@ __device__ __forceinline__ void segment_state(const SegArgs& a, int block, Lds<T
       chunk_barrier();
     }
     st.factors(g2, a.u, n, lane);
-    st.update(tile_k(ci), tile_v(ci), ct0, sv0, n == C ? an : an_short, lane);
+    const bool fine = fine_state(a.returned, g2, REV ? chunk_t0(ci) : len - chunk_t0(ci) - n);
+    st.update(tile_k(ci), tile_v(ci), ct0, sv0, n == C ? an : an_short, fine, lane);
   }
   st.save(a.seg_state + ((size_t)bh * a.nseg + seg) * a.K * a.V, a.V, 1, ct0, v0 + 16 * sv0, a.K, a.V, lane);
 }

@@ -125,7 +125,8 @@ hipError_t launch_decay_fwd(const void* q, const void* k, const void* v, const f
   const DecayPlan p = decay_plan(B, H, T_, K, V, sizeof(T) == 2, false);
   float* ws = reinterpret_cast<float*>(workspace);
   if (p.nseg > 1) {
-    const SegArgs g{k, v, nullptr, nullptr, log_decay, lengths, ws, 1.0f, B * H, H, T_, K, V, p.nseg, p.seglen};
+    const SegArgs g{k, v, nullptr, nullptr, log_decay, lengths, ws, 1.0f, B * H, H, T_, K, V, p.nseg, p.seglen,
+                    state_out != nullptr};
     hipError_t e = segments<T>(g, nullptr, false, s);
     if (e == hipSuccess) e = join(JoinArgs{ws, state_in}, nullptr, log_decay, lengths, B, H, T_, K * V, p, s);
     if (e != hipSuccess) return e;
@@ -153,8 +154,8 @@ hipError_t launch_decay_bwd(const void* q, const void* k, const void* v, const u
   const bool packed = q_sc != nullptr;                      // q, k and v, all or none
   hipError_t e = hipSuccess;
   if (p.nseg > 1) {
-    const SegArgs gs{k, v, k_sc, v_sc, log_decay, lengths, wS, 1.0f, B * H, H, T_, K, V, p.nseg, p.seglen};
-    const SegArgs gr{q, d_o, q_sc, nullptr, log_decay, lengths, wR, scale, B * H, H, T_, K, V, p.nseg, p.seglen};
+    const SegArgs gs{k, v, k_sc, v_sc, log_decay, lengths, wS, 1.0f, B * H, H, T_, K, V, p.nseg, p.seglen, false};
+    const SegArgs gr{q, d_o, q_sc, nullptr, log_decay, lengths, wR, scale, B * H, H, T_, K, V, p.nseg, p.seglen, true};
     e = segments<T>(gs, &gr, packed, s);
     const JoinArgs jr{wR, d_state_out};
     if (e == hipSuccess) e = join(JoinArgs{wS, state_in}, &jr, log_decay, lengths, B, H, T_, K * V, p, s);
