@@ -63,26 +63,30 @@ template <typename U> using Lds = __attribute__((address_space(3))) U;
 // lane % 16 and lane group g = lane / 16, DG / 4 of the group's indices: DG / 4 consecutive ones
 // when read along memory (`nat`), or those in which NACC accumulator tiles hold them (`from_acc`:
 // index 16 n + 4 g + r of tile n).  `tr` reads the transpose of a [index][column] tile in the
-// accumulator order.  Tile `ct` of 16 rows covers the rows row_of(ct, m), m = 0..15, which give a
-// lane's accumulator registers of NACC adjacent tiles DG / 4 consecutive rows.
+// accumulator order.  Tile `ct` of 16 rows covers the rows row_of(ct, m), m = 0..15: a lane's accumulator
+// registers hold four consecutive rows of each, and of NACC adjacent tiles DG / 4 consecutive rows.
 //
-// bf16 LDS tiles are [row][W elements] without padding; the 16-byte pieces of row t are stored in the
-// order piece ^ swz(t).  64 banks hold 16 pieces, so W's pieces per row leave some low bits of t to the address
-// and the rest, permuted, to swz: the 16 rows of a natural read, the 4 rows x 4 column blocks of each
-// transposing read and the 16 columns of the state image's writes all fall on different banks.  (With
-// rows padded by 16 bytes instead, over half of the LDS cycles were conflicts of the transposing reads.)
-// fp32 tiles have no transposing reads and rows padded by 16 bytes are free of conflicts.
+// LDS has 64 banks of 4 bytes.  One cycle serves 16 lanes of a 16-byte read, and these are not consecutive:
+// lanes 0-3, 12-15 and 20-27 of each 32, then the others (of a natural read, rows 0-3 and 12-15 at one piece
+// and rows 4-11 at the next); 32 consecutive lanes of an 8-byte read, 16 of an 8-byte write (measured, two
+// lanes at a time).  bf16 tiles are [row][W elements] without padding; the 16-byte pieces of row t are stored
+// in the order piece ^ swz(t).  64 banks hold 16 pieces, so W's pieces per row leave some low bits of t to
+// the address and the rest to swz, whose lowest bit differs between two rows of 4-11 (and of the others).
+// With row_of()'s halves, which alternate from one lane group to the next, every read above and the image's
+// writes then fall on different banks.  (Rows padded by 16 bytes, and rows in the order piece ^ t, took
+// twice the cycles for every one of these reads.)  fp32 rows are padded by 16 bytes: their transposed
+// reads are single words, free of conflicts; natural reads take two cycles for one.
 template <typename T> struct Lin;
 
 template <> struct Lin<bf16_t> {                 // v_mfma_f32_16x16x32_bf16
   static constexpr int DG = 32, NACC = 2, EPP = 8, PAD = 0, FINE = 3, COARSE = 2;
   typedef short8 frag;
   static __device__ __forceinline__ int row_of(int ct, int m) {
-    return 32 * (ct >> 1) + 8 * (m >> 2) + 4 * (ct & 1) + (m & 3);
+    return 32 * (ct >> 1) + 8 * (m >> 2) + 4 * ((ct ^ m >> 2) & 1) + (m & 3);
   }
   // IMG: the state image, whose natural reads take the rows row_of() of a tile
   template <int W, bool IMG> static __device__ __forceinline__ int swz(int t) {
-    const int lo = IMG ? ((t >> 4 ^ t >> 2) & 1) << 1 | (t >> 3 & 1) : t >> 2 & 3;
+    const int lo = IMG ? ((t >> 4 ^ t >> 2) & 1) << 1 | (t >> 3 & 1) : ((t >> 3 ^ t >> 2) & 1) << 1 | (t >> 2 & 1);
     if constexpr (W == 128) return (t & 3) << 2 | lo;
     else if constexpr (W == 64) return (t & 2) << 1 | lo;
     else return lo;
@@ -98,7 +102,7 @@ template <> struct Lin<bf16_t> {                 // v_mfma_f32_16x16x32_bf16
   // four columns and lane j receives column j of the group's 16
   template <int W, bool PERM> static __device__ __forceinline__ frag tr(const Lds<bf16_t>* base, int ct, int d0, int lane) {
     const int g = lane >> 4, r = (lane >> 2) & 3, m = lane & 3;
-    const int col = PERM ? 32 * (ct >> 1) + 8 * m + 4 * (ct & 1) : 16 * ct + 4 * m;
+    const int col = PERM ? row_of(ct, 4 * m) : 16 * ct + 4 * m;
     const Lds<bf16_t>* p = base + at<W, false>(d0 + 4 * g + r, col);     // (swz is the same 16 rows on)
     const short4v_t a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds<short4v_t>*)p);
     const short4v_t b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds<short4v_t>*)(p + 16 * W));
@@ -111,6 +115,14 @@ template <> struct Lin<bf16_t> {                 // v_mfma_f32_16x16x32_bf16
   static __device__ __forceinline__ frag from_acc(const floatx4* x) {
     return __builtin_bit_cast(short8, u32x4_t{pack_bf16x2(x[0][0], x[0][1]), pack_bf16x2(x[0][2], x[0][3]),
                                               pack_bf16x2(x[1][0], x[1][1]), pack_bf16x2(x[1][2], x[1][3])});
+  }
+  // the 8 consecutive rows that a lane holds of tiles ct, ct + 1 (ct even): in odd lane groups the second
+  // tile has the first four
+  static __device__ __forceinline__ u32x4_t row16(const floatx4* x, int lane) {
+    const u32x2_t a = {pack_bf16x2(x[0][0], x[0][1]), pack_bf16x2(x[0][2], x[0][3])};
+    const u32x2_t b = {pack_bf16x2(x[1][0], x[1][1]), pack_bf16x2(x[1][2], x[1][3])};
+    const bool odd = lane >> 4 & 1;
+    return u32x4_t{odd ? b[0] : a[0], odd ? b[1] : a[1], odd ? a[0] : b[0], odd ? a[1] : b[1]};
   }
   // x f as the sum of N bf16 parts, off by at most 2^-17 (two) or 2^-26 (three) of it
   template <int N> static __device__ __forceinline__ void scaled(frag x, const float* f, frag* out) {
@@ -156,6 +168,7 @@ template <> struct Lin<float> {                  // four v_mfma_f32_16x16x4_f32
     return c;
   }
   static __device__ __forceinline__ frag from_acc(const floatx4* x) { return x[0]; }
+  static __device__ __forceinline__ u32x4_t row16(const floatx4* x, int) { return __builtin_bit_cast(u32x4_t, x[0]); }
   template <int N> static __device__ __forceinline__ void scaled(frag x, const float* f, frag* out) {
     out[0] = floatx4{x[0] * f[0], x[1] * f[1], x[2] * f[2], x[3] * f[3]};
   }
@@ -295,7 +308,15 @@ template <typename T, int C, int DK, int DV, int DQ, int NW> struct Copy {
   typedef Tile<T, C, (DQ ? DQ : 32)> TQ;
   static constexpr int IK = TK::NP / 64, IV = TV::NP / 64, IQ = DQ ? TQ::NP / 64 : 0, NI = IK + IV + IQ;
   static constexpr int PER = (NI + NW - 1) / NW, MIN = NI / NW;
-  unsigned off[PER];                             // byte offset of this lane's piece from the chunk's first row
+  // byte offset of this lane's piece from the chunk's first row; q's are k's where the waves come round to the
+  // same places
+  static constexpr bool SAME = (IK + IV) % NW == 0 && DQ == DK;
+  static constexpr int NOFF = SAME ? (IK + IV) / NW : PER;
+  uint32_t off[(NOFF + 1) / 2];                  // two in a register, -1 outside the tensor's channels
+  static_assert(C * 128 * sizeof(T) <= 32768, "offsets of 15 bits");
+  __device__ __forceinline__ unsigned offset(int i) const {
+    return (unsigned)(i & 1 ? (int)off[i / 2] >> 16 : (int)(short)off[i / 2]);
+  }
 
   template <int DP> static __device__ __forceinline__ unsigned piece(int slot, int D, int ch0) {
     typedef Tile<T, C, DP> TL;
@@ -304,15 +325,17 @@ template <typename T, int C, int DK, int DV, int DQ, int NW> struct Copy {
     int pc = pos;
     if constexpr (Lin<T>::PAD == 0) pc = pos ^ (Lin<T>::template at<DP, false>(row, 0) - row * DP) / E;
     const int ch = ch0 + pc * E;
-    return row < C && pc < W && ch < D ? (unsigned)(row * D + ch) * (unsigned)sizeof(T) : 0xfffffff0u;
+    return row < C && pc < W && ch < D ? (unsigned)(row * D + ch) * (unsigned)sizeof(T) : 0xffffu;
   }
   __device__ __forceinline__ Copy(int wave, int lane, int K, int V, int v0) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
+    for (int i = 0; i < NOFF; ++i) {
       const int x = wave + i * NW;
-      off[i] = x < IK ? piece<DK>(64 * x + lane, K, 0)
-                      : x < IK + IV ? piece<DV>(64 * (x - IK) + lane, V, v0)
-                                    : piece<TQ::PPR * Lin<T>::EPP - Lin<T>::PAD>(64 * (x - IK - IV) + lane, K, 0);
+      const unsigned o = x < IK ? piece<DK>(64 * x + lane, K, 0)
+                                : x < IK + IV
+                                      ? piece<DV>(64 * (x - IK) + lane, V, v0)
+                                      : piece<TQ::PPR * Lin<T>::EPP - Lin<T>::PAD>(64 * (x - IK - IV) + lane, K, 0);
+      off[i / 2] = i & 1 ? off[i / 2] | o << 16 : o;
     }
   }
   // tokens from t0 into the tiles at lds (K, V and Q one behind the other)
@@ -324,7 +347,7 @@ template <typename T, int C, int DK, int DV, int DQ, int NW> struct Copy {
       const int x = wave + i * NW;
       if (x < NI) {
         const bool isv = x >= IK && x < IK + IV;
-        copy_to_lds(isv ? rv : (x < IK ? rk : rq), lds + x * 64 * Lin<T>::EPP, off[i], isv ? sv : sk);
+        copy_to_lds(isv ? rv : (x < IK ? rk : rq), lds + x * 64 * Lin<T>::EPP, offset(i < NOFF ? i : i - NOFF), isv ? sv : sk);
       }
     }
   }
@@ -339,6 +362,11 @@ __device__ __forceinline__ void wait_vm_all() { __builtin_amdgcn_s_waitcnt(0x0F7
 __device__ __forceinline__ void chunk_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
 // ------------------------------------------------------------------ decay
+// A value that is the same in all lanes, kept in a scalar register.
+__device__ __forceinline__ float uniform(float x) {
+  return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(x)));
+}
+
 // a^n for n >= 0 as hi + lo: the chunk factor multiplies the state once per chunk, and a bias of one
 // fp32 rounding would add up over the hundreds of chunks of a long sequence.
 struct Decay2 {
@@ -346,18 +374,12 @@ struct Decay2 {
 };
 __device__ __forceinline__ Decay2 decay_pow2(float g, int n) {
   const double x = n == 0 ? 1.0 : exp((double)g * n);
-  Decay2 d;
-  d.hi = (float)x;
-  d.lo = (float)(x - (double)d.hi);
-  return d;
+  const float hi = (float)x;
+  return Decay2{uniform(hi), uniform((float)(x - (double)hi))};
 }
 // a^n, g2 = log2(a); n = 0 gives 1 also for a = 0 (g2 = -inf)
 __device__ __forceinline__ float decay_pow(float g2, int n) { return n == 0 ? 1.0f : fast_exp2(g2 * (float)n); }
 
-// A value that is the same in all lanes, kept in a scalar register.
-__device__ __forceinline__ float uniform(float x) {
-  return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(x)));
-}
 
 // ------------------------------------------------------------------ state part of a chunk
 // The accumulators of one state wave: rows of the channel tiles ct0 .. ct0 + NK - 1, columns of
@@ -416,6 +438,7 @@ template <typename T, int KD, int VT, int C, int NK, int NV, bool REV> struct St
   __device__ __forceinline__ void factors(float g2, float u, int n, int lane) {
     if (n == n_of_f) return;
     n_of_f = n;
+    asm volatile("" : "+v"(lane));                 // computed here, not kept from before the loop
 #pragma unroll
     for (int d = 0; d < C / L::DG; ++d)
 #pragma unroll
@@ -483,8 +506,9 @@ template <int KD, int VT, int NW> struct StateShape {
   static_assert(NK >= 1 && NV >= 1, "tile too small for the waves");
 };
 
-// Four output waves: one per 16 tokens (and, in fp32's shorter chunks, per half of the value tile); four
-// state waves, of about the same length.
+constexpr int kWalkThreads = 512;
+// Four output waves: one per 16 tokens (and, in fp32's shorter chunks, per half of the value tile).  Four
+// state waves of about the same length.
 template <typename T, int KD, int VT> struct WalkShape {
   typedef Lin<T> L;
   static constexpr int C = sizeof(T) == 4 ? 32 : 64;
@@ -492,8 +516,8 @@ template <typename T, int KD, int VT> struct WalkShape {
   static constexpr int NO = VT / 16 / NVP;                            // value tiles of an output wave
   typedef StateShape<KD, VT, 4> S;
   static_assert(NO >= L::NACC, "tile too small for the waves");
-  // waves per SIMD that the registers are cut to.  A workgroup of 8 waves at up to 256 registers holds
-  // both roles' pipelines without spilling; narrower keys leave room for two workgroups per CU.
+  // waves per SIMD that the registers are cut to, none of which may spill (a spilled operand would wait for
+  // memory in every chunk): one workgroup of 8 waves per CU for the widest keys, two for narrower ones.
   static constexpr int EU = KD == 128 ? 2 : 4;
   static constexpr int kK = Tile<T, C, KD>::ELEMS, kV = Tile<T, C, VT>::ELEMS, kS = VT * (KD + L::PAD);
   static constexpr int kC = 2 * kK + kV;                              // a chunk's k, v and q
@@ -527,9 +551,8 @@ __device__ __forceinline__ void walk(const WalkArgs& a, int block, Lds<T>* smem)
   typedef Lin<T> L;
   typedef typename L::frag frag;
   typedef WalkShape<T, KD, VT> W;
-  constexpr int C = W::C, NT = 512, NTT = W::NTT, NO = W::NO, NKS = W::S::NK, NVS = W::S::NV;
+  constexpr int C = W::C, NT = kWalkThreads, NTT = W::NTT, NO = W::NO, NKS = W::S::NK, NVS = W::S::NV;
   constexpr int NQ = KD / L::DG, ND = C / L::DG;
-  constexpr int NH = NQ > 1 ? 2 : 1, HQ = NQ / NH;             // the read's contraction in NH steps
   static_assert(ND == 2, "two groups of tokens per chunk");
   constexpr bool DMA = !(PQ || PK || PV);
   constexpr int NS = DMA ? W::NS : 2;
@@ -563,7 +586,7 @@ __device__ __forceinline__ void walk(const WalkArgs& a, int block, Lds<T>* smem)
   // Both roles bring in the chunks.  Copies: chunk ci + NS - 1 is requested when chunk ci begins (its place
   // was last read in chunk ci - 1) and has arrived before chunk ci + NS - 2 ends.  Through registers: chunk
   // ci + 1 is written to LDS when chunk ci ends, and chunk ci + 2 requested.
-  const Copy<T, C, KD, VT, KD, 8> copy(wave, lane, a.K, a.V, v0);
+  const Copy<T, C, KD, VT, KD, NT / 64> copy(wave, lane, a.K, a.V, v0);
   Stage<T, PK, C, KD, NT> pk;
   Stage<T, PV, C, VT, NT> pv;
   Stage<T, PQ, C, KD, NT> pq;
@@ -591,7 +614,7 @@ __device__ __forceinline__ void walk(const WalkArgs& a, int block, Lds<T>* smem)
     request(ci + 1);
   };
   // end of chunk ci; an output wave's stores of the chunk (STORES) are behind the copies that it waits for
-  constexpr int COPIES = Copy<T, C, KD, VT, KD, 8>::MIN, STORES = NO / L::NACC;
+  constexpr int COPIES = Copy<T, C, KD, VT, KD, NT / 64>::MIN, STORES = NO / L::NACC;
   const auto end = [&](int ci) {
     if constexpr (DMA) {
       const bool more = NS == 3 && ci + 2 < nch;
@@ -666,20 +689,15 @@ __device__ __forceinline__ void walk(const WalkArgs& a, int block, Lds<T>* smem)
       frag qf[NQ];
 #pragma unroll
       for (int x = 0; x < NQ; ++x) qf[x] = L::template nat<KD, false>(tile_q(ci), tl, x * L::DG, lane);
-      frag kf[L::NACC][NQ], sf[HQ][NO], vf[NO];
       floatx4 p[L::NACC], acc[NO];
-      const auto read_k = [&](int d) {
-#pragma unroll
-        for (int x = 0; x < NQ; ++x)
-#pragma unroll
-          for (int s = 0; s < L::NACC; ++s)
-            kf[s][x] = L::template nat<KD, false>(cK, d * L::DG + 16 * s + (lane & 15), x * L::DG, lane);
-      };
       // scores (keys x tokens) of token group d; the tiles that the mask cuts off come out as zeros.
       // They are rounded to bf16 for the product with V (fp32 walks keep them): one rounding, 2^-8.
       const auto scores = [&](int d) {
 #pragma unroll
         for (int s = 0; s < L::NACC; ++s) p[s] = zero4();
+        const auto key = [&](int s, int x) {
+          return L::template nat<KD, false>(cK, d * L::DG + 16 * s + (lane & 15), x * L::DG, lane);
+        };
         // (the outer tile of the diagonal's group may be cut off whole)
         constexpr int IN = REV ? L::NACC - 1 : 0, OUT = L::NACC - 1 - IN;
         const bool outer = REV ? d * L::NACC + OUT >= ti : d * L::NACC + OUT <= ti;
@@ -687,13 +705,11 @@ __device__ __forceinline__ void walk(const WalkArgs& a, int block, Lds<T>* smem)
 #pragma unroll
           for (int x = 0; x < NQ; ++x)
 #pragma unroll
-            for (int s = 0; s < L::NACC; ++s) p[s] = L::mma(kf[s][x], qf[x], p[s]);
+            for (int s = 0; s < L::NACC; ++s) p[s] = L::mma(key(s, x), qf[x], p[s]);
         } else {
 #pragma unroll
-          for (int x = 0; x < NQ; ++x) p[IN] = L::mma(kf[IN][x], qf[x], p[IN]);
+          for (int x = 0; x < NQ; ++x) p[IN] = L::mma(key(IN, x), qf[x], p[IN]);
         }
-      };
-      const auto masked = [&](int d) {
 #pragma unroll
         for (int s = 0; s < L::NACC; ++s)
 #pragma unroll
@@ -703,26 +719,9 @@ __device__ __forceinline__ void walk(const WalkArgs& a, int block, Lds<T>* smem)
           }
         return L::from_acc(p);
       };
-      const auto read_s = [&](int hx) {
+      const auto value_out = [&](int d, frag b) {
 #pragma unroll
-        for (int x = 0; x < HQ; ++x)
-#pragma unroll
-          for (int j = 0; j < NO; ++j)
-            sf[x][j] = L::template nat<KD, true>(cS, L::row_of(ov0 + j, lane & 15), (hx * HQ + x) * L::DG, lane);
-      };
-      const auto read_out = [&](int hx) {
-#pragma unroll
-        for (int x = 0; x < HQ; ++x)
-#pragma unroll
-          for (int j = 0; j < NO; ++j) acc[j] = L::mma(sf[x][j], qf[hx * HQ + x], acc[j]);
-      };
-      const auto read_v = [&](int d) {
-#pragma unroll
-        for (int j = 0; j < NO; ++j) vf[j] = L::template tr<VT, true>(cV, ov0 + j, d * L::DG, lane);
-      };
-      const auto value_out = [&](frag b) {
-#pragma unroll
-        for (int j = 0; j < NO; ++j) acc[j] = L::mma(vf[j], b, acc[j]);
+        for (int j = 0; j < NO; ++j) acc[j] = L::mma(L::template tr<VT, true>(cV, ov0 + j, d * L::DG, lane), b, acc[j]);
       };
       // O^T = r a^e S^T Q + V^T scores: token groups 0 and 1 reach this wave's tokens, or only the one
       // that holds them (REV: 1, else 0)
@@ -730,34 +729,23 @@ __device__ __forceinline__ void walk(const WalkArgs& a, int block, Lds<T>* smem)
       constexpr int D0 = REV ? 1 : 0, D1 = 1 - D0;
 #pragma unroll
       for (int j = 0; j < NO; ++j) acc[j] = zero4();
-      read_k(D0);
-      read_s(0);
-      scores(D0);
-      frag b0 = masked(D0), b1;
-      if (both) read_k(D1);
-      read_out(0);
-      if (NH > 1) read_s(1);
-      if (both) {
-        scores(D1);
-        b1 = masked(D1);
-      }
-      read_v(D0);
-      if (NH > 1) read_out(1);
+#pragma unroll
+      for (int x = 0; x < NQ; ++x)
+#pragma unroll
+        for (int j = 0; j < NO; ++j)
+          acc[j] = L::mma(L::template nat<KD, true>(cS, L::row_of(ov0 + j, lane & 15), x * L::DG, lane), qf[x], acc[j]);
       const int e = REV ? n - 1 - tl : tl + 1;
       const float rf = a.r * decay_pow(g2, e < 0 ? 0 : e);
 #pragma unroll
       for (int j = 0; j < NO; ++j) acc[j] *= rf;
-      value_out(b0);
-      if (both) {
-        read_v(D1);
-        value_out(b1);
-      }
+      value_out(D0, scores(D0));
+      if (both) value_out(D1, scores(D1));
       const unsigned row = (unsigned)(chunk_t0(ci) + tl) * (unsigned)(a.V * sizeof(T));
 #pragma unroll
       for (int j = 0; j < NO; j += L::NACC) {
-        const int col = v0 + L::row_of(ov0 + j, 4 * (lane >> 4));
+        const int col = v0 + 16 * (ov0 + j) + (16 / (int)sizeof(T)) * (lane >> 4);
         const unsigned off = col < a.V ? row + (unsigned)(col * sizeof(T)) : 0xfffffff0u;
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, L::from_acc(acc + j)), ro, off, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(L::row16(acc + j, lane), ro, off, 0, 0);
       }
       if (ci + 1 < nch) end(ci);
     }
@@ -775,8 +763,8 @@ __device__ __forceinline__ void walk(const WalkArgs& a, int block, Lds<T>* smem)
 __host__ __device__ inline int walk_blocks(const WalkArgs& a, int VT) { return a.BH * a.nseg * ((a.V + VT - 1) / VT); }
 
 template <typename T, int KD, int VT>
-__global__ void __launch_bounds__(512, (WalkShape<T, KD, VT>::EU)) decay_fwd_kernel(WalkArgs a) {
-  __shared__ __align__(1024) T smem[walk_lds<T, KD, VT, false>()];
+__global__ void __launch_bounds__(kWalkThreads, (WalkShape<T, KD, VT>::EU)) decay_fwd_kernel(WalkArgs a) {
+  __shared__ __align__(16) T smem[walk_lds<T, KD, VT, false>()];
   static_assert(sizeof(smem) <= 160 * 1024, "LDS of one gfx950 workgroup exceeded");
   walk<T, KD, VT, false, false, false, false>(a, blockIdx.x, (Lds<T>*)smem);
 }
@@ -791,10 +779,10 @@ template <typename T, int KD, int VD, bool PACK> struct BwdShape {
   static constexpr int EU = PACK ? 2 : cmin(WalkShape<T, VD, VTK>::EU, WalkShape<T, KD, VTV>::EU);
 };
 template <typename T, int KD, int VD, bool PACK>
-__global__ void __launch_bounds__(512, (BwdShape<T, KD, VD, PACK>::EU))
+__global__ void __launch_bounds__(kWalkThreads, (BwdShape<T, KD, VD, PACK>::EU))
     decay_bwd_kernel(WalkArgs dq, WalkArgs dk, WalkArgs dv) {
   typedef BwdShape<T, KD, VD, PACK> S;
-  __shared__ __align__(1024) T smem[S::LDS];
+  __shared__ __align__(16) T smem[S::LDS];
   static_assert(sizeof(smem) <= 160 * 1024, "LDS of one gfx950 workgroup exceeded");
   const int n = walk_blocks(dq, S::VTK);
   int b = blockIdx.x;
@@ -891,9 +879,9 @@ __global__ void __launch_bounds__((64 * seg_waves<KD, VT>())) decay_segment_kern
 // widths up to 32.
 template <typename T, int KD> hipError_t launch_walk_fwd(const WalkArgs& a, hipStream_t s) {
   if (a.V <= 32)
-    hipLaunchKernelGGL((decay_fwd_kernel<T, KD, 32>), dim3(walk_blocks(a, 32)), dim3(512), 0, s, a);
+    hipLaunchKernelGGL((decay_fwd_kernel<T, KD, 32>), dim3(walk_blocks(a, 32)), dim3(kWalkThreads), 0, s, a);
   else
-    hipLaunchKernelGGL((decay_fwd_kernel<T, KD, 64>), dim3(walk_blocks(a, 64)), dim3(512), 0, s, a);
+    hipLaunchKernelGGL((decay_fwd_kernel<T, KD, 64>), dim3(walk_blocks(a, 64)), dim3(kWalkThreads), 0, s, a);
   return hipGetLastError();
 }
 
@@ -901,7 +889,7 @@ template <typename T, int KD, int VD, bool PACK>
 hipError_t launch_walk_bwd(const WalkArgs& dq, const WalkArgs& dk, const WalkArgs& dv, hipStream_t s) {
   typedef BwdShape<T, KD, VD, PACK> S;
   const int n = 2 * walk_blocks(dq, S::VTK) + walk_blocks(dv, S::VTV);
-  hipLaunchKernelGGL((decay_bwd_kernel<T, KD, VD, PACK>), dim3(n), dim3(512), 0, s, dq, dk, dv);
+  hipLaunchKernelGGL((decay_bwd_kernel<T, KD, VD, PACK>), dim3(n), dim3(kWalkThreads), 0, s, dq, dk, dv);
   return hipGetLastError();
 }
 
