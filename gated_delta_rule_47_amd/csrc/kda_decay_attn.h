@@ -299,56 +299,68 @@ __device__ __forceinline__ void copy_to_lds(u32x4_t r, const Lds<void>* lds, uns
                : "memory");
 }
 
-// The tiles of one chunk, copied from memory straight into LDS: each wave instruction fills 64
-// consecutive pieces, so the order of the pieces within a row is made by the address each lane reads.
-// A wave issues MIN or MIN + 1 instructions per chunk.  Rows behind the range read as zeros.
-template <typename T, int C, int DK, int DV, int DQ, int NW> struct Copy {
-  typedef Tile<T, C, DK> TK;
-  typedef Tile<T, C, DV> TV;
-  typedef Tile<T, C, (DQ ? DQ : 32)> TQ;
-  static constexpr int IK = TK::NP / 64, IV = TV::NP / 64, IQ = DQ ? TQ::NP / 64 : 0, NI = IK + IV + IQ;
-  static constexpr int PER = (NI + NW - 1) / NW, MIN = NI / NW;
-  // byte offset of this lane's piece from the chunk's first row; q's are k's where the waves come round to the
-  // same places
-  static constexpr bool SAME = (IK + IV) % NW == 0 && DQ == DK;
-  static constexpr int NOFF = SAME ? (IK + IV) / NW : PER;
-  uint32_t off[(NOFF + 1) / 2];                  // two in a register, -1 outside the tensor's channels
-  static_assert(C * 128 * sizeof(T) <= 32768, "offsets of 15 bits");
-  __device__ __forceinline__ unsigned offset(int i) const {
-    return (unsigned)(i & 1 ? (int)off[i / 2] >> 16 : (int)(short)off[i / 2]);
+// A tile copied from memory straight into LDS: each wave instruction fills 64 consecutive pieces, so the
+// order of the pieces within a row is made by the address each lane reads.  Rows behind the range read as
+// zeros.  bf16 rows repeat their order every 16, so a tile's instructions share PERIOD lane offsets and
+// differ by a scalar one.
+template <typename T, int C, int DP> struct CopyTile {
+  typedef Tile<T, C, DP> TL;
+  static constexpr int E = Lin<T>::EPP, N = TL::NP / 64;       // N instructions
+  static constexpr int PERIOD = Lin<T>::PAD == 0 ? cmax(1, 16 * TL::PPR / 64) : N;
+  unsigned off[PERIOD], row_bytes;
+  __device__ __forceinline__ CopyTile(int lane, int D, int ch0) {
+    row_bytes = (unsigned)(D * (int)sizeof(T));
+#pragma unroll
+    for (int i = 0; i < PERIOD; ++i) {
+      const int slot = 64 * i + lane, row = slot / TL::PPR, pos = slot % TL::PPR;
+      int pc = pos;
+      if constexpr (Lin<T>::PAD == 0) pc = pos ^ (Lin<T>::template at<DP, false>(row, 0) - row * DP) / E;
+      const int ch = ch0 + pc * E;
+      off[i] = row < C && pc < DP / E && ch < D ? (unsigned)row * row_bytes + (unsigned)(ch * (int)sizeof(T)) : 0xfffffff0u;
+    }
   }
+  // instruction I of the tile whose first row is token t0
+  template <int I> __device__ __forceinline__ void issue(u32x4_t r, int t0, const Lds<T>* lds) const {
+    constexpr unsigned rows = I / PERIOD * (PERIOD * 64 / TL::PPR);
+    copy_to_lds(r, lds + I * 64 * E, off[I % PERIOD], ((unsigned)t0 + rows) * row_bytes);
+  }
+  template <int I0, int I1> __device__ __forceinline__ void issue_range(u32x4_t r, int t0, const Lds<T>* lds) const {
+    if constexpr (I0 < I1) {
+      issue<I0>(r, t0, lds);
+      issue_range<I0 + 1, I1>(r, t0, lds);
+    }
+  }
+};
+// The k and v tiles of one chunk by all NW waves of a workgroup, MIN or MIN + 1 instructions each.
+template <typename T, int C, int DK, int DV, int NW> struct Copy {
+  static constexpr int IK = Tile<T, C, DK>::NP / 64, IV = Tile<T, C, DV>::NP / 64, NI = IK + IV;
+  static constexpr int PER = (NI + NW - 1) / NW, MIN = NI / NW;
+  unsigned off[PER];                             // byte offset of this lane's piece from the chunk's first row
 
   template <int DP> static __device__ __forceinline__ unsigned piece(int slot, int D, int ch0) {
     typedef Tile<T, C, DP> TL;
-    constexpr int E = Lin<T>::EPP, W = DP / E;
+    constexpr int E = Lin<T>::EPP;
     const int row = slot / TL::PPR, pos = slot % TL::PPR;
     int pc = pos;
     if constexpr (Lin<T>::PAD == 0) pc = pos ^ (Lin<T>::template at<DP, false>(row, 0) - row * DP) / E;
     const int ch = ch0 + pc * E;
-    return row < C && pc < W && ch < D ? (unsigned)(row * D + ch) * (unsigned)sizeof(T) : 0xffffu;
+    return row < C && pc < DP / E && ch < D ? (unsigned)(row * D + ch) * (unsigned)sizeof(T) : 0xfffffff0u;
   }
   __device__ __forceinline__ Copy(int wave, int lane, int K, int V, int v0) {
 #pragma unroll
-    for (int i = 0; i < NOFF; ++i) {
+    for (int i = 0; i < PER; ++i) {
       const int x = wave + i * NW;
-      const unsigned o = x < IK ? piece<DK>(64 * x + lane, K, 0)
-                                : x < IK + IV
-                                      ? piece<DV>(64 * (x - IK) + lane, V, v0)
-                                      : piece<TQ::PPR * Lin<T>::EPP - Lin<T>::PAD>(64 * (x - IK - IV) + lane, K, 0);
-      off[i / 2] = i & 1 ? off[i / 2] | o << 16 : o;
+      off[i] = x < IK ? piece<DK>(64 * x + lane, K, 0) : piece<DV>(64 * (x - IK) + lane, V, v0);
     }
   }
-  // tokens from t0 into the tiles at lds (K, V and Q one behind the other)
-  __device__ __forceinline__ void issue(u32x4_t rk, u32x4_t rv, u32x4_t rq, int t0, int K, int V, const Lds<T>* lds,
+  // tokens from t0 into the tiles at lds (v behind k)
+  __device__ __forceinline__ void issue(u32x4_t rk, u32x4_t rv, int t0, int K, int V, const Lds<T>* lds,
                                         int wave) const {
     const unsigned sk = (unsigned)t0 * (unsigned)(K * sizeof(T)), sv = (unsigned)t0 * (unsigned)(V * sizeof(T));
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int x = wave + i * NW;
-      if (x < NI) {
-        const bool isv = x >= IK && x < IK + IV;
-        copy_to_lds(isv ? rv : (x < IK ? rk : rq), lds + x * 64 * Lin<T>::EPP, offset(i < NOFF ? i : i - NOFF), isv ? sv : sk);
-      }
+      if (NI % NW == 0 || x < NI) copy_to_lds(x < IK ? rk : rv, lds + x * 64 * Lin<T>::EPP, off[i], x < IK ? sk : sv);
     }
   }
 };
@@ -583,22 +595,32 @@ __device__ __forceinline__ void walk(const WalkArgs& a, int block, Lds<T>* smem)
 
   const HeadRows<T, PQ> hq(a.q, a.q_sc, bh, a.T, a.K, t_end);
 
-  // Both roles bring in the chunks.  Copies: chunk ci + NS - 1 is requested when chunk ci begins (its place
-  // was last read in chunk ci - 1) and has arrived before chunk ci + NS - 2 ends.  Through registers: chunk
-  // ci + 1 is written to LDS when chunk ci ends, and chunk ci + 2 requested.
-  const Copy<T, C, KD, VT, KD, NT / 64> copy(wave, lane, a.K, a.V, v0);
+  // Copies are made by the two output waves that the mask leaves the least to do (a chunk's 24 to 40
+  // instructions take the memory pipe 16 cycles each, and a wave that issues them waits): one copies k and half
+  // of v, the other q and the rest.  Chunk ci + NS - 1 is requested when chunk ci begins (its place was last read
+  // in chunk ci - 1) and has arrived before chunk ci + NS - 2 ends.  8-bit operands pass through registers of
+  // all waves: chunk ci + 1 is written to LDS when chunk ci ends, and chunk ci + 2 requested.
+  const int issuer = wave >= 4 ? -1 : (NTT == 4 ? (REV ? wave - 2 : wave < 2 ? wave : -1)
+                                                : ((wave & 1) == (REV ? 1 : 0) ? wave >> 1 : -1));
+  const CopyTile<T, C, KD> ck(lane, a.K, 0);
+  const CopyTile<T, C, VT> cv(lane, a.V, v0);
+  constexpr int NCK = CopyTile<T, C, KD>::N, NCV = CopyTile<T, C, VT>::N;
   Stage<T, PK, C, KD, NT> pk;
   Stage<T, PV, C, VT, NT> pv;
   Stage<T, PQ, C, KD, NT> pq;
   const auto request = [&](int ci) {
     if (ci < nch) {
       const int t0 = chunk_t0(ci);
-      if constexpr (DMA) {
-        copy.issue(hk.words, hv.words, hq.words, t0, a.K, a.V, tile_k(ci), wave);
-      } else {
+      if constexpr (!DMA) {
         pk.load(hk, t0, 0, tid);
         pv.load(hv, t0, v0, tid);
         pq.load(hq, t0, 0, tid);
+      } else if (issuer == 0) {
+        ck.template issue_range<0, NCK>(hk.words, t0, tile_k(ci));
+        cv.template issue_range<0, NCV / 2>(hv.words, t0, tile_v(ci));
+      } else if (issuer == 1) {
+        ck.template issue_range<0, NCK>(hq.words, t0, tile_q(ci));
+        cv.template issue_range<NCV / 2, NCV>(hv.words, t0, tile_v(ci));
       }
     }
   };
@@ -613,20 +635,15 @@ __device__ __forceinline__ void walk(const WalkArgs& a, int block, Lds<T>* smem)
     }
     request(ci + 1);
   };
-  // end of chunk ci; an output wave's stores of the chunk (STORES) are behind the copies that it waits for
-  constexpr int COPIES = Copy<T, C, KD, VT, KD, NT / 64>::MIN, STORES = NO / L::NACC;
+  // end of chunk ci: the issuers wait for the next chunk's copies; behind those are the copies of the chunk
+  // after it and this wave's stores
+  constexpr int COPIES = NCK + NCV / 2, STORES = NO / L::NACC;
   const auto end = [&](int ci) {
-    if constexpr (DMA) {
-      const bool more = NS == 3 && ci + 2 < nch;
-      if (wave >= 4) {
-        if (more) wait_vm_but<COPIES>();
-        else wait_vm_but<0>();
-      } else {
-        if (more) wait_vm_but<COPIES + STORES>();
-        else wait_vm_but<STORES>();
-      }
-    } else {
+    if constexpr (!DMA) {
       stage(ci + 1);
+    } else if (issuer >= 0) {
+      if (NS == 3 && ci + 2 < nch) wait_vm_but<COPIES + STORES>();
+      else wait_vm_but<STORES>();
     }
     chunk_barrier();
   };
@@ -648,7 +665,6 @@ __device__ __forceinline__ void walk(const WalkArgs& a, int block, Lds<T>* smem)
     chunk_barrier();
     for (int ci = 0; ci < nch; ++ci) {
       const int n = chunk_n(ci);
-      begin(ci);
       st.factors(g2, a.u, n, lane);
       const bool fine = fine_state(a.state_out != nullptr, g2, REV ? chunk_t0(ci) : len - chunk_t0(ci) - n);
       st.update(tile_k(ci), tile_v(ci), ct0, sv0, n == C ? an : an_short, fine, lane);
@@ -824,14 +840,14 @@ __device__ __forceinline__ void segment_state(const SegArgs& a, int block, Lds<T
   const int ct0 = sw / S::WV * S::NK, sv0 = sw % S::WV * S::NV;
   StateTile<T, KD, VT, C, S::NK, S::NV, REV> st;
   st.zero();
-  const Copy<T, C, KD, VT, 0, NW> copy(sw, lane, a.K, a.V, v0);
+  const Copy<T, C, KD, VT, NW> copy(sw, lane, a.K, a.V, v0);
   Stage<T, PK, C, KD, NT> pk;
   Stage<T, PV, C, VT, NT> pv;
   const auto request = [&](int ci) {
     if (ci < nch) {
       const int t0 = chunk_t0(ci);
       if constexpr (DMA) {
-        copy.issue(hk.words, hv.words, hk.words, t0, a.K, a.V, tile_k(ci), sw);
+        copy.issue(hk.words, hv.words, t0, a.K, a.V, tile_k(ci), sw);
       } else {
         pk.load(hk, t0, 0, tid);
         pv.load(hv, t0, v0, tid);
@@ -845,7 +861,7 @@ __device__ __forceinline__ void segment_state(const SegArgs& a, int block, Lds<T
     const int n = chunk_n(ci);
     if constexpr (DMA) {
       // chunk ci has arrived; the one after it, requested a chunk later, may not have
-      if (ci + 1 < nch) wait_vm_but<Copy<T, C, KD, VT, 0, NW>::MIN>();
+      if (ci + 1 < nch) wait_vm_but<Copy<T, C, KD, VT, NW>::MIN>();
       else wait_vm_but<0>();
       chunk_barrier();
       request(ci + 2);                           // its place was last read in chunk ci - 1
