@@ -79,7 +79,7 @@ template <typename U> using Lds = __attribute__((address_space(3))) U;
 template <typename T> struct Lin;
 
 template <> struct Lin<bf16_t> {                 // v_mfma_f32_16x16x32_bf16
-  static constexpr int DG = 32, NACC = 2, EPP = 8, PAD = 0, FINE = 3, COARSE = 2;
+  static constexpr int DG = 32, NACC = 2, EPP = 8, PAD = 0, PARTS = 2;
   typedef short8 frag;
   static __device__ __forceinline__ int row_of(int ct, int m) {
     return 32 * (ct >> 1) + 8 * (m >> 2) + 4 * ((ct ^ m >> 2) & 1) + (m & 3);
@@ -124,22 +124,33 @@ template <> struct Lin<bf16_t> {                 // v_mfma_f32_16x16x32_bf16
     const bool odd = lane >> 4 & 1;
     return u32x4_t{odd ? b[0] : a[0], odd ? b[1] : a[1], odd ? a[0] : b[0], odd ? a[1] : b[1]};
   }
-  // x f as the sum of N bf16 parts, off by at most 2^-17 (two) or 2^-26 (three) of it
-  template <int N> static __device__ __forceinline__ void scaled(frag x, const float* f, frag* out) {
-    u32x4_t part[N];
+  // x f as bf16 parts: the sum of the first two is off by at most 2^-17 of it, with the third 2^-26
+  static __device__ __forceinline__ void scaled(frag x, const float* f, frag* out) {
+    u32x4_t part[2];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float a = bf2f((bf16_t)x[2 * e]) * f[2 * e], b = bf2f((bf16_t)x[2 * e + 1]) * f[2 * e + 1];
+      const uint32_t w = pack_bf16x2(a, b);
+      part[0][e] = w;
+      part[1][e] = pack_bf16x2(a - __uint_as_float(w << 16), b - __uint_as_float(w & 0xffff0000u));
+    }
+    out[0] = __builtin_bit_cast(short8, part[0]);
+    out[1] = __builtin_bit_cast(short8, part[1]);
+  }
+  static __device__ __forceinline__ frag third(frag x, const float* f) {
+    u32x4_t part;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       float a = bf2f((bf16_t)x[2 * e]) * f[2 * e], b = bf2f((bf16_t)x[2 * e + 1]) * f[2 * e + 1];
 #pragma unroll
-      for (int s = 0; s < N; ++s) {
+      for (int s = 0; s < 2; ++s) {
         const uint32_t w = pack_bf16x2(a, b);
-        part[s][e] = w;
         a -= __uint_as_float(w << 16);
         b -= __uint_as_float(w & 0xffff0000u);
       }
+      part[e] = pack_bf16x2(a, b);
     }
-#pragma unroll
-    for (int s = 0; s < N; ++s) out[s] = __builtin_bit_cast(short8, part[s]);
+    return __builtin_bit_cast(short8, part);
   }
   // token (within a group of DG) of fragment element e in the accumulator order
   static __device__ __forceinline__ int tok_of(int e, int g) { return 16 * (e >> 2) + 4 * g + (e & 3); }
@@ -149,7 +160,7 @@ template <> struct Lin<bf16_t> {                 // v_mfma_f32_16x16x32_bf16
 };
 
 template <> struct Lin<float> {                  // four v_mfma_f32_16x16x4_f32
-  static constexpr int DG = 16, NACC = 1, EPP = 4, PAD = 4, FINE = 1, COARSE = 1;
+  static constexpr int DG = 16, NACC = 1, EPP = 4, PAD = 4, PARTS = 1;
   typedef floatx4 frag;
   static __device__ __forceinline__ int row_of(int ct, int m) { return 16 * ct + m; }
   template <int W, bool IMG> static __device__ __forceinline__ int at(int t, int e) { return t * (W + PAD) + e; }
@@ -169,9 +180,10 @@ template <> struct Lin<float> {                  // four v_mfma_f32_16x16x4_f32
   }
   static __device__ __forceinline__ frag from_acc(const floatx4* x) { return x[0]; }
   static __device__ __forceinline__ u32x4_t row16(const floatx4* x, int) { return __builtin_bit_cast(u32x4_t, x[0]); }
-  template <int N> static __device__ __forceinline__ void scaled(frag x, const float* f, frag* out) {
+  static __device__ __forceinline__ void scaled(frag x, const float* f, frag* out) {
     out[0] = floatx4{x[0] * f[0], x[1] * f[1], x[2] * f[2], x[3] * f[3]};
   }
+  static __device__ __forceinline__ frag third(frag x, const float*) { return x; }     // (not used)
   static __device__ __forceinline__ int tok_of(int e, int g) { return 4 * g + e; }
   static __device__ __forceinline__ void store4(Lds<float>* p, floatx4 x) { *(Lds<floatx4>*)p = x; }
 };
@@ -379,7 +391,7 @@ __device__ __forceinline__ float uniform(float x) {
   return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(x)));
 }
 
-// a^n for n >= 0 as hi + lo: the chunk factor multiplies the state once per chunk, and a bias of one
+// a^n for n >= 0 as hi (1 + lo): the chunk factor multiplies the state once per chunk, and a bias of one
 // fp32 rounding would add up over the hundreds of chunks of a long sequence.
 struct Decay2 {
   float hi, lo;
@@ -387,7 +399,7 @@ struct Decay2 {
 __device__ __forceinline__ Decay2 decay_pow2(float g, int n) {
   const double x = n == 0 ? 1.0 : exp((double)g * n);
   const float hi = (float)x;
-  return Decay2{uniform(hi), uniform((float)(x - (double)hi))};
+  return Decay2{uniform(hi), uniform(hi > 0.0f ? (float)(x / (double)hi - 1.0) : 0.0f)};
 }
 // a^n, g2 = log2(a); n = 0 gives 1 also for a = 0 (g2 = -inf)
 __device__ __forceinline__ float decay_pow(float g2, int n) { return n == 0 ? 1.0f : fast_exp2(g2 * (float)n); }
@@ -462,38 +474,42 @@ template <typename T, int KD, int VT, int C, int NK, int NV, bool REV> struct St
   // `fine`: as exactly as fp32 holds it (see fine_state)
   __device__ __forceinline__ void update(const Lds<T>* sK, const Lds<T>* sV, int ct0, int vt0, Decay2 an, bool fine,
                                          int lane) {
+#pragma unroll
+    for (int i = 0; i < NK; ++i)
+#pragma unroll
+      for (int j = 0; j < NV; ++j) acc[i][j] *= an.hi;
     if (fine) {
 #pragma unroll
       for (int i = 0; i < NK; ++i)
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(acc[i][j][r], an.hi, acc[i][j][r] * an.lo);
-      add<L::FINE>(sK, sV, ct0, vt0, lane);
-    } else {
-#pragma unroll
-      for (int i = 0; i < NK; ++i)
-#pragma unroll
-        for (int j = 0; j < NV; ++j) acc[i][j] *= an.hi;
-      add<L::COARSE>(sK, sV, ct0, vt0, lane);
+          for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(acc[i][j][r], an.lo, acc[i][j][r]);
     }
-  }
-  template <int N>
-  __device__ __forceinline__ void add(const Lds<T>* sK, const Lds<T>* sV, int ct0, int vt0, int lane) {
 #pragma unroll
     for (int d = 0; d < C / L::DG; ++d) {
-      typename L::frag kf[NK], vf[NV][N];
+      typename L::frag kf[NK], v[NV], vf[NV][L::PARTS];
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
-        L::template scaled<N>(L::template tr<VT, false>(sV, vt0 + j, d * L::DG, lane), f[d], vf[j]);
+      for (int j = 0; j < NV; ++j) {
+        v[j] = L::template tr<VT, false>(sV, vt0 + j, d * L::DG, lane);
+        L::scaled(v[j], f[d], vf[j]);
+      }
 #pragma unroll
       for (int i = 0; i < NK; ++i) kf[i] = L::template tr<KD, true>(sK, ct0 + i, d * L::DG, lane);
 #pragma unroll
-      for (int s = 0; s < N; ++s)
+      for (int s = 0; s < L::PARTS; ++s)
 #pragma unroll
         for (int i = 0; i < NK; ++i)
 #pragma unroll
           for (int j = 0; j < NV; ++j) acc[i][j] = L::mma(kf[i], vf[j][s], acc[i][j]);
+      if (L::PARTS > 1 && fine) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          const typename L::frag t = L::third(v[j], f[d]);
+#pragma unroll
+          for (int i = 0; i < NK; ++i) acc[i][j] = L::mma(kf[i], t, acc[i][j]);
+        }
+      }
     }
   }
 };
@@ -569,9 +585,16 @@ __device__ __forceinline__ void walk(const WalkArgs& a, int block, Lds<T>* smem)
   constexpr bool DMA = !(PQ || PK || PV);
   constexpr int NS = DMA ? W::NS : 2;
   Lds<T>* const sS = smem + NS * W::kC;
-  const auto tile_k = [&](int ci) { return smem + ci % NS * W::kC; };
-  const auto tile_v = [&](int ci) { return smem + ci % NS * W::kC + W::kK; };
-  const auto tile_q = [&](int ci) { return smem + ci % NS * W::kC + W::kK + W::kV; };
+  // the chunk's place in LDS, kept as an offset in a scalar register (a remainder by NS would be carried
+  // through every lane's addresses)
+  const auto next_slot = [](unsigned s) {
+    s = s == (NS - 1) * W::kC ? 0u : s + (unsigned)W::kC;
+    asm volatile("" : "+s"(s));
+    return s;
+  };
+  const auto tile_k = [&](unsigned at) { return smem + at; };
+  const auto tile_v = [&](unsigned at) { return smem + at + W::kK; };
+  const auto tile_q = [&](unsigned at) { return smem + at + W::kK + W::kV; };
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int ntile = (a.V + VT - 1) / VT;
@@ -608,7 +631,7 @@ __device__ __forceinline__ void walk(const WalkArgs& a, int block, Lds<T>* smem)
   Stage<T, PK, C, KD, NT> pk;
   Stage<T, PV, C, VT, NT> pv;
   Stage<T, PQ, C, KD, NT> pq;
-  const auto request = [&](int ci) {
+  const auto request = [&](int ci, unsigned at) {
     if (ci < nch) {
       const int t0 = chunk_t0(ci);
       if constexpr (!DMA) {
@@ -616,40 +639,38 @@ __device__ __forceinline__ void walk(const WalkArgs& a, int block, Lds<T>* smem)
         pv.load(hv, t0, v0, tid);
         pq.load(hq, t0, 0, tid);
       } else if (issuer == 0) {
-        ck.template issue_range<0, NCK>(hk.words, t0, tile_k(ci));
-        cv.template issue_range<0, NCV / 2>(hv.words, t0, tile_v(ci));
+        ck.template issue_range<0, NCK>(hk.words, t0, tile_k(at));
+        cv.template issue_range<0, NCV / 2>(hv.words, t0, tile_v(at));
       } else if (issuer == 1) {
-        ck.template issue_range<0, NCK>(hq.words, t0, tile_q(ci));
-        cv.template issue_range<NCV / 2, NCV>(hv.words, t0, tile_v(ci));
+        ck.template issue_range<0, NCK>(hq.words, t0, tile_q(at));
+        cv.template issue_range<NCV / 2, NCV>(hv.words, t0, tile_v(at));
       }
     }
   };
-  const auto begin = [&](int ci) {
-    if constexpr (DMA) request(ci + NS - 1);
-  };
-  const auto stage = [&](int ci) {
+  const auto stage = [&](int ci, unsigned at) {
     if (ci < nch) {
-      pk.store(tile_k(ci), tid);
-      pv.store(tile_v(ci), tid);
-      pq.store(tile_q(ci), tid);
+      pk.store(tile_k(at), tid);
+      pv.store(tile_v(at), tid);
+      pq.store(tile_q(at), tid);
     }
-    request(ci + 1);
+    request(ci + 1, 0);
   };
   // end of chunk ci: the issuers wait for the next chunk's copies; behind those are the copies of the chunk
   // after it and this wave's stores
   constexpr int COPIES = NCK + NCV / 2, STORES = NO / L::NACC;
-  const auto end = [&](int ci) {
+  const auto end = [&](int ci, unsigned next) {
     if constexpr (!DMA) {
-      stage(ci + 1);
+      stage(ci + 1, next);
     } else if (issuer >= 0) {
       if (NS == 3 && ci + 2 < nch) wait_vm_but<COPIES + STORES>();
       else wait_vm_but<STORES>();
     }
     chunk_barrier();
   };
-  request(0);
-  if constexpr (DMA && NS == 3) request(1);
+  request(0, 0);
+  if constexpr (DMA && NS == 3) request(1, W::kC);
 
+  unsigned slot = 0;                                           // of chunk ci
   if (wave >= 4) {
     const int rw = wave - 4;
     const int ct0 = rw / W::S::WV * NKS, sv0 = rw % W::S::WV * NVS;
@@ -660,17 +681,18 @@ __device__ __forceinline__ void walk(const WalkArgs& a, int block, Lds<T>* smem)
     else st.zero();
     const Decay2 an = decay_pow2(g, C), an_short = decay_pow2(g, nch > 0 ? n_last : 0);
     if (nch > 0) st.image(sS, ct0, 16 * sv0, lane);
-    if constexpr (!DMA) stage(0);
+    if constexpr (!DMA) stage(0, 0);
     wait_vm_all();
     chunk_barrier();
     for (int ci = 0; ci < nch; ++ci) {
       const int n = chunk_n(ci);
       st.factors(g2, a.u, n, lane);
       const bool fine = fine_state(a.state_out != nullptr, g2, REV ? chunk_t0(ci) : len - chunk_t0(ci) - n);
-      st.update(tile_k(ci), tile_v(ci), ct0, sv0, n == C ? an : an_short, fine, lane);
+      st.update(tile_k(slot), tile_v(slot), ct0, sv0, n == C ? an : an_short, fine, lane);
       if (ci + 1 < nch) {
+        slot = next_slot(slot);
         st.image(sS + (ci + 1 & 1) * W::kS, ct0, 16 * sv0, lane);
-        end(ci);
+        end(ci, slot);
       }
     }
     if (a.state_out && seg == (REV ? 0 : a.nseg - 1))
@@ -693,18 +715,20 @@ __device__ __forceinline__ void walk(const WalkArgs& a, int block, Lds<T>* smem)
       const int k = REV ? s - ti : ti - s;
       far[s] = k < 1 ? 0.0f : uniform(decay_pow(g2, 16 * (k - 1)));
     }
-    if constexpr (!DMA) stage(0);
+    if constexpr (!DMA) stage(0, 0);
     wait_vm_all();
     chunk_barrier();
     for (int ci = 0; ci < nch; ++ci) {
       const int n = chunk_n(ci);
-      const Lds<T>* cK = tile_k(ci);
-      const Lds<T>* cV = tile_v(ci);
+      const Lds<T>* cK = tile_k(slot);
+      const Lds<T>* cV = tile_v(slot);
+      const Lds<T>* cQ = tile_q(slot);
       const Lds<T>* cS = sS + (ci & 1) * W::kS;
-      begin(ci);
+      slot = next_slot(slot);
+      if constexpr (DMA) request(ci + NS - 1, NS == 3 ? next_slot(slot) : slot);
       frag qf[NQ];
 #pragma unroll
-      for (int x = 0; x < NQ; ++x) qf[x] = L::template nat<KD, false>(tile_q(ci), tl, x * L::DG, lane);
+      for (int x = 0; x < NQ; ++x) qf[x] = L::template nat<KD, false>(cQ, tl, x * L::DG, lane);
       floatx4 p[L::NACC], acc[NO];
       // scores (keys x tokens) of token group d; the tiles that the mask cuts off come out as zeros.
       // They are rounded to bf16 for the product with V (fp32 walks keep them): one rounding, 2^-8.
@@ -763,7 +787,7 @@ __device__ __forceinline__ void walk(const WalkArgs& a, int block, Lds<T>* smem)
         const unsigned off = col < a.V ? row + (unsigned)(col * sizeof(T)) : 0xfffffff0u;
         __builtin_amdgcn_raw_buffer_store_b128(L::row16(acc + j, lane), ro, off, 0, 0);
       }
-      if (ci + 1 < nch) end(ci);
+      if (ci + 1 < nch) end(ci, slot);
     }
   }
   if (a.zero_tail) {
@@ -820,8 +844,11 @@ __device__ __forceinline__ void segment_state(const SegArgs& a, int block, Lds<T
   typedef StateShape<KD, VT, NW> S;
   constexpr int C = W::C, NT = 64 * NW, NS = kSegChunks;
   constexpr bool DMA = !(PK || PV);
-  const auto tile_k = [&](int ci) { return smem + ci % NS * (W::kK + W::kV); };
-  const auto tile_v = [&](int ci) { return smem + ci % NS * (W::kK + W::kV) + W::kK; };
+  const auto next_slot = [](unsigned s) {
+    s = s == (NS - 1) * (W::kK + W::kV) ? 0u : s + (unsigned)(W::kK + W::kV);
+    asm volatile("" : "+s"(s));
+    return s;
+  };
   const int tid = threadIdx.x, lane = tid & 63, sw = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int ntile = (a.V + VT - 1) / VT;
   int idx, tile;
@@ -843,19 +870,20 @@ __device__ __forceinline__ void segment_state(const SegArgs& a, int block, Lds<T
   const Copy<T, C, KD, VT, NW> copy(sw, lane, a.K, a.V, v0);
   Stage<T, PK, C, KD, NT> pk;
   Stage<T, PV, C, VT, NT> pv;
-  const auto request = [&](int ci) {
+  const auto request = [&](int ci, unsigned at) {
     if (ci < nch) {
       const int t0 = chunk_t0(ci);
       if constexpr (DMA) {
-        copy.issue(hk.words, hv.words, t0, a.K, a.V, tile_k(ci), sw);
+        copy.issue(hk.words, hv.words, t0, a.K, a.V, smem + at, sw);
       } else {
         pk.load(hk, t0, 0, tid);
         pv.load(hv, t0, v0, tid);
       }
     }
   };
-  request(0);
-  if constexpr (DMA) request(1);
+  request(0, 0);
+  if constexpr (DMA) request(1, W::kK + W::kV);
+  unsigned slot = 0;                             // of chunk ci
   const Decay2 an = decay_pow2(g, C), an_short = decay_pow2(g, nch > 0 ? n_last : 0);
   for (int ci = 0; ci < nch; ++ci) {
     const int n = chunk_n(ci);
@@ -864,16 +892,17 @@ __device__ __forceinline__ void segment_state(const SegArgs& a, int block, Lds<T
       if (ci + 1 < nch) wait_vm_but<Copy<T, C, KD, VT, NW>::MIN>();
       else wait_vm_but<0>();
       chunk_barrier();
-      request(ci + 2);                           // its place was last read in chunk ci - 1
+      request(ci + 2, next_slot(next_slot(slot)));                           // its place was last read in chunk ci - 1
     } else {
-      pk.store(tile_k(ci), tid);
-      pv.store(tile_v(ci), tid);
-      request(ci + 1);
+      pk.store(smem + slot, tid);
+      pv.store(smem + slot + W::kK, tid);
+      request(ci + 1, 0);
       chunk_barrier();
     }
     st.factors(g2, a.u, n, lane);
     const bool fine = fine_state(a.returned, g2, REV ? chunk_t0(ci) : len - chunk_t0(ci) - n);
-    st.update(tile_k(ci), tile_v(ci), ct0, sv0, n == C ? an : an_short, fine, lane);
+    st.update(smem + slot, smem + slot + W::kK, ct0, sv0, n == C ? an : an_short, fine, lane);
+    slot = next_slot(slot);
   }
   st.save(a.seg_state + ((size_t)bh * a.nseg + seg) * a.K * a.V, a.V, 1, ct0, v0 + 16 * sv0, a.K, a.V, lane);
 }

@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(256) decay_join_kernel(JoinArgs s, JoinArgs r,
         const long long left = (long long)len - (long long)seg * seglen;
         const int n = left < 0 ? 0 : (left < seglen ? (int)left : seglen);
         const Decay2 d = n == seglen ? whole : decay_pow2(g, n);
-        S = fmaf(S, d.hi, fmaf(S, d.lo, loc[b]));
+        S = fmaf(S, d.hi, fmaf(S * d.hi, d.lo, loc[b]));
       }
     }
   }
