@@ -31,11 +31,14 @@ struct WalkArgs {
   const float* state_in;     // element (i, j) of head bh at bh * K * V + i * si_k + j * si_v; null = 0
   const float* seg_state;    // states at the segments' starts (B*H, nseg, K, V), same strides; used if nseg > 1
   float* state_out;          // the end state, null = not written (same strides)
+  float* mid;                // null, or takes the states at the starts of nmid segments of midlen tokens that
+  int nmid, midlen;          // another walk is cut into (reverse walks of one segment; same strides)
   void* o;
   float c, r, u;             // scales of the intra-chunk term, the read and the update
   int si_k, si_v;
   int BH, H, T, K, V;        // K, V: the walk's key and value widths
   int nseg, seglen;          // seglen: a multiple of the chunk
+  int returned;              // the state, or one that follows from it, is returned (see fine_state)
   int zero_tail;             // write zeros to the rows of o behind a sequence's length
 };
 
@@ -675,8 +678,10 @@ __device__ __forceinline__ void walk(const WalkArgs& a, int block, Lds<T>* smem)
     const int rw = wave - 4;
     const int ct0 = rw / W::S::WV * NKS, sv0 = rw % W::S::WV * NVS;
     StateTile<T, KD, VT, C, NKS, NVS, REV> st;
-    const float* S0 = a.nseg > 1 ? a.seg_state + ((size_t)bh * a.nseg + seg) * hs
-                                 : (a.state_in ? a.state_in + (size_t)bh * hs : nullptr);
+    const bool first = REV ? t_end == len : seg == 0;
+    const float* S0 = !first ? a.seg_state + ((size_t)bh * a.nseg + seg) * hs
+                             : (a.state_in ? a.state_in + (size_t)bh * hs : nullptr);
+    int mid_seg = REV && a.mid && len > 0 ? (len - 1) / a.midlen : 0;
     if (S0) st.load(S0, a.si_k, a.si_v, ct0, v0 + 16 * sv0, a.K, a.V, lane);
     else st.zero();
     const Decay2 an = decay_pow2(g, C), an_short = decay_pow2(g, nch > 0 ? n_last : 0);
@@ -687,8 +692,16 @@ __device__ __forceinline__ void walk(const WalkArgs& a, int block, Lds<T>* smem)
     for (int ci = 0; ci < nch; ++ci) {
       const int n = chunk_n(ci);
       st.factors(g2, a.u, n, lane);
-      const bool fine = fine_state(a.state_out != nullptr, g2, REV ? chunk_t0(ci) : len - chunk_t0(ci) - n);
+      const bool fine = fine_state(a.returned, g2, REV ? chunk_t0(ci) : len - chunk_t0(ci) - n);
       st.update(tile_k(slot), tile_v(slot), ct0, sv0, n == C ? an : an_short, fine, lane);
+      if constexpr (REV) {
+        if (mid_seg > 0 && chunk_t0(ci) == mid_seg * a.midlen) {
+          --mid_seg;                             // the states behind this walk's chunks from there on
+          int ln = lane;
+          asm volatile("" : "+v"(ln));           // (addresses computed here, not kept from before the loop)
+          st.save(a.mid + ((size_t)bh * a.nmid + mid_seg) * hs, a.si_k, a.si_v, ct0, v0 + 16 * sv0, a.K, a.V, ln);
+        }
+      }
       if (ci + 1 < nch) {
         slot = next_slot(slot);
         st.image(sS + (ci + 1 & 1) * W::kS, ct0, 16 * sv0, lane);
@@ -812,7 +825,8 @@ __global__ void __launch_bounds__(kWalkThreads, (WalkShape<T, KD, VT>::EU)) deca
 // The three walks of a backward pass in one launch: dq (keys V, values K wide), dk (the same), dv (keys K,
 // values V wide).  Each has as many workgroups as the forward has, so that where those fill the chip once
 // the other walks' workgroups take the places of the first ones to end, and a small pass costs one launch.
-// PACK: q, k and v are kept in 8 bits.
+// PACK: q, k and v are kept in 8 bits.  first: the workgroups that an earlier launch had (where dv's segments
+// start from states of dk's walk, dv has a launch of its own).
 template <typename T, int KD, int VD, bool PACK> struct BwdShape {
   static constexpr int VTK = KD <= 32 ? 32 : 64, VTV = VD <= 32 ? 32 : 64;        // value tiles over K and over V
   static constexpr int LDS = cmax(walk_lds<T, VD, VTK, PACK>(), walk_lds<T, KD, VTV, PACK>());
@@ -820,12 +834,12 @@ template <typename T, int KD, int VD, bool PACK> struct BwdShape {
 };
 template <typename T, int KD, int VD, bool PACK>
 __global__ void __launch_bounds__(kWalkThreads, (BwdShape<T, KD, VD, PACK>::EU))
-    decay_bwd_kernel(WalkArgs dq, WalkArgs dk, WalkArgs dv) {
+    decay_bwd_kernel(WalkArgs dq, WalkArgs dk, WalkArgs dv, int first) {
   typedef BwdShape<T, KD, VD, PACK> S;
   __shared__ __align__(16) T smem[S::LDS];
   static_assert(sizeof(smem) <= 160 * 1024, "LDS of one gfx950 workgroup exceeded");
   const int n = walk_blocks(dq, S::VTK);
-  int b = blockIdx.x;
+  int b = blockIdx.x + first;
   if (b < n) {
     walk<T, VD, S::VTK, false, false, PACK, PACK>(dq, b, (Lds<T>*)smem);
   } else if ((b -= n) < n) {
@@ -933,8 +947,13 @@ template <typename T, int KD> hipError_t launch_walk_fwd(const WalkArgs& a, hipS
 template <typename T, int KD, int VD, bool PACK>
 hipError_t launch_walk_bwd(const WalkArgs& dq, const WalkArgs& dk, const WalkArgs& dv, hipStream_t s) {
   typedef BwdShape<T, KD, VD, PACK> S;
-  const int n = 2 * walk_blocks(dq, S::VTK) + walk_blocks(dv, S::VTV);
-  hipLaunchKernelGGL((decay_bwd_kernel<T, KD, VD, PACK>), dim3(n), dim3(kWalkThreads), 0, s, dq, dk, dv);
+  const int nqk = 2 * walk_blocks(dq, S::VTK), nv = walk_blocks(dv, S::VTV);
+  if (!dk.mid) {
+    hipLaunchKernelGGL((decay_bwd_kernel<T, KD, VD, PACK>), dim3(nqk + nv), dim3(kWalkThreads), 0, s, dq, dk, dv, 0);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL((decay_bwd_kernel<T, KD, VD, PACK>), dim3(nqk), dim3(kWalkThreads), 0, s, dq, dk, dv, 0);
+  hipLaunchKernelGGL((decay_bwd_kernel<T, KD, VD, PACK>), dim3(nv), dim3(kWalkThreads), 0, s, dq, dk, dv, nqk);
   return hipGetLastError();
 }
 

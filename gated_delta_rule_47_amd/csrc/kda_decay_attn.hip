@@ -19,27 +19,56 @@ KDA_DECAY_EXTERN(bf16_t, 128)
 // ------------------------------------------------------------------ segments
 // A walk is sequential over its chunks, so heads x value tiles alone may leave most of the 256 CUs
 // idle; then the tokens are cut into segments.  The price is a second read of k and v (the segments' local
-// states) and two more launches, so: no more segments than fill the chip once, four chunks at least in
-// each, none in sequences of under 16 chunks (which one walk passes in the time of the launches), and in a
-// forward pass not two of them (4 x 16 heads of 4096 tokens, K = V = 128, bf16: 114 us in two segments, 111
-// in one; backward, whose three walks share the segments' states, 268 and 330).
+// states) and two more launches.  The number of segments comes from a model in times of one chunk: workgroups
+// run in rounds of one per CU; a round costs its chunks and a fixed part, a chunk of the pass over the state
+// alone a share of a full one, the join and the launches a constant.  Measured, bf16, model in brackets:
+// 1 x 4 heads of 30011 tokens, K = V = 128, forward: 24, 32, 40 segments 59, 54, 71 us (56, 48, 71); 2 x 16 heads of
+// 8192: 1, 2, 3, 4 segments 152, 145, 108, 91 us (133, 127, 93, 75); backward, 8 x 8 heads of 4096, K = V = 64:
+// 1, 2, 4 segments 79, 99, 90 us (69, 112, 106).  Four chunks at least in a segment, none in sequences of under 16.
+// Of two plans within 5 % the one with more segments (a batch of unequal lengths spreads better).
+//
+// A backward pass whose walks of dq and dk fill the chip once, and which with dv's would need half of a second
+// round, gives dv's walk a launch of its own in two segments: dk's walk passes the state that the second
+// one starts from, so that costs no pass over the state (2 x 32 heads of 8192, K = V = 128, bf16: 350 us; all
+// three in one launch 395, in two segments 434).  Narrow heads, of which a CU holds two, gain nothing by that
+// (4 x 32 heads of 4096, K = V = 64: 137 and 140 us).
 DecayPlan decay_plan(int B, int H, int T, int K, int V, bool bf16, bool bwd) {
   const int C = bf16 ? 64 : 32;
-  const long long wgs = (long long)B * H * ((V + 63) / 64);
   const int nchunks = (T + C - 1) / C;
-  const long long fill = 256;
-  long long n = (fill + wgs - 1) / wgs;
-  if (n > nchunks / 4) n = nchunks / 4;
-  if (nchunks < 16 || n < (bwd ? 2 : 3)) n = 1;
-  DecayPlan p;
-  const int per = (nchunks + (int)n - 1) / (int)n;
-  p.seglen = (per < 1 ? 1 : per) * C;
-  p.nseg = nchunks ? (nchunks + per - 1) / per : 1;
+  const long long fill = 256, wk = (long long)B * H * ((K + 63) / 64), wv = (long long)B * H * ((V + 63) / 64);
+  const long long walks = bwd ? 2 * wk + wv : wv, states = bwd ? 2 * wv : wv;
+  const double fixed = bf16 ? 5 : 3, join = bf16 ? 14 : 7, share = bf16 ? 0.6 : 0.35;
+  const auto rounds = [&](long long blocks) { return (double)((blocks + fill - 1) / fill); };
+  const auto cost = [&](long long n) {
+    const double per = (double)((nchunks + n - 1) / n);
+    const double walk = rounds(walks * n) * (per + fixed);
+    return n == 1 ? walk : walk + rounds(states * (n - 1)) * (share * per + fixed) + join;
+  };
+  DecayPlan p{};
+  int n = 1;
+  if (nchunks >= 16) {
+    double best = cost(1);
+    for (int r = 1; r <= 3; ++r) {                           // as many as fill r rounds
+      long long m = r * fill / walks;
+      if (m > nchunks / 4) m = nchunks / 4;
+      if (m > n && cost(m) < 1.05 * best) best = cost(m), n = (int)m;
+    }
+    if (bwd && (K > 64 || V > 64) && 2 * wk <= fill && walks > fill && 1.5 * nchunks + 3 * fixed < best)
+      n = 1, p.vseg = 2;
+  }
+  const auto cut = [&](int n, int* seglen) {
+    const int per = (nchunks + n - 1) / n;
+    *seglen = (per < 1 ? 1 : per) * C;
+    return nchunks ? (nchunks + per - 1) / per : 1;
+  };
+  p.nseg = cut(n, &p.seglen);
+  p.vseg = cut(p.vseg ? p.vseg : 1, &p.vlen);
   return p;
 }
 
 size_t decay_states_bytes(int B, int H, int K, int V, const DecayPlan& p) {
-  return p.nseg > 1 ? (size_t)B * H * p.nseg * K * V * sizeof(float) : 0;
+  const int n = p.nseg > 1 ? p.nseg : p.vseg;
+  return n > 1 ? (size_t)B * H * n * K * V * sizeof(float) : 0;
 }
 
 // Local end states -> states at the segments' starts, in place and in walking order:
@@ -134,6 +163,7 @@ hipError_t launch_decay_fwd(const void* q, const void* k, const void* v, const f
   WalkArgs a{};
   a.q = q, a.k = k, a.v = v;
   a.log_decay = log_decay, a.lengths = lengths, a.state_in = state_in, a.seg_state = ws, a.state_out = state_out;
+  a.returned = state_out != nullptr;
   a.o = o;
   a.c = a.r = scale, a.u = 1.0f;
   a.si_k = V, a.si_v = 1;
@@ -150,7 +180,7 @@ hipError_t launch_decay_bwd(const void* q, const void* k, const void* v, const u
                             float* dstate_in, void* workspace, int B, int H, int T_, int K, int V, hipStream_t s) {
   const DecayPlan p = decay_plan(B, H, T_, K, V, sizeof(T) == 2, true);
   float* wS = reinterpret_cast<float*>(workspace);
-  float* wR = wS + decay_states_bytes(B, H, K, V, p) / sizeof(float);
+  float* wR = wS + (p.nseg > 1 ? decay_states_bytes(B, H, K, V, p) / sizeof(float) : 0);
   const bool packed = q_sc != nullptr;                      // q, k and v, all or none
   hipError_t e = hipSuccess;
   if (p.nseg > 1) {
@@ -181,6 +211,11 @@ hipError_t launch_decay_bwd(const void* q, const void* k, const void* v, const u
   dv_.state_in = d_state_out, dv_.seg_state = wR, dv_.state_out = dstate_in, dv_.o = dv;
   dv_.c = dv_.u = scale, dv_.r = 1.0f;
   dv_.si_k = V, dv_.si_v = 1, dv_.K = K, dv_.V = V;
+  dv_.returned = dstate_in != nullptr;
+  if (p.vseg > 1) {
+    dk_.mid = wR, dk_.nmid = dv_.nseg = p.vseg, dk_.midlen = dv_.seglen = p.vlen;
+    dk_.returned = dv_.returned;
+  }
   return packed ? walk_bwd<T, true>(dq_, dk_, dv_, s) : walk_bwd<T, false>(dq_, dk_, dv_, s);
 }
 

@@ -81,11 +81,12 @@ hipError_t launch_chunk_bwd_mfma(const float* q, const float* k, const float* v,
 
 // Linear attention with a constant decay per head (kda_decay_attn.hip).  The tokens are walked in nseg
 // segments of seglen tokens; nseg > 1 needs the segments' states in a workspace (two of them backward).
+// A backward pass with nseg = 1 may still cut the walk of dv, into vseg segments of vlen tokens (vseg > 1).
 struct DecayPlan {
-  int nseg, seglen;
+  int nseg, seglen, vseg, vlen;
 };
 DecayPlan decay_plan(int B, int H, int T, int K, int V, bool bf16, bool bwd);
-size_t decay_states_bytes(int B, int H, int K, int V, const DecayPlan& p);
+size_t decay_states_bytes(int B, int H, int K, int V, const DecayPlan& p);   // of S, and of dL/dS backward
 template <typename T>
 hipError_t launch_decay_fwd(const void* q, const void* k, const void* v, const float* log_decay, const int* lengths,
                             const float* state_in, float scale, void* o, float* state_out, void* workspace, int B,

@@ -37,10 +37,10 @@ bool attn_sizes(int B, int H, int T, int K, int V, int dtype) {
   return B >= 1 && H >= 1 && T >= 0 && valid_dim(K) && valid_dim(V) && (long long)B * H <= (1 << 24) &&
          ((size_t)T + 64) * (size_t)(K > V ? K : V) * esize(dtype) <= 0x7fffffffu;
 }
-// S forward, S and its gradient backward
 size_t attn_states(int B, int H, int T, int K, int V, int dtype, bool bwd) {
   if (!valid_dtype(dtype) || !attn_sizes(B, H, T, K, V, dtype)) return 0;
-  return (bwd ? 2 : 1) * decay_states_bytes(B, H, K, V, decay_plan(B, H, T, K, V, dtype == KDA_BF16, bwd));
+  const DecayPlan p = decay_plan(B, H, T, K, V, dtype == KDA_BF16, bwd);
+  return decay_states_bytes(B, H, K, V, p) * (bwd && p.nseg > 1 ? 2 : 1);
 }
 bool norm_sizes(int B, int H, int T, int D) {
   return B >= 1 && H >= 1 && T >= 0 && D >= 1 && D <= (1 << 24) && (long long)B * H <= (1 << 24) &&

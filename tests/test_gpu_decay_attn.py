@@ -120,17 +120,30 @@ def test_fwd_widths(K, V, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("B,H,T,K,V", [(1, 1, 1100, 64, 64), (1, 2, 2049, 16, 128), (2, 1, 1277, 128, 32),
+@pytest.mark.parametrize("B,H,T,K,V", [(1, 1, 2200, 64, 64), (1, 2, 2049, 16, 128), (2, 1, 1277, 128, 32),
                                        (1, 1, 2100, 128, 128)])
 def test_fwd_segments(B, H, T, K, V, dtype):
-    assert kda.decay_attn_workspace_bytes(B, H, T, K, V, dtype) > 0
+    assert T < 2000 or kda.decay_attn_workspace_bytes(B, H, T, K, V, dtype) > 0
     run_fwd(B, H, T, K, V, dtype)
     run_fwd(B, H, T, K, V, dtype, g=[-1e-4])
     run_bwd(B, H, T, K, V, dtype)
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("T", [70, 1100])
+@pytest.mark.parametrize("B,H,K,V,lengths,packed", [
+    (1, 65, 8, 128, None, ()), (1, 52, 128, 8, None, ()), (1, 43, 128, 128, None, ("q", "k", "v")),
+    (7, 10, 16, 128, [1100, 0, 576, 577, 1, 1099, 512], ()), (7, 10, 8, 128, [575, 1200, 288, 289, -1, 1, 600], ("q", "k", "v"))])
+def test_bwd_segments_of_dv_alone(B, H, K, V, lengths, packed, dtype):
+    """Heads enough that only the walk of dv is cut, in two (T of 17 chunks and a part): its second segment
+    starts from the state that the walk of dk leaves."""
+    T = 1100 if dtype == BF else 550
+    assert kda.decay_attn_bwd_workspace_bytes(B, H, T, K, V, dtype) == B * H * 2 * K * V * 4
+    run_bwd(B, H, T, K, V, dtype, lengths=lengths, packed=packed)
+    run_bwd(B, H, T, K, V, dtype, lengths=lengths, packed=packed, g=[-1e-4], state=False)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T", [70, 1100, 2200])
 def test_padded_batch(T, dtype):
     lengths = [T, 0, 1, T // 2, T - 1, 64, 65, T + 100, -3]
     run_fwd(9, 2, T, 32, 64, dtype, lengths=lengths)
@@ -161,8 +174,8 @@ def test_padding_may_hold_anything(dtype):
 @pytest.mark.parametrize("g", [0.0, -float("inf"), -30.0, -1e-5, -2.0])
 def test_decays(g, dtype):
     with np.errstate(over="ignore", invalid="ignore"):
-        run_fwd(1, 2, 1100, 32, 32, dtype, g=[g])
-        run_bwd(1, 2, 1100, 32, 32, dtype, g=[g])
+        run_fwd(1, 2, 2200, 32, 32, dtype, g=[g])
+        run_bwd(1, 2, 2200, 32, 32, dtype, g=[g])
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
@@ -192,11 +205,11 @@ def test_no_tokens(dtype):
 
 
 def test_state_in_place_scale_and_caller_buffers():
-    for T in (100, 1100):                                          # one segment, several
+    for T in (100, 2100):                                          # one segment, several
         x, d = make(1, 2, T, 32, 64, BF)
         o, S = kda.decay_attn_fwd(d["q"], d["k"], d["v"], d["g"], d["S0"], scale=0.25)
         need = kda.decay_attn_workspace_bytes(1, 2, T, 32, 64)
-        assert (need > 0) == (T == 1100)
+        assert (need > 0) == (T == 2100)
         ws = torch.full((max(need, 1),), 255, dtype=torch.uint8, device=DEV)      # contents are ignored
         state, out = d["S0"].clone(), torch.empty_like(o)
         o2, S2 = kda.decay_attn_fwd(d["q"], d["k"], d["v"], d["g"], state, scale=0.25, out=out, state_out=state,
@@ -268,7 +281,7 @@ def test_gradient_against_differences_of_the_forward(dtype):
 def test_another_stream_and_graph_replays():
     """Calls on a side stream; a captured forward and backward replayed with other work in between, on
     changed inputs, give the eager results bit for bit."""
-    B, H, T, K, V = 1, 2, 1100, 64, 64
+    B, H, T, K, V = 1, 2, 2100, 64, 64
     x, d = make(B, H, T, K, V, BF, 1)
     _, e = make(B, H, T, K, V, BF, 2)
     assert kda.decay_attn_workspace_bytes(B, H, T, K, V) > 0
