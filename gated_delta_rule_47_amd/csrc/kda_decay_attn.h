@@ -827,15 +827,16 @@ __global__ void __launch_bounds__(kWalkThreads, (WalkShape<T, KD, VT>::EU)) deca
 // the other walks' workgroups take the places of the first ones to end, and a small pass costs one launch.
 // PACK: q, k and v are kept in 8 bits.  first: the workgroups that an earlier launch had (where dv's segments
 // start from states of dk's walk, dv has a launch of its own).
-template <typename T, int KD, int VD, bool PACK> struct BwdShape {
-  static constexpr int VTK = KD <= 32 ? 32 : 64, VTV = VD <= 32 ? 32 : 64;        // value tiles over K and over V
+// VT: the widest value tile.
+template <typename T, int KD, int VD, bool PACK, int VT> struct BwdShape {
+  static constexpr int VTK = KD <= 32 ? 32 : VT, VTV = VD <= 32 ? 32 : VT;        // value tiles over K and over V
   static constexpr int LDS = cmax(walk_lds<T, VD, VTK, PACK>(), walk_lds<T, KD, VTV, PACK>());
   static constexpr int EU = PACK ? 2 : cmin(WalkShape<T, VD, VTK>::EU, WalkShape<T, KD, VTV>::EU);
 };
-template <typename T, int KD, int VD, bool PACK>
-__global__ void __launch_bounds__(kWalkThreads, (BwdShape<T, KD, VD, PACK>::EU))
+template <typename T, int KD, int VD, bool PACK, int VT>
+__global__ void __launch_bounds__(kWalkThreads, (BwdShape<T, KD, VD, PACK, VT>::EU))
     decay_bwd_kernel(WalkArgs dq, WalkArgs dk, WalkArgs dv, int first) {
-  typedef BwdShape<T, KD, VD, PACK> S;
+  typedef BwdShape<T, KD, VD, PACK, VT> S;
   __shared__ __align__(16) T smem[S::LDS];
   static_assert(sizeof(smem) <= 160 * 1024, "LDS of one gfx950 workgroup exceeded");
   const int n = walk_blocks(dq, S::VTK);
@@ -934,27 +935,39 @@ __global__ void __launch_bounds__((64 * seg_waves<KD, VT>())) decay_segment_kern
 }
 
 // ------------------------------------------------------------------ launchers
-// Instances by key and value widths padded to 32, 64 or 128; value tiles are 64 columns wide, or 32 for
-// widths up to 32.
+// Instances by key and value widths padded to 32, 64 or 128.  Value tiles are 64 columns wide; 32 for widths up
+// to 32, and where even those leave every workgroup a CU of its own: then a chunk's time is all that counts, and it
+// has half of the products with the state.  (K = V = 128, bf16, 900 tokens, backward: 20 heads 24.4 us in 32
+// columns, 30.0 in 64; 24 heads, which pass one round, 39.5 and 30.1; forward 1 x 8 heads 18.5 and 25.6.  fp32,
+// 400 tokens, backward: 16 heads 38 and 52, 24 heads 69 and 52.)
+constexpr int kNarrowFill = 256;                 // CUs
 template <typename T, int KD> hipError_t launch_walk_fwd(const WalkArgs& a, hipStream_t s) {
-  if (a.V <= 32)
+  if (a.V <= 32 || 2 * walk_blocks(a, 64) <= kNarrowFill)
     hipLaunchKernelGGL((decay_fwd_kernel<T, KD, 32>), dim3(walk_blocks(a, 32)), dim3(kWalkThreads), 0, s, a);
   else
     hipLaunchKernelGGL((decay_fwd_kernel<T, KD, 64>), dim3(walk_blocks(a, 64)), dim3(kWalkThreads), 0, s, a);
   return hipGetLastError();
 }
 
-template <typename T, int KD, int VD, bool PACK>
-hipError_t launch_walk_bwd(const WalkArgs& dq, const WalkArgs& dk, const WalkArgs& dv, hipStream_t s) {
-  typedef BwdShape<T, KD, VD, PACK> S;
+template <typename T, int KD, int VD, bool PACK, int VT>
+hipError_t launch_walk_bwd_vt(const WalkArgs& dq, const WalkArgs& dk, const WalkArgs& dv, hipStream_t s) {
+  typedef BwdShape<T, KD, VD, PACK, VT> S;
   const int nqk = 2 * walk_blocks(dq, S::VTK), nv = walk_blocks(dv, S::VTV);
   if (!dk.mid) {
-    hipLaunchKernelGGL((decay_bwd_kernel<T, KD, VD, PACK>), dim3(nqk + nv), dim3(kWalkThreads), 0, s, dq, dk, dv, 0);
+    hipLaunchKernelGGL((decay_bwd_kernel<T, KD, VD, PACK, VT>), dim3(nqk + nv), dim3(kWalkThreads), 0, s, dq, dk, dv, 0);
     return hipGetLastError();
   }
-  hipLaunchKernelGGL((decay_bwd_kernel<T, KD, VD, PACK>), dim3(nqk), dim3(kWalkThreads), 0, s, dq, dk, dv, 0);
-  hipLaunchKernelGGL((decay_bwd_kernel<T, KD, VD, PACK>), dim3(nv), dim3(kWalkThreads), 0, s, dq, dk, dv, nqk);
+  hipLaunchKernelGGL((decay_bwd_kernel<T, KD, VD, PACK, VT>), dim3(nqk), dim3(kWalkThreads), 0, s, dq, dk, dv, 0);
+  hipLaunchKernelGGL((decay_bwd_kernel<T, KD, VD, PACK, VT>), dim3(nv), dim3(kWalkThreads), 0, s, dq, dk, dv, nqk);
   return hipGetLastError();
+}
+template <typename T, int KD, int VD, bool PACK>
+hipError_t launch_walk_bwd(const WalkArgs& dq, const WalkArgs& dk, const WalkArgs& dv, hipStream_t s) {
+  if constexpr (KD > 32 || VD > 32) {
+    if (2 * (2 * walk_blocks(dq, 64) + walk_blocks(dv, 64)) > kNarrowFill)
+      return launch_walk_bwd_vt<T, KD, VD, PACK, 64>(dq, dk, dv, s);
+  }
+  return launch_walk_bwd_vt<T, KD, VD, PACK, 32>(dq, dk, dv, s);
 }
 
 template <typename T, int KD, int VT, bool PACK>

@@ -130,6 +130,17 @@ def test_fwd_segments(B, H, T, K, V, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("K,V", [(64, 64), (128, 128), (64, 128), (128, 64), (32, 128), (8, 64)])
+def test_many_heads(K, V, dtype):
+    """Heads enough that the value tiles are the wide ones."""
+    lengths = [131, 64, 0, 1, 97]
+    run_fwd(5, 30, 131, K, V, dtype, seed=K + V)
+    run_fwd(5, 30, 131, K, V, dtype, lengths=lengths, seed=K + V)
+    run_bwd(5, 30, 131, K, V, dtype, lengths=lengths)
+    run_bwd(1, 150, 131, K, V, dtype, packed=("q", "k", "v"))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("B,H,K,V,lengths,packed", [
     (1, 65, 8, 128, None, ()), (1, 52, 128, 8, None, ()), (1, 43, 128, 128, None, ("q", "k", "v")),
     (7, 10, 16, 128, [1100, 0, 576, 577, 1, 1099, 512], ()), (7, 10, 8, 128, [575, 1200, 288, 289, -1, 1, 600], ("q", "k", "v"))])
