@@ -33,8 +33,9 @@ template <int NI, int NO> bool any_overlap(const Buf (&ins)[NI], const Buf (&out
 }
 bool aligned(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 
+// (2^20 heads, so that no launch passes 2^32 threads)
 bool attn_sizes(int B, int H, int T, int K, int V, int dtype) {
-  return B >= 1 && H >= 1 && T >= 0 && valid_dim(K) && valid_dim(V) && (long long)B * H <= (1 << 24) &&
+  return B >= 1 && H >= 1 && T >= 0 && valid_dim(K) && valid_dim(V) && (long long)B * H <= (1 << 20) &&
          ((size_t)T + 64) * (size_t)(K > V ? K : V) * esize(dtype) <= 0x7fffffffu;
 }
 size_t attn_states(int B, int H, int T, int K, int V, int dtype, bool bwd) {
@@ -43,7 +44,7 @@ size_t attn_states(int B, int H, int T, int K, int V, int dtype, bool bwd) {
   return decay_states_bytes(B, H, K, V, p) * (bwd && p.nseg > 1 ? 2 : 1);
 }
 bool norm_sizes(int B, int H, int T, int D) {
-  return B >= 1 && H >= 1 && T >= 0 && D >= 1 && D <= (1 << 24) && (long long)B * H <= (1 << 24) &&
+  return B >= 1 && H >= 1 && T >= 0 && D >= 1 && D <= (1 << 24) && (long long)B * H <= (1 << 20) && (long long)H * D <= (1 << 28) &&
          (long long)B * H * T < 0x7fffffffLL;
 }
 int ckpt_group(int D) { return D < 32 ? D : 32; }

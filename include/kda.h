@@ -284,7 +284,7 @@ int kda_gate_bwd_noalloc(const void* z, const float* A_log, const float* dt_bias
  * Linear attention with a constant decay per head: the same state and read without the
  * delta rule, for layers whose decay is a fixed slope of the head.  With a = exp(log_decay[h]),
  *   S_t = a S_{t-1} + k_t v_t^T,   o_t = scale * S_t^T q_t
- * Layouts, sizes (K, V in {8, 16, 32, 64, 128}; B, H >= 1; T >= 0; B * H <= 2^24), streams and
+ * Layouts, sizes (K, V in {8, 16, 32, 64, 128}; B, H >= 1; T >= 0; B * H <= 2^20), streams and
  * errors are those of this file's conventions; `dtype` is the type of q, k, v, o, d_o and of the
  * gradients dq, dk, dv (which the projections' own backward takes in that type); states and their
  * gradients are float32.
@@ -299,7 +299,8 @@ int kda_gate_bwd_noalloc(const void* z, const float* A_log, const float* dt_bias
  *             (T + 64) * max(K, V) * element size < 2^31 (KDA_ERR_SHAPE).
  * KDA_F32 products run on fp32 MFMA.  KDA_BF16 products run on bf16 MFMA with fp32 accumulation: the
  * scores of a block of 64 tokens and the state as the read sees it are rounded to bf16 once; the
- * carried state is not (fp32, its products in two bf16 parts).  Results equal the token recurrence up
+ * carried state is not (fp32, its products in two bf16 parts, in three where they reach a returned state
+ * by more than 2^-10 of themselves).  Results equal the token recurrence up
  * to those roundings.  A non-finite value in a token can reach every output of its block of tokens. */
 
 /* Bytes of device workspace kda_decay_attn_fwd needs for these sizes: nonzero where B * H heads alone
@@ -345,9 +346,10 @@ int kda_decay_attn_bwd(const void* q, const void* k, const void* v, const unsign
  * Layer norm over the last axis of x (B,H,T,D) with one weight and bias row per head (H = 1: rows of a
  * whole layer), as the read of a linear-attention layer is normalised:
  *   y = (x - mean) * rstd * weight[h] + bias[h],   rstd = (mean((x - mean)^2) + eps)^-1/2
- *   x, y (B,H,T,D) in `dtype`, aligned to an element (rows that are 16-byte aligned run fastest)
+ *   x, y (B,H,T,D) in `dtype`, aligned to an element
  *   weight, bias (H,D) f32, NULL = ones / zeros;  mean, rstd (B,H,T) f32, NULL = not written
- *   eps >= 0 and finite (KDA_ERR_SHAPE otherwise);  D >= 1;  T >= 0;  B * H * T < 2^31
+ *   eps >= 0 and finite;  1 <= D <= 2^24;  T >= 0;  B * H <= 2^20;  H * D <= 2^28;  B * H * T < 2^31
+ *   (KDA_ERR_SHAPE otherwise)
  * Statistics are taken in float32 in two passes over the row.  y must not overlap an input. */
 int kda_layer_norm_fwd(const void* x, const float* weight, const float* bias, float eps, void* y, float* mean,
                        float* rstd, int B, int H, int T, int D, int dtype, void* stream);
@@ -361,8 +363,7 @@ size_t kda_layer_norm_bwd_workspace_bytes(int B, int H, int T, int D, int dtype)
  *   dx      (B,H,T,D) in `dtype` = rstd (p - mean(p) - xh mean(p xh))   (it is the d_o of the operator
  *           whose output was normalised)
  *   dweight (H,D) f32 = sum over b, t of dy xh, dbias (H,D) f32 = sum of dy; NULL = not computed
- *   x_scales NULL, or x is kept in 8 bits (codes 16-byte aligned for the fast path; D <= 32 or a
- *           multiple of 32) as kda_ckpt_pack writes it.
+ *   x_scales NULL, or x is kept in 8 bits (D <= 32 or a multiple of 32) as kda_ckpt_pack writes it.
  *   workspace kda_layer_norm_bwd_workspace_bytes() bytes, 16-byte aligned (NULL when that is 0 or
  *           neither sum is asked for); contents on entry ignored.
  * The sums over rows run in a fixed order (bitwise repeatable).  No output may overlap an input, another

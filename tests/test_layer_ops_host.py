@@ -61,6 +61,7 @@ def test_decay_attn_fwd_refusals():
     cases = [(dict(q=None), NULL), (dict(k=None), NULL), (dict(v=None), NULL), (dict(g=None), NULL),
              (dict(o=None), NULL), (dict(dt=5), DTYPE), (dict(B=0), SHAPE), (dict(H=0), SHAPE), (dict(T=-1), SHAPE),
              (dict(K=12), SHAPE), (dict(V=256), SHAPE), (dict(T=1 << 23), SHAPE), (dict(B=1 << 13, H=1 << 13), SHAPE),
+             (dict(B=1 << 11, H=1 << 10, T=1), SHAPE),
              (dict(q=P(q.value + 8)), ALIGN), (dict(o=P(o.value + 2)), ALIGN), (dict(ws=None), WORKSPACE),
              (dict(nws=1000), WORKSPACE), (dict(ws=P(ws.value + 16)), ALIGN), (dict(o=q), ALIAS),
              (dict(o=P(v.value + 16)), ALIAS), (dict(s1=k), ALIAS), (dict(s1=o), ALIAS), (dict(s1=g), ALIAS),
@@ -124,7 +125,8 @@ def test_layer_norm_refusals():
 
     for kw, status in ((dict(x=None), NULL), (dict(y=None), NULL), (dict(dt=9), DTYPE), (dict(D=0), SHAPE),
                        (dict(T=-1), SHAPE), (dict(B=0), SHAPE), (dict(eps=-1.0), SHAPE), (dict(eps=float("nan")), SHAPE),
-                       (dict(eps=float("inf")), SHAPE), (dict(T=1 << 30), SHAPE), (dict(x=P(x.value + 1)), ALIGN),
+                       (dict(eps=float("inf")), SHAPE), (dict(T=1 << 30), SHAPE),
+                       (dict(B=1 << 11, H=1 << 10), SHAPE), (dict(H=1 << 16, D=1 << 13), SHAPE), (dict(x=P(x.value + 1)), ALIGN),
                        (dict(y=P(y.value + 2), dt=F32), ALIGN), (dict(y=x), ALIAS), (dict(y=w), ALIAS),
                        (dict(m=x), ALIAS), (dict(m=r), ALIAS), (dict(r=y), ALIAS)):
         assert fwd(**kw) == status, kw
