@@ -528,7 +528,7 @@ template <typename T, int KD, int VT, int C, int NK, int NV, bool REV> struct St
 // every chunk of a long sequence), but only from chunks that the decay to the end leaves something of: a
 // chunk counts as fine, three parts (2^-26) and the decay in two floats, while a^{tokens behind it} is over
 // 2^-10, and nothing does where no end state is returned.  At 4 x 32 heads of 16384 tokens, K = V = 128,
-// slopes 1/2 to 1/512, all chunks fine take 535 us, by this rule 495 (the GPU runs these walks at its power
+// slopes 1/2 to 1/512, all chunks fine take 500 us, by this rule 455 (the GPU runs these walks at its power
 // limit, so time follows the matrix work).
 __device__ __forceinline__ bool fine_state(bool returned, float g2, int behind) {
   return returned && !(g2 * (float)behind <= -10.0f);                  // (also for -inf times 0)
@@ -856,7 +856,9 @@ __global__ void __launch_bounds__(kWalkThreads, (BwdShape<T, KD, VD, PACK, VT>::
   }
 }
 
-constexpr int kSegChunks = 3;                    // chunks in LDS
+// Chunks in LDS (four or five give the same: it is the state's arithmetic, 1.1 to 1.5 us per chunk, that takes the
+// time, 1 x 4 heads of 30011 tokens in 32 segments, K = V = 128, bf16: 23 us; so do tiles of 32 columns).
+constexpr int kSegChunks = 3;
 
 // Local end state of one segment (not the last in walking order) for one value tile.
 template <typename T, int KD, int VT, int NW, bool REV, bool PK, bool PV>

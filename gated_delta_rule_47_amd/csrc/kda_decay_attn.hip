@@ -22,8 +22,8 @@ KDA_DECAY_EXTERN(bf16_t, 128)
 // states) and two more launches.  The number of segments comes from a model in times of one chunk: workgroups
 // run in rounds of one per CU; a round costs its chunks and a fixed part, a chunk of the pass over the state
 // alone a share of a full one, the join and the launches a constant.  Measured, bf16, model in brackets:
-// 1 x 4 heads of 30011 tokens, K = V = 128, forward: 24, 32, 40 segments 59, 54, 71 us (56, 48, 71); 2 x 16 heads of
-// 8192: 1, 2, 3, 4 segments 152, 145, 108, 91 us (133, 127, 93, 75); backward, 8 x 8 heads of 4096, K = V = 64:
+// 1 x 4 heads of 30011 tokens, K = V = 128, forward: 24, 32, 40 segments 59, 54, 71 us (56, 48, 72); 2 x 16 heads of
+// 8192: 1, 2, 3, 4 segments 152, 145, 108, 91 us (133, 126, 93, 75); backward, 8 x 8 heads of 4096, K = V = 64:
 // 1, 2, 4 segments 79, 99, 90 us (69, 112, 106).  Four chunks at least in a segment, none in sequences of under 16.
 // Of two plans within 5 % the one with more segments (a batch of unequal lengths spreads better).
 //
@@ -73,7 +73,8 @@ size_t decay_states_bytes(int B, int H, int K, int V, const DecayPlan& p) {
 
 // Local end states -> states at the segments' starts, in place and in walking order:
 // x[s] <- S, S <- a^{n_s} S + (old x[s]).  One thread per state element; the locals of 16 segments are
-// fetched before the first is used, so the latency of memory is paid once in 16.  The first `nblock`
+// fetched before the first is used, so the latency of memory is paid once in 16 (4 heads of 32 segments, K = V = 128:
+// 8 us).  The first `nblock`
 // workgroups join S, those behind them (a backward pass) dL/dS from the last segment on.
 struct JoinArgs {
   float* x;
@@ -223,6 +224,7 @@ hipError_t launch_decay_bwd(const void* q, const void* k, const void* v, const u
 // S <- a S + k v^T and o = scale S^T q for one token per head.  Bound by the state's traffic (2 K V
 // fp32 per head): a thread holds four columns (one 16-byte access) of K / RG rows, all loaded before
 // the first is used; the RG partial sums of a column meet in LDS.  VS columns per workgroup.
+// bf16, K = V = 128: 192 x 32 heads 156 us (5.2 TB/s), 4 x 32 heads 4.5 us, where a launch alone takes as long.
 template <typename T, int VS>
 __global__ void __launch_bounds__(256) decay_step_kernel(const T* __restrict__ q, const T* __restrict__ k,
                                                          const T* __restrict__ v,
