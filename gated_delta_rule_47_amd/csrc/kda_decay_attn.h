@@ -482,6 +482,21 @@ template <typename T, int KD, int VT, int C, int NK, int NV, bool REV> struct St
   // `fine`: as exactly as fp32 holds it (see fine_state)
   __device__ __forceinline__ void update(const Lds<T>* sK, const Lds<T>* sV, int ct0, int vt0, Decay2 an, bool fine,
                                          int lane) {
+    // bf16: every operand requested at once, the decay behind the requests (8 x 8 heads of 4096 tokens, K = V = 64: 3 %
+    // faster); fp32, which has four times the products to hide a request behind, as it is used (2 % faster)
+    constexpr int ND = C / L::DG;
+    constexpr bool EARLY = L::PARTS > 1;
+    typename L::frag v[ND][NV], kf[ND][NK];
+    const auto read = [&](int d) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) v[d][j] = L::template tr<VT, false>(sV, vt0 + j, d * L::DG, lane);
+#pragma unroll
+      for (int i = 0; i < NK; ++i) kf[d][i] = L::template tr<KD, true>(sK, ct0 + i, d * L::DG, lane);
+    };
+    if constexpr (EARLY) {
+#pragma unroll
+      for (int d = 0; d < ND; ++d) read(d);
+    }
 #pragma unroll
     for (int i = 0; i < NK; ++i)
 #pragma unroll
@@ -495,29 +510,27 @@ template <typename T, int KD, int VT, int C, int NK, int NV, bool REV> struct St
           for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(acc[i][j][r], an.lo, acc[i][j][r]);
     }
 #pragma unroll
-    for (int d = 0; d < C / L::DG; ++d) {
-      typename L::frag kf[NK], v[NV], vf[NV][L::PARTS];
+    for (int d = 0; d < ND; ++d) {
+      if constexpr (!EARLY) read(d);
+      typename L::frag vf[NV][L::PARTS];
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        v[j] = L::template tr<VT, false>(sV, vt0 + j, d * L::DG, lane);
-        L::scaled(v[j], f[d], vf[j]);
-      }
-#pragma unroll
-      for (int i = 0; i < NK; ++i) kf[i] = L::template tr<KD, true>(sK, ct0 + i, d * L::DG, lane);
+      for (int j = 0; j < NV; ++j) L::scaled(v[d][j], f[d], vf[j]);
 #pragma unroll
       for (int s = 0; s < L::PARTS; ++s)
 #pragma unroll
         for (int i = 0; i < NK; ++i)
 #pragma unroll
-          for (int j = 0; j < NV; ++j) acc[i][j] = L::mma(kf[i], vf[j][s], acc[i][j]);
-      if (L::PARTS > 1 && fine) {
+          for (int j = 0; j < NV; ++j) acc[i][j] = L::mma(kf[d][i], vf[j][s], acc[i][j]);
+    }
+    if (L::PARTS > 1 && fine) {
+#pragma unroll
+      for (int d = 0; d < ND; ++d)
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-          const typename L::frag t = L::third(v[j], f[d]);
+          const typename L::frag t = L::third(v[d][j], f[d]);
 #pragma unroll
-          for (int i = 0; i < NK; ++i) acc[i][j] = L::mma(kf[i], t, acc[i][j]);
+          for (int i = 0; i < NK; ++i) acc[i][j] = L::mma(kf[d][i], t, acc[i][j]);
         }
-      }
     }
   }
 };
@@ -788,6 +801,7 @@ __device__ __forceinline__ void walk(const WalkArgs& a, int block, Lds<T>* smem)
       constexpr int D0 = REV ? 1 : 0, D1 = 1 - D0;
 #pragma unroll
       for (int j = 0; j < NO; ++j) acc[j] = zero4();
+      const frag p0 = scores(D0);
 #pragma unroll
       for (int x = 0; x < NQ; ++x)
 #pragma unroll
@@ -797,7 +811,7 @@ __device__ __forceinline__ void walk(const WalkArgs& a, int block, Lds<T>* smem)
       const float rf = a.r * decay_pow(g2, e < 0 ? 0 : e);
 #pragma unroll
       for (int j = 0; j < NO; ++j) acc[j] *= rf;
-      value_out(D0, scores(D0));
+      value_out(D0, p0);
       if (both) value_out(D1, scores(D1));
       const unsigned row = (unsigned)(chunk_t0(ci) + tl) * (unsigned)(a.V * sizeof(T));
 #pragma unroll
