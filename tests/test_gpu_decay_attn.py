@@ -387,3 +387,44 @@ def test_long_offsets():
     ro, rS = R.decay_attn(x["q"], x["k"], x["v"], x["g"])
     assert norm2(host(o[0, -1, -64:]), ro[0, 0]) <= U and norm2(host(S[0, -1]), rS[0, 0]) <= F32
     assert torch.all(o[0, 0] == 0) and torch.all(S[0, 0] == 0)
+
+
+def test_step_long_offsets():
+    """A state of more than 2^31 elements: the last batch's heads give what they give alone."""
+    B, H, K, V = 4200, 32, 128, 128
+    state = torch.zeros((B, H, K, V), device=DEV)
+    assert state.numel() > 2 ** 31
+    q, k, v = (torch.randn(B, H, D, device=DEV, dtype=BF) for D in (K, K, V))
+    g = torch.full((H,), -0.05, device=DEV)
+    state[-1].normal_()
+    alone = state[-1:].clone()
+    o1 = kda.decay_attn_step(q[-1:].contiguous(), k[-1:].contiguous(), v[-1:].contiguous(), g, alone)
+    o = kda.decay_attn_step(q, k, v, g, state)
+    assert torch.equal(o[-1:], o1) and torch.equal(state[-1:], alone)
+
+
+def test_two_graphs_on_two_streams():
+    """Two captured calls, each with its own workspace from the allocator, replayed at the same time on two
+    streams; a backward pass whose walk of dv has a launch of its own."""
+    calls = []
+    for seed in (1, 2):
+        _, d = make(1, 44, 1100, 128, 128, BF, seed)
+        want = kda.decay_attn_bwd(d["q"], d["k"], d["v"], d["g"], d["S0"], d["d_o"], d["dS"])
+        want = {n: t.clone() for n, t in want.items()}
+        graph = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            got = kda.decay_attn_bwd(d["q"], d["k"], d["v"], d["g"], d["S0"], d["d_o"], d["dS"])
+        calls.append((graph, torch.cuda.Stream(), d, got, want))
+    for _ in range(3):
+        for _, _, _, got, _ in calls:
+            for t in got.values():
+                t.zero_()
+        torch.cuda.synchronize()
+        for graph, s, _, _, _ in calls:
+            with torch.cuda.stream(s):
+                graph.replay()
+        torch.cuda.synchronize()
+        for _, _, _, got, want in calls:
+            for n in want:
+                assert torch.equal(got[n], want[n]), n

@@ -130,3 +130,24 @@ def test_options_and_no_rows():
     _, dw, db = kda.layer_norm_bwd(e, None, st, st, e)
     torch.cuda.synchronize()
     assert torch.all(dw == 0) and torch.all(db == 0)
+
+
+def test_long_offsets():
+    """Tensors of more than 2^31 elements: the last rows give what they give alone."""
+    B, H, T, D = 2, 2, 4300000, 128
+    x = torch.zeros((B, H, T, D), dtype=BF, device=DEV)
+    assert x.numel() > 2 ** 31
+    dy = torch.zeros_like(x)
+    x[-1, -1, -500:].normal_()
+    dy[-1, -1, -500:].normal_()
+    w, b = torch.randn(2, H, D, device=DEV).unbind(0)
+    y, mean, rstd = kda.layer_norm_fwd(x, w, b)
+    dx, dw, db = kda.layer_norm_bwd(x, w, mean, rstd, dy)
+    last = lambda t: t[-1:, -1:, -500:].contiguous()
+    y1, m1, r1 = kda.layer_norm_fwd(last(x), w[-1:], b[-1:])
+    dx1, dw1, db1 = kda.layer_norm_bwd(last(x), w[-1:], m1, r1, last(dy))
+    assert torch.equal(last(y), y1) and torch.equal(last(dx), dx1) and torch.equal(last(mean), m1)
+    assert torch.equal(last(rstd), r1)
+    # the other rows of the head add zeros to its sums, in another order
+    assert norm2(host(dw[-1]), host(dw1[0])) <= F32 and norm2(host(db[-1]), host(db1[0])) <= F32
+    assert torch.all(dw[0] == 0) and torch.all(db[0] == 0) and torch.all(y[0, 0, 0] == b[0].to(BF))
