@@ -16,9 +16,10 @@
 // the scores never touch LDS.  The roles overlap on every SIMD and meet at one barrier per chunk.
 //
 // What bounds it: 4 x 32 heads of 16384 tokens, K = V = 128, bf16: 446 us for 2.16 GB, 4.85 TB/s, the rate of a large
-// copy.  Where a walk has few chunks' company on its CU, the chain within a chunk does: 1.05 us per chunk of
-// 64 tokens at K = V = 64 and 1.4 us at 128, of which LDS traffic (272 KB at K = 128) is 0.9 and the matrix unit 0.45.
-// fp32 (1 x 16 heads of 8191, K = V = 128, backward, 430 us) has the matrix unit busy for 69 % of the cycles.
+// copy.  Shorter ones: the chain of a chunk in two in-order waves per SIMD, 1.05 us per 64 tokens at K = V = 64 (with
+// only the output or only the state waves at work 0.87 and 0.84) and 1.4 us at 128, where the matrix unit's share is
+// 0.45 and the LDS is busy for a third.  fp32 (1 x 16 heads of 8191, K = V = 128, backward, 430 us) has the matrix unit
+// busy for 69 % of the cycles.
 #pragma once
 
 #include <type_traits>
