@@ -160,6 +160,13 @@ __device__ __forceinline__ float ckpt_value(const uint8_t* codes, const uint8_t*
 // (var + eps)^-1/2; a variance that rounding left below zero is zero, NaN stays NaN
 __device__ __forceinline__ float rstd_of(float var, float eps) { return 1.0f / sqrtf((var < 0.0f ? 0.0f : var) + eps); }
 
+// Rows of one of the tiles of tile_rows rows that a head's T rows are cut into (the last may be short).  The kernels
+// count rows from the tile's first one: T may be next to 2^31, where the end of the last tile, or a row a step
+// behind the last one, is past an int.
+__device__ __forceinline__ int rows_of_tile(int T, int tile, int tile_rows) {
+  return min(tile_rows, T - tile * tile_rows);
+}
+
 // ------------------------------------------------------------------ forward
 // TAIL: D is not a multiple of E, so a row's last vector holds fewer elements.
 template <typename T, int L, int NV, bool TAIL>
@@ -184,18 +191,19 @@ __global__ void __launch_bounds__(kNormThreads) norm_fwd_kernel(const T* __restr
     params<E>(b ? b + at : nullptr, n[i], 0.0f, bv[i]);
   }
   const auto has = [&](int i, int e) { return TAIL ? e < n[i] : n[i] > 0; };
-  const int t_end = min(T_, (tile + 1) * tile_rows);
+  const int nrow = rows_of_tile(T_, tile, tile_rows);
+  const size_t row0 = (size_t)bh * T_ + (size_t)tile * tile_rows;
   Raw<T> next[NV];                                 // the row after this one, requested before this one's sums
   const auto request = [&](int t) {
-    if (t < t_end) {
+    if (t < nrow) {
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        if (n[i] > 0) next[i].load(x + ((size_t)bh * T_ + t) * D + (c + i * L) * E, TAIL ? n[i] : E);
+        if (n[i] > 0) next[i].load(x + (row0 + t) * D + (c + i * L) * E, TAIL ? n[i] : E);
     }
   };
-  request(tile * tile_rows + rr);
-  for (int t = tile * tile_rows + rr; t < t_end; t += RPW) {
-    const size_t row = (size_t)bh * T_ + t;
+  request(rr);
+  for (int t = rr; t < nrow; t += RPW) {
+    const size_t row = row0 + t;
     float v[NV][E];
     float s = 0.0f;
 #pragma unroll
@@ -287,13 +295,14 @@ __global__ void __launch_bounds__(kNormThreads)
 #pragma unroll
     for (int e = 0; e < E; ++e) dw[i][e] = db[i][e] = 0.0f;
   }
-  const int t_end = min(T_, (tile + 1) * tile_rows);
+  const int nrow = rows_of_tile(T_, tile, tile_rows);
+  const size_t row0 = (size_t)bh * T_ + (size_t)tile * tile_rows;
   typename std::conditional<PK, RawCodes<T>, Raw<T>>::type nx[NV];
   Raw<T> ndy[NV];
   float nm = 0.0f, nr = 0.0f;
   const auto request = [&](int t) {
-    if (t < t_end) {
-      const size_t row = (size_t)bh * T_ + t;
+    if (t < nrow) {
+      const size_t row = row0 + t;
       nm = mean[row];
       nr = rstd[row];
 #pragma unroll
@@ -306,9 +315,9 @@ __global__ void __launch_bounds__(kNormThreads)
         }
     }
   };
-  request(tile * tile_rows + rr);
-  for (int t = tile * tile_rows + rr; t < t_end; t += RPW) {
-    const size_t row = (size_t)bh * T_ + t;
+  request(rr);
+  for (int t = rr; t < nrow; t += RPW) {
+    const size_t row = row0 + t;
     const float m = nm, r = nr;
     float xh[NV][E], g[NV][E];
     float s1 = 0.0f, s2 = 0.0f;
@@ -377,9 +386,10 @@ __global__ void __launch_bounds__(kNormThreads)
   const int bh = blockIdx.x / ntile, tile = blockIdx.x - bh * ntile;
   const float* wr = w ? w + (size_t)(bh % H) * D : nullptr;
   float* out = part ? part + (size_t)blockIdx.x * 2 * D : nullptr;
-  const int t_beg = tile * tile_rows, t_end = min(T_, (tile + 1) * tile_rows);
-  for (int t = t_beg; t < t_end; ++t) {
-    const size_t row = (size_t)bh * T_ + t;
+  const int nrow = rows_of_tile(T_, tile, tile_rows);
+  const size_t row0 = (size_t)bh * T_ + (size_t)tile * tile_rows;
+  for (int t = 0; t < nrow; ++t) {
+    const size_t row = row0 + t;
     const float m = mean[row], r = rstd[row];
     const auto xhat = [&](int i) {
       const float xv = PK ? ckpt_value(xc, xs, row, i, D, grp) : to_f<T>(x[row * D + i]);
@@ -391,8 +401,8 @@ __global__ void __launch_bounds__(kNormThreads)
       s1 += p;
       s2 = fmaf(p, xh, s2);
       if (out) {
-        out[i] = (t == t_beg ? 0.0f : out[i]) + d * xh;
-        out[D + i] = (t == t_beg ? 0.0f : out[D + i]) + d;
+        out[i] = (t == 0 ? 0.0f : out[i]) + d * xh;
+        out[D + i] = (t == 0 ? 0.0f : out[D + i]) + d;
       }
     }
     const float c1 = row_sum<kNormThreads>(s1, red) / (float)D, c2 = row_sum<kNormThreads>(s2, red) / (float)D;
@@ -446,7 +456,7 @@ static NormPlan norm_plan(int B, int H, int T, int rpw) {
   if (want < 512) want = 512;
   if (want > 1024) want = 1024;
   long long tiles = (want + bh - 1) / bh;
-  const long long most = (T + rpw - 1) / rpw;      // a step of the workgroup's rows at least
+  const long long most = ((long long)T + rpw - 1) / rpw;   // a step of the workgroup's rows at least
   if (tiles > most) tiles = most;
   if (tiles < 1) tiles = 1;
   long long rows = (T + tiles - 1) / tiles;
