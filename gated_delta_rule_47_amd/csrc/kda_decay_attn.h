@@ -400,16 +400,28 @@ __device__ __forceinline__ float uniform(float x) {
   return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(x)));
 }
 
-// a^n for n >= 0 as hi (1 + lo): the chunk factor multiplies the state once per chunk, and a bias of one
-// fp32 rounding would add up over the hundreds of chunks of a long sequence.
-struct Decay2 {
-  float hi, lo;
+// a^n for n >= 0, once per walk.
+__device__ __forceinline__ double decay_pow64(float g, int n) { return n == 0 ? 1.0 : exp((double)g * n); }
+__device__ __forceinline__ float decay_pow32(float g, int n) { return uniform((float)decay_pow64(g, n)); }
+// The factors a^n of equal steps of n tokens, by which a state goes from one chunk (or segment) to the next.  a^n
+// rounded to fp32 is off by up to half a place, and to the same side in each of the thousands of chunks of a long
+// sequence (6e-5 after 2048 of them).  So what one factor is off by is owed to the next, and the product of any run
+// of them is off by one place.  (Adding lo x to the rounded product hi x does nothing, as it is below half of x's
+// last place.  Both in one rounding, fma(x, hi, x lo), is as exact; fp32 walks took 3.5 % longer with it.)
+struct DecaySteps {
+  float hi, lo, owed;
+  __device__ __forceinline__ DecaySteps(float g, int n) {
+    const double x = decay_pow64(g, n);
+    const float h = (float)x;
+    hi = uniform(h), lo = uniform((float)(x - (double)h)), owed = 0.0f;
+  }
+  __device__ __forceinline__ float next() {
+    owed += lo;
+    const float m = hi + owed;
+    owed = uniform(owed - (m - hi));
+    return m;
+  }
 };
-__device__ __forceinline__ Decay2 decay_pow2(float g, int n) {
-  const double x = n == 0 ? 1.0 : exp((double)g * n);
-  const float hi = (float)x;
-  return Decay2{uniform(hi), uniform(hi > 0.0f ? (float)(x / (double)hi - 1.0) : 0.0f)};
-}
 // a^n, g2 = log2(a); n = 0 gives 1 also for a = 0 (g2 = -inf)
 __device__ __forceinline__ float decay_pow(float g2, int n) { return n == 0 ? 1.0f : fast_exp2(g2 * (float)n); }
 
@@ -480,8 +492,8 @@ template <typename T, int KD, int VT, int C, int NK, int NV, bool REV> struct St
         f[d][e] = i < n ? u * decay_pow(g2, REV ? i + 1 : n - 1 - i) : 0.0f;
       }
   }
-  // `fine`: as exactly as fp32 holds it (see fine_state)
-  __device__ __forceinline__ void update(const Lds<T>* sK, const Lds<T>* sV, int ct0, int vt0, Decay2 an, bool fine,
+  // a: the chunk's decay; `fine`: the products as exactly as fp32 holds them (see fine_state)
+  __device__ __forceinline__ void update(const Lds<T>* sK, const Lds<T>* sV, int ct0, int vt0, float a, bool fine,
                                          int lane) {
     // bf16: every operand requested at once, the decay behind the requests (8 x 8 heads of 4096 tokens, K = V = 64: 3 %
     // faster); fp32, which has four times the products to hide a request behind, as it is used (2 % faster)
@@ -501,15 +513,7 @@ template <typename T, int KD, int VT, int C, int NK, int NV, bool REV> struct St
 #pragma unroll
     for (int i = 0; i < NK; ++i)
 #pragma unroll
-      for (int j = 0; j < NV; ++j) acc[i][j] *= an.hi;
-    if (fine) {
-#pragma unroll
-      for (int i = 0; i < NK; ++i)
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(acc[i][j][r], an.lo, acc[i][j][r]);
-    }
+      for (int j = 0; j < NV; ++j) acc[i][j] *= a;
 #pragma unroll
     for (int d = 0; d < ND; ++d) {
       if constexpr (!EARLY) read(d);
@@ -536,14 +540,13 @@ template <typename T, int KD, int VT, int C, int NK, int NV, bool REV> struct St
   }
 };
 
-// How exactly a chunk's part of the state is computed.  The state serves two ends.  The outputs read its
-// bf16 image: two bf16 parts of the decayed operand (2^-17) and a decay rounded to fp32 are far below that
-// rounding.  The end state is returned in fp32, where both would show (2.8e-6 of the state, and 6e-8 for
-// every chunk of a long sequence), but only from chunks that the decay to the end leaves something of: a
-// chunk counts as fine, three parts (2^-26) and the decay in two floats, while a^{tokens behind it} is over
-// 2^-10, and nothing does where no end state is returned.  At 4 x 32 heads of 16384 tokens, K = V = 128,
-// slopes 1/2 to 1/512, all chunks fine take 500 us, by this rule 455 (the GPU runs these walks at its power
-// limit, so time follows the matrix work).
+// How exactly a bf16 chunk's part of the state is computed (fp32 products need no parts).  The state serves two
+// ends.  The outputs read its bf16 image: two bf16 parts of the decayed operand (2^-17) are far below that
+// rounding.  The end state is returned in fp32, where they would show (2.8e-6 of the state), but only from chunks
+// that the decay to the end leaves something of: a chunk counts as fine, three parts (2^-26), while
+// a^{tokens behind it} is over 2^-10, and none does where no end state is returned.  At 4 x 32 heads of 16384
+// tokens, K = V = 128, slopes 1/2 to 1/512, all chunks fine take 500 us, by this rule 455 (the GPU runs these
+// walks at its power limit, so time follows the matrix work).
 __device__ __forceinline__ bool fine_state(bool returned, float g2, int behind) {
   return returned && !(g2 * (float)behind <= -10.0f);                  // (also for -inf times 0)
 }
@@ -704,7 +707,8 @@ __device__ __forceinline__ void walk(const WalkArgs& a, int block, Lds<T>* smem)
     int mid_seg = REV && a.mid && len > 0 ? (len - 1) / a.midlen : 0;
     if (S0) st.load(S0, a.si_k, a.si_v, ct0, v0 + 16 * sv0, a.K, a.V, lane);
     else st.zero();
-    const Decay2 an = decay_pow2(g, C), an_short = decay_pow2(g, nch > 0 ? n_last : 0);
+    DecaySteps an(g, C);
+    const float an_short = decay_pow32(g, nch > 0 ? n_last : 0);
     if (nch > 0) st.image(sS, ct0, 16 * sv0, lane);
     if constexpr (!DMA) stage(0, 0);
     wait_vm_all();
@@ -713,7 +717,7 @@ __device__ __forceinline__ void walk(const WalkArgs& a, int block, Lds<T>* smem)
       const int n = chunk_n(ci);
       st.factors(g2, a.u, n, lane);
       const bool fine = fine_state(a.returned, g2, REV ? chunk_t0(ci) : len - chunk_t0(ci) - n);
-      st.update(tile_k(slot), tile_v(slot), ct0, sv0, n == C ? an : an_short, fine, lane);
+      st.update(tile_k(slot), tile_v(slot), ct0, sv0, n == C ? an.next() : an_short, fine, lane);
       if constexpr (REV) {
         if (mid_seg > 0 && chunk_t0(ci) == mid_seg * a.midlen) {
           --mid_seg;                             // the states behind this walk's chunks from there on
@@ -922,7 +926,8 @@ __device__ __forceinline__ void segment_state(const SegArgs& a, int block, Lds<T
   request(0, 0);
   if constexpr (DMA) request(1, W::kK + W::kV);
   unsigned slot = 0;                             // of chunk ci
-  const Decay2 an = decay_pow2(g, C), an_short = decay_pow2(g, nch > 0 ? n_last : 0);
+  DecaySteps an(g, C);
+  const float an_short = decay_pow32(g, nch > 0 ? n_last : 0);
   for (int ci = 0; ci < nch; ++ci) {
     const int n = chunk_n(ci);
     if constexpr (DMA) {
@@ -939,7 +944,7 @@ __device__ __forceinline__ void segment_state(const SegArgs& a, int block, Lds<T
     }
     st.factors(g2, a.u, n, lane);
     const bool fine = fine_state(a.returned, g2, REV ? chunk_t0(ci) : len - chunk_t0(ci) - n);
-    st.update(smem + slot, smem + slot + W::kK, ct0, sv0, n == C ? an : an_short, fine, lane);
+    st.update(smem + slot, smem + slot + W::kK, ct0, sv0, n == C ? an.next() : an_short, fine, lane);
     slot = next_slot(slot);
   }
   st.save(a.seg_state + ((size_t)bh * a.nseg + seg) * a.K * a.V, a.V, 1, ct0, v0 + 16 * sv0, a.K, a.V, lane);

@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(256) decay_join_kernel(JoinArgs s, JoinArgs r,
   const float g = log_decay[bh % H];
   float* p = a.x + (size_t)bh * nseg * KV + e;
   float S = a.start ? a.start[(size_t)bh * KV + e] : 0.0f;
-  const Decay2 whole = decay_pow2(g, seglen);
+  DecaySteps whole(g, seglen);
   for (int s0 = 0; s0 < nseg; s0 += BATCH) {
     float loc[BATCH];
 #pragma unroll
@@ -110,8 +110,7 @@ __global__ void __launch_bounds__(256) decay_join_kernel(JoinArgs s, JoinArgs r,
         p[(size_t)seg * KV] = S;
         const long long left = (long long)len - (long long)seg * seglen;
         const int n = left < 0 ? 0 : (left < seglen ? (int)left : seglen);
-        const Decay2 d = n == seglen ? whole : decay_pow2(g, n);
-        S = fmaf(S, d.hi, fmaf(S * d.hi, d.lo, loc[b]));
+        S = fmaf(S, n == seglen ? whole.next() : decay_pow32(g, n), loc[b]);
       }
     }
   }

@@ -300,7 +300,9 @@ int kda_gate_bwd_noalloc(const void* z, const float* A_log, const float* dt_bias
  * KDA_F32 products run on fp32 MFMA.  KDA_BF16 products run on bf16 MFMA with fp32 accumulation: the
  * scores of a block of 64 tokens and the state as the read sees it are rounded to bf16 once; the
  * carried state is not (fp32, its products in two bf16 parts, in three where they reach a returned state
- * by more than 2^-10 of themselves).  Results equal the token recurrence up
+ * by more than 2^-10 of themselves, so the last bits of a KDA_BF16 output may depend on whether an end
+ * state is asked for).  The decay that a state takes over many blocks is right to one rounding of fp32,
+ * whatever their number.  Results equal the token recurrence up
  * to those roundings.  A non-finite value in a token can reach every output of its block of tokens. */
 
 /* Bytes of device workspace kda_decay_attn_fwd needs for these sizes: nonzero where B * H heads alone

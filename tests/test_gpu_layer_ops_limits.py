@@ -1,11 +1,13 @@
 """The layer operators at the ends of their documented ranges: the longest tensors, the slowest decays, the
 smallest numbers, gradients in place at every width."""
+import numpy as np
 import pytest
 import torch
 
 import gated_delta_rule_47_amd as kda
+from oracle import layer_ref as R
 
-from gpu_helpers import DEV, say
+from gpu_helpers import DEV, host, say, to_dev
 
 pytestmark = pytest.mark.gpu
 
@@ -42,3 +44,41 @@ def test_norm_of_as_many_rows_as_an_int_counts():
     assert torch.all(db == n)
     xh = (last(x).double() - m1.double().unsqueeze(-1)) * r1.double().unsqueeze(-1)
     assert torch.all((dw.double() - xh.sum((0, 2))).abs() <= 8600 * 2.0 ** -24 * xh.abs().sum((0, 2)))
+
+
+def test_slow_decay_over_thousands_of_chunks():
+    """fp32, one segment of 2048 chunks (heads enough that T is not cut), a decay whose power over a chunk lies in
+    the middle between two floats: taken as one float it would be off by 2^-25, always to the same side, and what
+    the walks carry by 2048 times that, 6e-5; o, dq, dk, dv and the gradient of the start state are right whether
+    the end state is asked for or not.  Bar: per chunk of 32 tokens a carried value takes at most 10 roundings
+    (decay in two floats, 8 products of 4), each 2^-24 / sqrt(3) RMS and of any sign: sqrt(10 * 2048 / 3) 2^-24
+    = 4.9e-6 of the 2-norm; twice that is allowed."""
+    B, H, T, D = 1, 256, 65536, 8
+    heads = [0, 255]
+    g = np.float32(np.log1p(-(536.5) * 2.0 ** -24) / 32)
+    a32 = np.exp(32.0 * float(g))
+    assert abs(np.float32(a32) - a32) > 0.45 * 2.0 ** -24
+    assert kda.decay_attn_workspace_bytes(B, H, T, D, D, FP) == 0
+    assert kda.decay_attn_bwd_workspace_bytes(B, H, T, D, D, FP) == 0
+    rng = np.random.default_rng(11)
+    x = {n: rng.standard_normal((B, 2, T, D)).astype(np.float32) for n in ("q", "k", "v", "d_o")}
+    for n in ("k", "d_o"):
+        x[n] *= np.float32(T ** -0.5)                             # the state stays of the size of its start
+    for n in ("S0", "dS"):
+        x[n] = rng.standard_normal((B, 2, D, D)).astype(np.float32)
+    d = {}
+    for n, a in x.items():
+        d[n] = torch.zeros((B, H, *a.shape[2:]), device=DEV)
+        d[n][:, heads] = to_dev(a, FP)
+    gd = torch.full((H,), float(g), device=DEV)
+    say("slow decay", B, H, T, D)
+    o, _ = kda.decay_attn_fwd(d["q"], d["k"], d["v"], gd, d["S0"], output_state=False)
+    o2, S = kda.decay_attn_fwd(d["q"], d["k"], d["v"], gd, d["S0"])
+    assert torch.equal(o, o2)
+    got = kda.decay_attn_bwd(d["q"], d["k"], d["v"], gd, d["S0"], d["d_o"], d["dS"])
+    got.update(o=o, state=S)
+    ref = R.decay_attn_adjoint(x["q"], x["k"], x["v"], [g, g], x["S0"], x["d_o"], x["dS"])
+    ref["o"], ref["state"] = R.decay_attn(x["q"], x["k"], x["v"], [g, g], x["S0"])
+    err = {n: np.linalg.norm(host(got[n][:, heads]) - ref[n]) / np.linalg.norm(ref[n]) for n in ref}
+    say("  ", {n: "%.2e" % e for n, e in err.items()})
+    assert max(err.values()) <= 1e-5, err
