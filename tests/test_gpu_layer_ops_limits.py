@@ -82,3 +82,31 @@ def test_slow_decay_over_thousands_of_chunks():
     err = {n: np.linalg.norm(host(got[n][:, heads]) - ref[n]) / np.linalg.norm(ref[n]) for n in ref}
     say("  ", {n: "%.2e" % e for n, e in err.items()})
     assert max(err.values()) <= 1e-5, err
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_thousands_of_tokens_with_a_slow_decay(dtype):
+    """4096 single tokens with a decay that lies in the middle between two floats: taken as one it would be off by
+    2^-25, and the state by 4096 times that, 1.2e-4.  Bar: three roundings a token (the product k v, the sum with
+    the decay's low part, the new state), each 2^-24 / sqrt(3) RMS and of any sign: sqrt(4096) 2^-24 = 3.8e-6 of the
+    2-norm; twice that is allowed.  Infinities in the state stay where they are."""
+    B, H, T, K, V = 1, 2, 4096, 16, 8
+    g = np.float32(np.log1p(-(536.5) * 2.0 ** -24))
+    assert abs(np.float32(np.exp(float(g))) - np.exp(float(g))) > 0.45 * 2.0 ** -24
+    rng = np.random.default_rng(12)
+    x = {n: rng.standard_normal((B, H, T, D)) * T ** -0.25 for n, D in (("q", K), ("k", K), ("v", V))}
+    d = {n: to_dev(a.astype(np.float32), dtype) for n, a in x.items()}
+    S0 = rng.standard_normal((B, H, K, V)).astype(np.float32)
+    S, gd = to_dev(S0, FP), torch.full((H,), float(g), device=DEV)
+    tok = [[d[n][:, :, t].contiguous() for n in ("q", "k", "v")] for t in range(T)]
+    out = [kda.decay_attn_step(*a, gd, S) for a in tok]
+    ro, rS = R.decay_attn(host(d["q"]), host(d["k"]), host(d["v"]), [g, g], S0)
+    norm2 = lambda a, b: np.linalg.norm(a - b) / np.linalg.norm(b)
+    e, eo = norm2(host(S), rS), norm2(host(torch.stack(out, 2)), ro)
+    say("  state %.2e, o %.2e" % (e, eo))
+    assert e <= 7.6e-6 and eo <= (2.0 ** -8 if dtype == BF else 7.6e-6 + 2e-6)      # o: and a sum of 16 products
+    S[0, 0, 3, 2], S[0, 1, 5, 1] = float("inf"), -float("inf")
+    for gg in (0.0, float(g), -3.0):
+        kda.decay_attn_step(*tok[0], torch.full((H,), gg, device=DEV), S)
+        assert S[0, 0, 3, 2] == float("inf") and S[0, 1, 5, 1] == -float("inf")
+        assert int(torch.isfinite(S).sum()) == S.numel() - 2
