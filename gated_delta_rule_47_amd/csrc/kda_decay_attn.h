@@ -311,13 +311,16 @@ template <typename T, bool PK, int C, int DP, int NT> struct Stage {
 // the wave's).  Past the buffer's range: zeros.  Written in asm, with no register as its output, because
 // the compiler would wait for every copy in flight before each transposing LDS read; the waits are
 // wait_vm_but()'s (the compiler's own waits for its loads and stores only grow stricter by operations that
-// it does not count).  m0, the copies' LDS address, is read by no other instruction of these kernels.
+// it does not count).  Nor does the compiler look into the block for hazards, so the block holds the wait states
+// itself, whatever stands in front of it: one between m0's write and its use, and five between a vector instruction
+// that writes a scalar register (a readlane of a spilled one, a readfirstlane) and a copy that reads it: the move
+// to m0 and the four of s_nop 3.
 __device__ __forceinline__ void copy_to_lds(u32x4_t r, const Lds<void>* lds, unsigned lane_off, unsigned off) {
   const uint32_t at = (uint32_t)(uintptr_t)lds;
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(
                    __builtin_amdgcn_readfirstlane((int)at)),
                "v"(lane_off), "s"(r), "s"(off)
-               : "memory");
+               : "memory", "m0");
 }
 
 // A tile copied from memory straight into LDS: each wave instruction fills 64 consecutive pieces, so the
