@@ -375,12 +375,13 @@ __global__ void __launch_bounds__(kNormThreads)
 }
 
 // Any width: a workgroup takes the tile's rows one after another; a thread's columns
-// (threadIdx.x + 256 i) keep their running sums in the workgroup's part of `part`.
+// (threadIdx.x + 256 i) keep their running sums in the workgroup's part of `part`.  dx may be dy, of which a thread
+// reads an element for the last time before it writes it.
 template <typename T, bool PK>
 __global__ void __launch_bounds__(kNormThreads)
     norm_bwd_any_kernel(const T* __restrict__ x, const uint8_t* __restrict__ xc, const uint8_t* __restrict__ xs,
                         const float* __restrict__ w, const float* __restrict__ mean, const float* __restrict__ rstd,
-                        const T* __restrict__ dy, T* __restrict__ dx, float* part, int H, int T_, int D, int grp,
+                        const T* dy, T* dx, float* part, int H, int T_, int D, int grp,
                         int ntile, int tile_rows) {
   __shared__ float red[kNormThreads / 64];
   const int bh = blockIdx.x / ntile, tile = blockIdx.x - bh * ntile;

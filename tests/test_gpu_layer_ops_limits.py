@@ -110,3 +110,16 @@ def test_thousands_of_tokens_with_a_slow_decay(dtype):
         kda.decay_attn_step(*tok[0], torch.full((H,), gg, device=DEV), S)
         assert S[0, 0, 3, 2] == float("inf") and S[0, 1, 5, 1] == -float("inf")
         assert int(torch.isfinite(S).sum()) == S.numel() - 2
+
+
+@pytest.mark.parametrize("dtype,D", [(BF, 40), (BF, 4100), (BF, 16384), (BF, 16392), (FP, 8192), (FP, 8200), (FP, 20001)])
+def test_norm_gradient_in_place_of_its_cotangent(dtype, D):
+    """dx written over dy, with the sums, in rows of a wave, of a workgroup, and wider: the same as apart."""
+    x, dy = (torch.randn(2, 2, 9, D, device=DEV).to(dtype) for _ in range(2))
+    w = torch.randn(2, D, device=DEV)
+    _, mean, rstd = kda.layer_norm_fwd(x, w)
+    want = kda.layer_norm_bwd(x, w, mean, rstd, dy)
+    got = kda.layer_norm_bwd(x, w, mean, rstd, dy, dx_out=dy)
+    assert got[0] is dy
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
