@@ -381,7 +381,8 @@ int kda_layer_norm_bwd(const void* x, const unsigned char* x_scales, const float
  * nearest-even OCP e4m3 value of x / 2^e.  Infinities and NaN become NaN.  D <= 32 or a multiple of 32
  * (KDA_ERR_SHAPE).
  *   x (rows, D) in `dtype`, aligned to an element; codes (rows, D) bytes; scales (rows, D / G) bytes
- * kda_ckpt_unpack writes the values the codes stand for (for KDA_BF16 exact, except below 2^-133).
+ * kda_ckpt_unpack writes the values the codes stand for: KDA_F32 exactly; KDA_BF16 exactly from 2^-130 up, the
+ * nearest (even) subnormal bf16 value below it.
  * Outputs must not overlap inputs or each other. */
 int kda_ckpt_pack(const void* x, unsigned char* codes, unsigned char* scales, long long rows, int D, int dtype,
                   void* stream);

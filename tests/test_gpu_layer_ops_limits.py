@@ -123,3 +123,41 @@ def test_norm_gradient_in_place_of_its_cotangent(dtype, D):
     assert got[0] is dy
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("D", [32, 31])
+def test_every_code_under_every_scale(D):
+    """Each of the 256 codes under each of the 256 scale bytes, in groups read eight at a time and one by one.  fp32
+    holds every value (the smallest is 2^-136, the largest 448 2^128 is infinite); bf16 rounds those below 2^-130
+    that are no multiple of 2^-133 to the nearest, ties to even."""
+    codes = np.tile(np.arange(256, dtype=np.uint8), (256, 1))
+    codes = np.concatenate([codes, np.zeros((256, -256 % D), np.uint8)], 1).reshape(-1, D)
+    scales = np.repeat(np.arange(256, dtype=np.uint8), len(codes) // 256)[:, None]
+    with np.errstate(over="ignore"):
+        want = torch.from_numpy(R.ckpt_unpack(codes, scales).astype(np.float32))
+    c, s = torch.from_numpy(codes).to(DEV), torch.from_numpy(scales).to(DEV)
+    ok = scales[:, 0] < 255                                       # (255 is no scale that a packed group has)
+    for dtype in (FP, BF):
+        got = kda.ckpt_unpack(c, s, dtype).cpu()[ok]
+        ref = want.to(dtype)[ok]
+        nan = torch.isnan(ref)
+        assert torch.equal(torch.isnan(got), nan)
+        assert torch.equal(got[~nan], ref[~nan]), dtype
+    big = np.abs(want.numpy())[ok]
+    exact = (want.to(BF).float() == want).numpy()[ok]
+    fin = np.isfinite(big) & (big > 0)
+    assert exact[fin & (big >= 2.0 ** -130)].all() and not exact[fin & (big < 2.0 ** -130) & (big > 2.0 ** -131)].all()
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_smallest_activations_in_8_bits(dtype):
+    """Subnormal and smallest normal values through pack and unpack: codes as defined, fp32 restored to the value of
+    its code, bf16 to that value rounded to nearest even."""
+    rng = np.random.default_rng(5)
+    x = (rng.standard_normal((64, 64)) * 2.0 ** rng.integers(-140, -115, (64, 1))).astype(np.float32)
+    d = torch.from_numpy(x).to(dtype).to(DEV)
+    codes, scales = kda.ckpt_pack(d)
+    rc, rs = R.ckpt_pack(d.float().cpu().numpy())
+    assert np.array_equal(codes.cpu().numpy(), rc) and np.array_equal(scales.cpu().numpy(), rs)
+    val = torch.from_numpy(R.ckpt_unpack(rc, rs).astype(np.float32)).to(dtype)
+    assert torch.equal(kda.ckpt_unpack(codes, scales, dtype).cpu(), val)
