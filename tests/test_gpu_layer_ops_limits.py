@@ -161,3 +161,34 @@ def test_smallest_activations_in_8_bits(dtype):
     assert np.array_equal(codes.cpu().numpy(), rc) and np.array_equal(scales.cpu().numpy(), rs)
     val = torch.from_numpy(R.ckpt_unpack(rc, rs).astype(np.float32)).to(dtype)
     assert torch.equal(kda.ckpt_unpack(codes, scales, dtype).cpu(), val)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("T", [1, 90, 1100])
+def test_gradients_along_themselves_against_differences(T, dtype):
+    """The float64 definition's loss along the direction of each computed gradient g: where t is the true one its
+    slope there is <t, g> / |g|, which differs from |g| by at most |g - t|.  That is u = 2^-8 of |g| in bf16 (scores,
+    state and the output, each rounded once, see test_gpu_decay_attn.py) and 2e-5 in fp32.  The loss is linear in q,
+    k, v and the start state each, so central differences are exact but for the rounding of two sums."""
+    B, H, K, V = 1, 2, 16, 32
+    rng = np.random.default_rng(T)
+    x = {n: rng.standard_normal((B, H, T, D)) for n, D in (("q", K), ("k", K), ("v", V), ("d_o", V))}
+    x["q"] /= K ** 0.5
+    d = {n: to_dev(a.astype(np.float32), dtype) for n, a in x.items()}
+    x = {n: host(t) for n, t in d.items()}
+    g = np.float32([-0.3, -0.01])
+    S0, dS = (rng.standard_normal((B, H, K, V)).astype(np.float32) for _ in range(2))
+    got = kda.decay_attn_bwd(d["q"], d["k"], d["v"], to_dev(g, FP), to_dev(S0, FP), d["d_o"], to_dev(dS, FP))
+    base = {"dq": x["q"], "dk": x["k"], "dv": x["v"], "dstate_in": S0.astype(np.float64)}
+
+    def loss(at):
+        o, S = R.decay_attn(at["dq"], at["dk"], at["dv"], g, at["dstate_in"])
+        return (o * x["d_o"]).sum() + (S * dS).sum()
+
+    for n in base:
+        a = host(got[n])
+        norm = np.linalg.norm(a)
+        up, dn = (loss({**base, n: base[n] + h * a / norm}) for h in (0.5, -0.5))
+        bar = 2.0 ** -8 if dtype == BF and n != "dstate_in" else 2e-5
+        say("  %-9s |g| %.6e, slope %.6e, off by %.1e (bar %.1e)" % (n, norm, up - dn, abs(up - dn - norm) / norm, bar))
+        assert abs(up - dn - norm) <= bar * norm + 1e-13 * (abs(up) + abs(dn)), n
