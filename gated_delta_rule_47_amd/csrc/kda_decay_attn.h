@@ -192,7 +192,6 @@ template <> struct Lin<float> {                  // four v_mfma_f32_16x16x4_f32
   static __device__ __forceinline__ void scaled(frag x, const float* f, frag* out) {
     out[0] = floatx4{x[0] * f[0], x[1] * f[1], x[2] * f[2], x[3] * f[3]};
   }
-  static __device__ __forceinline__ frag third(frag x, const float*) { return x; }     // (not used)
   static __device__ __forceinline__ int tok_of(int e, int g) { return 4 * g + e; }
   static __device__ __forceinline__ void store4(Lds<float>* p, floatx4 x) { *(Lds<floatx4>*)p = x; }
 };
@@ -323,6 +322,18 @@ __device__ __forceinline__ void copy_to_lds(u32x4_t r, const Lds<void>* lds, uns
                : "memory", "m0");
 }
 
+// Byte offset, from a tile's first row (channels from ch0, D in a row), of the 16-byte piece that belongs into
+// place `slot` of the tile's LDS image of C rows x DP channels; past any range for the places of its padding.
+template <typename T, int C, int DP> __device__ __forceinline__ unsigned copy_offset(int slot, int D, int ch0) {
+  typedef Tile<T, C, DP> TL;
+  constexpr int E = Lin<T>::EPP;
+  const int row = slot / TL::PPR, pos = slot % TL::PPR;
+  int pc = pos;
+  if constexpr (Lin<T>::PAD == 0) pc = pos ^ (Lin<T>::template at<DP, false>(row, 0) - row * DP) / E;
+  const int ch = ch0 + pc * E;
+  return row < C && pc < DP / E && ch < D ? (unsigned)(row * D + ch) * (unsigned)sizeof(T) : 0xfffffff0u;
+}
+
 // A tile copied from memory straight into LDS: each wave instruction fills 64 consecutive pieces, so the
 // order of the pieces within a row is made by the address each lane reads.  Rows behind the range read as
 // zeros.  bf16 rows repeat their order every 16, so a tile's instructions share PERIOD lane offsets and
@@ -335,13 +346,7 @@ template <typename T, int C, int DP> struct CopyTile {
   __device__ __forceinline__ CopyTile(int lane, int D, int ch0) {
     row_bytes = (unsigned)(D * (int)sizeof(T));
 #pragma unroll
-    for (int i = 0; i < PERIOD; ++i) {
-      const int slot = 64 * i + lane, row = slot / TL::PPR, pos = slot % TL::PPR;
-      int pc = pos;
-      if constexpr (Lin<T>::PAD == 0) pc = pos ^ (Lin<T>::template at<DP, false>(row, 0) - row * DP) / E;
-      const int ch = ch0 + pc * E;
-      off[i] = row < C && pc < DP / E && ch < D ? (unsigned)row * row_bytes + (unsigned)(ch * (int)sizeof(T)) : 0xfffffff0u;
-    }
+    for (int i = 0; i < PERIOD; ++i) off[i] = copy_offset<T, C, DP>(64 * i + lane, D, ch0);
   }
   // instruction I of the tile whose first row is token t0
   template <int I> __device__ __forceinline__ void issue(u32x4_t r, int t0, const Lds<T>* lds) const {
@@ -361,20 +366,11 @@ template <typename T, int C, int DK, int DV, int NW> struct Copy {
   static constexpr int PER = (NI + NW - 1) / NW, MIN = NI / NW;
   unsigned off[PER];                             // byte offset of this lane's piece from the chunk's first row
 
-  template <int DP> static __device__ __forceinline__ unsigned piece(int slot, int D, int ch0) {
-    typedef Tile<T, C, DP> TL;
-    constexpr int E = Lin<T>::EPP;
-    const int row = slot / TL::PPR, pos = slot % TL::PPR;
-    int pc = pos;
-    if constexpr (Lin<T>::PAD == 0) pc = pos ^ (Lin<T>::template at<DP, false>(row, 0) - row * DP) / E;
-    const int ch = ch0 + pc * E;
-    return row < C && pc < DP / E && ch < D ? (unsigned)(row * D + ch) * (unsigned)sizeof(T) : 0xfffffff0u;
-  }
   __device__ __forceinline__ Copy(int wave, int lane, int K, int V, int v0) {
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int x = wave + i * NW;
-      off[i] = x < IK ? piece<DK>(64 * x + lane, K, 0) : piece<DV>(64 * (x - IK) + lane, V, v0);
+      off[i] = x < IK ? copy_offset<T, C, DK>(64 * x + lane, K, 0) : copy_offset<T, C, DV>(64 * (x - IK) + lane, V, v0);
     }
   }
   // tokens from t0 into the tiles at lds (v behind k)
@@ -530,15 +526,17 @@ template <typename T, int KD, int VT, int C, int NK, int NV, bool REV> struct St
 #pragma unroll
           for (int j = 0; j < NV; ++j) acc[i][j] = L::mma(kf[d][i], vf[j][s], acc[i][j]);
     }
-    if (L::PARTS > 1 && fine) {
+    if constexpr (L::PARTS > 1) {
+      if (fine) {
 #pragma unroll
-      for (int d = 0; d < ND; ++d)
+        for (int d = 0; d < ND; ++d)
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-          const typename L::frag t = L::third(v[d][j], f[d]);
+          for (int j = 0; j < NV; ++j) {
+            const typename L::frag t = L::third(v[d][j], f[d]);
 #pragma unroll
-          for (int i = 0; i < NK; ++i) acc[i][j] = L::mma(kf[d][i], t, acc[i][j]);
-        }
+            for (int i = 0; i < NK; ++i) acc[i][j] = L::mma(kf[d][i], t, acc[i][j]);
+          }
+      }
     }
   }
 };

@@ -486,10 +486,15 @@ static NormShape norm_shape(int D, int E) {
   return p;
 }
 static int norm_rpw(const NormShape& n) { return n.NV ? kNormThreads / n.L : 1; }
-// The shapes above as instances: CASE(L, NV).
+// The shapes above as instances: CASE(L, NV), for those of them that rows of a type come to (norm_used).  Rows of
+// 8-bit codes end inside a vector only up to 32 channels (wider ones are multiples of 32).
 #define KDA_NORM_SHAPES(CASE)                                                                          \
   CASE(1, 1) CASE(2, 1) CASE(4, 1) CASE(8, 1) CASE(16, 1) CASE(32, 1) CASE(64, 1) CASE(64, 2)          \
   CASE(64, 4) CASE(64, 8) CASE(256, 2) CASE(256, 4) CASE(256, 8)
+constexpr bool norm_used(int L, int NV, int E) { return L == kNormThreads ? NV >= 16 / E : NV <= 32 / E; }
+constexpr bool norm_used(int L, int NV, int E, bool tail, bool packed) {
+  return norm_used(L, NV, E) && !(tail && packed && L * E > 32);
+}
 
 template <typename T>
 hipError_t launch_norm_fwd(const void* x, const float* w, const float* b, float eps, void* y, float* mean, float* rstd,
@@ -505,17 +510,20 @@ hipError_t launch_norm_fwd(const void* x, const float* w, const float* b, float 
   const dim3 grid((unsigned)(B * H * p.ntile));
   const bool tail = D % Wide<T>::E != 0;
 #define KDA_NORM(L_, NV_)                                                                                             \
-  if (n.L == L_ && n.NV == NV_) {                                                                                     \
-    if (tail)                                                                                                         \
-      hipLaunchKernelGGL((norm_fwd_kernel<T, L_, NV_, true>), grid, dim3(kNormThreads), 0, s, (const T*)x, w, b, eps, \
-                         (T*)y, mean, rstd, H, T_, D, p.ntile, p.rows);                                               \
-    else                                                                                                              \
-      hipLaunchKernelGGL((norm_fwd_kernel<T, L_, NV_, false>), grid, dim3(kNormThreads), 0, s, (const T*)x, w, b,     \
-                         eps, (T*)y, mean, rstd, H, T_, D, p.ntile, p.rows);                                          \
+  if constexpr (norm_used(L_, NV_, Wide<T>::E)) {                                                                     \
+    if (n.L == L_ && n.NV == NV_) {                                                                                   \
+      if (tail)                                                                                                       \
+        hipLaunchKernelGGL((norm_fwd_kernel<T, L_, NV_, true>), grid, dim3(kNormThreads), 0, s, (const T*)x, w, b,    \
+                           eps, (T*)y, mean, rstd, H, T_, D, p.ntile, p.rows);                                        \
+      else                                                                                                            \
+        hipLaunchKernelGGL((norm_fwd_kernel<T, L_, NV_, false>), grid, dim3(kNormThreads), 0, s, (const T*)x, w, b,   \
+                           eps, (T*)y, mean, rstd, H, T_, D, p.ntile, p.rows);                                        \
+      return hipGetLastError();                                                                                       \
+    }                                                                                                                 \
   }
   KDA_NORM_SHAPES(KDA_NORM)
 #undef KDA_NORM
-  return hipGetLastError();
+  return hipErrorInvalidValue;                     // (not reached)
 }
 
 // Partial sums of the workgroups, then those of the reduction's steps one behind the other.
@@ -539,21 +547,31 @@ static hipError_t norm_bwd(const void* x, const uint8_t* xs, const float* w, con
   const T* xt = PK ? nullptr : (const T*)x;
   const uint8_t* xc = PK ? (const uint8_t*)x : nullptr;
   const bool tail = D % Wide<T>::E != 0;
-  if (n.NV == 0)
+  if (n.NV == 0) {
     hipLaunchKernelGGL((norm_bwd_any_kernel<T, PK>), grid, dim3(kNormThreads), 0, s, xt, xc, xs, w, mean, rstd,
                        (const T*)dy, (T*)dx, part, H, T_, D, grp, p.ntile, p.rows);
+    return hipGetLastError();
+  }
 #define KDA_NORM(L_, NV_)                                                                                              \
   if (n.L == L_ && n.NV == NV_) {                                                                                      \
-    if (tail)                                                                                                          \
-      hipLaunchKernelGGL((norm_bwd_kernel<T, L_, NV_, true, PK>), grid, dim3(kNormThreads), 0, s, xt, xc, xs, w, mean, \
-                         rstd, (const T*)dy, (T*)dx, part, H, T_, D, grp, p.ntile, p.rows);                            \
-    else                                                                                                               \
-      hipLaunchKernelGGL((norm_bwd_kernel<T, L_, NV_, false, PK>), grid, dim3(kNormThreads), 0, s, xt, xc, xs, w,      \
-                         mean, rstd, (const T*)dy, (T*)dx, part, H, T_, D, grp, p.ntile, p.rows);                      \
+    if constexpr (norm_used(L_, NV_, Wide<T>::E, true, PK)) {                                                          \
+      if (tail) {                                                                                                      \
+        hipLaunchKernelGGL((norm_bwd_kernel<T, L_, NV_, true, PK>), grid, dim3(kNormThreads), 0, s, xt, xc, xs, w,     \
+                           mean, rstd, (const T*)dy, (T*)dx, part, H, T_, D, grp, p.ntile, p.rows);                    \
+        return hipGetLastError();                                                                                      \
+      }                                                                                                                \
+    }                                                                                                                  \
+    if constexpr (norm_used(L_, NV_, Wide<T>::E)) {                                                                    \
+      if (!tail) {                                                                                                     \
+        hipLaunchKernelGGL((norm_bwd_kernel<T, L_, NV_, false, PK>), grid, dim3(kNormThreads), 0, s, xt, xc, xs, w,    \
+                           mean, rstd, (const T*)dy, (T*)dx, part, H, T_, D, grp, p.ntile, p.rows);                    \
+        return hipGetLastError();                                                                                      \
+      }                                                                                                                \
+    }                                                                                                                  \
   }
   KDA_NORM_SHAPES(KDA_NORM)
 #undef KDA_NORM
-  return hipGetLastError();
+  return hipErrorInvalidValue;                     // (not reached)
 }
 
 template <typename T>
