@@ -192,3 +192,110 @@ def test_gradients_along_themselves_against_differences(T, dtype):
         bar = 2.0 ** -8 if dtype == BF and n != "dstate_in" else 2e-5
         say("  %-9s |g| %.6e, slope %.6e, off by %.1e (bar %.1e)" % (n, norm, up - dn, abs(up - dn - norm) / norm, bar))
         assert abs(up - dn - norm) <= bar * norm + 1e-13 * (abs(up) + abs(dn)), n
+
+
+@pytest.mark.parametrize("K,V", [(8, 8), (128, 128)])
+def test_as_many_heads_as_a_call_takes(K, V):
+    """2^20 heads of one and of two tokens, forward, single token and backward: the last head, one in the middle and
+    the first are what they are alone (the plans differ by the number of heads, but not for so few tokens: bit for
+    bit but for the value tiles' width, which changes no sum)."""
+    B, H = 1024, 1024
+    pick = lambda t: torch.stack([t[0, 0], t[511, 700], t[-1, -1]]).unsqueeze(0).contiguous()
+    for T in (1, 2):
+        q, k, v, d_o = (torch.randn(B, H, T, D, device=DEV, dtype=BF) for D in (K, K, V, V))
+        g = torch.full((H,), -0.25, device=DEV)
+        say("heads", B * H, K, V, T)
+        o, S = kda.decay_attn_fwd(q, k, v, g)
+        o1, S1 = kda.decay_attn_fwd(pick(q), pick(k), pick(v), g[:3])
+        assert torch.equal(pick(o), o1) and torch.equal(pick(S), S1)
+        if T == 1:
+            one = [t[:, :, 0].contiguous() for t in (q, k, v)]
+            o = kda.decay_attn_step(*one, g, S)
+            o1 = kda.decay_attn_step(*(pick(t) for t in one), g[:3], S1)
+            assert torch.equal(pick(o), o1) and torch.equal(pick(S), S1)
+        del o, S
+        got = kda.decay_attn_bwd(q, k, v, g, None, d_o)
+        one = kda.decay_attn_bwd(pick(q), pick(k), pick(v), g[:3], None, pick(d_o))
+        for n in got:
+            assert torch.equal(pick(got[n]), one[n]), n
+        del got
+
+
+def test_norm_of_as_many_heads_as_a_call_takes():
+    """2^20 heads, 2^28 weights: dw and db of a head with one row are its terms themselves."""
+    B, H, T, D = 1, 2 ** 20, 1, 256
+    x, dy = (torch.randn(B, H, T, D, device=DEV, dtype=BF) for _ in range(2))
+    w = torch.randn(H, D, device=DEV)
+    y, mean, rstd = kda.layer_norm_fwd(x, w)
+    dx, dw, db = kda.layer_norm_bwd(x, w, mean, rstd, dy)
+    xh = (x.float() - mean.unsqueeze(-1)) * rstd.unsqueeze(-1)
+    assert torch.equal(db, dy[0, :, 0].float())
+    assert torch.allclose(dw, (dy.float() * xh)[0, :, 0], rtol=2.0 ** -22, atol=0)       # three roundings
+    last = lambda t: t[:, -1:].contiguous()
+    y1, m1, r1 = kda.layer_norm_fwd(last(x), w[-1:])
+    assert torch.equal(last(y), y1) and torch.equal(last(mean), m1) and torch.equal(last(rstd), r1)
+    dx1, dw1, db1 = kda.layer_norm_bwd(last(x), w[-1:], m1, r1, last(dy))
+    assert torch.equal(last(dx), dx1) and torch.equal(dw[-1:], dw1) and torch.equal(db[-1:], db1)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("T", [70, 2100])
+def test_one_tensor_for_several_inputs(T, dtype):
+    """The same tensor as q, k, v and d_o, the same state as start and as cotangent: what copies of it give."""
+    x = torch.randn(1, 2, T, 64, device=DEV).to(dtype)
+    S = torch.randn(1, 2, 64, 64, device=DEV)
+    g = torch.tensor([-0.2, -0.01], device=DEV)
+    c = [x.clone() for _ in range(4)]
+    for a, b in zip(kda.decay_attn_fwd(x, x, x, g, S), kda.decay_attn_fwd(*c[:3], g, S.clone())):
+        assert torch.equal(a, b)
+    a = kda.decay_attn_bwd(x, x, x, g, S, x, S)
+    b = kda.decay_attn_bwd(*c[:3], g, S.clone(), c[3], S.clone())
+    for n in a:
+        assert torch.equal(a[n], b[n]), n
+    p = kda.ckpt_pack(x)
+    a, b = kda.decay_attn_bwd(p, p, p, g, S, x, S), kda.decay_attn_bwd(*(kda.ckpt_pack(t) for t in c[:3]), g, S, x, S)
+    for n in a:
+        assert torch.equal(a[n], b[n]), n
+    y, mean, rstd = kda.layer_norm_fwd(x)
+    for a, b in zip(kda.layer_norm_bwd(x, None, mean, rstd, x), kda.layer_norm_bwd(x, None, mean, rstd, c[0])):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("T", [200, 2200])
+def test_non_finite_tokens_reach_their_block_and_what_depends_on_them(T, dtype):
+    """A non-finite token in one head: outputs of earlier blocks of 64 tokens (in a backward pass the gradients that
+    flow the other way: later ones) and the other head are those of the clean call, bit for bit."""
+    B, H, D, t = 1, 2, 64, 130
+    d = {n: torch.randn(B, H, T, D, device=DEV).to(dtype) for n in ("q", "k", "v", "d_o")}
+    S, dS = (torch.randn(B, H, D, D, device=DEV) for _ in range(2))
+    g = torch.tensor([-0.05, -0.2], device=DEV)
+    fwd = lambda a: kda.decay_attn_fwd(a["q"], a["k"], a["v"], g, S)
+    bwd = lambda a: kda.decay_attn_bwd(a["q"], a["k"], a["v"], g, S, a["d_o"], dS)
+    o, E = fwd(d)
+    r = bwd(d)
+    for name, bad in (("q", float("nan")), ("k", float("inf")), ("v", float("nan")), ("d_o", -float("inf"))):
+        a = dict(d, **{name: d[name].clone()})
+        a[name][0, 0, t] = bad
+        o2, E2 = fwd(a)
+        assert torch.equal(o2[0, 1], o[0, 1]) and torch.equal(E2[0, 1], E[0, 1])
+        assert torch.equal(o2[0, 0, :128], o[0, 0, :128])
+        if name == "q":                                           # read by its own token only
+            assert torch.equal(o2[0, 0, 192:], o[0, 0, 192:]) and torch.equal(E2, E)
+            assert torch.isnan(o2[0, 0, t]).all()
+        r2 = bwd(a)
+        for n in r:
+            assert torch.equal(r2[n][0, 1], r[n][0, 1]), (name, n)
+        if name in ("k", "v"):                                    # dq of its block and later ones, its own dk or dv
+            assert torch.equal(r2["dq"][0, 0, :128], r["dq"][0, 0, :128])
+            for n in ("dk", "dv"):
+                assert torch.equal(r2[n][0, 0, :128], r[n][0, 0, :128]) and torch.equal(r2[n][0, 0, 192:], r[n][0, 0, 192:])
+            assert torch.equal(r2["dstate_in"], r["dstate_in"])
+        else:                                                     # dk and dv of its block and earlier ones
+            for n in ("dk", "dv"):
+                assert torch.equal(r2[n][0, 0, 192:], r[n][0, 0, 192:])
+            if name == "d_o":
+                assert torch.equal(r2["dq"][0, 0, :128], r["dq"][0, 0, :128])
+                assert torch.equal(r2["dq"][0, 0, 192:], r["dq"][0, 0, 192:])
+            else:
+                assert torch.equal(r2["dq"], r["dq"])
