@@ -4,7 +4,7 @@
 // the one rounding is that to e4m3 (nearest even).  Infinities and NaN become NaN (e4m3 has no
 // infinity) and do not move their group's scale.  Bound by memory: one read, one write; 8 channels per thread
 // (16 bytes of bf16, 8 of codes), a group's maximum taken among its lanes.  2 x 32 x 8192 rows of 128, bf16: pack
-// 38 us (5.4 TB/s), unpack 30 us (6.8 TB/s, two thirds of it writes).
+// 39 us (5.3 TB/s), unpack 30 us (6.8 TB/s, two thirds of it writes); fp32, both 154 us (4.4 TB/s).
 #include "kda_decay_attn.h"
 #include "kda_launch.h"
 

@@ -15,11 +15,11 @@
 // scores K Q^T come out of the matrix unit in the layout in which the product with V takes them, so
 // the scores never touch LDS.  The roles overlap on every SIMD and meet at one barrier per chunk.
 //
-// What bounds it: 4 x 32 heads of 16384 tokens, K = V = 128, bf16: 446 us for 2.16 GB, 4.85 TB/s, the rate of a large
-// copy.  Shorter ones: the chain of a chunk in two in-order waves per SIMD, 1.05 us per 64 tokens at K = V = 64 (with
+// What bounds it: 4 x 32 heads of 16384 tokens, K = V = 128, bf16: 446 to 458 us for 2.16 GB, 4.7 to 4.85 TB/s, the rate
+// of a large copy, at a socket power of 1395 W and clocks held at 1.65 GHz.  Shorter ones: the chain of a chunk in two in-order waves per SIMD, 1.05 us per 64 tokens at K = V = 64 (with
 // only the output or only the state waves at work 0.87 and 0.84) and 1.4 us at 128, where the matrix unit's share is
-// 0.45 and the LDS is busy for a third.  fp32 (1 x 16 heads of 8191, K = V = 128, backward, 430 us) has the matrix unit
-// busy for 69 % of the cycles.
+// 0.45 and the LDS is busy for a third.  fp32 (1 x 16 heads of 8191, K = V = 128, backward, 425 us) has the matrix unit
+// busy for 71 % of the walk's cycles.
 #pragma once
 
 #include <type_traits>
@@ -546,8 +546,8 @@ template <typename T, int KD, int VT, int C, int NK, int NV, bool REV> struct St
 // rounding.  The end state is returned in fp32, where they would show (2.8e-6 of the state), but only from chunks
 // that the decay to the end leaves something of: a chunk counts as fine, three parts (2^-26), while
 // a^{tokens behind it} is over 2^-10, and none does where no end state is returned.  At 4 x 32 heads of 16384
-// tokens, K = V = 128, slopes 1/2 to 1/512, all chunks fine take 500 us, by this rule 455 (the GPU runs these
-// walks at its power limit, so time follows the matrix work).
+// tokens, K = V = 128, log decays of -0.8 to -0.002, all chunks fine take 500 us, by this rule 459 (the GPU runs this
+// walk at its power limit, see above, so time follows the matrix work).
 __device__ __forceinline__ bool fine_state(bool returned, float g2, int behind) {
   return returned && !(g2 * (float)behind <= -10.0f);                  // (also for -inf times 0)
 }
@@ -570,8 +570,9 @@ template <typename T, int KD, int VT> struct WalkShape {
   static constexpr int NO = VT / 16 / NVP;                            // value tiles of an output wave
   typedef StateShape<KD, VT, 4> S;
   static_assert(NO >= L::NACC, "tile too small for the waves");
-  // waves per SIMD that the registers are cut to, none of which may spill (a spilled operand would wait for
-  // memory in every chunk): one workgroup of 8 waves per CU for the widest keys, two for narrower ones.
+  // waves per SIMD that the registers are cut to, none of which may spill to memory (a spilled operand would be
+  // waited for in every chunk): one workgroup of 8 waves per CU for the widest keys, two for narrower ones (of
+  // fp32 tiles of 64 x 64, 90 KB, the LDS holds one).
   static constexpr int EU = KD == 128 ? 2 : 4;
   static constexpr int kK = Tile<T, C, KD>::ELEMS, kV = Tile<T, C, VT>::ELEMS, kS = VT * (KD + L::PAD);
   static constexpr int kC = 2 * kK + kV;                              // a chunk's k, v and q
@@ -877,7 +878,7 @@ __global__ void __launch_bounds__(kWalkThreads, (BwdShape<T, KD, VD, PACK, VT>::
 }
 
 // Chunks in LDS (four or five give the same: it is the state's arithmetic, 1.1 to 1.5 us per chunk, that takes the
-// time, 1 x 4 heads of 30011 tokens in 32 segments, K = V = 128, bf16: 23 us; so do tiles of 32 columns).
+// time, 1 x 4 heads of 30011 tokens in 32 segments, K = V = 128, bf16: 22 us; so do tiles of 32 columns).
 constexpr int kSegChunks = 3;
 
 // Local end state of one segment (not the last in walking order) for one value tile.
@@ -966,9 +967,9 @@ __global__ void __launch_bounds__((64 * seg_waves<KD, VT>())) decay_segment_kern
 // ------------------------------------------------------------------ launchers
 // Instances by key and value widths padded to 32, 64 or 128.  Value tiles are 64 columns wide; 32 for widths up
 // to 32, and where even those leave every workgroup a CU of its own: then a chunk's time is all that counts, and it
-// has half of the products with the state.  (K = V = 128, bf16, 900 tokens, backward: 20 heads 24.4 us in 32
-// columns, 30.0 in 64; 24 heads, which pass one round, 39.5 and 30.1; forward 1 x 8 heads 18.5 and 25.6.  fp32,
-// 400 tokens, backward: 16 heads 38 and 52, 24 heads 69 and 52.)
+// has half of the products with the state.  (K = V = 128, bf16, 900 tokens, backward: 21 heads 23.6 us in 32
+// columns, 30.0 in 64; 22 heads, which pass one round, 38.6 and 30.1; forward 1 x 8 heads 18.4 and 24.5, 64 heads 21.5
+// and 26.1, 65 heads 36.2 and 26.0.  fp32, 400 tokens, backward: 21 heads 35.9 and 50.3, 22 heads 65.7 and 50.5.)
 constexpr int kNarrowFill = 256;                 // CUs
 template <typename T, int KD> hipError_t launch_walk_fwd(const WalkArgs& a, hipStream_t s) {
   if (a.V <= 32 || 2 * walk_blocks(a, 64) <= kNarrowFill)

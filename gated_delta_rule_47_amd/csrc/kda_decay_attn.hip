@@ -22,16 +22,23 @@ KDA_DECAY_EXTERN(bf16_t, 128)
 // states) and two more launches.  The number of segments comes from a model in times of one chunk: workgroups
 // run in rounds of one per CU; a round costs its chunks and a fixed part, a chunk of the pass over the state
 // alone a share of a full one, the join and the launches a constant.  Measured, bf16, model in brackets:
-// 1 x 4 heads of 30011 tokens, K = V = 128, forward: 24, 32, 40 segments 59, 54, 71 us (56, 48, 72); 2 x 16 heads of
-// 8192: 1, 2, 3, 4 segments 152, 145, 108, 91 us (133, 126, 93, 75); backward, 8 x 8 heads of 4096, K = V = 64:
-// 1, 2, 4 segments 79, 99, 90 us (69, 112, 106).  Four chunks at least in a segment, none in sequences of under 16.
-// Of two plans within 5 % the one with more segments (a batch of unequal lengths spreads better).
+// 1 x 4 heads of 30011 tokens, K = V = 128, forward: 24, 32, 40 segments 62, 56, 73 us (56, 48, 72); 2 x 16 heads of
+// 8192: 1, 2, 3, 4 segments 120, 130, 107, 96 us (133, 126, 93, 75); backward, 8 x 8 heads of 4096, K = V = 64:
+// 1, 2, 4 segments 65, 93, 91 us (69, 112, 106).  Four chunks at least in a segment, none in sequences of under 16.
+// Of two plans within 5 % the one with more segments (a batch of unequal lengths spreads better).  fp32, 1 x 16 heads
+// of 8191, K = V = 128: forward 1, 4, 8, 16 segments 573, 245, 165, 169 us, backward 1, 5, 8, 10 segments 576, 441, 424,
+// 468.  The model counts one workgroup per CU also where a CU holds two (bf16, widths up to 64): 8 x 8 heads of 4096,
+// K = V = 64, forward, 1, 2, 4, 8, 16 segments: 50, 59, 44, 44, 52 us, with lengths spread from 0 to 4096 49, 60, 41,
+// 38, 43; it takes 4.
 //
 // A backward pass whose walks of dq and dk fill the chip once, and which with dv's would need half of a second
 // round, gives dv's walk a launch of its own in two segments: dk's walk passes the state that the second
-// one starts from, so that costs no pass over the state (2 x 32 heads of 8192, K = V = 128, bf16: 350 us; all
-// three in one launch 395, in two segments 434).  Narrow heads, of which a CU holds two, gain nothing by that
-// (4 x 32 heads of 4096, K = V = 64: 137 and 140 us).
+// one starts from, so that costs no pass over the state.  2 x 32 heads of 8192, K = V = 128, bf16: 381 us, all
+// three in one launch 405, in two segments 457; from 8 bits 399, 453, 475; fp32, 1 x 43 heads of 4096: 635, 825, 734 (four
+// segments 676).  Heads of up to 64 in both widths are left alone: bf16, of which a CU holds two, gains nothing by
+// it (4 x 32 heads of 4096, K = V = 64: 135 and 137 us); fp32 would (483 and 417).  Where keys are narrow and values
+// wide dv's two segments pass one round themselves, which the rule does not see: fp32, 65 heads of 4096, K = 8, V = 128
+// take 449 us by it, in one launch 309.
 DecayPlan decay_plan(int B, int H, int T, int K, int V, bool bf16, bool bwd) {
   const int C = bf16 ? 64 : 32;
   const int nchunks = (T + C - 1) / C;
@@ -225,7 +232,8 @@ hipError_t launch_decay_bwd(const void* q, const void* k, const void* v, const u
 // the first is used; the RG partial sums of a column meet in LDS.  VS columns per workgroup.  The decay is taken
 // as hi + lo: rounded to fp32 it would be off to the same side in every call of a long answer (1e-4 of the state
 // after 4096 of them).
-// bf16, K = V = 128: 192 x 32 heads 156 us (5.2 TB/s), 4 x 32 heads 4.5 us, where a launch alone takes as long.
+// bf16, K = V = 128: 192 x 32 heads 157 to 162 us (5.0 to 5.2 TB/s; fp32 161), 4 x 32 heads 4.6 us, where a launch alone
+// takes as long.
 template <typename T, int VS>
 __global__ void __launch_bounds__(256) decay_step_kernel(const T* __restrict__ q, const T* __restrict__ k,
                                                          const T* __restrict__ v,
