@@ -24,7 +24,10 @@ __all__ = ["KdaError", "read_scale", "gate", "chunk_fwd", "chunk_fwd_scalar", "c
            "GATE_BWD_SCRATCH_BYTES", "counters", "status_string",
            "library_path", "decay_attn_workspace_bytes", "decay_attn_fwd", "decay_attn_step",
            "decay_attn_bwd_workspace_bytes", "decay_attn_bwd", "layer_norm_fwd", "layer_norm_bwd_workspace_bytes",
-           "layer_norm_bwd", "ckpt_pack", "ckpt_unpack"]
+           "layer_norm_bwd", "ckpt_pack", "ckpt_unpack", "short_conv_fwd", "short_conv_step",
+           "short_conv_bwd_workspace_bytes", "short_conv_bwd", "qk_norm_rope_fwd", "qk_norm_rope_bwd_workspace_bytes",
+           "qk_norm_rope_bwd", "rope_frequencies", "GATED_SCAN_CHUNK", "gated_scan_workspace_bytes", "gated_scan_fwd",
+           "gated_scan_step", "gated_scan_bwd_workspace_bytes", "gated_scan_bwd"]
 
 
 class KdaError(RuntimeError):
@@ -365,3 +368,7 @@ def gate_bwd_noalloc(z, A_log, dt_bias, dg, dz_out=None, dA_out=None, ddb_out=No
 from .layer_ops import (ckpt_pack, ckpt_unpack, decay_attn_bwd, decay_attn_bwd_workspace_bytes,  # noqa: E402
                         decay_attn_fwd, decay_attn_step, decay_attn_workspace_bytes, layer_norm_bwd,
                         layer_norm_bwd_workspace_bytes, layer_norm_fwd)
+from .sequence_ops import (GATED_SCAN_CHUNK, gated_scan_bwd, gated_scan_bwd_workspace_bytes,  # noqa: E402
+                           gated_scan_fwd, gated_scan_step, gated_scan_workspace_bytes, qk_norm_rope_bwd,
+                           qk_norm_rope_bwd_workspace_bytes, qk_norm_rope_fwd, rope_frequencies, short_conv_bwd,
+                           short_conv_bwd_workspace_bytes, short_conv_fwd, short_conv_step)

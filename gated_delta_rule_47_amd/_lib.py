@@ -18,6 +18,10 @@ EXPORTED = ("kda_read_scale", "kda_gate", "kda_chunk_fwd_workspace_bytes", "kda_
             "kda_decay_attn_workspace_bytes", "kda_decay_attn_fwd", "kda_decay_attn_step",
             "kda_decay_attn_bwd_workspace_bytes", "kda_decay_attn_bwd", "kda_layer_norm_fwd",
             "kda_layer_norm_bwd_workspace_bytes", "kda_layer_norm_bwd", "kda_ckpt_pack", "kda_ckpt_unpack",
+            "kda_short_conv_fwd", "kda_short_conv_step", "kda_short_conv_bwd_workspace_bytes", "kda_short_conv_bwd",
+            "kda_qk_norm_rope_fwd", "kda_qk_norm_rope_bwd_workspace_bytes", "kda_qk_norm_rope_bwd", "kda_rope_frequencies",
+            "kda_gated_scan_workspace_bytes", "kda_gated_scan_fwd", "kda_gated_scan_step",
+            "kda_gated_scan_bwd_workspace_bytes", "kda_gated_scan_bwd",
             "kda_status_string", "kda_get_counters")
 
 _lib = None
@@ -27,6 +31,7 @@ _i = ctypes.c_int
 _f = ctypes.c_float
 _sz = ctypes.c_size_t
 _ll = ctypes.c_longlong
+_d = ctypes.c_double
 
 _PROTOS = {
     "kda_read_scale": (_f, [_i]),
@@ -59,6 +64,23 @@ _PROTOS = {
     "kda_layer_norm_bwd": (_i, [_p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _sz, _i, _i, _i, _i, _i, _p]),
     "kda_ckpt_pack": (_i, [_p, _p, _p, _ll, _i, _i, _p]),
     "kda_ckpt_unpack": (_i, [_p, _p, _p, _ll, _i, _i, _p]),
+    "kda_short_conv_fwd": (_i, [_p, _ll, _ll, _p, _p, _p, _p, _i, _p, _p, _i, _i, _i, _i, _i, _i, _p]),
+    "kda_short_conv_step": (_i, [_p, _ll, _p, _p, _i, _p, _p, _i, _i, _i, _i, _i, _p]),
+    "kda_short_conv_bwd_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i]),
+    "kda_short_conv_bwd": (_i, [_p, _ll, _ll, _p, _p, _p, _p, _i, _p, _p, _p, _ll, _ll, _p, _p, _p, _p, _sz,
+                                _i, _i, _i, _i, _i, _i, _p]),
+    "kda_qk_norm_rope_fwd": (_i, [_p, _ll, _ll, _ll, _p, _ll, _ll, _ll, _p, _i, _p, _i, _i, _f, _p, _p, _f, _i, _p, _p,
+                                  _i, _i, _i, _i, _i, _i, _i, _p]),
+    "kda_qk_norm_rope_bwd_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
+    "kda_qk_norm_rope_bwd": (_i, [_p, _ll, _ll, _ll, _p, _ll, _ll, _ll, _p, _i, _p, _i, _i, _f, _p, _p, _f, _i, _p, _p,
+                                  _p, _ll, _ll, _ll, _p, _ll, _ll, _ll, _p, _p, _p, _sz, _i, _i, _i, _i, _i, _i, _i, _p]),
+    "kda_rope_frequencies": (_i, [ctypes.POINTER(_d), ctypes.POINTER(_d), _i, _d, _i, _d, _d, _d, _d]),
+    "kda_gated_scan_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
+    "kda_gated_scan_fwd": (_i, [_p, _p, _p, _p, _p, _p, _p, _i, _p, _p, _p, _p, _sz, _i, _i, _i, _i, _i, _p]),
+    "kda_gated_scan_step": (_i, [_p, _p, _p, _p, _p, _i, _p, _p, _i, _i, _i, _i, _p]),
+    "kda_gated_scan_bwd_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
+    "kda_gated_scan_bwd": (_i, [_p, _p, _p, _p, _p, _p, _i, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _sz,
+                                _i, _i, _i, _i, _i, _p]),
     "kda_status_string": (ctypes.c_char_p, [_i]),
     "kda_get_counters": (_i, [ctypes.POINTER(ctypes.c_ulonglong), _i]),
 }

@@ -117,6 +117,56 @@ template <typename T>
 hipError_t launch_ckpt_unpack(const uint8_t* codes, const uint8_t* scales, void* x, long long rows, int D,
                               hipStream_t s);
 
+// Short causal convolution (kda_short_conv.hip): x (B, T, C = H D) at strides xb, xt; y, dy (B, H, T, D).
+template <typename T>
+hipError_t launch_conv_fwd(const void* x, long long xb, long long xt, const float* w, const float* bias,
+                           const int* lengths, const void* state_in, int silu, void* y, void* state_out, int B, int H,
+                           int T_, int D, int W, hipStream_t s);
+template <typename T>
+hipError_t launch_conv_step(const void* x, long long xb, const float* w, const float* bias, int silu, void* state,
+                            void* y, int B, int C, int W, hipStream_t s);
+size_t conv_bwd_workspace_bytes(int B, int H, int T, int D, int W, bool bf16);
+template <typename T>
+hipError_t launch_conv_bwd(const void* x, long long xb, long long xt, const float* w, const float* bias,
+                           const int* lengths, const void* state_in, int silu, const void* dy, const float* d_state,
+                           void* dx, long long dxb, long long dxt, float* dw, float* db, float* d_state_in,
+                           void* workspace, int B, int H, int T_, int D, int W, hipStream_t s);
+
+// Norm of queries and keys with their rotation (kda_qk_rope.hip): [0] the queries, [1] the keys (H = 0: none).
+struct QkSideDesc {
+  const void* x;
+  long long xb, xt, xh;        // strides of the batch, the token and the head, in elements
+  const float* w;              // (Hw, D) or null; per_head: Hw = H, not one row for all heads
+  int H, per_head;
+  void* y;                     // forward: out; backward: the cotangent
+  void* dx;
+  long long db, dt, dh;
+};
+template <typename T>
+hipError_t launch_qk_fwd(const QkSideDesc* d, const double* freqs, const int* positions, int norm, float eps,
+                         float rope_scale, int interleaved, int B, int T_, int D, int R, hipStream_t s);
+size_t qk_bwd_workspace_bytes(int B, int T, int Hq, int Hk, int D, int q_per_head, int k_per_head);
+template <typename T>
+hipError_t launch_qk_bwd(const QkSideDesc* d, const double* freqs, const int* positions, int norm, float eps,
+                         float rope_scale, int interleaved, float* dwq, float* dwk, void* workspace, int B, int T_,
+                         int D, int R, hipStream_t s);
+
+// Gated linear recurrence (kda_gated_scan.hip); i null: no input gate; ckpt null: not kept.
+size_t scan_workspace_bytes(int B, int H, int T, int D, bool bf16);
+size_t scan_bwd_workspace_bytes(int B, int H, int T, int D, bool bf16);
+template <typename T>
+hipError_t launch_scan_fwd(const void* x, const void* z, const float* A_log, const float* dt_bias, const void* i,
+                           const int* lengths, const float* state_in, int normalize, void* y, float* state_out,
+                           float* ckpt, void* workspace, int B, int H, int T_, int D, hipStream_t s);
+template <typename T>
+hipError_t launch_scan_step(const void* x, const void* z, const float* A_log, const float* dt_bias, const void* i,
+                            int normalize, float* state, void* y, int B, int H, int D, hipStream_t s);
+template <typename T>
+hipError_t launch_scan_bwd(const void* x, const void* z, const float* A_log, const float* dt_bias, const void* i,
+                           const int* lengths, int normalize, const float* ckpt, const void* dy, const float* d_state,
+                           void* dx, void* dz, void* di, float* dA_log, float* d_dt_bias, float* d_state_in,
+                           void* workspace, int B, int H, int T_, int D, hipStream_t s);
+
 // Counters of kda_api.hip: a rejected call (returns its status), an accepted one.
 int reject(int status);
 void count_call(int counter);

@@ -17,6 +17,7 @@
 
 #include "kda_decay_attn.h"
 #include "kda_launch.h"
+#include "kda_vec.h"
 
 namespace kda {
 
@@ -24,23 +25,8 @@ constexpr int kNormThreads = 256;
 
 // Sum over the L lanes of a row: a power of two up to 64, or the whole workgroup (whose four waves add
 // in a fixed order through `red`); every lane of the row gets it.
-// Lanes exchange within the register file (DPP within 16 lanes, lane swaps beyond), not through LDS.
-template <int CTRL> __device__ __forceinline__ float dpp(float x) {
-  return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(x), CTRL, 0xf, 0xf, true));
-}
 template <int L> __device__ __forceinline__ float row_sum(float x, float* red) {
-  if constexpr (L >= 2) x += dpp<0xB1>(x);       // lane ^ 1
-  if constexpr (L >= 4) x += dpp<0x4E>(x);       // lane ^ 2
-  if constexpr (L >= 8) x += dpp<0x141>(x);      // mirrored in 8: the other four's sum
-  if constexpr (L >= 16) x += dpp<0x140>(x);     // mirrored in 16: the other eight's
-  if constexpr (L >= 32) {
-    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
-  }
-  if constexpr (L >= 64) {
-    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
-  }
+  x = lane_sum<(L < 64 ? L : 64)>(x);
   if constexpr (L > 64) {
     static_assert(L == kNormThreads, "rows of a wave or of the workgroup");
     __syncthreads();
@@ -55,9 +41,6 @@ template <int L> __device__ __forceinline__ float row_sum(float x, float* red) {
 // 16-byte access at any address.  n < E: the last vector of a row, whose elements are taken one by one.
 template <typename T> struct Wide {
   static constexpr int E = 16 / (int)sizeof(T);
-};
-template <int N, int A> struct __attribute__((packed, aligned(A))) Words {
-  uint32_t u[N];
 };
 template <typename T> struct Raw {                // as loaded
   static constexpr int E = Wide<T>::E;

@@ -389,13 +389,172 @@ int kda_ckpt_pack(const void* x, unsigned char* codes, unsigned char* scales, lo
 int kda_ckpt_unpack(const unsigned char* codes, const unsigned char* scales, void* x, long long rows, int D,
                     int dtype, void* stream);
 
+/* ---------------------------------------------------------------------------------
+ * Short causal depthwise convolution of a projection, as the queries, keys and values of a linear-attention layer
+ * and the input of a recurrent block pass through one:
+ *   pre[b,t,c] = bias[c] + sum_j weight[c][j] x[b, t - W + 1 + j, c]     (j = 0 .. W - 1),   y = act(pre)
+ * C = H * D channels; x is a projection, token by token, and y is written head by head.
+ *   x         (B,T,C) in `dtype`, channels next to each other; x_batch and x_token are the strides of the batch and of the
+ *             token in elements (>= 0; T * C and C for a contiguous tensor, the row length of a wider projection otherwise)
+ *   weight    (C,W) f32;  bias (C) f32 or NULL (= 0);  act: KDA_ACT_NONE or KDA_ACT_SILU
+ *   lengths   (B) int32 on the device, or NULL: sequence b ends before token lengths[b], clamped to 0..T.  Tokens behind it
+ *             are not read, their rows of y stay as they were, their rows of dx become zero.
+ *   state     (B,W-1,C) in `dtype`: the W - 1 inputs before the first token, oldest first; state_out holds those before
+ *             the sequence's end.  The state's gradient is f32 of the same shape.
+ *   D a multiple of 8;  W in {2, 3, 4};  B, H >= 1;  T <= 2^28;  B, C <= 2^20;  B * C <= 2^31;  every row within 2^48 elements
+ *             (KDA_ERR_SHAPE otherwise).  Pointers need the alignment of an element only.
+ * Sums in fp32, one rounding to `dtype`. */
+typedef enum { KDA_ACT_NONE = 0, KDA_ACT_SILU = 1 } kda_act;
+
+/* y (B,H,T,D) in `dtype`; state_in NULL = zeros; state_out NULL = not written.  y and state_out must not overlap an input
+ * or each other (state_out is not state_in: another workgroup reads it). */
+int kda_short_conv_fwd(const void* x, long long x_batch, long long x_token, const float* weight, const float* bias,
+                       const int* lengths, const void* state_in, int act, void* y, void* state_out,
+                       int B, int H, int T, int D, int W, int dtype, void* stream);
+
+/* One token: x (B,C) with x_batch between sequences, y (B,C), state updated in place. */
+int kda_short_conv_step(const void* x, long long x_batch, const float* weight, const float* bias, int act, void* state,
+                        void* y, int B, int H, int D, int W, int dtype, void* stream);
+
+/* Bytes of device workspace kda_short_conv_bwd needs when dweight or dbias is asked for (0 on bad sizes). */
+size_t kda_short_conv_bwd_workspace_bytes(int B, int H, int T, int D, int W, int dtype);
+
+/* Adjoint of kda_short_conv_fwd for L = sum(y * dy) + sum(state_out * d_state_out).
+ *   dy (B,H,T,D) in `dtype`;  d_state_out (B,W-1,C) f32 or NULL (= 0)
+ *   dx (B,T,C) in `dtype` at strides dx_batch and dx_token, whose rows must not overlap (KDA_ERR_SHAPE);
+ *   d_state_in (B,W-1,C) f32;  dweight (C,W), dbias (C) f32, NULL = not computed (their sums run in a fixed order)
+ *   workspace 16-byte aligned, contents on entry ignored; NULL when neither sum is asked for.
+ * No output may overlap an input, another output or the workspace; dx may lie between the rows of x or of another
+ * tensor (a slice of a wider projection's gradient). */
+int kda_short_conv_bwd(const void* x, long long x_batch, long long x_token, const float* weight, const float* bias,
+                       const int* lengths, const void* state_in, int act, const void* dy, const float* d_state_out,
+                       void* dx, long long dx_batch, long long dx_token, float* dweight, float* dbias, float* d_state_in,
+                       void* workspace, size_t workspace_bytes,
+                       int B, int H, int T, int D, int W, int dtype, void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * Norm of every head's query and key with the rotation by the token's position in the same pass.  Per head and row:
+ *   r = (mean(x^2) + eps)^-1/2 (KDA_QK_RMS), (sum(x^2) + eps)^-1/2 (KDA_QK_L2) or 1 (KDA_QK_NONE: positions alone)
+ *   y = Rot(x * r * weight)
+ * Rot turns pair p < R / 2 of the first R channels by the angle position * freqs[p] and multiplies it by rope_scale:
+ * (u, v) -> rope_scale (u cos - v sin, v cos + u sin).  A pair is channels p and p + R / 2, or 2 p and 2 p + 1 when
+ * `interleaved`; the other D - R channels keep their values.
+ *   q (B,T,Hq,D), k (B,T,Hk,D) in `dtype`, channels next to each other; *_batch, *_token, *_head are strides in
+ *             elements (>= 0), as slices of a fused projection have them.  Hq or Hk may be 0 (that side is then not
+ *             looked at).
+ *   q_weight, k_weight (Hqw,D), (Hkw,D) f32, NULL = ones; Hqw, Hkw: 1 (a row for all heads) or the number of heads.
+ *             KDA_QK_NONE takes none (KDA_ERR_SHAPE).
+ *   freqs     (R / 2) float64 on the device, radians per token (kda_rope_frequencies); not read when R = 0
+ *   positions (B,T) int32, any sign, or NULL (a token's index)
+ *   q_out (B,Hq,T,D), k_out (B,Hk,T,D) in `dtype`
+ *   D a multiple of 8 up to 256;  R a multiple of 8 up to D, or 0;  B >= 1;  T >= 0;  B * T <= 2^30;  Hq, Hk <= 65536, not both
+ *             0;  eps >= 0 and rope_scale finite;  outputs within 2^48 elements (KDA_ERR_SHAPE otherwise).  Pointers need the
+ *             alignment of an element only.
+ * The angle is formed and reduced in float64 (right to 2^-50 of itself), everything else in fp32 with one rounding to
+ * `dtype`.  A row of zeros with eps = 0 gives NaN, as the formula does; a non-finite value reaches its own row only.
+ * Outputs must not overlap inputs or each other. */
+typedef enum { KDA_QK_NONE = 0, KDA_QK_RMS = 1, KDA_QK_L2 = 2 } kda_qk_norm;
+
+int kda_qk_norm_rope_fwd(const void* q, long long q_batch, long long q_token, long long q_head,
+                         const void* k, long long k_batch, long long k_token, long long k_head,
+                         const float* q_weight, int Hqw, const float* k_weight, int Hkw, int norm, float eps,
+                         const double* freqs, const int* positions, float rope_scale, int interleaved,
+                         void* q_out, void* k_out, int B, int T, int Hq, int Hk, int D, int R, int dtype, void* stream);
+
+/* Bytes of device workspace kda_qk_norm_rope_bwd needs when a weight's gradient is asked for (0 on bad sizes). */
+size_t kda_qk_norm_rope_bwd_workspace_bytes(int B, int T, int Hq, int Hqw, int Hk, int Hkw, int D);
+
+/* Adjoint for cotangents d_q (B,Hq,T,D) and d_k (B,Hk,T,D) in `dtype` on the outputs: with p = Rot^T dy and xh = x r,
+ *   dx = r (p w - xh mean(p w xh)) (RMS; the sum in place of the mean for L2; p alone for NONE, where q and k may be NULL)
+ *   dq (B,T,Hq,D), dk (B,T,Hk,D) in `dtype` at the strides dq_* and dk_*, whose rows must not overlap
+ *   dq_weight (Hqw,D), dk_weight (Hkw,D) f32 = sum over rows of p xh, NULL = not computed (fixed order of the sums)
+ *   workspace 16-byte aligned, contents on entry ignored; NULL when neither is asked for.
+ * No output may overlap an input, another output or the workspace; dq and dk may lie between each other's rows (slices of
+ * a fused projection's gradient with the same batch and token strides). */
+int kda_qk_norm_rope_bwd(const void* q, long long q_batch, long long q_token, long long q_head,
+                         const void* k, long long k_batch, long long k_token, long long k_head,
+                         const float* q_weight, int Hqw, const float* k_weight, int Hkw, int norm, float eps,
+                         const double* freqs, const int* positions, float rope_scale, int interleaved,
+                         const void* d_q, const void* d_k,
+                         void* dq, long long dq_batch, long long dq_token, long long dq_head,
+                         void* dk, long long dk_batch, long long dk_token, long long dk_head,
+                         float* dq_weight, float* dk_weight, void* workspace, size_t workspace_bytes,
+                         int B, int T, int Hq, int Hk, int D, int R, int dtype, void* stream);
+
+/* Frequencies of R / 2 pairs and the scale that goes with them, for contexts beyond the trained length.  Host-only: `freqs`
+ * (R / 2) and `rope_scale` are HOST memory.  With f_p = base^(-2 p / R):
+ *   KDA_ROPE_PLAIN   f_p
+ *   KDA_ROPE_LINEAR  f_p / factor (positions squeezed into the trained range)
+ *   KDA_ROPE_BASE    base * factor^(R / (R - 2)) in place of base (the slowest pair slowed by factor, the fastest left; R > 2)
+ *   KDA_ROPE_PARTS   pairs that turn more than fast_turns times over trained_length tokens are left, those below slow_turns are
+ *                    slowed by factor, with a linear share of both between (over the pair's index, from the last whole
+ *                    pair in front to the first behind); rope_scale = 0.1 ln(factor) + 1
+ * rope_scale is 1 otherwise.  R even and > 0, base > 1, factor >= 1, trained_length > 0, fast_turns > slow_turns > 0
+ * (KDA_ERR_SHAPE; the last three only matter to KDA_ROPE_PARTS). */
+typedef enum { KDA_ROPE_PLAIN = 0, KDA_ROPE_LINEAR = 1, KDA_ROPE_BASE = 2, KDA_ROPE_PARTS = 3 } kda_rope_scaling;
+int kda_rope_frequencies(double* freqs, double* rope_scale, int R, double base, int scaling, double factor,
+                         double trained_length, double fast_turns, double slow_turns);
+
+/* ---------------------------------------------------------------------------------
+ * Gated linear recurrence, one state per channel, with the library's decay gate (kda_gate) inside:
+ *   g = -exp(clamp(A_log[h], -10, 20)) * softplus(z + dt_bias[h,:]),  a = exp(g)
+ *   n = sqrt(1 - a^2) when `normalize` (keeps the state's variance), 1 otherwise;  s = sigmoid(input_gate), 1 without one
+ *   h_t = a_t h_{t-1} + n_t s_t x_t,   y_t = h_t
+ *   x, z, input_gate, y, dy, dx, dz, d_input_gate (B,H,T,D) in `dtype`, contiguous (H = 1: rows of a whole layer);
+ *             input_gate may be NULL
+ *   A_log (H) f32;  dt_bias (H,D) f32 or NULL (= 0);  states (B,H,D) f32
+ *   lengths   (B) int32 on the device, or NULL, as above: rows of y behind a sequence stay as they were, the gradients'
+ *             rows there become zero, the final state is the one after the last token.
+ *   B, H, D >= 1;  T >= 0;  T <= 2^28;  B * H * D <= 2^28;  B * H * T * D <= 2^46 (KDA_ERR_SHAPE).  Pointers need the
+ *             alignment of an element only.
+ * Gates, states and sums are fp32; a decay within 1/8 of 1 in the logarithm is held as its distance from 1, so slow decays do
+ * not drift over long sequences.  A non-finite value reaches its own channel only, from its token on. */
+
+/* Tokens between the states that the forward pass keeps for the backward pass. */
+#define KDA_GATED_SCAN_CHUNK 32
+
+/* Bytes of device workspace kda_gated_scan_fwd needs for these sizes (may be 0; 0 on bad sizes). */
+size_t kda_gated_scan_workspace_bytes(int B, int H, int T, int D, int dtype);
+
+/* state_in NULL = 0;  state_out NULL = not written, may equal state_in;
+ * ckpt (B,H,ceil(T / KDA_GATED_SCAN_CHUNK),D) f32: the state in front of every KDA_GATED_SCAN_CHUNK tokens, for the adjoint;
+ *           NULL = not kept.  (Behind a sequence's end: its final state.)
+ * workspace 256-byte aligned, contents on entry ignored; two calls in flight at once must not share one. */
+int kda_gated_scan_fwd(const void* x, const void* z, const float* A_log, const float* dt_bias, const void* input_gate,
+                       const int* lengths, const float* state_in, int normalize, void* y, float* state_out, float* ckpt,
+                       void* workspace, size_t workspace_bytes,
+                       int B, int H, int T, int D, int dtype, void* stream);
+
+/* One token: x, z, input_gate, y (B,H,D); state (B,H,D) f32 updated in place. */
+int kda_gated_scan_step(const void* x, const void* z, const float* A_log, const float* dt_bias, const void* input_gate,
+                        int normalize, float* state, void* y, int B, int H, int D, int dtype, void* stream);
+
+/* Bytes of device workspace kda_gated_scan_bwd needs for these sizes (0 on bad sizes). */
+size_t kda_gated_scan_bwd_workspace_bytes(int B, int H, int T, int D, int dtype);
+
+/* Adjoint of kda_gated_scan_fwd for L = sum(y * dy) + sum(state_out * d_state_out), from the forward's inputs and ckpt.
+ * With r_t = dL/dh_t = dy_t + a_{t+1} r_{t+1}:
+ *   dx = r n s,  d_input_gate = r n x s (1 - s),  dg = r (a h_{t-1} - a^2 / n s x) (the last term with normalize),
+ *   dz = -dg exp(A_log) sigmoid(z + dt_bias)
+ *   dA_log (H) f32 = sum dg g, 0 where A_log lies outside [-10, 20];  d_dt_bias (H,D) f32 = sum over b, t of dz (also when
+ *             dt_bias is NULL); NULL = not computed.  Fixed order of the sums.
+ *   d_state_out (B,H,D) f32 or NULL (= 0);  d_state_in (B,H,D) f32
+ * d_input_gate is written exactly when input_gate is given (both or neither: KDA_ERR_NULL).  Where a decay is exactly 1, n = 0
+ * and the term with a^2 / n counts as its limit in dz, 0. */
+int kda_gated_scan_bwd(const void* x, const void* z, const float* A_log, const float* dt_bias, const void* input_gate,
+                       const int* lengths, int normalize, const float* ckpt, const void* dy, const float* d_state_out,
+                       void* dx, void* dz, void* d_input_gate, float* dA_log, float* d_dt_bias, float* d_state_in,
+                       void* workspace, size_t workspace_bytes,
+                       int B, int H, int T, int D, int dtype, void* stream);
+
 /* Static string for a status code ("ok", "null pointer", ...). Never NULL. */
 const char* kda_status_string(int status);
 
 /* Copies up to n counters into out and returns how many exist (KDA_NUM_COUNTERS).
  * Counters are process-wide and monotonic: calls accepted per entry point (the decay
- * attention counts with the entry point of its kind: forward, step, adjoint; the layer
- * norm and the 8-bit activations are not counted) and calls rejected with an error status (modelled on the page's dispatch counters,
+ * attention and the gated recurrence count with the entry point of their kind: forward, step,
+ * adjoint; the layer norm, the 8-bit activations, the short convolution and the norm with
+ * rotation are not counted) and calls rejected with an error status (modelled on the page's dispatch counters,
  * "The fused KDA adjoint" page, section 6). */
 #define KDA_NUM_COUNTERS 6
 #define KDA_COUNTER_GATE 0
