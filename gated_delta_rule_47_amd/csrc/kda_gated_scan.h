@@ -1,0 +1,196 @@
+// Gated linear recurrence, one state per channel: what the forward, the adjoint and the single token share.
+//
+//   g = -m softplus(z + dt_bias), m = exp(clamp(A_log, -10, 20)),  a = e^g,  n = (1 - a^2)^1/2 or 1,  s = sigmoid(i) or 1
+//   h_t = a_t h_{t-1} + n_t s_t x_t,  y = h
+//   r_t = dL/dh_t = dy_t + a_{t+1} r_{t+1}:  dx = r n s,  di = r n x s (1 - s),
+//   dg = r (a h_{t-1} - a^2 / n s x),  dz = -dg m sigmoid(z + dt_bias),  dA_log = sum dg g,  ddt_bias = sum dz
+//
+// Channels of all heads and sequences stand side by side: 64 lanes of E channels make a channel tile (E = 2 packs a
+// 4-byte access of bf16; odd head sizes and fp32 take 1).  Time is cut into tiles of NW waves of S tokens, one workgroup
+// each.  A wave keeps the decays and inputs of its S tokens in registers, so memory is read once: it folds them to one
+// pair (sum of g, state from zero), the workgroup's waves exchange these through LDS, and the state in front of the tile
+// comes from the tiles before it while the workgroup waits (look_back); then the wave runs over its tokens again from
+// the true state.
+//
+// Tiles hand their states on through the workspace.  Each publishes its own pair as soon as it has it, without
+// waiting for anything, then takes the pairs of the tiles before it back to the nearest one that knows its final state,
+// and publishes its own final state.  Workgroups take tiles by a counter, in time order: whatever a tile waits for
+// belongs to a workgroup that already runs and that publishes without waiting, so every wait ends.  Words are written
+// and read by device-scope atomics (past the XCDs' own L2), each record complete before its flag.
+#pragma once
+
+#include "kda_launch.h"
+#include "kda_vec.h"
+
+namespace kda {
+
+__device__ __forceinline__ float scan_sigmoid(float x) { return fast_rcp(1.0f + fast_exp2(-kLog2e * x)); }
+
+// log2(1 + 2^x2) for every x2 >= 0 or below: with y = 2^-|x2| and u = fl(1 + y), log2(1 + y) = log2(u) + (y - (u - 1)) / u
+// log2(e) + ..., and the correction only matters where u is next to 1 (y itself where u rounds to 1).
+__device__ __forceinline__ float scan_softplus2(float x2, float& y) {
+  y = fast_exp2(-fabsf(x2));
+  const float u = 1.0f + y;
+  return fmaf(y - (u - 1.0f), kLog2e, fast_log2(u)) + fmaxf(x2, 0.f);
+}
+
+// The decay e^g of g = g2 ln 2 <= 0 in one word.  A decay next to 1 rounded to fp32 is off to the same side in every
+// token of a channel whose gate hardly moves, by up to 2^-25 / |g| of the state after the 1 / |g| tokens it remembers.  So a
+// weak one (|g| < 1/8) is held as e = a - 1, with its sign bit set even when it is 0, a strong one as a.
+// e / g2 is a cubic within 3.5e-8 of (2^g2 - 1) / g2 there (interpolated at Chebyshev points).
+__device__ __forceinline__ float decay_word(float g2) {
+  const float e = g2 * fmaf(g2, fmaf(g2, fmaf(g2, 0.009150667116f, 0.05545188114f), 0.2402246296f), 0.6931471825f);
+  return g2 > -0.18033688f ? -fabsf(e) : fast_exp2(g2);
+}
+__device__ __forceinline__ bool decay_weak(float v) { return (int)__float_as_uint(v) < 0; }
+__device__ __forceinline__ float decay_step(float v, float h, float u) { return fmaf(v, h, (decay_weak(v) ? h : 0.f) + u); }   // a h + u
+__device__ __forceinline__ float decay_a(float v) { return decay_weak(v) ? 1.f + v : v; }
+__device__ __forceinline__ float decay_n2(float v) { return decay_weak(v) ? -v * (2.f + v) : fmaf(-v, v, 1.f); }               // 1 - a^2
+constexpr float kNoDecay = -0.0f;
+
+// E elements of a row as loaded, at a byte offset from the tensor's start (32 bits where the tensors are below 4 GiB:
+// one offset then serves every tensor, which stay in scalar registers).
+template <typename T, int E> struct ScanRaw {
+  uint32_t u;
+  static_assert((int)sizeof(T) * E <= 4, "one word");
+  template <typename Off> __device__ __forceinline__ void load(const void* p, Off off) {
+    const char* q = (const char*)p + off;
+    if constexpr (sizeof(T) * E == 4) u = reinterpret_cast<const Words<1, sizeof(T)>*>(q)->u[0];
+    else u = *reinterpret_cast<const uint16_t*>(q);
+  }
+  __device__ __forceinline__ float at(int e) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(u);
+    else return __uint_as_float(e ? u & 0xffff0000u : u << 16);
+  }
+};
+template <typename T, int E, typename Off> __device__ __forceinline__ void scan_store(void* p, Off off, const float (&f)[E]) {
+  char* q = (char*)p + off;
+  if constexpr (sizeof(T) == 4) *reinterpret_cast<float*>(q) = f[0];
+  else if constexpr (E == 2) reinterpret_cast<Words<1, sizeof(T)>*>(q)->u[0] = pack_bf16x2(f[0], f[1]);
+  else *reinterpret_cast<bf16_t*>(q) = f2bf(f[0]);
+}
+
+// What links the tiles of a channel tile: a counter, a flag per tile (0 nothing, 1 its pair, 2 its final state too), the
+// records (64 lanes of E pairs, 64 lanes of E states).
+struct ScanLink {
+  uint32_t *ticket, *flags;
+  float *pairs, *states;
+};
+struct ScanArgs {
+  const void *x, *z, *i;
+  const float *A_log, *dt_bias;
+  const int* lengths;
+  const float* state_in;
+  void* y;
+  float *state_out, *ckpt;
+  const void* dy;                          // backward
+  const float* d_state;
+  void *dx, *dz, *di;
+  float *d_state_in, *parts;               // (2, tiles, B H D): sums of dz, of dg g
+  ScanLink link;
+  int B, H, T, D, normalize, ctiles, tiles;
+};
+
+// A lane's E floats by device-scope accesses.
+template <int E> __device__ __forceinline__ void put_words(float* p, const float (&f)[E]) {
+#pragma unroll
+  for (int e = 0; e < E; ++e) __hip_atomic_store(p + e * 64, f[e], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <int E> __device__ __forceinline__ void get_words(const float* p, float (&f)[E]) {
+#pragma unroll
+  for (int e = 0; e < E; ++e) f[e] = __hip_atomic_load(p + e * 64, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+// The record's stores have reached memory before the flag is written.
+__device__ __forceinline__ void publish(uint32_t* flag, uint32_t value) {
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  if ((threadIdx.x & 63) == 0) __hip_atomic_store(flag, value, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// State in front of tile j > 0 (in the order of the tickets) of the channel tile whose first record is `first`; one wave.
+template <int E> __device__ __forceinline__ void look_back(const ScanLink& l, size_t first, int j, int lane, float (&h)[E]) {
+  float G[E], acc[E];                      // the tiles taken so far: state behind them = acc + e^G state in front
+#pragma unroll
+  for (int e = 0; e < E; ++e) G[e] = acc[e] = 0.f;
+  for (int at = j - 1;;) {                 // the next tile to take; tile 0 always publishes its final state
+    const int p = at - lane;
+    const uint32_t f = p >= 0 ? __hip_atomic_load(l.flags + first + p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0u;
+    const unsigned long long none = ~__ballot(f >= 1u), final = __ballot(f == 2u);
+    const int ready = none ? __builtin_ctzll(none) : 64;
+    const int stop = final ? __builtin_ctzll(final) : 64;
+    const int use = min(ready, stop);
+    asm volatile("" ::: "memory");
+    constexpr int U = 4;
+    for (int k = 0; k < use; k += U) {
+      float pg[U][E], ph[U][E];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float* r = l.pairs + (first + (at - min(k + u, use - 1))) * (128 * E) + lane;
+        get_words<E>(r, pg[u]);
+        get_words<E>(r + 64 * E, ph[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (k + u < use)
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            acc[e] = decay_step(decay_word(G[e]), ph[u][e], acc[e]);
+            G[e] += pg[u][e];
+          }
+    }
+    if (stop <= ready && stop < 64) {
+      get_words<E>(l.states + (first + (at - stop)) * (64 * E) + lane, h);
+#pragma unroll
+      for (int e = 0; e < E; ++e) h[e] = decay_step(decay_word(G[e]), h[e], acc[e]);
+      return;
+    }
+    at -= use;
+    if (!use) __builtin_amdgcn_s_sleep(1);
+  }
+}
+
+// The tile of this workgroup: channel tile c, place j in the order of the tickets.
+struct ScanTile {
+  int c, j;
+};
+__device__ __forceinline__ ScanTile scan_tile(const ScanArgs& a, uint32_t* slot) {
+  uint32_t k = blockIdx.x;
+  if (a.tiles > 1) {
+    if (threadIdx.x == 0) *slot = __hip_atomic_fetch_add(a.link.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    k = (uint32_t)__builtin_amdgcn_readfirstlane((int)*slot);
+  }
+  return {(int)(k % (uint32_t)a.ctiles), (int)(k / (uint32_t)a.ctiles)};
+}
+
+// A lane's channels: index among all of them, head, sequence's tokens, parameters.
+template <int E> struct ScanLane {
+  long long ch;
+  int h, d, n;
+  long long bh;
+  bool on;
+  float m, bias2[E];                       // bias2 = dt_bias log2(e)
+};
+template <int E> __device__ __forceinline__ ScanLane<E> scan_lane(const ScanArgs& a, int c, int lane) {
+  const long long N = (long long)a.B * a.H * a.D;
+  ScanLane<E> l;
+  l.ch = ((long long)c * 64 + lane) * E;
+  l.on = l.ch < N;
+  const uint32_t ch = l.on ? (uint32_t)l.ch : 0u, bh = ch / (uint32_t)a.D;      // N <= 2^28
+  l.bh = bh;
+  l.d = (int)(ch - bh * (uint32_t)a.D);
+  const uint32_t b = bh / (uint32_t)a.H;
+  l.h = (int)(bh - b * (uint32_t)a.H);
+  l.n = !l.on ? 0 : a.lengths ? min(max(a.lengths[b], 0), a.T) : a.T;
+  l.m = gate_multiplier(a.A_log[l.h]);
+#pragma unroll
+  for (int e = 0; e < E; ++e) l.bias2[e] = a.dt_bias ? a.dt_bias[(size_t)l.h * a.D + l.d + e] * kLog2e : 0.f;
+  return l;
+}
+
+// Tile shapes.  Forward: S = 16 tokens of decay and input are 64 registers at E = 2.  Backward: seven values a token.
+constexpr int kScanFwdWaves = 8, kScanFwdTokens = 16, kScanBwdWaves = 4, kScanBwdTokens = 8;
+
+template <typename T> hipError_t launch_scan_fwd_tiles(const ScanArgs& a, bool pairs, hipStream_t s);
+template <typename T> hipError_t launch_scan_bwd_tiles(const ScanArgs& a, bool pairs, hipStream_t s);
+
+}  // namespace kda

@@ -1,167 +1,63 @@
-// Gated linear recurrence, one state per channel: prompts, single tokens, adjoint.
-//
-//   g = -m softplus(z + dt_bias), m = exp(clamp(A_log, -10, 20)),  a = e^g,  n = (1 - a^2)^1/2 or 1,  s = sigmoid(i) or 1
-//   h_t = a_t h_{t-1} + n_t s_t x_t,  y = h
-//   r_t = dL/dh_t = dy_t + a_{t+1} r_{t+1}:  dx = r n s,  di = r n x s (1 - s),
-//   dg = r (a h_{t-1} - a^2 / n s x),  dz = -dg m sigmoid(z + dt_bias),  dA_log = sum dg g,  ddt_bias = sum dz
-#include "../../include/kda.h"
-#include "kda_launch.h"
-#include "kda_vec.h"
+// Host side of the gated recurrence, its single token, and the small kernels around the tiles (kda_gated_scan.h).
+#include "kda_gated_scan.h"
 
 namespace kda {
 namespace {
 
 constexpr int kScanThreads = 256;
-constexpr int kScanChunk = KDA_GATED_SCAN_CHUNK;
 
-__device__ __forceinline__ float sigmoid_f(float x) { return fast_rcp(1.0f + fast_exp2(-kLog2e * x)); }
-
-// The decay of one token.  A decay next to 1 rounded to fp32 is off to the same side in every token of a channel whose
-// gate hardly moves, by up to 2^-25 / |g| of the state after the 1 / |g| tokens it remembers.  So a weak one (|g| < 1/8)
-// is held as e = a - 1, a strong one as a.
-struct Decay {
-  float v;                                 // e or a
-  bool weak;
-  __device__ __forceinline__ float step(float h, float u) const { return fmaf(v, h, (weak ? h : 0.f) + u); }
-  __device__ __forceinline__ float a() const { return weak ? 1.f + v : v; }
-  __device__ __forceinline__ float n2() const { return weak ? -v * (2.f + v) : fmaf(-v, v, 1.f); }   // 1 - a^2
-};
-__device__ __forceinline__ Decay decay_of(float g2) {     // g2 = g log2(e)
-  // e^g - 1 to the fifth power of g: the sixth is below 2^-27 of it at 1/8
-  const float g = g2 * kLn2;
-  const float e = g * fmaf(g, fmaf(g, fmaf(g, fmaf(g, 1.f / 120, 1.f / 24), 1.f / 6), 0.5f), 1.f);
-  Decay d;
-  d.weak = g > -0.125f;
-  d.v = d.weak ? e : fast_exp2(g2);
-  return d;
+// Clears the counter and the flags (a kernel, not a memset: it may be captured into a graph).
+__global__ __launch_bounds__(kScanThreads) void scan_clear_kernel(uint32_t* p, uint32_t n) {
+  const uint32_t i = blockIdx.x * kScanThreads + threadIdx.x;
+  if (i < n) p[i] = 0u;
 }
 
-struct ScanArgs {
-  const void *x, *z, *i;
-  const float *A_log, *dt_bias;
-  const int* lengths;
-  const float* state_in;
-  void* y;
-  float *state_out, *ckpt;
-  const void* dy;                          // backward
-  const float* d_state;
-  void *dx, *dz, *di;
-  float *d_state_in, *parts;
-  int B, H, T, D, normalize;
-};
-
-template <typename T> __global__ __launch_bounds__(kScanThreads) void scan_fwd_kernel(ScanArgs a) {
-  const long long N = (long long)a.B * a.H * a.D, ch = (long long)blockIdx.x * kScanThreads + threadIdx.x;
-  if (ch >= N) return;
-  const int bh = (int)(ch / a.D), d = (int)(ch % a.D), h = bh % a.H, b = bh / a.H;
-  const float m = gate_multiplier(a.A_log[h]), bias = a.dt_bias ? a.dt_bias[h * a.D + d] : 0.f;
-  const int n = a.lengths ? min(max(a.lengths[b], 0), a.T) : a.T;
-  const size_t base = (size_t)bh * a.T * a.D + d;
-  const int chunks = (a.T + kScanChunk - 1) / kScanChunk;
-  float st = a.state_in ? a.state_in[ch] : 0.f;
-  for (int t = 0; t < a.T; ++t) {
-    if (a.ckpt && t % kScanChunk == 0) a.ckpt[((size_t)bh * chunks + t / kScanChunk) * a.D + d] = st;
-    if (t >= n) continue;
-    const size_t o = base + (size_t)t * a.D;
-    const Decay dec = decay_of(-m * softplus2_f((to_f<T>(((const T*)a.z)[o]) + bias) * kLog2e, true));
-    float u = to_f<T>(((const T*)a.x)[o]);
-    if (a.i) u *= sigmoid_f(to_f<T>(((const T*)a.i)[o]));
-    if (a.normalize) u *= sqrtf(dec.n2());
-    st = dec.step(st, u);
-    ((T*)a.y)[o] = from_f<T>(st);
-  }
-  if (a.state_out) a.state_out[ch] = st;
+// ddt_bias, and the sums of dg g over time and sequences, from the tiles' parts.
+__global__ __launch_bounds__(kSumThreads) void scan_params_kernel(const float* parts, size_t half, int n_parts, int n,
+                                                                  float* d_dt_bias, float* sums) {
+  float* out = blockIdx.y ? sums : d_dt_bias;
+  if (!out) return;
+  sum_parts(parts + blockIdx.y * half, n, n_parts, n, [=](int i, float s) { out[i] = s; });
 }
-
-template <typename T> __global__ __launch_bounds__(kScanThreads) void scan_bwd_kernel(ScanArgs a) {
-  const long long N = (long long)a.B * a.H * a.D, ch = (long long)blockIdx.x * kScanThreads + threadIdx.x;
-  if (ch >= N) return;
-  const int bh = (int)(ch / a.D), d = (int)(ch % a.D), h = bh % a.H, b = bh / a.H;
-  const float m = gate_multiplier(a.A_log[h]), bias = a.dt_bias ? a.dt_bias[h * a.D + d] : 0.f;
-  const int n = a.lengths ? min(max(a.lengths[b], 0), a.T) : a.T;
-  const size_t base = (size_t)bh * a.T * a.D + d;
-  const int chunks = (a.T + kScanChunk - 1) / kScanChunk;
-  float r = a.d_state ? a.d_state[ch] : 0.f, sz = 0.f, sa = 0.f;
-  for (int t = n; t < a.T; ++t) {
-    const size_t o = base + (size_t)t * a.D;
-    ((T*)a.dx)[o] = ((T*)a.dz)[o] = from_f<T>(0.f);
-    if (a.di) ((T*)a.di)[o] = from_f<T>(0.f);
-  }
-  for (int c = (n + kScanChunk - 1) / kScanChunk - 1; c >= 0; --c) {
-    float before[kScanChunk];
-    float st = a.ckpt[((size_t)bh * chunks + c) * a.D + d];
-    for (int k = 0; k < kScanChunk; ++k) {
-      const int t = c * kScanChunk + k;
-      if (t >= n) break;
-      const size_t o = base + (size_t)t * a.D;
-      before[k] = st;
-      const Decay dec = decay_of(-m * softplus2_f((to_f<T>(((const T*)a.z)[o]) + bias) * kLog2e, true));
-      float u = to_f<T>(((const T*)a.x)[o]);
-      if (a.i) u *= sigmoid_f(to_f<T>(((const T*)a.i)[o]));
-      if (a.normalize) u *= sqrtf(dec.n2());
-      st = dec.step(st, u);
-    }
-    for (int k = kScanChunk - 1; k >= 0; --k) {
-      const int t = c * kScanChunk + k;
-      if (t >= n) continue;
-      const size_t o = base + (size_t)t * a.D;
-      const float p = to_f<T>(((const T*)a.z)[o]) + bias, x = to_f<T>(((const T*)a.x)[o]);
-      const float sp2 = softplus2_f(p * kLog2e, true);
-      const Decay dec = decay_of(-m * sp2);
-      const float s = a.i ? sigmoid_f(to_f<T>(((const T*)a.i)[o])) : 1.f;
-      const float nn = fmaxf(dec.n2(), 1e-38f), rn = a.normalize ? __builtin_amdgcn_rsqf(nn) : 1.f;
-      const float nrm = a.normalize ? dec.n2() * rn : 1.f, av = dec.a();
-      r += to_f<T>(((const T*)a.dy)[o]);
-      const float q = m * sigmoid_f(p);
-      ((T*)a.dx)[o] = from_f<T>(r * nrm * s);
-      if (a.di) ((T*)a.di)[o] = from_f<T>(r * nrm * x * s * (1.f - s));
-      float w = av * before[k] * q;
-      if (a.normalize) w -= q * av * av * s * x * rn;
-      ((T*)a.dz)[o] = from_f<T>(-r * w);
-      sz -= r * w;
-      float dg = av * before[k];
-      if (a.normalize) dg -= av * av * s * x * rn;
-      sa += r * dg * (-m * sp2 * kLn2);
-      r = dec.step(r, 0.f);
-    }
-  }
-  a.d_state_in[ch] = r;
-  a.parts[ch] = sz;
-  a.parts[N + ch] = sa;
-}
-
-__global__ void scan_params_kernel(ScanArgs a, float* dA_log, float* d_dt_bias) {
-  const long long N = (long long)a.B * a.H * a.D;
-  const int hd = a.H * a.D;
-  for (int k = blockIdx.x * blockDim.x + threadIdx.x; k < hd; k += gridDim.x * blockDim.x) {
-    float s = 0.f;
-    for (int b = 0; b < a.B; ++b) s += a.parts[(size_t)b * hd + k];
-    if (d_dt_bias) d_dt_bias[k] = s;
-  }
-  for (int h = blockIdx.x * blockDim.x + threadIdx.x; h < a.H; h += gridDim.x * blockDim.x) {
-    float s = 0.f;
-    for (int b = 0; b < a.B; ++b)
-      for (int d = 0; d < a.D; ++d) s += a.parts[N + ((size_t)b * a.H + h) * a.D + d];
-    if (dA_log) dA_log[h] = a.A_log[h] >= kALogMin && a.A_log[h] <= kALogMax ? s : 0.f;
+// dA_log of head blockIdx.x: the sum over its channels, in a fixed order.
+__global__ __launch_bounds__(kScanThreads) void scan_head_kernel(const float* sums, const float* A_log, int D, float* dA_log) {
+  __shared__ float red[kScanThreads / 64];
+  const float* p = sums + (size_t)blockIdx.x * D;
+  float s = 0.f;
+  for (int d = threadIdx.x; d < D; d += kScanThreads) s += p[d];
+  s = lane_sum<64>(s);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const float al = A_log[blockIdx.x];
+    s = (red[0] + red[1]) + (red[2] + red[3]);
+    dA_log[blockIdx.x] = al < kALogMin || al > kALogMax ? 0.f : s;      // the clamp holds the multiplier constant there
   }
 }
 
-template <typename T> __global__ __launch_bounds__(kScanThreads) void scan_step_kernel(ScanArgs a) {
-  const long long N = (long long)a.B * a.H * a.D, ch = (long long)blockIdx.x * kScanThreads + threadIdx.x;
-  if (ch >= N) return;
-  const int d = (int)(ch % a.D), h = (int)(ch / a.D % a.H);
-  const float m = gate_multiplier(a.A_log[h]), bias = a.dt_bias ? a.dt_bias[h * a.D + d] : 0.f;
-  const Decay dec = decay_of(-m * softplus2_f((to_f<T>(((const T*)a.z)[ch]) + bias) * kLog2e, true));
-  float u = to_f<T>(((const T*)a.x)[ch]);
-  if (a.i) u *= sigmoid_f(to_f<T>(((const T*)a.i)[ch]));
-  if (a.normalize) u *= sqrtf(dec.n2());
-  const float st = dec.step(a.state_out[ch], u);
-  a.state_out[ch] = st;
-  ((T*)a.y)[ch] = from_f<T>(st);
-}
-
-unsigned scan_grid(const ScanArgs& a) {
-  return (unsigned)(((long long)a.B * a.H * a.D + kScanThreads - 1) / kScanThreads);
+// One token: bound by launch and memory latency; a lane takes E neighbouring channels.
+template <typename T, int E> __global__ __launch_bounds__(kScanThreads) void scan_step_kernel(ScanArgs a) {
+  const uint32_t ch = (blockIdx.x * kScanThreads + threadIdx.x) * E;
+  if (ch >= (uint32_t)(a.B * a.H * a.D)) return;
+  const uint32_t row = ch / (uint32_t)a.D, d = ch - row * (uint32_t)a.D, h = row % (uint32_t)a.H;
+  const uint32_t off = ch * sizeof(T);     // B H D <= 2^28
+  ScanRaw<T, E> rz, rx, ri;
+  rz.load(a.z, off);
+  rx.load(a.x, off);
+  if (a.i) ri.load(a.i, off);
+  const float m = gate_multiplier(a.A_log[h]);
+  float st[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    float y, u = rx.at(e);
+    const float bias2 = a.dt_bias ? a.dt_bias[(size_t)h * a.D + d + e] * kLog2e : 0.f;
+    const float v = decay_word(-m * scan_softplus2(fmaf(rz.at(e), kLog2e, bias2), y));
+    if (a.i) u *= scan_sigmoid(ri.at(e));
+    if (a.normalize) u *= __builtin_amdgcn_sqrtf(decay_n2(v));
+    st[e] = decay_step(v, a.state_out[ch + e], u);
+    a.state_out[ch + e] = st[e];
+  }
+  scan_store<T, E>(a.y, off, st);
 }
 
 ScanArgs scan_args(const void* x, const void* z, const float* A_log, const float* dt_bias, const void* i,
@@ -172,19 +68,54 @@ ScanArgs scan_args(const void* x, const void* z, const float* A_log, const float
   return a;
 }
 
+// Channels per lane: two bf16 that no head's end separates.
+int scan_e(int D, bool bf16) { return bf16 && D % 2 == 0 ? 2 : 1; }
+
+struct ScanPlan {
+  int E, ctiles, tiles;
+  size_t clear, pairs, states, parts, sums, total;   // bytes cleared; offsets
+};
+size_t up(size_t n) { return (n + 255) / 256 * 256; }
+ScanPlan scan_plan(int B, int H, int T, int D, bool bf16, bool bwd) {
+  ScanPlan p;
+  const long long N = (long long)B * H * D;
+  const int tokens = bwd ? kScanBwdWaves * kScanBwdTokens : kScanFwdWaves * kScanFwdTokens;
+  p.E = scan_e(D, bf16);
+  p.ctiles = (int)((N + 64 * p.E - 1) / (64 * p.E));
+  p.tiles = T > tokens ? (T + tokens - 1) / tokens : 1;
+  const size_t n = p.tiles > 1 ? (size_t)p.ctiles * p.tiles : 0;
+  p.clear = n ? 256 + n * 4 : 0;
+  p.pairs = up(p.clear);
+  p.states = p.pairs + n * 128 * p.E * 4;
+  p.parts = p.states + n * 64 * p.E * 4;
+  p.sums = p.parts + (bwd ? up((size_t)p.tiles * N * 8) : 0);
+  p.total = p.sums + (bwd ? (size_t)H * D * 4 : 0);
+  return p;
+}
+void scan_link(ScanArgs& a, const ScanPlan& p, void* workspace, hipStream_t s) {
+  char* w = (char*)workspace;
+  a.ctiles = p.ctiles, a.tiles = p.tiles;
+  if (!p.clear) return;
+  a.link.ticket = (uint32_t*)w, a.link.flags = (uint32_t*)(w + 256);
+  a.link.pairs = (float*)(w + p.pairs), a.link.states = (float*)(w + p.states);
+  const uint32_t n = (uint32_t)(p.clear / 4);
+  scan_clear_kernel<<<(n + kScanThreads - 1) / kScanThreads, kScanThreads, 0, s>>>((uint32_t*)w, n);
+}
+
 }  // namespace
 
-size_t scan_workspace_bytes(int, int, int, int, bool) { return 0; }
-size_t scan_bwd_workspace_bytes(int B, int H, int, int D, bool) { return (size_t)B * H * D * 8; }
+size_t scan_workspace_bytes(int B, int H, int T, int D, bool bf16) { return scan_plan(B, H, T, D, bf16, false).total; }
+size_t scan_bwd_workspace_bytes(int B, int H, int T, int D, bool bf16) { return scan_plan(B, H, T, D, bf16, true).total; }
 
 template <typename T>
 hipError_t launch_scan_fwd(const void* x, const void* z, const float* A_log, const float* dt_bias, const void* i,
                            const int* lengths, const float* state_in, int normalize, void* y, float* state_out,
-                           float* ckpt, void*, int B, int H, int T_, int D, hipStream_t s) {
+                           float* ckpt, void* workspace, int B, int H, int T_, int D, hipStream_t s) {
   ScanArgs a = scan_args(x, z, A_log, dt_bias, i, lengths, normalize, B, H, T_, D);
   a.state_in = state_in, a.y = y, a.state_out = state_out, a.ckpt = ckpt;
-  scan_fwd_kernel<T><<<scan_grid(a), kScanThreads, 0, s>>>(a);
-  return hipGetLastError();
+  const ScanPlan p = scan_plan(B, H, T_, D, sizeof(T) == 2, false);
+  scan_link(a, p, workspace, s);
+  return launch_scan_fwd_tiles<T>(a, p.E == 2, s);
 }
 
 template <typename T>
@@ -192,7 +123,14 @@ hipError_t launch_scan_step(const void* x, const void* z, const float* A_log, co
                             int normalize, float* state, void* y, int B, int H, int D, hipStream_t s) {
   ScanArgs a = scan_args(x, z, A_log, dt_bias, i, nullptr, normalize, B, H, 1, D);
   a.state_out = state, a.y = y;
-  scan_step_kernel<T><<<scan_grid(a), kScanThreads, 0, s>>>(a);
+  const int E = scan_e(D, sizeof(T) == 2);
+  const unsigned grid = (unsigned)(((long long)B * H * D / E + kScanThreads - 1) / kScanThreads);
+  if constexpr (sizeof(T) == 2)
+    if (E == 2) {
+      scan_step_kernel<T, 2><<<grid, kScanThreads, 0, s>>>(a);
+      return hipGetLastError();
+    }
+  scan_step_kernel<T, 1><<<grid, kScanThreads, 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -203,11 +141,19 @@ hipError_t launch_scan_bwd(const void* x, const void* z, const float* A_log, con
                            void* workspace, int B, int H, int T_, int D, hipStream_t s) {
   ScanArgs a = scan_args(x, z, A_log, dt_bias, i, lengths, normalize, B, H, T_, D);
   a.ckpt = const_cast<float*>(ckpt), a.dy = dy, a.d_state = d_state, a.dx = dx, a.dz = dz, a.di = di;
-  a.d_state_in = d_state_in, a.parts = (float*)workspace;
-  scan_bwd_kernel<T><<<scan_grid(a), kScanThreads, 0, s>>>(a);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  scan_params_kernel<<<64, kScanThreads, 0, s>>>(a, dA_log, d_dt_bias);
+  a.d_state_in = d_state_in;
+  const ScanPlan p = scan_plan(B, H, T_, D, sizeof(T) == 2, true);
+  float* sums = (float*)((char*)workspace + p.sums);
+  if (dA_log || d_dt_bias) a.parts = (float*)((char*)workspace + p.parts);
+  scan_link(a, p, workspace, s);
+  hipError_t e = launch_scan_bwd_tiles<T>(a, p.E == 2, s);
+  if (e != hipSuccess || !a.parts) return e;
+  const int n = H * D;
+  scan_params_kernel<<<dim3((n + 63) / 64, 2), kSumThreads, 0, s>>>(a.parts, (size_t)p.tiles * B * n, p.tiles * B, n,
+                                                                    d_dt_bias, dA_log ? sums : nullptr);
+  e = hipGetLastError();
+  if (e != hipSuccess || !dA_log) return e;
+  scan_head_kernel<<<H, kScanThreads, 0, s>>>(sums, A_log, D, dA_log);
   return hipGetLastError();
 }
 

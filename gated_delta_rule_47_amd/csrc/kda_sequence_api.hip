@@ -85,7 +85,7 @@ bool qk_sizes(int B, int T, int Hq, int Hqw, int Hk, int Hkw, int D) {
 }
 bool scan_sizes(int B, int H, int T, int D) {
   return B >= 1 && H >= 1 && D >= 1 && T >= 0 && T <= (1 << 28) && (ll)B * H <= (1 << 28) && (ll)B * H * D <= (1 << 28) &&
-         (ll)B * H * D * (T ? T : 1) <= (1LL << 46);
+         (((ll)B * H * D + 63) / 64) * (((ll)T + KDA_GATED_SCAN_CHUNK - 1) / KDA_GATED_SCAN_CHUNK) <= (1LL << 23);
 }
 bool finite_f(float x) { return x >= -3.4e38f && x <= 3.4e38f; }
 

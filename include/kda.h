@@ -505,8 +505,8 @@ int kda_rope_frequencies(double* freqs, double* rope_scale, int R, double base, 
  *   A_log (H) f32;  dt_bias (H,D) f32 or NULL (= 0);  states (B,H,D) f32
  *   lengths   (B) int32 on the device, or NULL, as above: rows of y behind a sequence stay as they were, the gradients'
  *             rows there become zero, the final state is the one after the last token.
- *   B, H, D >= 1;  T >= 0;  T <= 2^28;  B * H * D <= 2^28;  B * H * T * D <= 2^46 (KDA_ERR_SHAPE).  Pointers need the
- *             alignment of an element only.
+ *   B, H, D >= 1;  T >= 0;  T <= 2^28;  B * H * D <= 2^28;  ceil(B * H * D / 64) * ceil(T / 32) <= 2^23 (KDA_ERR_SHAPE;
+ *             2^34 elements of many channels).  Pointers need the alignment of an element only.
  * Gates, states and sums are fp32; a decay within 1/8 of 1 in the logarithm is held as its distance from 1, so slow decays do
  * not drift over long sequences.  A non-finite value reaches its own channel only, from its token on. */
 
