@@ -13,7 +13,7 @@
 // the true state.
 //
 // Tiles hand their states on through the workspace.  Each publishes its own pair as soon as it has it, without
-// waiting for anything, then takes the pairs of the tiles before it back to the nearest one that knows its final state,
+// waiting for anything, then takes the pairs of the tiles before it from the nearest one on that knows its final state,
 // and publishes its own final state.  Workgroups take tiles by a counter, in time order: whatever a tile waits for
 // belongs to a workgroup that already runs and that publishes without waiting, so every wait ends.  Words are written
 // and read by device-scope atomics (past the XCDs' own L2), each record complete before its flag.
@@ -107,44 +107,42 @@ __device__ __forceinline__ void publish(uint32_t* flag, uint32_t value) {
 }
 
 // State in front of tile j > 0 (in the order of the tickets) of the channel tile whose first record is `first`; one wave.
+// It starts from the nearest tile that knows its final state and takes the pairs behind it one after the other, as each of
+// those tiles does for its own final state: so the result is the same bit by bit wherever it starts.
 template <int E> __device__ __forceinline__ void look_back(const ScanLink& l, size_t first, int j, int lane, float (&h)[E]) {
-  float G[E], acc[E];                      // the tiles taken so far: state behind them = acc + e^G state in front
-#pragma unroll
-  for (int e = 0; e < E; ++e) G[e] = acc[e] = 0.f;
-  for (int at = j - 1;;) {                 // the next tile to take; tile 0 always publishes its final state
+  int from;                                // that tile; tile 0 always becomes one
+  for (int at = j - 1;;) {                 // the newest tile of a window of 64; all newer ones have their pairs
     const int p = at - lane;
     const uint32_t f = p >= 0 ? __hip_atomic_load(l.flags + first + p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0u;
     const unsigned long long none = ~__ballot(f >= 1u), final = __ballot(f == 2u);
-    const int ready = none ? __builtin_ctzll(none) : 64;
-    const int stop = final ? __builtin_ctzll(final) : 64;
-    const int use = min(ready, stop);
-    asm volatile("" ::: "memory");
-    constexpr int U = 4;
-    for (int k = 0; k < use; k += U) {
-      float pg[U][E], ph[U][E];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const float* r = l.pairs + (first + (at - min(k + u, use - 1))) * (128 * E) + lane;
-        get_words<E>(r, pg[u]);
-        get_words<E>(r + 64 * E, ph[u]);
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (k + u < use)
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            acc[e] = decay_step(decay_word(G[e]), ph[u][e], acc[e]);
-            G[e] += pg[u][e];
-          }
+    const int ready = none ? __builtin_ctzll(none) : 64, stop = final ? __builtin_ctzll(final) : 64;
+    if (stop < ready) {
+      from = at - stop;
+      break;
     }
-    if (stop <= ready && stop < 64) {
-      get_words<E>(l.states + (first + (at - stop)) * (64 * E) + lane, h);
-#pragma unroll
-      for (int e = 0; e < E; ++e) h[e] = decay_step(decay_word(G[e]), h[e], acc[e]);
-      return;
+    if (ready == 64) {
+      at -= 64;
+    } else {                               // its workgroup runs and will publish; nearer tiles may have finished since
+      at = j - 1;
+      __builtin_amdgcn_s_sleep(1);
     }
-    at -= use;
-    if (!use) __builtin_amdgcn_s_sleep(1);
+  }
+  asm volatile("" ::: "memory");
+  get_words<E>(l.states + (first + from) * (64 * E) + lane, h);
+  constexpr int U = 4;
+  for (int k = from + 1; k < j; k += U) {
+    float pg[U][E], ph[U][E];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float* r = l.pairs + (first + min(k + u, j - 1)) * (128 * E) + lane;
+      get_words<E>(r, pg[u]);
+      get_words<E>(r + 64 * E, ph[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (k + u < j)
+#pragma unroll
+        for (int e = 0; e < E; ++e) h[e] = decay_step(decay_word(pg[u][e]), h[e], ph[u][e]);
   }
 }
 

@@ -67,8 +67,8 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(3))) vo
       c[k][e] = s;
       k4[k][e] = 0.f;
       if constexpr (NORM) {
-        // n = 0 (a decay of exactly 1): 1 / n is held at 1e19, and q = 0 or tiny takes the term to its limit 0 in dz
-        const float n2 = decay_n2(v[k][e]), rn = __builtin_amdgcn_rsqf(fmaxf(n2, 1e-38f)), av = decay_a(v[k][e]);
+        // n = 0 (a decay of exactly 1): 1 / n is held at 1e18, and q = 0 or tiny takes the term to its limit 0 in dz
+        const float n2 = decay_n2(v[k][e]), rn = __builtin_amdgcn_rsqf(fmaxf(n2, 1e-36f)), av = decay_a(v[k][e]);
         c[k][e] = s * (n2 * rn);
         k4[k][e] = av * av * rn * (s * x);
       }

@@ -104,9 +104,6 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4))) vo
     if (tile.j + 1 < a.tiles) {
       put_words<E>(a.link.states + rec * (64 * E) + lane, Ht);
       publish(a.link.flags + rec, 2u);
-    } else if (a.state_out && l.on) {
-#pragma unroll
-      for (int e = 0; e < E; ++e) a.state_out[l.ch + e] = Ht[e];
     }
   }
   __syncthreads();
@@ -125,6 +122,9 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4))) vo
     for (int e = 0; e < E; ++e) h[e] = decay_step(v[k][e], h[e], u[k][e]);
     if (full || t0 + k < l.n) scan_store<T, E>(a.y, base + k * row, h);
   }
+  if (w == NW - 1 && tile.j + 1 == a.tiles && a.state_out && l.on)
+#pragma unroll
+    for (int e = 0; e < E; ++e) a.state_out[l.ch + e] = h[e];
 }
 
 template <typename T, int E, typename Off> void launch_e(const ScanArgs& a, hipStream_t s) {

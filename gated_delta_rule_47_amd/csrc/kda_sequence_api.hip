@@ -16,28 +16,52 @@ bool valid_dtype(int t) { return t == KDA_F32 || t == KDA_BF16; }
 size_t esize(int dtype) { return dtype == KDA_BF16 ? 2 : 4; }
 bool aligned(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 
-// A buffer of rows: `row` bytes at every place b * batch + t * token (bytes; batch * n0 and token * n1 of them).
+// A buffer of rows: `row` bytes at every place i0 * s[0] + i1 * s[1] + i2 * s[2] (bytes; batch, token, head), ik < n[k].
 struct Rows {
   const void* p;
-  ll row, n0, batch, n1, token;
-  bool none() const { return !p || row <= 0 || n0 <= 0 || n1 <= 0; }
-  ll span() const { return (n0 - 1) * batch + (n1 - 1) * token + row; }
+  ll row, n[3], s[3];
+  bool none() const { return !p || row <= 0 || n[0] <= 0 || n[1] <= 0 || n[2] <= 0; }
+  ll span() const { return (n[0] - 1) * s[0] + (n[1] - 1) * s[1] + (n[2] - 1) * s[2] + row; }
 };
-Rows flat(const void* p, ll bytes) { return {p, bytes, 1, 0, 1, 0}; }
+Rows flat(const void* p, ll bytes) { return {p, bytes, {1, 1, 1}, {0, 0, 0}}; }
 
-// Whether two buffers may share a byte.  Spans that do not meet share none; rows at the same strides share none either
-// where both fit side by side into the smaller stride.
+// Whether b, which starts `off` bytes behind a, lies beside it within a period that both share: one dimension k whose
+// stride holds what either covers in its smaller dimensions side by side, and larger dimensions that both share too and
+// whose strides hold all the periods inside them.
+bool beside(const Rows& a, const Rows& b, ll off) {
+  for (int k = 0; k < 3; ++k) {
+    if (a.n[k] < 2 || a.n[k] != b.n[k] || a.s[k] != b.s[k]) continue;
+    ll ra = a.row, rb = b.row, on[2], os[2];
+    int outer = 0;
+    bool ok = true;
+    for (int i = 0; i < 3; ++i) {
+      if (i == k) continue;
+      const bool oa = a.n[i] > 1 && a.s[i] >= a.s[k], ob = b.n[i] > 1 && b.s[i] >= b.s[k];
+      if (oa || ob) {
+        ok = ok && a.n[i] == b.n[i] && a.s[i] == b.s[i];
+        on[outer] = a.n[i], os[outer++] = a.s[i];
+      } else {
+        ra += (a.n[i] - 1) * a.s[i], rb += (b.n[i] - 1) * b.s[i];
+      }
+    }
+    if (!ok || off < ra || off + rb > a.s[k]) continue;
+    const int lo = outer == 2 && os[1] < os[0];
+    ll all = a.n[k] * a.s[k];
+    for (int i = 0; i < outer; ++i) {
+      const int o = i ^ lo;
+      ok = ok && os[o] >= all;
+      all = on[o] * os[o];
+    }
+    if (ok) return true;
+  }
+  return false;
+}
+// Whether two buffers may share a byte.
 bool meet(const Rows& a, const Rows& b) {
   if (a.none() || b.none()) return false;
   const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
   if (x + (uintptr_t)a.span() <= y || y + (uintptr_t)b.span() <= x) return false;
-  if (y < x) return meet(b, a);
-  if (a.n0 != b.n0 || a.n1 != b.n1 || (a.n0 > 1 && a.batch != b.batch) || (a.n1 > 1 && a.token != b.token)) return true;
-  ll inner = a.token, n = a.n1, outer = a.batch, m = a.n0;
-  if (n == 1 || (m > 1 && outer < inner)) inner = a.batch, n = a.n0, outer = a.token, m = a.n1;
-  if (n == 1) return true;                                   // one row each, whose spans meet
-  const ll off = (ll)(y - x);
-  return !(off >= a.row && off + b.row <= inner && (m == 1 || outer >= n * inner));
+  return y >= x ? !beside(a, b, (ll)(y - x)) : !beside(b, a, (ll)(x - y));
 }
 template <int NI, int NO> bool any_meet(const Rows (&ins)[NI], const Rows (&outs)[NO]) {
   for (int i = 0; i < NO; ++i) {
@@ -116,12 +140,10 @@ int qk_check(const QkCall& c, bool needed) {
     return KDA_ERR_ALIGN;
   return KDA_OK;
 }
-// A side's heads as one row per token where the token's (or the batch's) stride spans them, else its whole span.
-Rows qk_rows(const void* p, ll b, ll t, ll h, int B, int T, int H, int D, size_t es) {
-  const ll heads = (H - 1) * h + D;
-  if (H == 0) return flat(nullptr, 0);
-  return {p, heads * (ll)es, B, b * (ll)es, T, t * (ll)es};
+Rows qk_rows(const void* p, ll b, ll t, ll h, int B, int T, int H, int D, ll es) {
+  return {p, D * es, {B, T, H}, {b * es, t * es, h * es}};
 }
+Rows conv_rows(const void* p, ll b, ll t, int B, int T, ll C, ll es) { return {p, C * es, {B, T, 1}, {b * es, t * es, 0}}; }
 QkSideDesc side_of(const void* x, ll b, ll t, ll h, const float* w, int Hw, int H, void* y) {
   QkSideDesc d = {};
   d.x = x, d.xb = b, d.xt = t, d.xh = h, d.w = w, d.H = H, d.per_head = w && Hw > 1, d.y = y;
@@ -146,7 +168,7 @@ int kda_short_conv_fwd(const void* x, ll x_batch, ll x_token, const float* weigh
   if (!aligned(x, es) || !aligned(y, es) || !aligned(state_in, es) || !aligned(state_out, es) || !aligned(weight, 4) ||
       !aligned(bias, 4) || !aligned(lengths, 4))
     return reject(KDA_ERR_ALIGN);
-  const Rows ins[] = {{x, C * es, B, x_batch * es, T, x_token * es}, flat(weight, C * W * 4), flat(bias, C * 4),
+  const Rows ins[] = {conv_rows(x, x_batch, x_token, B, T, C, es), flat(weight, C * W * 4), flat(bias, C * 4),
                       flat(lengths, (ll)B * 4), flat(state_in, (ll)B * (W - 1) * C * es)};
   const Rows outs[] = {flat(y, (ll)B * T * C * es), flat(state_out, (ll)B * (W - 1) * C * es)};
   if (any_meet(ins, outs)) return reject(KDA_ERR_ALIAS);
@@ -167,7 +189,7 @@ int kda_short_conv_step(const void* x, ll x_batch, const float* weight, const fl
   if (!strides_fit(C, n, st)) return reject(KDA_ERR_SHAPE);
   if (!aligned(x, es) || !aligned(y, es) || !aligned(state, es) || !aligned(weight, 4) || !aligned(bias, 4))
     return reject(KDA_ERR_ALIGN);
-  const Rows ins[] = {{x, C * es, B, x_batch * es, 1, 0}, flat(weight, C * W * 4), flat(bias, C * 4)};
+  const Rows ins[] = {conv_rows(x, x_batch, 0, B, 1, C, es), flat(weight, C * W * 4), flat(bias, C * 4)};
   const Rows outs[] = {flat(y, (ll)B * C * es), flat(state, (ll)B * (W - 1) * C * es)};
   if (any_meet(ins, outs)) return reject(KDA_ERR_ALIAS);
   hipStream_t s = (hipStream_t)stream;
@@ -198,9 +220,9 @@ int kda_short_conv_bwd(const void* x, ll x_batch, ll x_token, const float* weigh
   if (need && (!workspace || workspace_bytes < need)) return reject(KDA_ERR_WORKSPACE);
   if (need && !aligned(workspace, 16)) return reject(KDA_ERR_ALIGN);
   const ll ns = (ll)B * (W - 1) * C;
-  const Rows ins[] = {{x, C * es, B, x_batch * es, T, x_token * es}, flat(weight, C * W * 4), flat(bias, C * 4),
+  const Rows ins[] = {conv_rows(x, x_batch, x_token, B, T, C, es), flat(weight, C * W * 4), flat(bias, C * 4),
                       flat(lengths, (ll)B * 4), flat(state_in, ns * es), flat(dy, (ll)B * T * C * es), flat(d_state_out, ns * 4)};
-  const Rows outs[] = {{dx, C * es, B, dx_batch * es, T, dx_token * es}, flat(dweight, C * W * 4), flat(dbias, C * 4),
+  const Rows outs[] = {conv_rows(dx, dx_batch, dx_token, B, T, C, es), flat(dweight, C * W * 4), flat(dbias, C * 4),
                        flat(d_state_in, ns * 4), flat(need ? workspace : nullptr, (ll)need)};
   if (any_meet(ins, outs)) return reject(KDA_ERR_ALIAS);
   hipStream_t s = (hipStream_t)stream;

@@ -37,7 +37,7 @@ def _one_of(name, value, table):
 def _strided(name, t, shape, dtype, dev):
     """Address of a tensor of this shape whose last axis is dense; its strides are the caller's."""
     try:
-        if t.shape == shape and t.dtype is dtype and t.get_device() == dev and (t.stride(-1) == 1 or shape[-1] == 1):
+        if t.shape == shape and t.dtype is dtype and t.get_device() == dev and (t.stride(-1) == 1 or shape[-1] == 1 or not t.numel()):
             return t.data_ptr()
     except AttributeError:
         pass

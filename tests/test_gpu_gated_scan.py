@@ -1,0 +1,406 @@
+"""Gated linear recurrence on the GPU against float64.
+
+Tolerances, element by element, with e = 2^-24 and U = 2^-8 for a rounding to bf16 (fp32: e).  Per token, for the error of
+  g   12 e |g| (softplus: six roundings, the multiplier: four, the product) and 4 e m sigmoid(z') (|z| + |dt_bias|) of its argument
+  a   a times that, and 3 e |g| where it is held as a - 1 (the cubic is within 0.6 e), 3 e a elsewhere
+  n   a / n times that, and 4 e n;   s: (|i| + 8) e s;   u = n s x: the sum of the three relative ones and 3 e
+  h   E_t = a E_{t-1} + |h_{t-1}| (that of a) + (that of u) + 5 e (|h_t| + |h_{t-1}| + |u_t|): two roundings of a step, and
+      three for the joins of 8 to 128 tokens' states, in each of which a carried state is rounded four times and its
+      decay is off by at most 20 e of |G| e^G <= 0.37
+  r   the same recurrence backwards
+and products of these for the gradients; sums add N e of the absolute sum for N additions one behind the other.
+"""
+import numpy as np
+import pytest
+import torch
+
+import gated_delta_rule_47_amd as kda
+from oracle import sequence_ref as R
+
+from gpu_helpers import DEV, host, say, to_dev
+
+pytestmark = pytest.mark.gpu
+BF, FP = torch.bfloat16, torch.float32
+E32 = 2.0 ** -24
+U = {BF: 2.0 ** -8, FP: E32}
+
+
+def within(name, got, ref, lim):
+    g = host(got)
+    assert g.shape == ref.shape, name
+    over = np.abs(g - ref) - lim
+    assert np.all(over <= 0), (name, float(over.max()), np.unravel_index(over.argmax(), over.shape))
+
+
+def inputs(B, H, T, D, dtype, seed=0, gated=True, bias=True, state=True, slow=False):
+    rng = np.random.default_rng(seed)
+    n = rng.standard_normal
+    d = {"x": to_dev(n((B, H, T, D)), dtype), "z": to_dev(n((B, H, T, D)), dtype)}
+    d["i"] = to_dev(n((B, H, T, D)), dtype) if gated else None
+    d["A"] = to_dev(rng.uniform(-1, 1, H), FP)
+    rate = np.exp(rng.uniform(np.log(1e-4 if slow else 1e-3), np.log(1e-3 if slow else 2.0), (H, D)))
+    d["b"] = to_dev(np.log(np.expm1(rate)), FP) if bias else None
+    d["s"] = to_dev(n((B, H, D)), FP) if state else None
+    d["dy"], d["ds"] = to_dev(n((B, H, T, D)), dtype), to_dev(n((B, H, D)), FP)
+    return d
+
+
+def _opt(t):
+    return None if t is None else host(t)
+
+
+def _errors(d, lens, normalize):
+    """The float64 values and the limits of every token (B,H,T,D), identity behind a sequence's end."""
+    x, z, i, b = host(d["x"]), host(d["z"]), _opt(d["i"]), _opt(d["b"])
+    g, a, n, slope = R.scan_gates(z, host(d["A"]), b, normalize)
+    bb = np.zeros(z.shape) if b is None else np.broadcast_to(b[None, :, None], z.shape)
+    q, size = np.abs(slope), np.abs(z) + np.abs(bb)
+    s = np.ones_like(x) if i is None else 1 / (1 + np.exp(-i))
+    ls = np.zeros_like(x) if i is None else (np.abs(i) + 8) * E32
+    eg = 12 * E32 * np.abs(g) + 4 * E32 * q * size
+    ea = a * eg + np.where(g > -0.126, 3 * E32 * np.abs(g), 3 * E32 * a)
+    with np.errstate(divide="ignore", invalid="ignore"):
+        en = np.where(n > 0, a * ea / n, 0.0) + 4 * E32 * n if normalize else np.zeros_like(n)
+        rn = np.where(n > 0, en / n, 0.0)
+    u = n * s * x
+    eu = np.abs(u) * (rn + ls + 3 * E32)
+    inside = np.zeros(x.shape, bool)
+    for k, m in enumerate(lens):
+        inside[k, :, :m] = True
+    return dict(x=x, g=g, a=a, n=n, q=q, s=s, u=u, size=size, ls=ls, eg=eg, ea=ea, en=en, rn=rn, eu=eu, inside=inside)
+
+
+def _forward_limits(v, before, y, end, T):
+    """E behind every token and behind the last."""
+    E = np.zeros(before[:, :, 0].shape) if T else np.zeros(end.shape)
+    out, first = np.zeros(before.shape), np.zeros(before.shape)
+    for t in range(T):
+        first[:, :, t] = E
+        h0 = np.abs(before[:, :, t])
+        new = v["a"][:, :, t] * E + v["ea"][:, :, t] * h0 + v["eu"][:, :, t] + 5 * E32 * (np.abs(y[:, :, t]) + h0 + np.abs(v["u"][:, :, t]))
+        E = np.where(v["inside"][:, :, t], new, E)
+        out[:, :, t] = E
+    return first, out, E
+
+
+def check(B, H, T, D, dtype, lengths=None, gated=True, normalize=True, bias=True, state=True, seed=0, slow=False, backward=True,
+          d=None):
+    say("scan", B, H, T, D, dtype, lengths, gated, normalize, bias, state)
+    d = d or inputs(B, H, T, D, dtype, seed, gated, bias, state, slow)
+    lens = R._lens(lengths, B, T)
+    lt = None if lengths is None else torch.tensor(lengths, dtype=torch.int32, device=DEV)
+    out = torch.full((B, H, T, D), 7.0, dtype=dtype, device=DEV)
+    y, end, ckpt = kda.gated_scan_fwd(d["x"], d["z"], d["A"], d["b"], d["s"], d["i"], lt, normalize, want_ckpt=True, out=out)
+    torch.cuda.synchronize()
+    ry, rend, before = R.gated_scan(host(d["x"]), host(d["z"]), host(d["A"]), _opt(d["b"]), _opt(d["s"]), _opt(d["i"]), lengths, normalize)
+    v = _errors(d, lens, normalize)
+    Eb, Ey, Eend = _forward_limits(v, before, ry, rend, T)
+    for k, n in enumerate(lens):
+        assert torch.all(out[k, :, n:] == 7)               # rows behind a sequence stay
+        ry[k, :, n:] = 7
+    within("y", y, ry, np.where(v["inside"], Ey + U[dtype] * np.abs(ry), 0))
+    within("state", end, rend, Eend + E32 * np.abs(rend))
+    C = kda.GATED_SCAN_CHUNK
+    within("ckpt", ckpt, before[:, :, ::C], Eb[:, :, ::C] + E32 * np.abs(before[:, :, ::C]))
+    if not backward:
+        return d, y, end, ckpt
+    got = kda.gated_scan_bwd(d["x"], d["z"], d["A"], d["b"], ckpt, d["dy"], d["ds"], d["i"], lt, normalize)
+    torch.cuda.synchronize()
+    ref = R.gated_scan_adjoint(host(d["x"]), host(d["z"]), host(d["A"]), _opt(d["b"]), _opt(d["s"]), host(d["dy"]), host(d["ds"]), _opt(d["i"]),
+                               lengths, normalize)
+    r, dyv = ref["R"], np.abs(host(d["dy"]))
+    ER, E, rn_ = np.zeros(r.shape), np.zeros((B, H, D)), np.abs(host(d["ds"]))
+    for t in reversed(range(T)):
+        ins = v["inside"][:, :, t]
+        new = E + 5 * E32 * (np.abs(r[:, :, t]) + rn_ + dyv[:, :, t])
+        ER[:, :, t] = np.where(ins, new, 0)
+        nxt = v["a"][:, :, t] * new + v["ea"][:, :, t] * np.abs(r[:, :, t]) + 2 * E32 * v["a"][:, :, t] * np.abs(r[:, :, t])
+        E = np.where(ins, nxt, E)
+        rn_ = np.where(ins, np.abs(v["a"][:, :, t] * r[:, :, t]), rn_)
+    ar, ax, n, s, a = np.abs(r), np.abs(v["x"]), v["n"], v["s"], v["a"]
+    low = U[dtype]
+    within("dx", got["dx"], ref["dx"], ER * n * s + ar * v["en"] * s + np.abs(ref["dx"]) * (v["ls"] + 6 * E32 + low))
+    if gated:
+        di = np.abs(ref["dinput_gate"])
+        lim = (ER * n + ar * v["en"]) * ax * s * (1 - s) + ar * n * ax * s * (v["ls"] * s + E32) + di * (v["ls"] + 8 * E32 + low)
+        within("dinput_gate", got["dinput_gate"], ref["dinput_gate"], lim)
+    else:
+        assert got["dinput_gate"] is None
+    with np.errstate(divide="ignore", invalid="ignore"):
+        k4 = np.where(n > 0, a * a * s * ax / n, 0.0) if normalize else 0.0 * ax
+        sx = np.where(n > 0, s * v["x"] * a * a / n, 0.0) if normalize else 0.0 * ax
+    ab = np.abs(before)
+    K = np.abs(a * before - sx)
+    eK = a * Eb + v["ea"] * ab + k4 * (2 * v["ea"] / np.maximum(a, 1e-30) + v["rn"] + v["ls"] + 10 * E32) + 4 * E32 * (a * ab + k4)
+    ldg = ER * K + ar * eK + 2 * E32 * ar * K
+    dz, dg = np.abs(ref["dz"]), ar * K
+    ldz = v["q"] * ldg + dz * (14 + 4 * v["size"]) * E32
+    within("dz", got["dz"], ref["dz"], ldz + low * dz)
+    within("dstate_in", got["dstate_in"], ref["dstate_in"], E + 4 * E32 * np.abs(ref["dstate_in"]) + 4 * E32 * rn_)
+    N = 8 + 4 + B * (T // C + 1) / 16 + 16
+    within("ddt_bias", got["ddt_bias"], ref["ddt_bias"], ldz.sum((0, 2)) + N * E32 * dz.sum((0, 2)))
+    lA = (ldg * np.abs(v["g"]) + dg * v["eg"]) * v["inside"]
+    within("dA_log", got["dA_log"], ref["dA_log"], lA.sum((0, 2, 3)) + (N + D / 256 + 16) * E32 * (dg * np.abs(v["g"])).sum((0, 2, 3)))
+    return d, y, end, ckpt
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("T", [1, 2, 7, 8, 9, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 257, 600])
+def test_lengths(T, dtype):
+    check(2, 1, T, 6, dtype, seed=T)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("H,D", [(1, 1), (1, 2), (3, 1), (1, 3), (2, 5), (5, 8), (1, 63), (1, 64), (1, 65), (1, 127), (2, 64), (1, 129),
+                                 (7, 37), (40, 16), (1, 1000)])
+def test_channels(H, D, dtype):
+    check(2, H, 70, D, dtype, seed=H * D)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("gated", [True, False])
+@pytest.mark.parametrize("normalize", [True, False])
+def test_forms(normalize, gated, dtype):
+    check(2, 2, 150, 10, dtype, gated=gated, normalize=normalize, seed=1)
+    check(1, 2, 40, 7, dtype, gated=gated, normalize=normalize, bias=False, state=False, seed=2)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("D", [5, 8, 64])
+def test_padded_batches(D, dtype):
+    """Sequences of different lengths side by side in a channel tile; 0, 1, one beyond and both sides of the tiles' ends."""
+    check(8, 2, 300, D, dtype, lengths=[300, 0, 1, 128, 129, 127, 32, 33], seed=D)
+    check(3, 1, 90, D, dtype, lengths=[-3, 500, 64], seed=D)
+    check(2, 1, 20, D, dtype, lengths=[0, 0], seed=D)
+
+
+def test_many_tiles():
+    """More tiles than run at once, and more than one window of 64 to look back over."""
+    check(1, 1, 9000, 4, FP, seed=5)
+    check(1, 3, 5000, 50, BF, seed=6, slow=True)
+    check(2, 1, 2500, 700, BF, lengths=[2500, 1300], seed=7)
+
+
+def test_slow_decays_do_not_drift():
+    """A gate that never moves: a decay of 1 - 2^-14 or so, 65536 tokens.  Held as one float it would be off by up to
+    2^-25 2^14 of the state.  Rounding errors of either sign: per token three of e / sqrt(3) RMS over 2^14 tokens' memory
+    is 128 e of the state, one in 10^4 of a thousand channels four times that; the gate itself is off by 12 e (all tokens
+    alike), which moves the state by 12 e of |G| e^G and of its steady value."""
+    T, D = 65536, 64
+    for lim, shift in ((600 * E32, 0.0), (600 * E32, 0.37)):
+        rate = 2.0 ** -14 * (1 + np.arange(D) / D) * (1 + shift)
+        A, b = to_dev(np.zeros(1), FP), to_dev(np.log(np.expm1(rate))[None], FP)
+        z = torch.zeros((1, 1, T, D), device=DEV)
+        x = torch.ones_like(z)
+        y, end, _ = kda.gated_scan_fwd(x, z, A, b, torch.full((1, 1, D), 3.0, device=DEV), normalize=False)
+        g = -np.logaddexp(host(b)[0], 0.0)
+        for t in (1, 1000, 30000, T):
+            # h = e^{G} 3 + (1 - e^{G}) / (1 - e^{g})
+            ref = 3 * np.exp(g * t) + np.expm1(g * t) / np.expm1(g)
+            assert np.all(np.abs(host(y)[0, 0, t - 1] - ref) <= lim * ref), t
+        assert np.array_equal(host(end)[0, 0], host(y)[0, 0, -1])
+
+
+def test_strong_decays_and_silence():
+    """What is left of a state after tokens of nothing keeps its relative accuracy (a strong decay is held as itself)."""
+    T, D = 40, 16
+    rate = np.linspace(0.05, 8.0, D)
+    A, b = to_dev(np.zeros(1), FP), to_dev(np.log(np.expm1(rate))[None], FP)
+    z = torch.zeros((1, 1, T, D), device=DEV)
+    y, _, _ = kda.gated_scan_fwd(torch.zeros_like(z), z, A, b, torch.ones(1, 1, D, device=DEV))
+    g = -np.logaddexp(host(b)[0], 0.0)
+    for t in (0, 3, 10):
+        ref = np.exp(g * (t + 1))
+        assert np.all(np.abs(host(y)[0, 0, t] - ref) <= (t + 2) * (16 * np.abs(g) + 6) * E32 * ref)
+
+
+def test_extreme_gates():
+    """Decays of exactly 1 and of 0, gates of infinity: the formula's limits, gradients finite."""
+    T = 6
+    z = torch.zeros((1, 1, T, 8), device=DEV)
+    z[..., 0], z[..., 1], z[..., 2], z[..., 3] = float("-inf"), float("inf"), -200.0, 1e4
+    x, i = torch.ones_like(z), torch.zeros_like(z)
+    i[..., 4], i[..., 5] = float("inf"), float("-inf")
+    s = torch.full((1, 1, 8), 2.0, device=DEV)
+    A = torch.zeros(1, device=DEV)
+    y, end, ckpt = kda.gated_scan_fwd(x, z, A, None, s, i, want_ckpt=True)
+    assert torch.all(y[..., 0] == 2) and torch.all(y[..., 2] == 2)          # a = 1, n = 0
+    assert torch.all(y[..., 1] == 0.5) and torch.all(y[..., 3] == 0.5)      # a = 0, n = 1
+    assert torch.isfinite(y).all()
+    assert torch.allclose(y[0, 0, :, 5], 2.0 * torch.exp(-np.log(2.0) * torch.arange(1, T + 1, device=DEV)), rtol=1e-5)
+    r = kda.gated_scan_bwd(x, z, A, None, ckpt, torch.ones_like(x), None, i)
+    for n in ("dx", "dz", "dinput_gate", "ddt_bias", "dstate_in"):
+        assert torch.isfinite(r[n]).all(), n
+    assert not r["dz"][..., 0].any() and not r["dz"][..., 2].any() and torch.all(r["dstate_in"][..., 0] == T)
+    assert not r["dinput_gate"][..., 4:6].any()
+
+
+def test_multipliers_at_and_beyond_the_clamp():
+    B, H, T, D = 1, 5, 40, 4
+    d = inputs(B, H, T, D, FP, 3)
+    d["A"] = torch.tensor([-50.0, -10.0, 0.5, 3.0, 25.0], device=DEV)
+    d["b"] = d["b"] - 4
+    y, _, ckpt = kda.gated_scan_fwd(d["x"], d["z"], d["A"], d["b"], d["s"], d["i"], want_ckpt=True)
+    ry, _, _ = R.gated_scan(host(d["x"]), host(d["z"]), host(d["A"]), host(d["b"]), host(d["s"]), host(d["i"]))
+    assert np.linalg.norm(host(y) - ry) <= 1e-5 * np.linalg.norm(ry)
+    r = kda.gated_scan_bwd(d["x"], d["z"], d["A"], d["b"], ckpt, d["dy"], None, d["i"])
+    dA = host(r["dA_log"])
+    assert dA[0] == 0 and dA[4] == 0 and dA[1] != 0 and dA[2] != 0
+
+
+def test_non_finite_values_keep_to_their_channel():
+    B, H, T, D = 2, 2, 200, 12
+    for dtype in (BF, FP):
+        d = inputs(B, H, T, D, dtype, 4)
+        lens = torch.tensor([200, 90], dtype=torch.int32, device=DEV)
+        call = lambda d: kda.gated_scan_fwd(d["x"], d["z"], d["A"], d["b"], d["s"], d["i"], lens, want_ckpt=True,
+                                            out=torch.zeros((B, H, T, D), dtype=dtype, device=DEV))
+        back = lambda d, c: kda.gated_scan_bwd(d["x"], d["z"], d["A"], d["b"], c, d["dy"], d["ds"], d["i"], lens)
+        y0, e0, c0 = call(d)
+        g0 = back(d, c0)
+        bad = {k: t.clone() for k, t in d.items()}
+        for k in ("x", "z", "i", "dy"):
+            bad[k][1, :, 90:] = float("nan")                       # behind the sequence: never read
+        y1, e1, c1 = call(bad)
+        g1 = back(bad, c1)
+        assert torch.equal(y0, y1) and torch.equal(e0, e1) and torch.equal(c0, c1) and all(torch.equal(g0[k], g1[k]) for k in g0)
+        bad = {k: t.clone() for k, t in d.items()}
+        bad["x"][0, 1, 150, 7] = float("inf")
+        bad["z"][1, 0, 40, 3] = float("nan")
+        y2, e2, _ = call(bad)
+        hit = y2 != y0                                             # (NaN differs from everything)
+        assert hit[0, 1, 150:, 7].all() and hit[1, 0, 40:90, 3].all()
+        hit[0, 1, 150:, 7] = hit[1, 0, 40:90, 3] = False
+        assert not hit.any() and (e2 != e0).sum() == 2
+
+
+def test_segments_and_steps_continue_a_sequence():
+    B, H, T, D = 2, 2, 330, 16
+    for dtype in (BF, FP):
+        d = inputs(B, H, T, D, dtype, 8)
+        cut = lambda t, a, b: t[:, :, a:b].contiguous()
+        part = lambda a, b, s: kda.gated_scan_fwd(cut(d["x"], a, b), cut(d["z"], a, b), d["A"], d["b"], s, cut(d["i"], a, b))
+        y, end, _ = part(0, T, d["s"])
+        y1, mid, _ = part(0, 141, d["s"])
+        y2, end2, _ = part(141, T, mid)
+        # the same sums joined elsewhere: roundings of e per join, three joins in the memory of 20 tokens or so
+        joined = torch.cat((y1, y2), 2)
+        assert np.linalg.norm(host(joined) - host(y)) <= (2.0 ** -9 if dtype == BF else 20 * E32) * np.linalg.norm(host(y))
+        assert np.linalg.norm(host(end2) - host(end)) <= 20 * E32 * np.linalg.norm(host(end))
+        st = mid.clone()
+        for t in range(141, 180):
+            yt = kda.gated_scan_step(d["x"][:, :, t].contiguous(), d["z"][:, :, t].contiguous(), d["A"], d["b"], st,
+                                     d["i"][:, :, t].contiguous())
+            n = np.linalg.norm(host(y[:, :, t]))
+            assert np.linalg.norm(host(yt) - host(y[:, :, t])) <= (2.0 ** -8 if dtype == BF else 20 * E32) * n, t
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("B,H,D", [(1, 1, 1), (3, 2, 5), (2, 3, 64), (192, 1, 4096), (5, 1, 1001)])
+def test_one_token(B, H, D, dtype):
+    for gated, normalize, bias in ((True, True, True), (False, False, False)):
+        d = inputs(B, H, 1, D, dtype, D, gated, bias)
+        st = d["s"].clone()
+        y = kda.gated_scan_step(d["x"][:, :, 0], d["z"][:, :, 0], d["A"], d["b"], st, None if d["i"] is None else d["i"][:, :, 0], normalize)
+        ry, rend, before = R.gated_scan(host(d["x"]), host(d["z"]), host(d["A"]), _opt(d["b"]), host(d["s"]), _opt(d["i"]), None, normalize)
+        v = _errors(d, [1] * B, normalize)
+        _, _, E = _forward_limits(v, before, ry, rend, 1)
+        within("state", st, rend, E + E32 * np.abs(rend))
+        within("y", y, rend, E + U[dtype] * np.abs(rend))
+
+
+def test_no_tokens():
+    d = inputs(2, 3, 0, 8, BF, 1)
+    y, end, ckpt = kda.gated_scan_fwd(d["x"], d["z"], d["A"], d["b"], d["s"], d["i"], want_ckpt=True)
+    assert y.shape == (2, 3, 0, 8) and torch.equal(end, d["s"]) and ckpt.shape == (2, 3, 0, 8)
+    assert not kda.gated_scan_fwd(d["x"], d["z"], d["A"])[1].any()
+    r = kda.gated_scan_bwd(d["x"], d["z"], d["A"], d["b"], ckpt, y, d["ds"], d["i"])
+    assert torch.equal(r["dstate_in"], d["ds"]) and not r["dA_log"].any() and not r["ddt_bias"].any()
+
+
+def test_options_workspaces_and_state_in_place():
+    B, H, T, D = 2, 2, 300, 32
+    d = inputs(B, H, T, D, BF, 2)
+    args = (d["x"], d["z"], d["A"], d["b"])
+    y, end, ckpt = kda.gated_scan_fwd(*args, d["s"], d["i"], want_ckpt=True)
+    y2, none, none2 = kda.gated_scan_fwd(*args, d["s"], d["i"], output_state=False)
+    assert none is None and none2 is None and torch.equal(y, y2)
+    for fill in (0, 1, 2, 255):                                    # contents on entry are ignored
+        ws = torch.full((kda.gated_scan_workspace_bytes(B, H, T, D),), fill, dtype=torch.uint8, device=DEV)
+        wb = torch.full((kda.gated_scan_bwd_workspace_bytes(B, H, T, D),), fill, dtype=torch.uint8, device=DEV)
+        st = d["s"].clone()
+        for _ in range(2):
+            st.copy_(d["s"])
+            got = kda.gated_scan_fwd(*args, st, d["i"], state_out=st, workspace=ws)
+            assert torch.equal(got[0], y) and torch.equal(st, end)
+            r = kda.gated_scan_bwd(*args, ckpt, d["dy"], d["ds"], d["i"], workspace=wb)
+            first = kda.gated_scan_bwd(*args, ckpt, d["dy"], d["ds"], d["i"])
+            assert all(torch.equal(r[k], first[k]) for k in r)     # repeatable bit by bit
+    with pytest.raises(kda.KdaError) as e:
+        kda.gated_scan_fwd(*args, d["s"], d["i"], workspace=ws[:-256])
+    assert e.value.status == -7
+    same, _, _ = kda.gated_scan_fwd(d["x"], d["x"], d["A"], d["b"], d["s"], d["x"])     # one tensor for all inputs
+    ref = R.gated_scan(host(d["x"]), host(d["x"]), host(d["A"]), host(d["b"]), host(d["s"]), host(d["x"]))[0]
+    assert np.linalg.norm(host(same) - ref) <= 2.0 ** -8 * np.linalg.norm(ref)
+
+
+@pytest.mark.parametrize("shift", [1, 3])
+def test_rows_off_their_alignment(shift):
+    B, H, T, D = 1, 2, 140, 6
+    for dtype in (BF, FP):
+        d = inputs(B, H, T, D, dtype, 6)
+        y, end, ckpt = kda.gated_scan_fwd(d["x"], d["z"], d["A"], d["b"], d["s"], d["i"], want_ckpt=True)
+        r = kda.gated_scan_bwd(d["x"], d["z"], d["A"], d["b"], ckpt, d["dy"], None, d["i"])
+
+        def moved(t):
+            return torch.zeros(t.numel() + shift, dtype=dtype, device=DEV)[shift:].view(t.shape).copy_(t)
+
+        m = {k: moved(d[k]) for k in ("x", "z", "i", "dy")}
+        y2, end2, c2 = kda.gated_scan_fwd(m["x"], m["z"], d["A"], d["b"], d["s"], m["i"], want_ckpt=True, out=moved(y))
+        r2 = kda.gated_scan_bwd(m["x"], m["z"], d["A"], d["b"], c2, m["dy"], None, m["i"])
+        assert torch.equal(y, y2) and torch.equal(end, end2) and all(torch.equal(r[k], r2[k]) for k in r)
+
+
+def test_gradients_against_differences_of_the_kernel():
+    """Along random directions: the loss is a float64 sum of 2600 terms of size 1, each off by 50 e or so, over 2 h = 2^-6:
+    sqrt(2600) 50 2^-24 2^6 = 1e-2; cubic terms h^2 / 6 of third derivatives of size 10: 2600 4e-4 of either sign, 2e-2."""
+    B, H, T, D = 2, 2, 130, 5
+    d = inputs(B, H, T, D, FP, 12)
+    names = ["x", "z", "A", "b", "s", "i"]
+
+    def loss(v):
+        y, e, _ = kda.gated_scan_fwd(v["x"], v["z"], v["A"], v["b"], v["s"], v["i"])
+        return float((y.double() * d["dy"]).sum() + (e.double() * d["ds"]).sum())
+
+    ckpt = kda.gated_scan_fwd(*(d[k] for k in ("x", "z", "A", "b", "s", "i")), want_ckpt=True)[2]
+    g = kda.gated_scan_bwd(d["x"], d["z"], d["A"], d["b"], ckpt, d["dy"], d["ds"], d["i"])
+    grads = dict(x="dx", z="dz", A="dA_log", b="ddt_bias", s="dstate_in", i="dinput_gate")
+    h = 2.0 ** -7
+    for n in names:
+        v = torch.randn_like(d[n]) * 0.5
+        fd = (loss({**d, n: d[n] + h * v}) - loss({**d, n: d[n] - h * v})) / (2 * h)
+        an = float((g[grads[n]].double() * v).sum())
+        assert abs(fd - an) <= 0.05 + 3e-3 * abs(an), (n, fd, an)
+
+
+def test_offsets_past_32_bits():
+    """More than 2^32 bytes per tensor: the last head's last tokens give what they give alone from the same state."""
+    B, H, T, D = 1, 2, 1100000, 1024
+    x = torch.zeros((B, H, T, D), dtype=BF, device=DEV)
+    assert x.numel() > 2 ** 31
+    z = torch.zeros_like(x)
+    n = 600
+    x[-1, -1, -n:].normal_()
+    z[-1, -1, -n:].normal_()
+    A, b = torch.zeros(H, device=DEV), torch.full((H, D), -1.0, device=DEV)
+    y, end, ckpt = kda.gated_scan_fwd(x, z, A, b, want_ckpt=True)
+    last = lambda t: t[:, -1:, -n:].contiguous()
+    y1, end1, c1 = kda.gated_scan_fwd(last(x), last(z), A[:1], b[:1], want_ckpt=True)
+    tol = lambda a, r: np.linalg.norm(host(a) - host(r)) <= 2.0 ** -9 * np.linalg.norm(host(r))
+    assert tol(last(y), y1) and tol(end[:, -1:], end1) and not y[0, 0].any()
+    dy = y.zero_()
+    dy[-1, -1, -n:].normal_()
+    r = kda.gated_scan_bwd(x, z, A, b, ckpt, dy)
+    r1 = kda.gated_scan_bwd(last(x), last(z), A[:1], b[:1], c1, last(dy))
+    assert tol(last(r["dx"]), r1["dx"]) and tol(last(r["dz"]), r1["dz"]) and not r["dx"][0, 0].any()
+    assert np.abs(host(r["ddt_bias"][-1]) - host(r1["ddt_bias"][0])).max() <= 1e-4 * np.abs(host(r1["ddt_bias"])).max()
