@@ -8,9 +8,9 @@
 // Channels of all heads and sequences stand side by side: 64 lanes of E channels make a channel tile (E = 2 packs a
 // 4-byte access of bf16; odd head sizes and fp32 take 1).  Time is cut into tiles of NW waves of S tokens, one workgroup
 // each.  A wave keeps the decays and inputs of its S tokens in registers, so memory is read once: it folds them to one
-// pair (sum of g, state from zero), the workgroup's waves exchange these through LDS, and the state in front of the tile
-// comes from the tiles before it while the workgroup waits (look_back); then the wave runs over its tokens again from
-// the true state.
+// pair (decay over all of them, state from zero), the workgroup's waves put these into LDS, one wave fetches the state in
+// front of the tile from the tiles before it (look_back); then every wave takes that state over the pairs of the waves
+// in front of it and runs over its tokens again from the true one.
 //
 // Tiles hand their states on through the workspace.  Each publishes its own pair as soon as it has it, without
 // waiting for anything, then takes the pairs of the tiles before it from the nearest one on that knows its final state,
@@ -34,19 +34,35 @@ __device__ __forceinline__ float scan_softplus2(float x2, float& y) {
   return fmaf(y - (u - 1.0f), kLog2e, fast_log2(u)) + fmaxf(x2, 0.f);
 }
 
-// The decay e^g of g = g2 ln 2 <= 0 in one word.  A decay next to 1 rounded to fp32 is off to the same side in every
-// token of a channel whose gate hardly moves, by up to 2^-25 / |g| of the state after the 1 / |g| tokens it remembers.  So a
-// weak one (|g| < 1/8) is held as e = a - 1, with its sign bit set even when it is 0, a strong one as a.
-// e / g2 is a cubic within 3.5e-8 of (2^g2 - 1) / g2 there (interpolated at Chebyshev points).
-__device__ __forceinline__ float decay_word(float g2) {
-  const float e = g2 * fmaf(g2, fmaf(g2, fmaf(g2, 0.009150667116f, 0.05545188114f), 0.2402246296f), 0.6931471825f);
-  return g2 > -0.18033688f ? -fabsf(e) : fast_exp2(g2);
+// A token's decay e^g, g = g2 ln 2 <= 0, is held as e = e^g - 1.  A decay next to 1 rounded to fp32 would be off to the same
+// side in every token of a channel whose gate hardly moves, by up to 2^-25 / |g| of the state after the 1 / |g| tokens it
+// remembers; e is right to a rounding of itself there.  (Next to 0 it is right to 2^-25: what is left of a state after a
+// strong decay is right to 2^-24 of what it was a token before.)  For |g| < 1/8, e / g2 is a cubic within 3.5e-8 of
+// (2^g2 - 1) / g2 (interpolated at Chebyshev points).
+constexpr float kWeak = -0.18033688f;      // -1/8 in units of log2(e)
+__device__ __forceinline__ float decay_weak(float g2) {
+  return g2 * fmaf(g2, fmaf(g2, fmaf(g2, 0.009150667116f, 0.05545188114f), 0.2402246296f), 0.6931471825f);
 }
-__device__ __forceinline__ bool decay_weak(float v) { return (int)__float_as_uint(v) < 0; }
-__device__ __forceinline__ float decay_step(float v, float h, float u) { return fmaf(v, h, (decay_weak(v) ? h : 0.f) + u); }   // a h + u
-__device__ __forceinline__ float decay_a(float v) { return decay_weak(v) ? 1.f + v : v; }
-__device__ __forceinline__ float decay_n2(float v) { return decay_weak(v) ? -v * (2.f + v) : fmaf(-v, v, 1.f); }               // 1 - a^2
-constexpr float kNoDecay = -0.0f;
+__device__ __forceinline__ float decay_of(float g2) {
+  const float e = decay_weak(g2), f = fast_exp2(g2) - 1.0f;          // (both, and a selection: no branch)
+  return g2 > kWeak ? e : f;
+}
+__device__ __forceinline__ float decay_step(float e, float h, float u) { return fmaf(e, h, h) + u; }   // a h + u
+__device__ __forceinline__ float decay_n2(float e) { return -e * (2.f + e); }                         // 1 - a^2
+
+// The decay over many tokens in one word, which keeps its relative accuracy at both ends (a state may have been larger
+// than what is left of it by any factor): next to 1 its distance from 1, with the sign bit set even for 0, the decay
+// itself otherwise.
+__device__ __forceinline__ bool word_weak(float w) { return (int)__float_as_uint(w) < 0; }
+__device__ __forceinline__ float word_of(float g2) {
+  const float e = -fabsf(decay_weak(g2)), a = fast_exp2(g2);
+  return g2 > kWeak ? e : a;
+}
+__device__ __forceinline__ float word_step(float w, float h, float u) { return fmaf(w, h, (word_weak(w) ? h : 0.f) + u); }
+
+// A gate's argument (in units of log2(e)) whose softplus is 0, for tokens behind a sequence: g = 0, the state stays, and
+// with inputs of 0 nothing is added to it.
+constexpr float kNoDecay = -1e30f;
 
 // E elements of a row as loaded, at a byte offset from the tensor's start (32 bits where the tensors are below 4 GiB:
 // one offset then serves every tensor, which stay in scalar registers).
@@ -130,6 +146,7 @@ template <int E> __device__ __forceinline__ void look_back(const ScanLink& l, si
   asm volatile("" ::: "memory");
   get_words<E>(l.states + (first + from) * (64 * E) + lane, h);
   constexpr int U = 4;
+#pragma unroll 1
   for (int k = from + 1; k < j; k += U) {
     float pg[U][E], ph[U][E];
 #pragma unroll
@@ -142,7 +159,7 @@ template <int E> __device__ __forceinline__ void look_back(const ScanLink& l, si
     for (int u = 0; u < U; ++u)
       if (k + u < j)
 #pragma unroll
-        for (int e = 0; e < E; ++e) h[e] = decay_step(decay_word(pg[u][e]), h[e], ph[u][e]);
+        for (int e = 0; e < E; ++e) h[e] = word_step(pg[u][e], h[e], ph[u][e]);
   }
 }
 
@@ -166,7 +183,8 @@ template <int E> struct ScanLane {
   int h, d, n;
   long long bh;
   bool on;
-  float m, bias2[E];                       // bias2 = dt_bias log2(e)
+  float a_log, bias[E];                    // as loaded: nothing waits for them before the tile's own loads are issued
+  __device__ __forceinline__ float m() const { return gate_multiplier(a_log); }
 };
 template <int E> __device__ __forceinline__ ScanLane<E> scan_lane(const ScanArgs& a, int c, int lane) {
   const long long N = (long long)a.B * a.H * a.D;
@@ -179,14 +197,18 @@ template <int E> __device__ __forceinline__ ScanLane<E> scan_lane(const ScanArgs
   const uint32_t b = bh / (uint32_t)a.H;
   l.h = (int)(bh - b * (uint32_t)a.H);
   l.n = !l.on ? 0 : a.lengths ? min(max(a.lengths[b], 0), a.T) : a.T;
-  l.m = gate_multiplier(a.A_log[l.h]);
+  l.a_log = a.A_log[l.h];
 #pragma unroll
-  for (int e = 0; e < E; ++e) l.bias2[e] = a.dt_bias ? a.dt_bias[(size_t)l.h * a.D + l.d + e] * kLog2e : 0.f;
+  for (int e = 0; e < E; ++e) l.bias[e] = 0.f;
+  if (a.dt_bias)
+#pragma unroll
+    for (int e = 0; e < E; ++e) l.bias[e] = a.dt_bias[(size_t)l.h * a.D + l.d + e];
   return l;
 }
 
 // Tile shapes.  Forward: S = 16 tokens of decay and input are 64 registers at E = 2.  Backward: seven values a token.
-constexpr int kScanFwdWaves = 8, kScanFwdTokens = 16, kScanBwdWaves = 4, kScanBwdTokens = 8;
+constexpr int kScanFwdWaves = 8, kScanFwdTokens = 16;
+constexpr int kScanBwdWaves = 4, kScanBwdTokens = 8;
 
 template <typename T> hipError_t launch_scan_fwd_tiles(const ScanArgs& a, bool pairs, hipStream_t s);
 template <typename T> hipError_t launch_scan_bwd_tiles(const ScanArgs& a, bool pairs, hipStream_t s);

@@ -51,7 +51,7 @@ template <typename T, int E> __global__ __launch_bounds__(kScanThreads) void sca
   for (int e = 0; e < E; ++e) {
     float y, u = rx.at(e);
     const float bias2 = a.dt_bias ? a.dt_bias[(size_t)h * a.D + d + e] * kLog2e : 0.f;
-    const float v = decay_word(-m * scan_softplus2(fmaf(rz.at(e), kLog2e, bias2), y));
+    const float v = decay_of(-m * scan_softplus2(fmaf(rz.at(e), kLog2e, bias2), y));
     if (a.i) u *= scan_sigmoid(ri.at(e));
     if (a.normalize) u *= __builtin_amdgcn_sqrtf(decay_n2(v));
     st[e] = decay_step(v, a.state_out[ch + e], u);

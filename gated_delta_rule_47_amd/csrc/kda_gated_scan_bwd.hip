@@ -11,44 +11,40 @@ namespace {
 constexpr int NW = kScanBwdWaves, S = kScanBwdTokens;
 static_assert(NW * S == KDA_GATED_SCAN_CHUNK, "one kept state per tile");
 
-template <typename T, int E, bool GATE, bool NORM, typename Off>
-__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(3))) void scan_bwd_kernel(ScanArgs a) {
-  __shared__ uint32_t slot;
-  __shared__ float sG[NW][E][64], sH[NW][E][64], sR[NW][E][64], sIn[E][64];
-  const ScanTile tile = scan_tile(a, &slot);
-  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const ScanLane<E> l = scan_lane<E>(a, tile.c, lane);
+template <int E> struct ScanShared {
+  uint32_t slot;
+  float G[NW][E][64], W[NW][E][64], H[NW][E][64], R[NW][E][64], in[E][64];     // as forward; R: r from zero
+  float sum[2][NW][E][64];
+};
+
+// FULL: every token of the tile lies inside its sequence, in every lane (the same for all waves).
+template <typename T, int E, bool GATE, bool NORM, bool FULL, typename Off>
+__device__ __forceinline__ void scan_bwd_tile(const ScanArgs& a, ScanShared<E>& sh, const ScanTile tile, const ScanLane<E>& l,
+                                              int lane, int w) {
   const int jt = a.tiles - 1 - tile.j;     // place in time
   const int t0 = (jt * NW + w) * S;
   const Off row = (Off)a.D * sizeof(T);
-  const Off base = ((Off)l.bh * a.T + t0) * a.D * sizeof(T) + (Off)l.d * sizeof(T);
-  const bool full = __all(t0 + S <= l.n);
+  Off base = ((Off)l.bh * a.T + t0) * a.D * sizeof(T) + (Off)l.d * sizeof(T);
 
   ScanRaw<T, E> rz[S], rx[S], ri[S], rd[S];
-  if (full) {
 #pragma unroll
-    for (int k = 0; k < S; ++k) {
+  for (int k = 0; k < S; ++k) {
+    if constexpr (!FULL) rz[k].u = rx[k].u = ri[k].u = rd[k].u = 0;
+    if (FULL || t0 + k < l.n) {
       rz[k].load(a.z, base + k * row);
-      rx[k].load(a.x, base + k * row);
       if constexpr (GATE) ri[k].load(a.i, base + k * row);
+      rx[k].load(a.x, base + k * row);
       rd[k].load(a.dy, base + k * row);
     }
-  } else {
-#pragma unroll
-    for (int k = 0; k < S; ++k) {
-      rz[k].u = rx[k].u = ri[k].u = rd[k].u = 0;
-      if (t0 + k < l.n) {
-        rz[k].load(a.z, base + k * row);
-        rx[k].load(a.x, base + k * row);
-        if constexpr (GATE) ri[k].load(a.i, base + k * row);
-        rd[k].load(a.dy, base + k * row);
-      }
-    }
   }
-  float h0[E];
+  float h[E];
 #pragma unroll
-  for (int e = 0; e < E; ++e) h0[e] = l.on && jt * NW * S < a.T ? a.ckpt[((size_t)l.bh * a.tiles + jt) * a.D + l.d + e] : 0.f;
+  for (int e = 0; e < E; ++e) h[e] = FULL || (l.on && jt * NW * S < a.T) ? a.ckpt[((size_t)l.bh * a.tiles + jt) * a.D + l.d + e] : 0.f;
 
+  const float m = l.m();
+  float bias2[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) bias2[e] = l.bias[e] * kLog2e;
   // per token: the decay v, g2, q = m sigmoid(z'), c = n s, sm = 1 - s, k4 = a^2 s x / n
   float v[S][E], g[S][E], q[S][E], c[S][E], sm[S][E], k4[S][E], G[E], H[E], R[E];
 #pragma unroll
@@ -58,74 +54,75 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(3))) vo
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       float y;
-      const float p = fmaf(rz[k].at(e), kLog2e, l.bias2[e]);
-      g[k][e] = -l.m * scan_softplus2(p, y);
-      q[k][e] = l.m * fast_rcp(1.f + y) * (p >= 0.f ? 1.f : y);
-      v[k][e] = decay_word(g[k][e]);
+      const float p = FULL || t0 + k < l.n ? fmaf(rz[k].at(e), kLog2e, bias2[e]) : kNoDecay;
+      g[k][e] = -m * scan_softplus2(p, y);
+      q[k][e] = m * fast_rcp(1.f + y) * (p >= 0.f ? 1.f : y);
+      v[k][e] = decay_of(g[k][e]);
       const float s = GATE ? scan_sigmoid(ri[k].at(e)) : 1.f, x = rx[k].at(e);
       sm[k][e] = 1.f - s;
       c[k][e] = s;
       k4[k][e] = 0.f;
       if constexpr (NORM) {
         // n = 0 (a decay of exactly 1): 1 / n is held at 1e18, and q = 0 or tiny takes the term to its limit 0 in dz
-        const float n2 = decay_n2(v[k][e]), rn = __builtin_amdgcn_rsqf(fmaxf(n2, 1e-36f)), av = decay_a(v[k][e]);
+        const float n2 = decay_n2(v[k][e]), rn = __builtin_amdgcn_rsqf(fmaxf(n2, 1e-36f)), av = 1.f + v[k][e];
         c[k][e] = s * (n2 * rn);
         k4[k][e] = av * av * rn * (s * x);
       }
-      if (!full && t0 + k >= l.n) {        // behind the sequence: the state stays, nothing has a gradient
-        v[k][e] = kNoDecay;
-        g[k][e] = q[k][e] = c[k][e] = k4[k][e] = 0.f;
-      }
       G[e] += g[k][e];
       H[e] = decay_step(v[k][e], H[e], c[k][e] * x);
+      // (kept as they are: what the compiler would compute later from their parts takes more registers)
+      asm volatile("" : "+v"(v[k][e]), "+v"(g[k][e]), "+v"(q[k][e]));
+      if constexpr (GATE || NORM) asm volatile("" : "+v"(c[k][e]));
+      if constexpr (GATE) asm volatile("" : "+v"(sm[k][e]));
+      if constexpr (NORM) asm volatile("" : "+v"(k4[k][e]));
     }
+#pragma unroll
+  for (int k = 0; k < S; ++k) asm volatile("" : "+v"(rx[k].u), "+v"(rd[k].u));
 #pragma unroll
   for (int k = S - 1; k >= 0; --k)
 #pragma unroll
-    for (int e = 0; e < E; ++e) R[e] = decay_step(v[k][e], R[e] + rd[k].at(e), 0.f);
+    for (int e = 0; e < E; ++e) {
+      const float r = R[e] + rd[k].at(e);
+      R[e] = fmaf(v[k][e], r, r);
+    }
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    sG[w][e][lane] = G[e];
-    sH[w][e][lane] = H[e];
-    sR[w][e][lane] = R[e];
+    sh.G[w][e][lane] = G[e];
+    sh.W[w][e][lane] = word_of(G[e]);
+    sh.H[w][e][lane] = H[e];
+    sh.R[w][e][lane] = R[e];
   }
   __syncthreads();
-  // h in front of this wave's tokens; r behind them from a zero behind the tile
-  float h[E], Gs[E], Rs[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    h[e] = h0[e];
-    for (int p = 0; p < w; ++p) h[e] = decay_step(decay_word(sG[p][e][lane]), h[e], sH[p][e][lane]);
-    Gs[e] = Rs[e] = 0.f;
-    for (int p = NW - 1; p > w; --p) {
-      Rs[e] = decay_step(decay_word(sG[p][e][lane]), Rs[e], sR[p][e][lane]);
-      Gs[e] += sG[p][e][lane];
-    }
-  }
+  float r[E];
   if (w == 0) {
-    float Gt[E], Rt[E], in[E];
     const size_t first = (size_t)tile.c * a.tiles, rec = first + tile.j;
+    float Wt[E], Rt[E];                    // the tile's pair
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      Rt[e] = decay_step(decay_word(G[e]), Rs[e], R[e]);
-      Gt[e] = Gs[e] + G[e];
-      in[e] = 0.f;
-    }
+    for (int e = 0; e < E; ++e) Wt[e] = Rt[e] = r[e] = 0.f;
+#pragma unroll 1                           // (the registers are full of the wave's tokens)
+    for (int p = NW - 1; p >= 0; --p)
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        Rt[e] = word_step(sh.W[p][e][lane], Rt[e], sh.R[p][e][lane]);
+        Wt[e] += sh.G[p][e][lane];
+      }
+#pragma unroll
+    for (int e = 0; e < E; ++e) Wt[e] = word_of(Wt[e]);
     if (tile.j == 0) {
       if (a.d_state && l.on)
 #pragma unroll
-        for (int e = 0; e < E; ++e) in[e] = a.d_state[l.ch + e];
+        for (int e = 0; e < E; ++e) r[e] = a.d_state[l.ch + e];
     } else {
       float* pair = a.link.pairs + rec * (128 * E) + lane;
-      put_words<E>(pair, Gt);
+      put_words<E>(pair, Wt);
       put_words<E>(pair + 64 * E, Rt);
       publish(a.link.flags + rec, 1u);
-      look_back<E>(a.link, first, tile.j, lane, in);
+      look_back<E>(a.link, first, tile.j, lane, r);
     }
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      sIn[e][lane] = in[e];
-      Rt[e] = decay_step(decay_word(Gt[e]), in[e], Rt[e]);
+      sh.in[e][lane] = r[e];
+      Rt[e] = word_step(Wt[e], r[e], Rt[e]);
     }
     if (tile.j + 1 < a.tiles) {
       put_words<E>(a.link.states + rec * (64 * E) + lane, Rt);
@@ -135,21 +132,32 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(3))) vo
       for (int e = 0; e < E; ++e) a.d_state_in[l.ch + e] = Rt[e];
     }
   }
+  // h in front of this wave's tokens
+#pragma unroll 1
+  for (int p = 0; p < w; ++p)
+#pragma unroll
+    for (int e = 0; e < E; ++e) h[e] = word_step(sh.W[p][e][lane], h[e], sh.H[p][e][lane]);
   // dg / r = a h_{t-1} - a^2 s x / n of every token
 #pragma unroll
   for (int k = 0; k < S; ++k)
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      k4[k][e] = fmaf(decay_a(v[k][e]), h[e], -k4[k][e]);
-      h[e] = decay_step(v[k][e], h[e], c[k][e] * rx[k].at(e));
+      const float ah = fmaf(v[k][e], h[e], h[e]);
+      k4[k][e] = ah - k4[k][e];
+      h[e] = fmaf(c[k][e], rx[k].at(e), ah);
     }
   __syncthreads();
-  float r[E], sz[E], sa[E];
+  float sz[E], sa[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    r[e] = decay_step(decay_word(Gs[e]), sIn[e][lane], Rs[e]);
+    r[e] = sh.in[e][lane];
     sz[e] = sa[e] = 0.f;
   }
+#pragma unroll 1
+  for (int p = NW - 1; p > w; --p)
+#pragma unroll
+    for (int e = 0; e < E; ++e) r[e] = word_step(sh.W[p][e][lane], r[e], sh.R[p][e][lane]);
+  asm volatile("" : "+v"(base));           // the stores' offsets are computed anew, not kept in registers since the loads
 #pragma unroll
   for (int k = S - 1; k >= 0; --k) {
     float dx[E], dz[E], di[E];
@@ -160,25 +168,25 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(3))) vo
       di[e] = dx[e] * rx[k].at(e) * sm[k][e];
       const float dg = r[e] * k4[k][e];
       dz[e] = -dg * q[k][e];
-      if (!full && t0 + k >= l.n) dx[e] = di[e] = dz[e] = 0.f;
+      if (!FULL && t0 + k >= l.n) dx[e] = di[e] = dz[e] = 0.f;
       else {
         sz[e] += dz[e];
         sa[e] = fmaf(dg, g[k][e], sa[e]);
       }
-      r[e] = decay_step(v[k][e], r[e], 0.f);
+      r[e] = fmaf(v[k][e], r[e], r[e]);
     }
-    if (full || (l.on && t0 + k < a.T)) {
+    if (FULL || (l.on && t0 + k < a.T)) {
       scan_store<T, E>(a.dx, base + k * row, dx);
       scan_store<T, E>(a.dz, base + k * row, dz);
       if constexpr (GATE) scan_store<T, E>(a.di, base + k * row, di);
     }
   }
   if (!a.parts) return;
-  // the waves' sums in a fixed order (the exchange's arrays are free: every wave has read them before the barrier)
+  // the waves' sums in a fixed order
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    sG[w][e][lane] = sz[e];
-    sH[w][e][lane] = sa[e] * kLn2;
+    sh.sum[0][w][e][lane] = sz[e];
+    sh.sum[1][w][e][lane] = sa[e] * kLn2;
   }
   __syncthreads();
   if (w == 0 && l.on) {
@@ -188,13 +196,23 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(3))) vo
       float z = 0.f, s = 0.f;
 #pragma unroll
       for (int p = 0; p < NW; ++p) {
-        z += sG[p][e][lane];
-        s += sH[p][e][lane];
+        z += sh.sum[0][p][e][lane];
+        s += sh.sum[1][p][e][lane];
       }
       a.parts[(size_t)jt * N + l.ch + e] = z;
       a.parts[((size_t)a.tiles + jt) * N + l.ch + e] = s;
     }
   }
+}
+
+template <typename T, int E, bool GATE, bool NORM, typename Off>
+__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(3))) void scan_bwd_kernel(ScanArgs a) {
+  __shared__ ScanShared<E> sh;
+  const ScanTile tile = scan_tile(a, &sh.slot);
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const ScanLane<E> l = scan_lane<E>(a, tile.c, lane);
+  if (__all((a.tiles - tile.j) * (NW * S) <= l.n)) scan_bwd_tile<T, E, GATE, NORM, true, Off>(a, sh, tile, l, lane, w);
+  else scan_bwd_tile<T, E, GATE, NORM, false, Off>(a, sh, tile, l, lane, w);
 }
 
 template <typename T, int E, typename Off> void launch_e(const ScanArgs& a, hipStream_t s) {

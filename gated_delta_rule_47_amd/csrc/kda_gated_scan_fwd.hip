@@ -8,37 +8,34 @@ namespace {
 
 constexpr int NW = kScanFwdWaves, S = kScanFwdTokens;
 
-template <typename T, int E, bool GATE, bool NORM, typename Off>
-__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4))) void scan_fwd_kernel(ScanArgs a) {
-  __shared__ uint32_t slot;
-  __shared__ float sG[NW][E][64], sH[NW][E][64], sIn[E][64];
-  const ScanTile tile = scan_tile(a, &slot);
-  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const ScanLane<E> l = scan_lane<E>(a, tile.c, lane);
+template <int E> struct ScanShared {
+  uint32_t slot;
+  float G[NW][E][64], W[NW][E][64], H[NW][E][64], in[E][64];     // sums of g2, the decays over them, states from zero
+};
+
+// FULL: every token of the tile lies inside its sequence, in every lane (the same for all waves, whose lanes are the
+// same channels).
+template <typename T, int E, bool GATE, bool NORM, bool FULL, typename Off>
+__device__ __forceinline__ void scan_fwd_tile(const ScanArgs& a, ScanShared<E>& sh, const ScanTile tile, const ScanLane<E>& l,
+                                              int lane, int w) {
   const int t0 = (tile.j * NW + w) * S;
   const Off row = (Off)a.D * sizeof(T);
-  const Off base = ((Off)l.bh * a.T + t0) * a.D * sizeof(T) + (Off)l.d * sizeof(T);
-  const bool full = __all(t0 + S <= l.n);
+  Off base = ((Off)l.bh * a.T + t0) * a.D * sizeof(T) + (Off)l.d * sizeof(T);
 
   ScanRaw<T, E> rz[S], rx[S], ri[S];
-  if (full) {
 #pragma unroll
-    for (int k = 0; k < S; ++k) {
+  for (int k = 0; k < S; ++k) {
+    if constexpr (!FULL) rz[k].u = rx[k].u = ri[k].u = 0;
+    if (FULL || t0 + k < l.n) {
       rz[k].load(a.z, base + k * row);
       rx[k].load(a.x, base + k * row);
       if constexpr (GATE) ri[k].load(a.i, base + k * row);
     }
-  } else {
-#pragma unroll
-    for (int k = 0; k < S; ++k) {
-      rz[k].u = rx[k].u = ri[k].u = 0;
-      if (t0 + k < l.n) {
-        rz[k].load(a.z, base + k * row);
-        rx[k].load(a.x, base + k * row);
-        if constexpr (GATE) ri[k].load(a.i, base + k * row);
-      }
-    }
   }
+  const float m = l.m();
+  float bias2[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) bias2[e] = l.bias[e] * kLog2e;
   float v[S][E], u[S][E], G[E], H[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) G[e] = H[e] = 0.f;
@@ -47,59 +44,55 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4))) vo
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       float y;
-      float g2 = -l.m * scan_softplus2(fmaf(rz[k].at(e), kLog2e, l.bias2[e]), y);
+      const float p = FULL || t0 + k < l.n ? fmaf(rz[k].at(e), kLog2e, bias2[e]) : kNoDecay;
+      const float g2 = -m * scan_softplus2(p, y);
       float uu = rx[k].at(e);
-      v[k][e] = decay_word(g2);
       if constexpr (GATE) uu *= scan_sigmoid(ri[k].at(e));
-      if constexpr (NORM) uu *= __builtin_amdgcn_sqrtf(decay_n2(v[k][e]));
-      if (!full && t0 + k >= l.n) {        // behind the sequence: the state stays
-        v[k][e] = kNoDecay;
-        uu = g2 = 0.f;
-      }
+      const float d = decay_of(g2);
+      if constexpr (NORM) uu *= __builtin_amdgcn_sqrtf(decay_n2(d));
+      v[k][e] = d;
       u[k][e] = uu;
       G[e] += g2;
-      H[e] = decay_step(v[k][e], H[e], uu);
+      H[e] = decay_step(d, H[e], uu);
+      asm volatile("" : "+v"(v[k][e]), "+v"(u[k][e]));     // (not to be computed later from parts that take more registers)
     }
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    sG[w][e][lane] = G[e];
-    sH[w][e][lane] = H[e];
+    sh.G[w][e][lane] = G[e];
+    sh.W[w][e][lane] = word_of(G[e]);
+    sh.H[w][e][lane] = H[e];
   }
   __syncthreads();
-  // the waves in front of this one, from a state of zero
-  float Gp[E], Hp[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    Gp[e] = Hp[e] = 0.f;
-    for (int p = 0; p < w; ++p) {
-      Hp[e] = decay_step(decay_word(sG[p][e][lane]), Hp[e], sH[p][e][lane]);
-      Gp[e] += sG[p][e][lane];
-    }
-  }
+  float h[E];
   if (w == NW - 1) {
-    float Gt[E], Ht[E], in[E];
     const size_t first = (size_t)tile.c * a.tiles, rec = first + tile.j;
+    float Wt[E], Ht[E];                    // the tile's pair
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      Ht[e] = decay_step(decay_word(G[e]), Hp[e], H[e]);
-      Gt[e] = Gp[e] + G[e];
-      in[e] = 0.f;
-    }
+    for (int e = 0; e < E; ++e) Wt[e] = Ht[e] = h[e] = 0.f;
+#pragma unroll 1                           // (the registers are full of the wave's tokens)
+    for (int p = 0; p < NW; ++p)
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        Ht[e] = word_step(sh.W[p][e][lane], Ht[e], sh.H[p][e][lane]);
+        Wt[e] += sh.G[p][e][lane];
+      }
+#pragma unroll
+    for (int e = 0; e < E; ++e) Wt[e] = word_of(Wt[e]);
     if (tile.j == 0) {
       if (a.state_in && l.on)
 #pragma unroll
-        for (int e = 0; e < E; ++e) in[e] = a.state_in[l.ch + e];
+        for (int e = 0; e < E; ++e) h[e] = a.state_in[l.ch + e];
     } else {
       float* pair = a.link.pairs + rec * (128 * E) + lane;
-      put_words<E>(pair, Gt);
+      put_words<E>(pair, Wt);
       put_words<E>(pair + 64 * E, Ht);
       publish(a.link.flags + rec, 1u);
-      look_back<E>(a.link, first, tile.j, lane, in);
+      look_back<E>(a.link, first, tile.j, lane, h);
     }
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      sIn[e][lane] = in[e];
-      Ht[e] = decay_step(decay_word(Gt[e]), in[e], Ht[e]);
+      sh.in[e][lane] = h[e];
+      Ht[e] = word_step(Wt[e], h[e], Ht[e]);
     }
     if (tile.j + 1 < a.tiles) {
       put_words<E>(a.link.states + rec * (64 * E) + lane, Ht);
@@ -107,24 +100,38 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4))) vo
     }
   }
   __syncthreads();
-  float h[E];
 #pragma unroll
-  for (int e = 0; e < E; ++e) h[e] = decay_step(decay_word(Gp[e]), sIn[e][lane], Hp[e]);
+  for (int e = 0; e < E; ++e) h[e] = sh.in[e][lane];
+#pragma unroll 1
+  for (int p = 0; p < w; ++p)
+#pragma unroll
+    for (int e = 0; e < E; ++e) h[e] = word_step(sh.W[p][e][lane], h[e], sh.H[p][e][lane]);
   static_assert(KDA_GATED_SCAN_CHUNK % S == 0, "a kept state stands in front of a wave's tokens");
   if (a.ckpt && t0 % KDA_GATED_SCAN_CHUNK == 0 && t0 < a.T && l.on) {
     const int chunks = (a.T + KDA_GATED_SCAN_CHUNK - 1) / KDA_GATED_SCAN_CHUNK;
 #pragma unroll
     for (int e = 0; e < E; ++e) a.ckpt[((size_t)l.bh * chunks + t0 / KDA_GATED_SCAN_CHUNK) * a.D + l.d + e] = h[e];
   }
+  asm volatile("" : "+v"(base));           // the stores' offsets are computed anew, not kept in registers since the loads
 #pragma unroll
   for (int k = 0; k < S; ++k) {
 #pragma unroll
     for (int e = 0; e < E; ++e) h[e] = decay_step(v[k][e], h[e], u[k][e]);
-    if (full || t0 + k < l.n) scan_store<T, E>(a.y, base + k * row, h);
+    if (FULL || t0 + k < l.n) scan_store<T, E>(a.y, base + k * row, h);
   }
   if (w == NW - 1 && tile.j + 1 == a.tiles && a.state_out && l.on)
 #pragma unroll
     for (int e = 0; e < E; ++e) a.state_out[l.ch + e] = h[e];
+}
+
+template <typename T, int E, bool GATE, bool NORM, typename Off>
+__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4))) void scan_fwd_kernel(ScanArgs a) {
+  __shared__ ScanShared<E> sh;
+  const ScanTile tile = scan_tile(a, &sh.slot);
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const ScanLane<E> l = scan_lane<E>(a, tile.c, lane);
+  if (__all((tile.j + 1) * (NW * S) <= l.n)) scan_fwd_tile<T, E, GATE, NORM, true, Off>(a, sh, tile, l, lane, w);
+  else scan_fwd_tile<T, E, GATE, NORM, false, Off>(a, sh, tile, l, lane, w);
 }
 
 template <typename T, int E, typename Off> void launch_e(const ScanArgs& a, hipStream_t s) {

@@ -507,8 +507,8 @@ int kda_rope_frequencies(double* freqs, double* rope_scale, int R, double base, 
  *             rows there become zero, the final state is the one after the last token.
  *   B, H, D >= 1;  T >= 0;  T <= 2^28;  B * H * D <= 2^28;  ceil(B * H * D / 64) * ceil(T / 32) <= 2^23 (KDA_ERR_SHAPE;
  *             2^34 elements of many channels).  Pointers need the alignment of an element only.
- * Gates, states and sums are fp32; a decay within 1/8 of 1 in the logarithm is held as its distance from 1, so slow decays do
- * not drift over long sequences.  A non-finite value reaches its own channel only, from its token on. */
+ * Gates, states and sums are fp32.  A decay is held as its distance from 1: slow ones do not drift over long sequences, and
+ * what a strong one leaves of a state is right to 2^-24 of the state before it.  A non-finite value reaches its own channel only, from its token on. */
 
 /* Tokens between the states that the forward pass keeps for the backward pass. */
 #define KDA_GATED_SCAN_CHUNK 32
