@@ -13,7 +13,7 @@
 namespace kda {
 namespace {
 
-constexpr int kConvThreads = 256;
+constexpr int kConvThreads = 256, kConvStepBatch = 2;
 
 __device__ __forceinline__ float sigmoid_f(float x) { return fast_rcp(1.0f + fast_exp2(-kLog2e * x)); }
 
@@ -95,7 +95,7 @@ template <typename T, int W, int E> __global__ __launch_bounds__(kConvThreads) v
     }
     const T* x = (const T*)a.x + p.b * a.xb + p.t0 * a.xt + p.c;
     T* y = (T*)a.y + (((size_t)p.b * a.H + p.c / a.D) * a.T + p.t0) * a.D + p.c % a.D;
-    constexpr int U = 8;
+    constexpr int U = sizeof(T) == 2 ? 8 : 4;
     for (int t = p.t0; t < t1; t += U, x += U * a.xt, y += (size_t)U * a.D) {
       Elems<T, E> raw[U];
 #pragma unroll
@@ -131,30 +131,42 @@ template <typename T, int W, int E> __global__ __launch_bounds__(kConvThreads) v
     }
 }
 
-// One token: the state's rows move up by one.
+// One token: the state's rows move up by one.  A lane takes NB sequences of its channels, whose weights it reads once.
 template <typename T, int W, int E> __global__ __launch_bounds__(kConvThreads) void conv_step_kernel(ConvArgs a) {
+  constexpr int NB = kConvStepBatch;
   const unsigned id = blockIdx.x * kConvThreads + threadIdx.x, vecs = a.C / E;
-  const unsigned b = id / vecs;
+  const unsigned b0 = id / vecs * NB;
   const int c = (int)(id % vecs) * E;
-  if (b >= (unsigned)a.B) return;
-  T* state = (T*)a.state_out + (size_t)b * (W - 1) * a.C + c;
-  Elems<T, E> row[W];
-  row[W - 1].load((const T*)a.x + b * a.xb + c);
+  if (b0 >= (unsigned)a.B) return;
+  Elems<T, E> row[NB][W];
 #pragma unroll
-  for (int j = 0; j < W - 1; ++j) row[j].load(state + (size_t)j * a.C);
-  float w[W][E], o[E];
-  conv_weights<W, E>(a, c, w, o);
+  for (int k = 0; k < NB; ++k) {
+    if (b0 + k >= (unsigned)a.B) break;
+    const T* state = (const T*)a.state_out + (size_t)(b0 + k) * (W - 1) * a.C + c;
+    row[k][W - 1].load((const T*)a.x + (b0 + k) * a.xb + c);
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-#pragma unroll
-    for (int j = 0; j < W; ++j) o[e] = fmaf(w[j][e], row[j].at(e), o[e]);
-    if (a.silu) o[e] *= sigmoid_f(o[e]);
+    for (int j = 0; j < W - 1; ++j) row[k][j].load(state + (size_t)j * a.C);
   }
-  Elems<T, E> out;
-  out.set(o);
-  out.store((T*)a.y + (size_t)b * a.C + c);
+  float w[W][E], bias[E];
+  conv_weights<W, E>(a, c, w, bias);
 #pragma unroll
-  for (int j = 0; j < W - 1; ++j) row[j + 1].store(state + (size_t)j * a.C);
+  for (int k = 0; k < NB; ++k) {
+    if (b0 + k >= (unsigned)a.B) break;
+    T* state = (T*)a.state_out + (size_t)(b0 + k) * (W - 1) * a.C + c;
+    float o[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      o[e] = bias[e];
+#pragma unroll
+      for (int j = 0; j < W; ++j) o[e] = fmaf(w[j][e], row[k][j].at(e), o[e]);
+      if (a.silu) o[e] *= sigmoid_f(o[e]);
+    }
+    Elems<T, E> out;
+    out.set(o);
+    out.store((T*)a.y + (size_t)(b0 + k) * a.C + c);
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) row[k][j + 1].store(state + (size_t)j * a.C);
+  }
 }
 
 // Tokens t0 .. t0 + run - 1 give their dx and their share of dw and db; dpre is computed for W - 1 tokens more.
@@ -186,18 +198,28 @@ template <typename T, int W, int E> __global__ __launch_bounds__(kConvThreads) v
     const T* x = (const T*)a.x + p.b * a.xb + p.t0 * a.xt + p.c;
     const T* dy = (const T*)a.dy + (((size_t)p.b * a.H + p.c / a.D) * a.T + p.t0) * a.D + p.c % a.D;
     T* dx = (T*)a.dx + p.b * a.db + ((long long)p.t0 - (W - 1)) * a.dt + p.c;
-    constexpr int U = 4;
-    for (int t = p.t0; t < t1; t += U, x += U * a.xt, dy += (size_t)U * a.D, dx += U * a.dt) {
-      Elems<T, E> rx[U], rd[U];
+    constexpr int U = 2;
+    // the next U tokens' rows are on their way while these are worked on
+    Elems<T, E> nx[U], nd[U];
+    const auto fetch = [&](int t) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        rx[u].zero();
-        rd[u].zero();
+        nx[u].zero();
+        nd[u].zero();
         if (t + u < t1 && t + u < n) {
-          rx[u].load(x + u * a.xt);
-          rd[u].load(dy + (size_t)u * a.D);
+          nx[u].load(x + u * a.xt);
+          nd[u].load(dy + (size_t)u * a.D);
         }
       }
+      x += U * a.xt;
+      dy += (size_t)U * a.D;
+    };
+    fetch(p.t0);
+    for (int t = p.t0; t < t1; t += U, dx += U * a.dt) {
+      Elems<T, E> rx[U], rd[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) rx[u] = nx[u], rd[u] = nd[u];
+      fetch(t + U);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int r = t + u - (W - 1);   // the row whose gradient is complete with dpre of t + u
@@ -284,8 +306,9 @@ template <int W> __global__ __launch_bounds__(kSumThreads) void conv_params_kern
 
 template <typename T> constexpr int conv_e(bool bwd) { return bwd || sizeof(T) == 4 ? 4 : 8; }
 
-// Lanes along the channels (all of them, up to a wave), tokens of a run: about 2^18 lanes over the chip (16 waves per
-// CU), a run of 8 to 128 tokens, longer where the grid would pass 2^23 workgroups.
+// Lanes along the channels (all of them, up to a wave), tokens of a run: about 2^17 lanes over the chip (8 waves per
+// CU, which a run of 128 tokens keeps in flight; 2^18 lanes: forward 124 for 109 us at 2 x 16384 x 4096, backward 95 for 93 at
+// 2 x 8192 x 4096), a run of 8 to 128 tokens, longer where the grid would pass 2^23 workgroups.
 void conv_plan(ConvArgs& a, int E) {
   const int vecs = a.C / E;
   a.lanes_log2 = 0;
@@ -293,7 +316,7 @@ void conv_plan(ConvArgs& a, int E) {
   const int lanes = 1 << a.lanes_log2, runs = kConvThreads / lanes;
   const long long cblocks = (vecs + lanes - 1) / lanes;
   long long run = 8;
-  while (run < 128 && (long long)a.B * a.T / run * vecs > (1 << 18)) run *= 2;
+  while (run < 128 && (long long)a.B * a.T / run * vecs > (1 << 17)) run *= 2;
   while (a.B * cblocks * ((a.T + run * runs - 1) / (run * runs)) > (1 << 23) && run * runs < a.T) run *= 2;
   a.run = (int)run;
   a.blocks_t = (int)((a.T + run * runs - 1) / (run * runs));
@@ -332,7 +355,7 @@ hipError_t launch_conv_step(const void* x, long long xb, const float* w, const f
   ConvArgs a = {};
   a.x = x, a.xb = xb, a.w = w, a.bias = bias, a.y = y, a.state_out = state, a.B = B, a.C = C, a.silu = silu;
   constexpr int E = conv_e<T>(false);
-  const unsigned grid = (unsigned)(((long long)B * (C / E) + kConvThreads - 1) / kConvThreads);
+  const unsigned grid = (unsigned)(((long long)((B + kConvStepBatch - 1) / kConvStepBatch) * (C / E) + kConvThreads - 1) / kConvThreads);
   KDA_CONV_W(W_, (conv_step_kernel<T, W, E><<<grid, kConvThreads, 0, s>>>(a)))
   return hipGetLastError();
 }

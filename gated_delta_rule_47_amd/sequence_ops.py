@@ -13,7 +13,7 @@ import ctypes
 import torch
 
 from . import _lib, KdaError
-from .layer_ops import _F32, _I32, _bytes, _code, _gpu, _opt, _ptr, _refuse, _run, _workspace
+from .layer_ops import _F32, _I32, _U8, _bytes, _code, _gpu, _opt, _ptr, _refuse
 
 __all__ = ["short_conv_fwd", "short_conv_step", "short_conv_bwd_workspace_bytes", "short_conv_bwd", "qk_norm_rope_fwd",
            "qk_norm_rope_bwd_workspace_bytes", "qk_norm_rope_bwd", "rope_frequencies", "GATED_SCAN_CHUNK",
@@ -35,15 +35,47 @@ def _one_of(name, value, table):
 
 
 def _strided(name, t, shape, dtype, dev):
-    """Address of a tensor of this shape whose last axis is dense; its strides are the caller's."""
+    """(address, strides) of a tensor of this shape whose last axis is dense; the other strides are the caller's."""
     try:
-        if t.shape == shape and t.dtype is dtype and t.get_device() == dev and (t.stride(-1) == 1 or shape[-1] == 1 or not t.numel()):
-            return t.data_ptr()
+        st = t.stride()
+        if t.shape == shape and t.dtype is dtype and t.get_device() == dev and (st[-1] == 1 or shape[-1] == 1 or not t.numel()):
+            return t.data_ptr(), st
     except AttributeError:
         pass
     if isinstance(t, torch.Tensor) and tuple(t.shape) == tuple(shape) and t.dtype == dtype and t.get_device() == dev:
         raise ValueError("%s must have its channels next to each other" % name)
     _refuse(name, t, shape, dtype, dev)
+
+
+_entries = {}
+_stream = torch._C._cuda_getCurrentRawStream
+_device = torch._C._cuda_getDevice
+
+
+def _run(dev, fn, *args):
+    """The call on GPU dev's current stream, with dev current while it launches."""
+    f = _entries.get(fn)
+    if f is None:
+        f = _entries[fn] = getattr(_lib.load(), fn)
+    if dev == _device():
+        st = f(*args, _stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            st = f(*args, _stream(dev))
+    if st:
+        raise KdaError(fn, st)
+
+
+def _workspace(workspace, need, like):
+    """(tensor kept alive, address, bytes): the caller's, or `need` bytes from torch's caching allocator."""
+    if workspace is None:
+        if not need:
+            return None, None, 0
+        workspace = like.new_empty(need, dtype=_U8)
+        return workspace, workspace.data_ptr(), need
+    if workspace.get_device() != like.get_device() or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous and on the call's GPU")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def short_conv_fwd(x, weight, bias=None, state_in=None, lengths=None, activation="silu", heads=1, output_state=True,
@@ -60,20 +92,20 @@ def short_conv_fwd(x, weight, bias=None, state_in=None, lengths=None, activation
     if heads < 1 or C % heads:
         raise ValueError("%d channels do not make %r heads" % (C, heads))
     shape, state = (B, heads, T, C // heads), (B, W - 1, C)
-    px = _strided("x", x, (B, T, C), dt, dev)
+    px, sx = _strided("x", x, (B, T, C), dt, dev)
     pw, pb = _ptr("weight", weight, (C, W), _F32, dev), _opt("bias", bias, (C,), _F32, dev)
     pn, ps = _opt("lengths", lengths, (B,), _I32, dev), _opt("state_in", state_in, state, dt, dev)
     po, pe = _opt("out", out, shape, dt, dev), _opt("state_out", state_out, state, dt, dev)
     _gpu(dev)
     if out is None:
-        out = torch.empty(shape, dtype=dt, device=x.device)
+        out = x.new_empty(shape)
         po = out.data_ptr()
     if not output_state:
         state_out = pe = None
     elif state_out is None:
-        state_out = torch.empty(state, dtype=dt, device=x.device)
+        state_out = x.new_empty(state)
         pe = state_out.data_ptr()
-    _run(dev, "kda_short_conv_fwd", px, x.stride(0), x.stride(1), pw, pb, pn, ps, act, po, pe, B, heads, T, C // heads, W,
+    _run(dev, "kda_short_conv_fwd", px, sx[0], sx[1], pw, pb, pn, ps, act, po, pe, B, heads, T, C // heads, W,
          code)
     return out, state_out
 
@@ -84,15 +116,15 @@ def short_conv_step(x, weight, bias, state, activation="silu", out=None):
     W = weight.shape[-1]
     dt, dev = x.dtype, x.get_device()
     code, act = _code(dt), _one_of("activation", activation, _ACTS)
-    px = _strided("x", x, (B, C), dt, dev)
+    px, sx = _strided("x", x, (B, C), dt, dev)
     pw, pb = _ptr("weight", weight, (C, W), _F32, dev), _opt("bias", bias, (C,), _F32, dev)
     ps = _ptr("state", state, (B, W - 1, C), dt, dev)
     po = _opt("out", out, (B, C), dt, dev)
     _gpu(dev)
     if out is None:
-        out = torch.empty((B, C), dtype=dt, device=x.device)
+        out = x.new_empty((B, C))
         po = out.data_ptr()
-    _run(dev, "kda_short_conv_step", px, x.stride(0), pw, pb, act, ps, po, B, 1, C, W, code)
+    _run(dev, "kda_short_conv_step", px, sx[0], pw, pb, act, ps, po, B, 1, C, W, code)
     return out
 
 
@@ -112,26 +144,24 @@ def short_conv_bwd(x, weight, bias, state_in, dy, d_state_out=None, lengths=None
     H = dy.shape[1]
     if H < 1 or C % H:
         raise ValueError("%d channels do not make %d heads" % (C, H))
-    px = _strided("x", x, (B, T, C), dt, dev)
+    px, sx = _strided("x", x, (B, T, C), dt, dev)
     pw, pb = _ptr("weight", weight, (C, W), _F32, dev), _opt("bias", bias, (C,), _F32, dev)
     pn, ps = _opt("lengths", lengths, (B,), _I32, dev), _opt("state_in", state_in, (B, W - 1, C), dt, dev)
     pd = _ptr("dy", dy, (B, H, T, C // H), dt, dev)
     pe = _opt("d_state_out", d_state_out, (B, W - 1, C), _F32, dev)
-    pdx = None if dx_out is None else _strided("dx_out", dx_out, (B, T, C), dt, dev)
-    _gpu(dev)
     if dx_out is None:
-        dx_out = torch.empty((B, T, C), dtype=dt, device=x.device)
-        pdx = dx_out.data_ptr()
-    d0 = torch.empty((B, W - 1, C), dtype=_F32, device=x.device)
+        dx_out = x.new_empty((B, T, C))
+    pdx, sdx = _strided("dx_out", dx_out, (B, T, C), dt, dev)
+    _gpu(dev)
+    d0 = weight.new_empty((B, W - 1, C))
     dw = db = pdw = pdb = None
     need = 0
     if want_params:
-        dw, db = torch.empty((C, W), dtype=_F32, device=x.device), torch.empty((C,), dtype=_F32, device=x.device)
+        dw, db = torch.empty_like(weight), weight.new_empty((C,))
         pdw, pdb = dw.data_ptr(), db.data_ptr()
         need = _bytes("kda_short_conv_bwd_workspace_bytes", B, H, T, C // H, W, code)
-    ws, pws, nws = _workspace(workspace, need, dev)
-    _run(dev, "kda_short_conv_bwd", px, x.stride(0), x.stride(1), pw, pb, pn, ps, act, pd, pe, pdx, dx_out.stride(0),
-         dx_out.stride(1), pdw, pdb, d0.data_ptr(), pws, nws, B, H, T, C // H, W, code)
+    ws, pws, nws = _workspace(workspace, need, weight)
+    _run(dev, "kda_short_conv_bwd", px, sx[0], sx[1], pw, pb, pn, ps, act, pd, pe, pdx, sdx[0], sdx[1], pdw, pdb, d0.data_ptr(), pws, nws, B, H, T, C // H, W, code)
     return dict(dx=dx_out, dweight=dw, dbias=db, dstate_in=d0)
 
 
@@ -158,14 +188,14 @@ def _side(name, x, B, T, D, weight, dt, dev):
             raise ValueError("%s_weight without %s" % (name, name))
         return 0, 1, None, (0, 0, 0), None
     H = x.shape[2]
-    px = _strided(name, x, (B, T, H, D), dt, dev)
+    px, sx = _strided(name, x, (B, T, H, D), dt, dev)
     pw, Hw = None, 1
     if weight is not None:
         Hw = weight.shape[0]
         if Hw not in (1, H):
             raise ValueError("%s_weight has %d rows for %d heads" % (name, Hw, H))
         pw = _ptr(name + "_weight", weight, (Hw, D), _F32, dev)
-    return H, Hw, px, x.stride()[:3], pw
+    return H, Hw, px, sx[:3], pw
 
 
 def _rope(freqs, positions, B, T, dev):
@@ -190,12 +220,12 @@ def qk_norm_rope_fwd(q, k, freqs, positions=None, norm="rms", q_weight=None, k_w
     pe = None if k is None else _opt("k_out", k_out, (B, Hk, T, D), dt, dev)
     _gpu(dev)
     if q_out is None:
-        q_out = torch.empty((B, Hq, T, D), dtype=dt, device=q.device)
+        q_out = q.new_empty((B, Hq, T, D))
         po = q_out.data_ptr()
     if k is None:
         k_out = None
     elif k_out is None:
-        k_out = torch.empty((B, Hk, T, D), dtype=dt, device=q.device)
+        k_out = q.new_empty((B, Hk, T, D))
         pe = k_out.data_ptr()
     _run(dev, "kda_qk_norm_rope_fwd", pq, *sq, pk, *sk, pqw, Hqw, pkw, Hkw, kind, float(eps), pf, pp, float(rope_scale),
          int(bool(interleaved)), po, pe, B, T, Hq, Hk, D, R, code)
@@ -219,20 +249,17 @@ def qk_norm_rope_bwd(q, k, freqs, d_q, d_k, positions=None, norm="rms", q_weight
     R, pf, pp = _rope(freqs, positions, B, T, dev)
     pdq = _ptr("d_q", d_q, (B, Hq, T, D), dt, dev)
     pdk = None if k is None else _ptr("d_k", d_k, (B, Hk, T, D), dt, dev)
-    poq = None if dq_out is None else _strided("dq_out", dq_out, (B, T, Hq, D), dt, dev)
-    pok = None if k is None or dk_out is None else _strided("dk_out", dk_out, (B, T, Hk, D), dt, dev)
-    _gpu(dev)
     if dq_out is None:
-        dq_out = torch.empty((B, T, Hq, D), dtype=dt, device=q.device)
-        poq = dq_out.data_ptr()
-    soq, sok = dq_out.stride()[:3], (0, 0, 0)
+        dq_out = q.new_empty((B, T, Hq, D))
+    poq, soq = _strided("dq_out", dq_out, (B, T, Hq, D), dt, dev)
+    pok, sok = None, (0, 0, 0, 1)
     if k is None:
         dk_out = None
     else:
         if dk_out is None:
-            dk_out = torch.empty((B, T, Hk, D), dtype=dt, device=q.device)
-            pok = dk_out.data_ptr()
-        sok = dk_out.stride()[:3]
+            dk_out = q.new_empty((B, T, Hk, D))
+        pok, sok = _strided("dk_out", dk_out, (B, T, Hk, D), dt, dev)
+    _gpu(dev)
     dqw = dkw = pgq = pgk = None
     if q_weight is not None:
         dqw = torch.empty_like(q_weight)
@@ -243,9 +270,9 @@ def qk_norm_rope_bwd(q, k, freqs, d_q, d_k, positions=None, norm="rms", q_weight
     need = 0
     if pgq is not None or pgk is not None:
         need = _bytes("kda_qk_norm_rope_bwd_workspace_bytes", B, T, Hq, Hqw, Hk, Hkw, D)
-    ws, pws, nws = _workspace(workspace, need, dev)
+    ws, pws, nws = _workspace(workspace, need, q)
     _run(dev, "kda_qk_norm_rope_bwd", pq, *sq, pk, *sk, pqw, Hqw, pkw, Hkw, kind, float(eps), pf, pp, float(rope_scale),
-         int(bool(interleaved)), pdq, pdk, poq, *soq, pok, *sok, pgq, pgk, pws, nws, B, T, Hq, Hk, D, R, code)
+         int(bool(interleaved)), pdq, pdk, poq, *soq[:3], pok, *sok[:3], pgq, pgk, pws, nws, B, T, Hq, Hk, D, R, code)
     return dict(dq=dq_out, dk=dk_out, dq_weight=dqw, dk_weight=dkw)
 
 
@@ -272,18 +299,18 @@ def gated_scan_fwd(x, z, A_log, dt_bias=None, state_in=None, input_gate=None, le
     po, pe = _opt("out", out, shape, dt, dev), _opt("state_out", state_out, state, _F32, dev)
     _gpu(dev)
     if out is None:
-        out = torch.empty(shape, dtype=dt, device=x.device)
+        out = torch.empty_like(x)
         po = out.data_ptr()
     if not output_state:
         state_out = pe = None
     elif state_out is None:
-        state_out = torch.empty(state, dtype=_F32, device=x.device)
+        state_out = A_log.new_empty(state)
         pe = state_out.data_ptr()
     ckpt = pc = None
     if want_ckpt:
-        ckpt = torch.empty((B, H, -(-T // GATED_SCAN_CHUNK), D), dtype=_F32, device=x.device)
+        ckpt = A_log.new_empty((B, H, -(-T // GATED_SCAN_CHUNK), D))
         pc = ckpt.data_ptr()
-    ws, pw, nw = _workspace(workspace, _bytes("kda_gated_scan_workspace_bytes", B, H, T, D, code), dev)
+    ws, pw, nw = _workspace(workspace, _bytes("kda_gated_scan_workspace_bytes", B, H, T, D, code), A_log)
     _run(dev, "kda_gated_scan_fwd", px, pz, pa, pb, pi, pn, ps, int(bool(normalize)), po, pe, pc, pw, nw, B, H, T, D, code)
     return out, state_out, ckpt
 
@@ -326,14 +353,13 @@ def gated_scan_bwd(x, z, A_log, dt_bias, ckpt, dy, d_state_out=None, input_gate=
     pc = _ptr("ckpt", ckpt, (B, H, -(-T // GATED_SCAN_CHUNK), D), _F32, dev)
     pe, pn = _opt("d_state_out", d_state_out, state, _F32, dev), _opt("lengths", lengths, (B,), _I32, dev)
     _gpu(dev)
-    dx, dz = torch.empty(shape, dtype=dt, device=x.device), torch.empty(shape, dtype=dt, device=x.device)
+    dx, dz = torch.empty_like(x), torch.empty_like(x)
     di = pdi = None
     if input_gate is not None:
-        di = torch.empty(shape, dtype=dt, device=x.device)
+        di = torch.empty_like(x)
         pdi = di.data_ptr()
-    dA, db = torch.empty((H,), dtype=_F32, device=x.device), torch.empty((H, D), dtype=_F32, device=x.device)
-    ds = torch.empty(state, dtype=_F32, device=x.device)
-    ws, pw, nw = _workspace(workspace, _bytes("kda_gated_scan_bwd_workspace_bytes", B, H, T, D, code), dev)
+    dA, db, ds = torch.empty_like(A_log), A_log.new_empty((H, D)), A_log.new_empty(state)
+    ws, pw, nw = _workspace(workspace, _bytes("kda_gated_scan_bwd_workspace_bytes", B, H, T, D, code), A_log)
     _run(dev, "kda_gated_scan_bwd", px, pz, pa, pb, pi, pn, int(bool(normalize)), pc, pd, pe, dx.data_ptr(), dz.data_ptr(),
          pdi, dA.data_ptr(), db.data_ptr(), ds.data_ptr(), pw, nw, B, H, T, D, code)
     return dict(dx=dx, dz=dz, dinput_gate=di, dA_log=dA, ddt_bias=db, dstate_in=ds)
