@@ -126,7 +126,7 @@ __device__ __forceinline__ void publish(uint32_t* flag, uint32_t value) {
 // It starts from the nearest tile that knows its final state and takes the pairs behind it one after the other, as each of
 // those tiles does for its own final state: so the result is the same bit by bit wherever it starts.
 template <int E> __device__ __forceinline__ void look_back(const ScanLink& l, size_t first, int j, int lane, float (&h)[E]) {
-  int from;                                // that tile; tile 0 always becomes one
+  int from;                                // that tile; the first of its channels always becomes one without waiting
   for (int at = j - 1;;) {                 // the newest tile of a window of 64; all newer ones have their pairs
     const int p = at - lane;
     const uint32_t f = p >= 0 ? __hip_atomic_load(l.flags + first + p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0u;

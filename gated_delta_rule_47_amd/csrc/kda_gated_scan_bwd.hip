@@ -39,7 +39,7 @@ __device__ __forceinline__ void scan_bwd_tile(const ScanArgs& a, ScanShared<E>& 
   }
   float h[E];
 #pragma unroll
-  for (int e = 0; e < E; ++e) h[e] = FULL || (l.on && jt * NW * S < a.T) ? a.ckpt[((size_t)l.bh * a.tiles + jt) * a.D + l.d + e] : 0.f;
+  for (int e = 0; e < E; ++e) h[e] = FULL || jt * NW * S < l.n ? a.ckpt[((size_t)l.bh * a.tiles + jt) * a.D + l.d + e] : 0.f;
 
   const float m = l.m();
   float bias2[E];
@@ -108,7 +108,7 @@ __device__ __forceinline__ void scan_bwd_tile(const ScanArgs& a, ScanShared<E>& 
       }
 #pragma unroll
     for (int e = 0; e < E; ++e) Wt[e] = word_of(Wt[e]);
-    if (tile.j == 0) {
+    if (!__any(l.n > (jt + 1) * (NW * S))) {     // no sequence goes on behind this tile
       if (a.d_state && l.on)
 #pragma unroll
         for (int e = 0; e < E; ++e) r[e] = a.d_state[l.ch + e];
@@ -205,13 +205,34 @@ __device__ __forceinline__ void scan_bwd_tile(const ScanArgs& a, ScanShared<E>& 
   }
 }
 
+// A tile behind every lane's sequence: its gradients are zeros.  No other tile waits for it.
+template <typename T, int E, bool GATE, typename Off>
+__device__ __forceinline__ void scan_bwd_zeros(const ScanArgs& a, const ScanLane<E>& l, int jt, int w) {
+  const float zero[E] = {};
+  if (!l.on) return;
+  for (int k = 0; k < S; ++k) {
+    const int t = (jt * NW + w) * S + k;
+    if (t >= a.T) break;
+    const Off off = (((Off)l.bh * a.T + t) * a.D + l.d) * sizeof(T);
+    scan_store<T, E>(a.dx, off, zero);
+    scan_store<T, E>(a.dz, off, zero);
+    if constexpr (GATE) scan_store<T, E>(a.di, off, zero);
+  }
+  if (a.parts && w == 0)
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      a.parts[(size_t)jt * a.B * a.H * a.D + l.ch + e] = a.parts[((size_t)a.tiles + jt) * a.B * a.H * a.D + l.ch + e] = 0.f;
+}
+
 template <typename T, int E, bool GATE, bool NORM, typename Off>
 __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(3))) void scan_bwd_kernel(ScanArgs a) {
   __shared__ ScanShared<E> sh;
   const ScanTile tile = scan_tile(a, &sh.slot);
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const ScanLane<E> l = scan_lane<E>(a, tile.c, lane);
-  if (__all((a.tiles - tile.j) * (NW * S) <= l.n)) scan_bwd_tile<T, E, GATE, NORM, true, Off>(a, sh, tile, l, lane, w);
+  const int jt = a.tiles - 1 - tile.j;
+  if (jt > 0 && !__any(l.n > jt * (NW * S))) scan_bwd_zeros<T, E, GATE, Off>(a, l, jt, w);
+  else if (__all((jt + 1) * (NW * S) <= l.n)) scan_bwd_tile<T, E, GATE, NORM, true, Off>(a, sh, tile, l, lane, w);
   else scan_bwd_tile<T, E, GATE, NORM, false, Off>(a, sh, tile, l, lane, w);
 }
 

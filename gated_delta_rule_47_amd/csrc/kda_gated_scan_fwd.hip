@@ -107,7 +107,7 @@ __device__ __forceinline__ void scan_fwd_tile(const ScanArgs& a, ScanShared<E>& 
 #pragma unroll
     for (int e = 0; e < E; ++e) h[e] = word_step(sh.W[p][e][lane], h[e], sh.H[p][e][lane]);
   static_assert(KDA_GATED_SCAN_CHUNK % S == 0, "a kept state stands in front of a wave's tokens");
-  if (a.ckpt && t0 % KDA_GATED_SCAN_CHUNK == 0 && t0 < a.T && l.on) {
+  if (a.ckpt && t0 % KDA_GATED_SCAN_CHUNK == 0 && t0 < l.n) {
     const int chunks = (a.T + KDA_GATED_SCAN_CHUNK - 1) / KDA_GATED_SCAN_CHUNK;
 #pragma unroll
     for (int e = 0; e < E; ++e) a.ckpt[((size_t)l.bh * chunks + t0 / KDA_GATED_SCAN_CHUNK) * a.D + l.d + e] = h[e];
@@ -119,7 +119,9 @@ __device__ __forceinline__ void scan_fwd_tile(const ScanArgs& a, ScanShared<E>& 
     for (int e = 0; e < E; ++e) h[e] = decay_step(v[k][e], h[e], u[k][e]);
     if (FULL || t0 + k < l.n) scan_store<T, E>(a.y, base + k * row, h);
   }
-  if (w == NW - 1 && tile.j + 1 == a.tiles && a.state_out && l.on)
+  // the tile of a sequence's last token (or the first one) has its final state: behind it the state stays
+  const int start = tile.j * (NW * S);
+  if (w == NW - 1 && a.state_out && l.on && l.n <= start + NW * S && (l.n > start || tile.j == 0))
 #pragma unroll
     for (int e = 0; e < E; ++e) a.state_out[l.ch + e] = h[e];
 }
@@ -130,6 +132,7 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4))) vo
   const ScanTile tile = scan_tile(a, &sh.slot);
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const ScanLane<E> l = scan_lane<E>(a, tile.c, lane);
+  if (tile.j > 0 && !__any(l.n > tile.j * (NW * S))) return;     // behind every lane's sequence, as are the tiles after it
   if (__all((tile.j + 1) * (NW * S) <= l.n)) scan_fwd_tile<T, E, GATE, NORM, true, Off>(a, sh, tile, l, lane, w);
   else scan_fwd_tile<T, E, GATE, NORM, false, Off>(a, sh, tile, l, lane, w);
 }

@@ -518,7 +518,7 @@ size_t kda_gated_scan_workspace_bytes(int B, int H, int T, int D, int dtype);
 
 /* state_in NULL = 0;  state_out NULL = not written, may equal state_in;
  * ckpt (B,H,ceil(T / KDA_GATED_SCAN_CHUNK),D) f32: the state in front of every KDA_GATED_SCAN_CHUNK tokens, for the adjoint;
- *           NULL = not kept.  (Behind a sequence's end: its final state.)
+ *           NULL = not kept.  Chunks that start at or behind a sequence's end are not written (nor read by the adjoint).
  * workspace 256-byte aligned, contents on entry ignored; two calls in flight at once must not share one. */
 int kda_gated_scan_fwd(const void* x, const void* z, const float* A_log, const float* dt_bias, const void* input_gate,
                        const int* lengths, const float* state_in, int normalize, void* y, float* state_out, float* ckpt,

@@ -101,7 +101,10 @@ def check(B, H, T, D, dtype, lengths=None, gated=True, normalize=True, bias=True
     within("y", y, ry, np.where(v["inside"], Ey + U[dtype] * np.abs(ry), 0))
     within("state", end, rend, Eend + E32 * np.abs(rend))
     C = kda.GATED_SCAN_CHUNK
-    within("ckpt", ckpt, before[:, :, ::C], Eb[:, :, ::C] + E32 * np.abs(before[:, :, ::C]))
+    kept = v["inside"][:, :, ::C]                          # (chunks that start inside their sequence)
+    ckpt.masked_fill_(torch.from_numpy(~kept).to(DEV), float("nan"))      # what is behind them must not be read
+    within("ckpt", torch.where(torch.from_numpy(kept).to(DEV), ckpt, 0.0), np.where(kept, before[:, :, ::C], 0.0),
+           Eb[:, :, ::C] + E32 * np.abs(before[:, :, ::C]))
     if not backward:
         return d, y, end, ckpt
     got = kda.gated_scan_bwd(d["x"], d["z"], d["A"], d["b"], ckpt, d["dy"], d["ds"], d["i"], lt, normalize)
@@ -274,8 +277,9 @@ def test_non_finite_values_keep_to_their_channel():
         for k in ("x", "z", "i", "dy"):
             bad[k][1, :, 90:] = float("nan")                       # behind the sequence: never read
         y1, e1, c1 = call(bad)
+        c1[1, :, 3:] = float("nan")                                # (chunks behind the sequence)
         g1 = back(bad, c1)
-        assert torch.equal(y0, y1) and torch.equal(e0, e1) and torch.equal(c0, c1) and all(torch.equal(g0[k], g1[k]) for k in g0)
+        assert torch.equal(y0, y1) and torch.equal(e0, e1) and all(torch.equal(g0[k], g1[k]) for k in g0)
         bad = {k: t.clone() for k, t in d.items()}
         bad["x"][0, 1, 150, 7] = float("inf")
         bad["z"][1, 0, 40, 3] = float("nan")
