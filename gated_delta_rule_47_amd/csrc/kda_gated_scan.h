@@ -14,8 +14,9 @@
 //
 // Tiles hand their states on through the workspace.  Each publishes its own pair as soon as it has it, without
 // waiting for anything, then takes the pairs of the tiles before it from the nearest one on that knows its final state,
-// and publishes its own final state.  Workgroups take tiles by a counter, in time order: whatever a tile waits for
-// belongs to a workgroup that already runs and that publishes without waiting, so every wait ends.  Words are written
+// and publishes its own final state.  A channel tile's workgroups take its tiles by a counter, in time order: whatever a
+// tile waits for belongs to a workgroup that already runs and that publishes without waiting, so every wait ends.  (One
+// counter per channel tile, on a line of its own: a single one for all is bound by its atomics, 15 ns each.)  Words are written
 // and read by device-scope atomics (past the XCDs' own L2), each record complete before its flag.
 #pragma once
 
@@ -86,10 +87,11 @@ template <typename T, int E, typename Off> __device__ __forceinline__ void scan_
   else *reinterpret_cast<bf16_t*>(q) = f2bf(f[0]);
 }
 
-// What links the tiles of a channel tile: a counter, a flag per tile (0 nothing, 1 its pair, 2 its final state too), the
+// What links the tiles of a channel tile: a counter (every `every` words), a flag per tile (0 nothing, 1 its pair, 2 its final state too), the
 // records (64 lanes of E pairs, 64 lanes of E states).
 struct ScanLink {
-  uint32_t *ticket, *flags;
+  uint32_t *tickets, *flags;
+  uint32_t every;
   float *pairs, *states;
 };
 struct ScanArgs {
@@ -145,7 +147,7 @@ template <int E> __device__ __forceinline__ void look_back(const ScanLink& l, si
   }
   asm volatile("" ::: "memory");
   get_words<E>(l.states + (first + from) * (64 * E) + lane, h);
-  constexpr int U = 4;
+  constexpr int U = 2;
 #pragma unroll 1
   for (int k = from + 1; k < j; k += U) {
     float pg[U][E], ph[U][E];
@@ -168,13 +170,15 @@ struct ScanTile {
   int c, j;
 };
 __device__ __forceinline__ ScanTile scan_tile(const ScanArgs& a, uint32_t* slot) {
-  uint32_t k = blockIdx.x;
+  const uint32_t c = blockIdx.x % (uint32_t)a.ctiles;
+  uint32_t j = 0;
   if (a.tiles > 1) {
-    if (threadIdx.x == 0) *slot = __hip_atomic_fetch_add(a.link.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (threadIdx.x == 0)
+      *slot = __hip_atomic_fetch_add(a.link.tickets + c * a.link.every, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     __syncthreads();
-    k = (uint32_t)__builtin_amdgcn_readfirstlane((int)*slot);
+    j = (uint32_t)__builtin_amdgcn_readfirstlane((int)*slot);
   }
-  return {(int)(k % (uint32_t)a.ctiles), (int)(k / (uint32_t)a.ctiles)};
+  return {(int)c, (int)j};
 }
 
 // A lane's channels: index among all of them, head, sequence's tokens, parameters.
@@ -207,7 +211,10 @@ template <int E> __device__ __forceinline__ ScanLane<E> scan_lane(const ScanArgs
 }
 
 // Tile shapes.  Forward: S = 16 tokens of decay and input are 64 registers at E = 2.  Backward: seven values a token.
-constexpr int kScanFwdWaves = 8, kScanFwdTokens = 16;
+#ifndef FWV
+#define FWV 8
+#endif
+constexpr int kScanFwdWaves = FWV, kScanFwdTokens = 16;
 constexpr int kScanBwdWaves = 4, kScanBwdTokens = 8;
 
 template <typename T> hipError_t launch_scan_fwd_tiles(const ScanArgs& a, bool pairs, hipStream_t s);

@@ -6,7 +6,7 @@ namespace {
 
 constexpr int kScanThreads = 256;
 
-// Clears the counter and the flags (a kernel, not a memset: it may be captured into a graph).
+// Clears the counters and the flags (a kernel, not a memset: it may be captured into a graph).
 __global__ __launch_bounds__(kScanThreads) void scan_clear_kernel(uint32_t* p, uint32_t n) {
   const uint32_t i = blockIdx.x * kScanThreads + threadIdx.x;
   if (i < n) p[i] = 0u;
@@ -73,7 +73,7 @@ int scan_e(int D, bool bf16) { return bf16 && D % 2 == 0 ? 2 : 1; }
 
 struct ScanPlan {
   int E, ctiles, tiles;
-  size_t clear, pairs, states, parts, sums, total;   // bytes cleared; offsets
+  size_t every, flags, clear, pairs, states, parts, sums, total;   // words per counter; offsets and the bytes cleared
 };
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
 ScanPlan scan_plan(int B, int H, int T, int D, bool bf16, bool bwd) {
@@ -84,7 +84,9 @@ ScanPlan scan_plan(int B, int H, int T, int D, bool bf16, bool bwd) {
   p.ctiles = (int)((N + 64 * p.E - 1) / (64 * p.E));
   p.tiles = T > tokens ? (T + tokens - 1) / tokens : 1;
   const size_t n = p.tiles > 1 ? (size_t)p.ctiles * p.tiles : 0;
-  p.clear = n ? 256 + n * 4 : 0;
+  p.every = p.ctiles <= 4096 ? 32 : 1;
+  p.flags = up(n ? p.every * p.ctiles * 4 : 0);
+  p.clear = p.flags + n * 4;
   p.pairs = up(p.clear);
   p.states = p.pairs + n * 128 * p.E * 4;
   p.parts = p.states + n * 64 * p.E * 4;
@@ -96,7 +98,7 @@ void scan_link(ScanArgs& a, const ScanPlan& p, void* workspace, hipStream_t s) {
   char* w = (char*)workspace;
   a.ctiles = p.ctiles, a.tiles = p.tiles;
   if (!p.clear) return;
-  a.link.ticket = (uint32_t*)w, a.link.flags = (uint32_t*)(w + 256);
+  a.link.tickets = (uint32_t*)w, a.link.flags = (uint32_t*)(w + p.flags), a.link.every = (uint32_t)p.every;
   a.link.pairs = (float*)(w + p.pairs), a.link.states = (float*)(w + p.states);
   const uint32_t n = (uint32_t)(p.clear / 4);
   scan_clear_kernel<<<(n + kScanThreads - 1) / kScanThreads, kScanThreads, 0, s>>>((uint32_t*)w, n);

@@ -13,8 +13,8 @@ static_assert(NW * S == KDA_GATED_SCAN_CHUNK, "one kept state per tile");
 
 template <int E> struct ScanShared {
   uint32_t slot;
-  float G[NW][E][64], W[NW][E][64], H[NW][E][64], R[NW][E][64], in[E][64];     // as forward; R: r from zero
-  float sum[2][NW][E][64];
+  float G[NW][E][64], H[NW][E][64], R[NW][E][64], in[E][64];     // sums of g2, states and r from zero
+  float2 qg[NW][S][E][64];                 // q and g2 of every token, each lane's own: what the last pass alone needs
 };
 
 // FULL: every token of the tile lies inside its sequence, in every lane (the same for all waves).
@@ -45,8 +45,8 @@ __device__ __forceinline__ void scan_bwd_tile(const ScanArgs& a, ScanShared<E>& 
   float bias2[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) bias2[e] = l.bias[e] * kLog2e;
-  // per token: the decay v, g2, q = m sigmoid(z'), c = n s, sm = 1 - s, k4 = a^2 s x / n
-  float v[S][E], g[S][E], q[S][E], c[S][E], sm[S][E], k4[S][E], G[E], H[E], R[E];
+  // per token: the decay v, c = n s, sm = 1 - s, k4 = a^2 s x / n; in LDS q = m sigmoid(z') and g2
+  float v[S][E], c[S][E], sm[S][E], k4[S][E], G[E], H[E], R[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) G[e] = H[e] = R[e] = 0.f;
 #pragma unroll
@@ -55,9 +55,9 @@ __device__ __forceinline__ void scan_bwd_tile(const ScanArgs& a, ScanShared<E>& 
     for (int e = 0; e < E; ++e) {
       float y;
       const float p = FULL || t0 + k < l.n ? fmaf(rz[k].at(e), kLog2e, bias2[e]) : kNoDecay;
-      g[k][e] = -m * scan_softplus2(p, y);
-      q[k][e] = m * fast_rcp(1.f + y) * (p >= 0.f ? 1.f : y);
-      v[k][e] = decay_of(g[k][e]);
+      const float g = -m * scan_softplus2(p, y);
+      sh.qg[w][k][e][lane] = float2{m * fast_rcp(1.f + y) * (p >= 0.f ? 1.f : y), g};
+      v[k][e] = decay_of(g);
       const float s = GATE ? scan_sigmoid(ri[k].at(e)) : 1.f, x = rx[k].at(e);
       sm[k][e] = 1.f - s;
       c[k][e] = s;
@@ -68,10 +68,10 @@ __device__ __forceinline__ void scan_bwd_tile(const ScanArgs& a, ScanShared<E>& 
         c[k][e] = s * (n2 * rn);
         k4[k][e] = av * av * rn * (s * x);
       }
-      G[e] += g[k][e];
+      G[e] += g;
       H[e] = decay_step(v[k][e], H[e], c[k][e] * x);
       // (kept as they are: what the compiler would compute later from their parts takes more registers)
-      asm volatile("" : "+v"(v[k][e]), "+v"(g[k][e]), "+v"(q[k][e]));
+      asm volatile("" : "+v"(v[k][e]));
       if constexpr (GATE || NORM) asm volatile("" : "+v"(c[k][e]));
       if constexpr (GATE) asm volatile("" : "+v"(sm[k][e]));
       if constexpr (NORM) asm volatile("" : "+v"(k4[k][e]));
@@ -88,7 +88,6 @@ __device__ __forceinline__ void scan_bwd_tile(const ScanArgs& a, ScanShared<E>& 
 #pragma unroll
   for (int e = 0; e < E; ++e) {
     sh.G[w][e][lane] = G[e];
-    sh.W[w][e][lane] = word_of(G[e]);
     sh.H[w][e][lane] = H[e];
     sh.R[w][e][lane] = R[e];
   }
@@ -103,7 +102,7 @@ __device__ __forceinline__ void scan_bwd_tile(const ScanArgs& a, ScanShared<E>& 
     for (int p = NW - 1; p >= 0; --p)
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        Rt[e] = word_step(sh.W[p][e][lane], Rt[e], sh.R[p][e][lane]);
+        Rt[e] = word_step(word_of(sh.G[p][e][lane]), Rt[e], sh.R[p][e][lane]);
         Wt[e] += sh.G[p][e][lane];
       }
 #pragma unroll
@@ -136,7 +135,7 @@ __device__ __forceinline__ void scan_bwd_tile(const ScanArgs& a, ScanShared<E>& 
 #pragma unroll 1
   for (int p = 0; p < w; ++p)
 #pragma unroll
-    for (int e = 0; e < E; ++e) h[e] = word_step(sh.W[p][e][lane], h[e], sh.H[p][e][lane]);
+    for (int e = 0; e < E; ++e) h[e] = word_step(word_of(sh.G[p][e][lane]), h[e], sh.H[p][e][lane]);
   // dg / r = a h_{t-1} - a^2 s x / n of every token
 #pragma unroll
   for (int k = 0; k < S; ++k)
@@ -156,7 +155,7 @@ __device__ __forceinline__ void scan_bwd_tile(const ScanArgs& a, ScanShared<E>& 
 #pragma unroll 1
   for (int p = NW - 1; p > w; --p)
 #pragma unroll
-    for (int e = 0; e < E; ++e) r[e] = word_step(sh.W[p][e][lane], r[e], sh.R[p][e][lane]);
+    for (int e = 0; e < E; ++e) r[e] = word_step(word_of(sh.G[p][e][lane]), r[e], sh.R[p][e][lane]);
   asm volatile("" : "+v"(base));           // the stores' offsets are computed anew, not kept in registers since the loads
 #pragma unroll
   for (int k = S - 1; k >= 0; --k) {
@@ -167,11 +166,12 @@ __device__ __forceinline__ void scan_bwd_tile(const ScanArgs& a, ScanShared<E>& 
       dx[e] = r[e] * c[k][e];
       di[e] = dx[e] * rx[k].at(e) * sm[k][e];
       const float dg = r[e] * k4[k][e];
-      dz[e] = -dg * q[k][e];
+      const float2 qg = sh.qg[w][k][e][lane];
+      dz[e] = -dg * qg.x;
       if (!FULL && t0 + k >= l.n) dx[e] = di[e] = dz[e] = 0.f;
       else {
         sz[e] += dz[e];
-        sa[e] = fmaf(dg, g[k][e], sa[e]);
+        sa[e] = fmaf(dg, qg.y, sa[e]);
       }
       r[e] = fmaf(v[k][e], r[e], r[e]);
     }
@@ -185,8 +185,7 @@ __device__ __forceinline__ void scan_bwd_tile(const ScanArgs& a, ScanShared<E>& 
   // the waves' sums in a fixed order
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    sh.sum[0][w][e][lane] = sz[e];
-    sh.sum[1][w][e][lane] = sa[e] * kLn2;
+    sh.qg[w][0][e][lane] = float2{sz[e], sa[e] * kLn2};        // (in the place of the wave's own, which it has used)
   }
   __syncthreads();
   if (w == 0 && l.on) {
@@ -196,8 +195,9 @@ __device__ __forceinline__ void scan_bwd_tile(const ScanArgs& a, ScanShared<E>& 
       float z = 0.f, s = 0.f;
 #pragma unroll
       for (int p = 0; p < NW; ++p) {
-        z += sh.sum[0][p][e][lane];
-        s += sh.sum[1][p][e][lane];
+        const float2 f = sh.qg[p][0][e][lane];
+        z += f.x;
+        s += f.y;
       }
       a.parts[(size_t)jt * N + l.ch + e] = z;
       a.parts[((size_t)a.tiles + jt) * N + l.ch + e] = s;
@@ -225,7 +225,7 @@ __device__ __forceinline__ void scan_bwd_zeros(const ScanArgs& a, const ScanLane
 }
 
 template <typename T, int E, bool GATE, bool NORM, typename Off>
-__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(3))) void scan_bwd_kernel(ScanArgs a) {
+__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4))) void scan_bwd_kernel(ScanArgs a) {
   __shared__ ScanShared<E> sh;
   const ScanTile tile = scan_tile(a, &sh.slot);
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
