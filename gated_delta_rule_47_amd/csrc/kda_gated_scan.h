@@ -16,7 +16,7 @@
 // waiting for anything, then takes the pairs of the tiles before it from the nearest one on that knows its final state,
 // and publishes its own final state.  A channel tile's workgroups take its tiles by a counter, in time order: whatever a
 // tile waits for belongs to a workgroup that already runs and that publishes without waiting, so every wait ends.  (One
-// counter per channel tile, on a line of its own: a single one for all is bound by its atomics, 15 ns each.)  Words are written
+// counter per channel tile, on a line of its own: with a single one the padded batch of 8 x 8 x 4096 x 64 took 48 us for 42.)  Words are written
 // and read by device-scope atomics (past the XCDs' own L2), each record complete before its flag.
 #pragma once
 
@@ -195,7 +195,7 @@ template <int E> __device__ __forceinline__ ScanLane<E> scan_lane(const ScanArgs
   ScanLane<E> l;
   l.ch = ((long long)c * 64 + lane) * E;
   l.on = l.ch < N;
-  const uint32_t ch = l.on ? (uint32_t)l.ch : 0u, bh = ch / (uint32_t)a.D;      // N <= 2^28
+  const uint32_t ch = l.on ? (uint32_t)l.ch : 0u, bh = ch / (uint32_t)a.D;      // N <= 2^26
   l.bh = bh;
   l.d = (int)(ch - bh * (uint32_t)a.D);
   const uint32_t b = bh / (uint32_t)a.H;
@@ -210,12 +210,13 @@ template <int E> __device__ __forceinline__ ScanLane<E> scan_lane(const ScanArgs
   return l;
 }
 
-// Tile shapes.  Forward: S = 16 tokens of decay and input are 64 registers at E = 2.  Backward: seven values a token.
-#ifndef FWV
-#define FWV 8
-#endif
-constexpr int kScanFwdWaves = FWV, kScanFwdTokens = 16;
-constexpr int kScanBwdWaves = 4, kScanBwdTokens = 8;
+// Tile shapes.  Forward: S = 16 tokens of decay and input are 64 registers at E = 2; eight waves, or four where the channel
+// tiles are many (scan_fwd_waves).  Backward: four values a token in registers and two in LDS.
+constexpr int kScanFwdTokens = 16, kScanBwdWaves = 4, kScanBwdTokens = 8;
+// Five workgroups of four waves fit a CU and two of eight.  The smaller ones overlap better (8 x 8192 x 4096: 434 us for 460) and
+// put twice as many tiles into a channel's line, of which 256 CUs hold more at once the fewer channels there are (1 x
+// 30011 x 4096: 241 us for 222).
+constexpr int scan_fwd_waves(int ctiles) { return ctiles >= 128 ? 4 : 8; }
 
 template <typename T> hipError_t launch_scan_fwd_tiles(const ScanArgs& a, bool pairs, hipStream_t s);
 template <typename T> hipError_t launch_scan_bwd_tiles(const ScanArgs& a, bool pairs, hipStream_t s);

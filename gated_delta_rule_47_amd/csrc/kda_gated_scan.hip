@@ -19,19 +19,35 @@ __global__ __launch_bounds__(kSumThreads) void scan_params_kernel(const float* p
   if (!out) return;
   sum_parts(parts + blockIdx.y * half, n, n_parts, n, [=](int i, float s) { out[i] = s; });
 }
-// dA_log of head blockIdx.x: the sum over its channels, in a fixed order.
-__global__ __launch_bounds__(kScanThreads) void scan_head_kernel(const float* sums, const float* A_log, int D, float* dA_log) {
-  __shared__ float red[kScanThreads / 64];
-  const float* p = sums + (size_t)blockIdx.x * D;
+// dA_log of head h: the sum of n_parts rows of its D channels, `stride` apart, in a fixed order.
+__device__ __forceinline__ void scan_head_sum(const float* in, size_t stride, int n_parts, const float* A_log, int D, int h,
+                                              float* dA_log) {
+  __shared__ float red[kSumThreads / 64];
+  const float* p = in + (size_t)h * D;
+  const long long n = (long long)n_parts * D;
   float s = 0.f;
-  for (int d = threadIdx.x; d < D; d += kScanThreads) s += p[d];
+  for (long long i = threadIdx.x; i < n; i += kSumThreads) s += p[(size_t)(i / D) * stride + i % D];
   s = lane_sum<64>(s);
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
   __syncthreads();
   if (threadIdx.x == 0) {
-    const float al = A_log[blockIdx.x];
-    s = (red[0] + red[1]) + (red[2] + red[3]);
-    dA_log[blockIdx.x] = al < kALogMin || al > kALogMax ? 0.f : s;      // the clamp holds the multiplier constant there
+    s = 0.f;
+    for (int k = 0; k < kSumThreads / 64; ++k) s += red[k];
+    const float al = A_log[h];
+    dA_log[h] = al < kALogMin || al > kALogMax ? 0.f : s;              // the clamp holds the multiplier constant there
+  }
+}
+__global__ __launch_bounds__(kSumThreads) void scan_head_kernel(const float* sums, const float* A_log, int D, float* dA_log) {
+  scan_head_sum(sums, 0, 1, A_log, D, blockIdx.x, dA_log);
+}
+// Both in one launch where a head has few values: first the workgroups of ddt_bias, then one per head.
+__global__ __launch_bounds__(kSumThreads) void scan_small_params_kernel(const float* parts, size_t half, int n_parts, int n,
+                                                                        const float* A_log, int D, float* d_dt_bias, float* dA_log) {
+  const int blocks = (n + 63) / 64, b = blockIdx.x;
+  if (b < blocks) {
+    if (d_dt_bias) sum_parts(parts, n, n_parts, n, [=](int i, float s) { d_dt_bias[i] = s; });
+  } else if (dA_log) {
+    scan_head_sum(parts + half, n, n_parts, A_log, D, b - blocks, dA_log);
   }
 }
 
@@ -40,7 +56,7 @@ template <typename T, int E> __global__ __launch_bounds__(kScanThreads) void sca
   const uint32_t ch = (blockIdx.x * kScanThreads + threadIdx.x) * E;
   if (ch >= (uint32_t)(a.B * a.H * a.D)) return;
   const uint32_t row = ch / (uint32_t)a.D, d = ch - row * (uint32_t)a.D, h = row % (uint32_t)a.H;
-  const uint32_t off = ch * sizeof(T);     // B H D <= 2^28
+  const uint32_t off = ch * sizeof(T);     // B H D <= 2^26
   ScanRaw<T, E> rz, rx, ri;
   rz.load(a.z, off);
   rx.load(a.x, off);
@@ -79,9 +95,9 @@ size_t up(size_t n) { return (n + 255) / 256 * 256; }
 ScanPlan scan_plan(int B, int H, int T, int D, bool bf16, bool bwd) {
   ScanPlan p;
   const long long N = (long long)B * H * D;
-  const int tokens = bwd ? kScanBwdWaves * kScanBwdTokens : kScanFwdWaves * kScanFwdTokens;
   p.E = scan_e(D, bf16);
   p.ctiles = (int)((N + 64 * p.E - 1) / (64 * p.E));
+  const int tokens = bwd ? kScanBwdWaves * kScanBwdTokens : scan_fwd_waves(p.ctiles) * kScanFwdTokens;
   p.tiles = T > tokens ? (T + tokens - 1) / tokens : 1;
   const size_t n = p.tiles > 1 ? (size_t)p.ctiles * p.tiles : 0;
   p.every = p.ctiles <= 4096 ? 32 : 1;
@@ -151,11 +167,17 @@ hipError_t launch_scan_bwd(const void* x, const void* z, const float* A_log, con
   hipError_t e = launch_scan_bwd_tiles<T>(a, p.E == 2, s);
   if (e != hipSuccess || !a.parts) return e;
   const int n = H * D;
+  // up to 64 values per thread of a head's workgroup; beyond, the channels are summed over time first, by many workgroups
+  if ((long long)p.tiles * B * D <= 64 * kSumThreads) {
+    scan_small_params_kernel<<<(n + 63) / 64 + H, kSumThreads, 0, s>>>(a.parts, (size_t)p.tiles * B * n, p.tiles * B, n, A_log, D,
+                                                                       d_dt_bias, dA_log);
+    return hipGetLastError();
+  }
   scan_params_kernel<<<dim3((n + 63) / 64, 2), kSumThreads, 0, s>>>(a.parts, (size_t)p.tiles * B * n, p.tiles * B, n,
                                                                     d_dt_bias, dA_log ? sums : nullptr);
   e = hipGetLastError();
   if (e != hipSuccess || !dA_log) return e;
-  scan_head_kernel<<<H, kScanThreads, 0, s>>>(sums, A_log, D, dA_log);
+  scan_head_kernel<<<H, kSumThreads, 0, s>>>(sums, A_log, D, dA_log);
   return hipGetLastError();
 }
 

@@ -145,6 +145,8 @@ __device__ __forceinline__ void scan_bwd_tile(const ScanArgs& a, ScanShared<E>& 
       k4[k][e] = ah - k4[k][e];
       h[e] = fmaf(c[k][e], rx[k].at(e), ah);
     }
+#pragma unroll
+  for (int k = 0; k < S; ++k) asm volatile("" : "+v"(rx[k].u));
   __syncthreads();
   float sz[E], sa[E];
 #pragma unroll

@@ -6,17 +6,17 @@
 namespace kda {
 namespace {
 
-constexpr int NW = kScanFwdWaves, S = kScanFwdTokens;
+constexpr int S = kScanFwdTokens;
 
-template <int E> struct ScanShared {
+template <int E, int NW> struct ScanShared {
   uint32_t slot;
   float G[NW][E][64], W[NW][E][64], H[NW][E][64], in[E][64];     // sums of g2, the decays over them, states from zero
 };
 
 // FULL: every token of the tile lies inside its sequence, in every lane (the same for all waves, whose lanes are the
 // same channels).
-template <typename T, int E, bool GATE, bool NORM, bool FULL, typename Off>
-__device__ __forceinline__ void scan_fwd_tile(const ScanArgs& a, ScanShared<E>& sh, const ScanTile tile, const ScanLane<E>& l,
+template <typename T, int E, int NW, bool GATE, bool NORM, bool FULL, typename Off>
+__device__ __forceinline__ void scan_fwd_tile(const ScanArgs& a, ScanShared<E, NW>& sh, const ScanTile tile, const ScanLane<E>& l,
                                               int lane, int w) {
   const int t0 = (tile.j * NW + w) * S;
   const Off row = (Off)a.D * sizeof(T);
@@ -126,23 +126,26 @@ __device__ __forceinline__ void scan_fwd_tile(const ScanArgs& a, ScanShared<E>& 
     for (int e = 0; e < E; ++e) a.state_out[l.ch + e] = h[e];
 }
 
-template <typename T, int E, bool GATE, bool NORM, typename Off>
+template <typename T, int E, int NW, bool GATE, bool NORM, typename Off>
 __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4))) void scan_fwd_kernel(ScanArgs a) {
-  __shared__ ScanShared<E> sh;
+  __shared__ ScanShared<E, NW> sh;
   const ScanTile tile = scan_tile(a, &sh.slot);
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const ScanLane<E> l = scan_lane<E>(a, tile.c, lane);
   if (tile.j > 0 && !__any(l.n > tile.j * (NW * S))) return;     // behind every lane's sequence, as are the tiles after it
-  if (__all((tile.j + 1) * (NW * S) <= l.n)) scan_fwd_tile<T, E, GATE, NORM, true, Off>(a, sh, tile, l, lane, w);
-  else scan_fwd_tile<T, E, GATE, NORM, false, Off>(a, sh, tile, l, lane, w);
+  if (__all((tile.j + 1) * (NW * S) <= l.n)) scan_fwd_tile<T, E, NW, GATE, NORM, true, Off>(a, sh, tile, l, lane, w);
+  else scan_fwd_tile<T, E, NW, GATE, NORM, false, Off>(a, sh, tile, l, lane, w);
 }
 
-template <typename T, int E, typename Off> void launch_e(const ScanArgs& a, hipStream_t s) {
+template <typename T, int E, int NW, typename Off> void launch_nw(const ScanArgs& a, hipStream_t s) {
   const unsigned grid = (unsigned)a.ctiles * (unsigned)a.tiles;
-#define KDA_SCAN(G_, N_) scan_fwd_kernel<T, E, G_, N_, Off><<<grid, NW * 64, 0, s>>>(a)
+#define KDA_SCAN(G_, N_) scan_fwd_kernel<T, E, NW, G_, N_, Off><<<grid, NW * 64, 0, s>>>(a)
   if (a.i) a.normalize ? KDA_SCAN(true, true) : KDA_SCAN(true, false);
   else a.normalize ? KDA_SCAN(false, true) : KDA_SCAN(false, false);
 #undef KDA_SCAN
+}
+template <typename T, int E, typename Off> void launch_e(const ScanArgs& a, hipStream_t s) {
+  scan_fwd_waves(a.ctiles) == 4 ? launch_nw<T, E, 4, Off>(a, s) : launch_nw<T, E, 8, Off>(a, s);
 }
 
 }  // namespace

@@ -103,12 +103,12 @@ bool conv_sizes(int B, int H, int T, int D, int W) {
          D <= (1 << 20) && (ll)H * D <= (1 << 20) && (ll)B * H * D <= (1LL << 31) && (ll)B * H * D * (T ? T : 1) <= kMostElements;
 }
 bool qk_sizes(int B, int T, int Hq, int Hqw, int Hk, int Hkw, int D) {
-  return B >= 1 && T >= 0 && (ll)B * T <= (1 << 30) && Hq >= 0 && Hk >= 0 && Hq <= 65536 && Hk <= 65536 && Hq + Hk > 0 && D >= 8 &&
+  return B >= 1 && T >= 0 && (ll)B * T <= (1 << 30) && Hq >= 0 && Hk >= 0 && Hq <= 32767 && Hk <= 32767 && Hq + Hk > 0 && D >= 8 &&
          D <= 256 && D % 8 == 0 && (Hq == 0 || Hqw == 1 || Hqw == Hq) && (Hk == 0 || Hkw == 1 || Hkw == Hk) &&
          (ll)B * T * (Hq > Hk ? Hq : Hk) * D <= kMostElements;
 }
 bool scan_sizes(int B, int H, int T, int D) {
-  return B >= 1 && H >= 1 && D >= 1 && T >= 0 && T <= (1 << 28) && (ll)B * H <= (1 << 28) && (ll)B * H * D <= (1 << 28) &&
+  return B >= 1 && H >= 1 && D >= 1 && T >= 0 && T <= (1 << 28) && (ll)B * H <= (1 << 20) && (ll)B * H * D <= (1 << 26) &&
          (((ll)B * H * D + 63) / 64) * (((ll)T + KDA_GATED_SCAN_CHUNK - 1) / KDA_GATED_SCAN_CHUNK) <= (1LL << 23);
 }
 bool finite_f(float x) { return x >= -3.4e38f && x <= 3.4e38f; }

@@ -447,7 +447,7 @@ int kda_short_conv_bwd(const void* x, long long x_batch, long long x_token, cons
  *   freqs     (R / 2) float64 on the device, radians per token (kda_rope_frequencies); not read when R = 0
  *   positions (B,T) int32, any sign, or NULL (a token's index)
  *   q_out (B,Hq,T,D), k_out (B,Hk,T,D) in `dtype`
- *   D a multiple of 8 up to 256;  R a multiple of 8 up to D, or 0;  B >= 1;  T >= 0;  B * T <= 2^30;  Hq, Hk <= 65536, not both
+ *   D a multiple of 8 up to 256;  R a multiple of 8 up to D, or 0;  B >= 1;  T >= 0;  B * T <= 2^30;  Hq, Hk <= 32767, not both
  *             0;  eps >= 0 and rope_scale finite;  outputs within 2^48 elements (KDA_ERR_SHAPE otherwise).  Pointers need the
  *             alignment of an element only.
  * The angle is formed and reduced in float64 (right to 2^-50 of itself), everything else in fp32 with one rounding to
@@ -505,8 +505,8 @@ int kda_rope_frequencies(double* freqs, double* rope_scale, int R, double base, 
  *   A_log (H) f32;  dt_bias (H,D) f32 or NULL (= 0);  states (B,H,D) f32
  *   lengths   (B) int32 on the device, or NULL, as above: rows of y behind a sequence stay as they were, the gradients'
  *             rows there become zero, the final state is the one after the last token.
- *   B, H, D >= 1;  T >= 0;  T <= 2^28;  B * H * D <= 2^28;  ceil(B * H * D / 64) * ceil(T / 32) <= 2^23 (KDA_ERR_SHAPE;
- *             2^34 elements of many channels).  Pointers need the alignment of an element only.
+ *   B, H, D >= 1;  T >= 0;  T <= 2^28;  B * H <= 2^20;  B * H * D <= 2^26;  ceil(B * H * D / 64) * ceil(T / 32) <= 2^23
+ *             (KDA_ERR_SHAPE; 2^34 elements of many channels).  Pointers need the alignment of an element only.
  * Gates, states and sums are fp32.  A decay is held as its distance from 1: slow ones do not drift over long sequences, and
  * what a strong one leaves of a state is right to 2^-24 of the state before it.  A non-finite value reaches its own channel only, from its token on. */
 

@@ -185,6 +185,8 @@ def test_many_tiles():
     check(1, 1, 9000, 4, FP, seed=5)
     check(1, 3, 5000, 50, BF, seed=6, slow=True)
     check(2, 1, 2500, 700, BF, lengths=[2500, 1300], seed=7)
+    check(1, 1, 700, 8300, FP, seed=8)                             # (130 channel tiles: smaller tiles forward)
+    check(3, 1, 200, 6000, BF, lengths=[200, 64, 65], seed=9)
 
 
 def test_slow_decays_do_not_drift():

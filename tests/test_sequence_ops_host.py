@@ -53,7 +53,7 @@ def test_workspace_bytes():
     assert f(1, 8, 64, 64, F32) == 0 and f(1, 8, 0, 64, F32) == 0 and f(1, 1, 30011, 4096, BF16) > 0
     assert b(1, 8, 32, 64, F32) >= 8 * 64 * 8 and b(1, 1, 1 << 14, 4096, BF16) > b(1, 1, 1 << 13, 4096, BF16)
     for args in ((0, 1, 64, 64, F32), (1, 0, 64, 64, F32), (1, 1, -1, 64, F32), (1, 1, 64, 0, F32), (1, 1, 64, 64, 5),
-                 (1, 1, (1 << 28) + 1, 1, F32), (1, 2, 1 << 28, 64, F32), (1, 1, 1, (1 << 28) + 1, F32)):
+                 (1, 1, (1 << 28) + 1, 1, F32), (1, 2, 1 << 28, 64, F32), (1, 1, 1, (1 << 26) + 1, F32), (1 << 11, 1 << 10, 1, 1, F32)):
         assert f(*args) == 0 and b(*args) == 0, args
     c = lib.kda_short_conv_bwd_workspace_bytes
     assert c(8, 8, 4096, 64, 4, BF16) % (512 * 5 * 4) == 0 and c(8, 8, 4096, 64, 4, BF16) > 0
@@ -63,7 +63,7 @@ def test_workspace_bytes():
     q = lib.kda_qk_norm_rope_bwd_workspace_bytes
     assert q(1, 128, 4, 1, 4, 1, 64) % 256 == 0 and q(1, 128, 4, 1, 4, 1, 64) > 0 and q(1, 128, 4, 4, 0, 1, 64) > 0
     for args in ((1, 128, 4, 2, 4, 1, 64), (1, 128, 0, 1, 0, 1, 64), (1, 128, 4, 1, 4, 1, 264), (1, 128, 4, 1, 4, 1, 60),
-                 (1 << 16, 1 << 16, 4, 1, 4, 1, 64), (1, 128, 1 << 17, 1, 4, 1, 64)):
+                 (1 << 16, 1 << 16, 4, 1, 4, 1, 64), (1, 128, 1 << 15, 1, 4, 1, 64)):
         assert q(*args) == 0, args
 
 
