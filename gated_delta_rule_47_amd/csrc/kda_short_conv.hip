@@ -169,21 +169,93 @@ template <typename T, int W, int E> __global__ __launch_bounds__(kConvThreads) v
   }
 }
 
-// Tokens t0 .. t0 + run - 1 give their dx and their share of dw and db; dpre is computed for W - 1 tokens more.
-template <typename T, int W, int E> __global__ __launch_bounds__(kConvThreads) void conv_bwd_kernel(ConvArgs a) {
-  __shared__ float red[kConvThreads * (W + 1) * E];
-  const ConvPlace p = conv_place<E>(a);
-  float dw[W][E], db[E];
+// What a run of the adjoint holds in registers: weights, the last W - 1 inputs and cotangents, its sums.
+template <int W, int E> struct ConvRun {
+  float w[W][E], bias[E], win[W][E], dp[W][E], dw[W][E], db[E];
+};
+
+// One token: its cotangent dpre (0 behind the sequence), its share of the sums, and in o the gradient of the input W - 1
+// tokens before it, which is complete with it.
+template <bool SILU, bool FAST, int W, int E, typename RT>
+__device__ __forceinline__ void conv_bwd_token(ConvRun<W, E>& c, const RT& rx, const RT& rd, bool inside, bool own, float (&o)[E]) {
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    db[e] = 0.f;
+    c.win[W - 1][e] = rx.at(e);
+    float d = rd.at(e);
+    if constexpr (SILU) {
+      float s = c.bias[e];
 #pragma unroll
-    for (int j = 0; j < W; ++j) dw[j][e] = 0.f;
+      for (int j = 0; j < W; ++j) s = fmaf(c.w[j][e], c.win[j][e], s);
+      const float g = sigmoid_f(s);
+      d *= fmaf(s, g * (1.f - g), g);
+    }
+    if (!FAST && !inside) d = 0.f;
+    c.dp[W - 1][e] = d;
+    if (FAST || (inside && own)) {
+      c.db[e] += d;
+#pragma unroll
+      for (int j = 0; j < W; ++j) c.dw[j][e] = fmaf(d, c.win[j][e], c.dw[j][e]);
+    }
+    o[e] = 0.f;
+#pragma unroll
+    for (int k = 0; k < W; ++k) o[e] = fmaf(c.w[W - 1 - k][e], c.dp[k][e], o[e]);
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) {
+      c.win[j][e] = c.win[j + 1][e];
+      c.dp[j][e] = c.dp[j + 1][e];
+    }
   }
-  if (p.on && (p.t0 < a.T || p.t0 == 0)) {
-    const int n = length_of(a, p.b), own = min(p.t0 + a.run, a.T), t1 = own + W - 1;
-    float w[W][E], bias[E], win[W][E], dp[W][E];
-    conv_weights<W, E>(a, p.c, w, bias);
+}
+
+// Tokens t0 .. t0 + run - 1 give their dx and their share of dw and db; dpre is computed for W - 1 tokens more.  The
+// tokens in the middle of a run inside its sequence take a path without conditions.
+template <typename T, int W, int E, bool SILU> __global__ __launch_bounds__(kConvThreads) void conv_bwd_kernel(ConvArgs a) {
+  __shared__ float red[kConvThreads * (W + 1) * E];
+  const ConvPlace p = conv_place<E>(a);
+  ConvRun<W, E> c;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    c.db[e] = 0.f;
+#pragma unroll
+    for (int j = 0; j < W; ++j) c.dw[j][e] = 0.f;
+  }
+  const int n = p.on ? length_of(a, p.b) : 0, own = min(p.t0 + a.run, a.T);
+  if (p.on && p.t0 > 0 && p.t0 >= n) {                 // a run behind its sequence
+    Elems<T, E> zero;
+    zero.zero();
+    T* dx = (T*)a.dx + p.b * a.db + p.t0 * a.dt + p.c;
+    for (int t = p.t0; t < own; ++t, dx += a.dt) zero.store(dx);
+  } else if (p.on) {
+    const int t1 = own + W - 1, in = min(n, t1);       // tokens whose inputs are read: t < in
+    conv_weights<W, E>(a, p.c, c.w, c.bias);
+    const T* x = (const T*)a.x + p.b * a.xb + p.t0 * a.xt + p.c;
+    const T* dy = (const T*)a.dy + (((size_t)p.b * a.H + p.c / a.D) * a.T + p.t0) * a.D + p.c % a.D;
+    T* dx = (T*)a.dx + p.b * a.db + ((long long)p.t0 - (W - 1)) * a.dt + p.c;
+    constexpr int U = 4;
+    // the next U tokens' rows are on their way while these are worked on
+    Elems<T, E> nx[U], nd[U];
+    const auto fetch = [&](int t) {
+      if (t + U <= in) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          nx[u].load(x + u * a.xt);
+          nd[u].load(dy + (size_t)u * a.D);
+        }
+      } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          nx[u].zero();
+          nd[u].zero();
+          if (t + u < in) {
+            nx[u].load(x + u * a.xt);
+            nd[u].load(dy + (size_t)u * a.D);
+          }
+        }
+      }
+      x += U * a.xt;
+      dy += (size_t)U * a.D;
+    };
+    fetch(p.t0);
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) {
       Elems<T, E> r;
@@ -191,67 +263,32 @@ template <typename T, int W, int E> __global__ __launch_bounds__(kConvThreads) v
       if (p.t0 - (W - 1) + j < n) conv_row<T, W, E>(a, p.b, p.c, p.t0 - (W - 1) + j, r);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        win[j][e] = r.at(e);
-        dp[j][e] = 0.f;                  // (of tokens whose inputs' gradients are another run's, or in front of the first)
+        c.win[j][e] = r.at(e);
+        c.dp[j][e] = 0.f;                // (of tokens whose inputs' gradients are another run's, or in front of the first)
       }
     }
-    const T* x = (const T*)a.x + p.b * a.xb + p.t0 * a.xt + p.c;
-    const T* dy = (const T*)a.dy + (((size_t)p.b * a.H + p.c / a.D) * a.T + p.t0) * a.D + p.c % a.D;
-    T* dx = (T*)a.dx + p.b * a.db + ((long long)p.t0 - (W - 1)) * a.dt + p.c;
-    constexpr int U = 2;
-    // the next U tokens' rows are on their way while these are worked on
-    Elems<T, E> nx[U], nd[U];
-    const auto fetch = [&](int t) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        nx[u].zero();
-        nd[u].zero();
-        if (t + u < t1 && t + u < n) {
-          nx[u].load(x + u * a.xt);
-          nd[u].load(dy + (size_t)u * a.D);
-        }
-      }
-      x += U * a.xt;
-      dy += (size_t)U * a.D;
-    };
-    fetch(p.t0);
     for (int t = p.t0; t < t1; t += U, dx += U * a.dt) {
       Elems<T, E> rx[U], rd[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) rx[u] = nx[u], rd[u] = nd[u];
       fetch(t + U);
+      if (t >= p.t0 + W - 1 && t + U <= min(n, own)) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          float o[E];
+          conv_bwd_token<SILU, true>(c, rx[u], rd[u], true, true, o);
+          Elems<T, E> out;
+          out.set(o);
+          out.store(dx + u * a.dt);
+        }
+        continue;
+      }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int r = t + u - (W - 1);   // the row whose gradient is complete with dpre of t + u
+        const int r = t + u - (W - 1);   // the row whose gradient is complete with this token
         if (t + u >= t1) break;
         float o[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          win[W - 1][e] = rx[u].at(e);
-          float d = rd[u].at(e);         // 0 behind the sequence
-          if (a.silu) {
-            float s = bias[e];
-#pragma unroll
-            for (int j = 0; j < W; ++j) s = fmaf(w[j][e], win[j][e], s);
-            const float g = sigmoid_f(s);
-            d *= fmaf(s, g * (1.f - g), g);
-          }
-          if (t + u >= n) d = 0.f;
-          dp[W - 1][e] = d;
-          if (t + u < own && t + u < n) {
-            db[e] += d;
-#pragma unroll
-            for (int j = 0; j < W; ++j) dw[j][e] = fmaf(d, win[j][e], dw[j][e]);
-          }
-          o[e] = 0.f;
-#pragma unroll
-          for (int k = 0; k < W; ++k) o[e] = fmaf(w[W - 1 - k][e], dp[k][e], o[e]);
-#pragma unroll
-          for (int j = 0; j < W - 1; ++j) {
-            win[j][e] = win[j + 1][e];
-            dp[j][e] = dp[j + 1][e];
-          }
-        }
+        conv_bwd_token<SILU, false>(c, rx[u], rd[u], t + u < n, t + u < own, o);
         if (a.d_state && r < n && r >= n - (W - 1)) {
           float f[E];
           load_f32<E>(a.d_state + ((size_t)p.b * (W - 1) + (r - n + W - 1)) * a.C + p.c, f);
@@ -276,8 +313,8 @@ template <typename T, int W, int E> __global__ __launch_bounds__(kConvThreads) v
 #pragma unroll
   for (int e = 0; e < E; ++e) {
 #pragma unroll
-    for (int j = 0; j < W; ++j) mine[(j * E + e) * kConvThreads] = dw[j][e];
-    mine[(W * E + e) * kConvThreads] = db[e];
+    for (int j = 0; j < W; ++j) mine[(j * E + e) * kConvThreads] = c.dw[j][e];
+    mine[(W * E + e) * kConvThreads] = c.db[e];
   }
   __syncthreads();
   const int lanes = 1 << a.lanes_log2, runs = kConvThreads >> a.lanes_log2;
@@ -380,7 +417,11 @@ hipError_t launch_conv_bwd(const void* x, long long xb, long long xt, const floa
   constexpr int E = conv_e<T>(true);
   conv_plan(a, E);
   const int parts = B * a.blocks_t;
-  KDA_CONV_W(W_, (conv_bwd_kernel<T, W, E><<<conv_grid(a, E), kConvThreads, 0, s>>>(a)))
+  if (silu) {
+    KDA_CONV_W(W_, (conv_bwd_kernel<T, W, E, true><<<conv_grid(a, E), kConvThreads, 0, s>>>(a)))
+  } else {
+    KDA_CONV_W(W_, (conv_bwd_kernel<T, W, E, false><<<conv_grid(a, E), kConvThreads, 0, s>>>(a)))
+  }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !a.parts) return e;
   KDA_CONV_W(W_, (conv_params_kernel<W><<<((W + 1) * a.C + 63) / 64, kSumThreads, 0, s>>>(a.parts, parts, a.C, dw, db)))
