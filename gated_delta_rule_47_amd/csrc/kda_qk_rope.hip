@@ -185,7 +185,7 @@ template <typename T, int L, bool INTER> __global__ __launch_bounds__(kQkThreads
   const QkSide& sd = a.side[hs.side];
   const size_t yh = (size_t)a.T * a.D;
   float w[8], dw[8];
-  qk_weight(sd.w + (sd.per_head ? (size_t)hs.h0 * a.D : 0), it, w);
+  qk_weight(sd.w && sd.per_head ? sd.w + (size_t)hs.h0 * a.D : sd.w, it, w);      // (a row per head without weights: ones)
 #pragma unroll
   for (int e = 0; e < 8; ++e) dw[e] = 0.f;
   for (int k = 0; k < a.tokens; ++k) {

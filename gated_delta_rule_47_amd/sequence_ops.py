@@ -48,8 +48,6 @@ def _strided(name, t, shape, dtype, dev):
 
 
 _entries = {}
-_stream = torch._C._cuda_getCurrentRawStream
-_device = torch._C._cuda_getDevice
 
 
 def _run(dev, fn, *args):
@@ -57,11 +55,12 @@ def _run(dev, fn, *args):
     f = _entries.get(fn)
     if f is None:
         f = _entries[fn] = getattr(_lib.load(), fn)
-    if dev == _device():
-        st = f(*args, _stream(dev))
+    c = torch._C
+    if dev == c._cuda_getDevice():
+        st = f(*args, c._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
-            st = f(*args, _stream(dev))
+            st = f(*args, c._cuda_getCurrentRawStream(dev))
     if st:
         raise KdaError(fn, st)
 

@@ -228,6 +228,32 @@ def test_zero_and_non_finite_rows():
     assert torch.isfinite(g["dq_weight"]).all() and torch.isfinite(g["dq"]).all()
 
 
+def test_gradients_of_weights_that_are_not_given():
+    """The C entry takes the weights' gradients without weights (ones), a row per head or one for all, and keys alone."""
+    from gated_delta_rule_47_amd import _lib
+    lib = _lib.load()
+    B, T, H, D = 2, 40, 3, 32
+    x, dy = torch.randn(B, T, H, D, device=DEV), torch.randn(B, H, T, D, device=DEV)
+    f = kda.rope_frequencies(D, device=DEV)[0]
+    st = x.stride()[:3]
+    for rows in (1, H):
+        want = kda.qk_norm_rope_bwd(x, None, f, dy, None, q_weight=torch.ones(rows, D, device=DEV))
+        for keys in (False, True):
+            dx, dw = torch.zeros_like(x), torch.zeros(rows, D, device=DEV)
+            need = lib.kda_qk_norm_rope_bwd_workspace_bytes(B, T, 0 if keys else H, 1 if keys else rows, H if keys else 0, rows, D)
+            ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+            side, none = (x.data_ptr(), *st), (None, 0, 0, 0)
+            out = (dx.data_ptr(), *st)
+            a = (none, side) if keys else (side, none)
+            o = (none, out) if keys else (out, none)
+            r = lib.kda_qk_norm_rope_bwd(*a[0], *a[1], None, 1 if keys else rows, None, rows, 1, 1e-6, f.data_ptr(), None, 1.0, 0,
+                                         None if keys else dy.data_ptr(), dy.data_ptr() if keys else None, *o[0], *o[1],
+                                         None if keys else dw.data_ptr(), dw.data_ptr() if keys else None, ws.data_ptr(), need,
+                                         B, T, 0 if keys else H, H if keys else 0, D, D, 0, torch.cuda.current_stream().cuda_stream)
+            torch.cuda.synchronize()
+            assert r == 0 and torch.equal(dx, want["dq"]) and torch.equal(dw, want["dq_weight"]), (rows, keys)
+
+
 def test_no_tokens():
     x = torch.empty(2, 0, 3, 16, device=DEV)
     f = kda.rope_frequencies(16, device=DEV)[0]
