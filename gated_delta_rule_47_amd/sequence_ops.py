@@ -118,10 +118,11 @@ def short_conv_step(x, weight, bias, state, activation="silu", out=None):
     px, sx = _strided("x", x, (B, C), dt, dev)
     pw, pb = _ptr("weight", weight, (C, W), _F32, dev), _opt("bias", bias, (C,), _F32, dev)
     ps = _ptr("state", state, (B, W - 1, C), dt, dev)
-    po = _opt("out", out, (B, C), dt, dev)
-    _gpu(dev)
-    if out is None:
-        out = x.new_empty((B, C))
+    po = None if out is None else _ptr("out", out, (B, C), dt, dev)
+    if dev < 0:
+        _gpu(dev)
+    if po is None:
+        out = torch.empty_like(x) if sx[0] == C else x.new_empty((B, C))
         po = out.data_ptr()
     _run(dev, "kda_short_conv_step", px, sx[0], pw, pb, act, ps, po, B, 1, C, W, code)
     return out
@@ -185,22 +186,23 @@ def _side(name, x, B, T, D, weight, dt, dev):
     if x is None:
         if weight is not None:
             raise ValueError("%s_weight without %s" % (name, name))
-        return 0, 1, None, (0, 0, 0), None
+        return 0, 1, None, (0, 0, 0, 1), None
     H = x.shape[2]
     px, sx = _strided(name, x, (B, T, H, D), dt, dev)
-    pw, Hw = None, 1
-    if weight is not None:
-        Hw = weight.shape[0]
-        if Hw not in (1, H):
-            raise ValueError("%s_weight has %d rows for %d heads" % (name, Hw, H))
-        pw = _ptr(name + "_weight", weight, (Hw, D), _F32, dev)
-    return H, Hw, px, sx[:3], pw
+    if weight is None:
+        return H, 1, px, sx, None
+    Hw = weight.shape[0]
+    if Hw != 1 and Hw != H:
+        raise ValueError("%s_weight has %d rows for %d heads" % (name, Hw, H))
+    return H, Hw, px, sx, _ptr(name + "_weight", weight, (Hw, D), _F32, dev)
 
 
 def _rope(freqs, positions, B, T, dev):
-    R = 0 if freqs is None else 2 * freqs.shape[0]
-    pf = None if freqs is None else _ptr("freqs", freqs, (R // 2,), _F64, dev)
-    return R, pf, _opt("positions", positions, (B, T), _I32, dev)
+    pp = None if positions is None else _ptr("positions", positions, (B, T), _I32, dev)
+    if freqs is None:
+        return 0, None, pp
+    n = freqs.shape[0]
+    return 2 * n, _ptr("freqs", freqs, (n,), _F64, dev), pp
 
 
 def qk_norm_rope_fwd(q, k, freqs, positions=None, norm="rms", q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
@@ -215,9 +217,10 @@ def qk_norm_rope_fwd(q, k, freqs, positions=None, norm="rms", q_weight=None, k_w
     Hq, Hqw, pq, sq, pqw = _side("q", q, B, T, D, q_weight, dt, dev)
     Hk, Hkw, pk, sk, pkw = _side("k", k, B, T, D, k_weight, dt, dev)
     R, pf, pp = _rope(freqs, positions, B, T, dev)
-    po = _opt("q_out", q_out, (B, Hq, T, D), dt, dev)
-    pe = None if k is None else _opt("k_out", k_out, (B, Hk, T, D), dt, dev)
-    _gpu(dev)
+    po = None if q_out is None else _ptr("q_out", q_out, (B, Hq, T, D), dt, dev)
+    pe = None if k is None or k_out is None else _ptr("k_out", k_out, (B, Hk, T, D), dt, dev)
+    if dev < 0:
+        _gpu(dev)
     if q_out is None:
         q_out = q.new_empty((B, Hq, T, D))
         po = q_out.data_ptr()
@@ -226,8 +229,8 @@ def qk_norm_rope_fwd(q, k, freqs, positions=None, norm="rms", q_weight=None, k_w
     elif k_out is None:
         k_out = q.new_empty((B, Hk, T, D))
         pe = k_out.data_ptr()
-    _run(dev, "kda_qk_norm_rope_fwd", pq, *sq, pk, *sk, pqw, Hqw, pkw, Hkw, kind, float(eps), pf, pp, float(rope_scale),
-         int(bool(interleaved)), po, pe, B, T, Hq, Hk, D, R, code)
+    _run(dev, "kda_qk_norm_rope_fwd", pq, sq[0], sq[1], sq[2], pk, sk[0], sk[1], sk[2], pqw, Hqw, pkw, Hkw, kind, float(eps), pf, pp,
+         float(rope_scale), 1 if interleaved else 0, po, pe, B, T, Hq, Hk, D, R, code)
     return q_out, k_out
 
 
@@ -270,7 +273,7 @@ def qk_norm_rope_bwd(q, k, freqs, d_q, d_k, positions=None, norm="rms", q_weight
     if pgq is not None or pgk is not None:
         need = _bytes("kda_qk_norm_rope_bwd_workspace_bytes", B, T, Hq, Hqw, Hk, Hkw, D)
     ws, pws, nws = _workspace(workspace, need, q)
-    _run(dev, "kda_qk_norm_rope_bwd", pq, *sq, pk, *sk, pqw, Hqw, pkw, Hkw, kind, float(eps), pf, pp, float(rope_scale),
+    _run(dev, "kda_qk_norm_rope_bwd", pq, *sq[:3], pk, *sk[:3], pqw, Hqw, pkw, Hkw, kind, float(eps), pf, pp, float(rope_scale),
          int(bool(interleaved)), pdq, pdk, poq, *soq[:3], pok, *sok[:3], pgq, pgk, pws, nws, B, T, Hq, Hk, D, R, code)
     return dict(dq=dq_out, dk=dk_out, dq_weight=dqw, dk_weight=dkw)
 
@@ -316,20 +319,20 @@ def gated_scan_fwd(x, z, A_log, dt_bias=None, state_in=None, input_gate=None, le
 
 def gated_scan_step(x, z, A_log, dt_bias, state, input_gate=None, normalize=True, out=None):
     """One token per channel: x, z, input_gate (B,H,D).  Updates `state` (B,H,D) float32 in place and returns y (B,H,D)."""
-    B, H, D = x.shape
-    dt, dev = x.dtype, x.get_device()
+    shape, dt, dev = x.shape, x.dtype, x.get_device()
+    B, H, D = shape
     code = _code(dt)
-    shape = (B, H, D)
-    px, pz = _ptr("x", x, shape, dt, dev), _ptr("z", z, shape, dt, dev)
-    pi = _opt("input_gate", input_gate, shape, dt, dev)
-    pa, pb = _ptr("A_log", A_log, (H,), _F32, dev), _opt("dt_bias", dt_bias, (H, D), _F32, dev)
+    pi = None if input_gate is None else _ptr("input_gate", input_gate, shape, dt, dev)
+    pb = None if dt_bias is None else _ptr("dt_bias", dt_bias, (H, D), _F32, dev)
+    px, pz, pa = _ptr("x", x, shape, dt, dev), _ptr("z", z, shape, dt, dev), _ptr("A_log", A_log, (H,), _F32, dev)
     ps = _ptr("state", state, shape, _F32, dev)
-    po = _opt("out", out, shape, dt, dev)
-    _gpu(dev)
-    if out is None:
+    po = None if out is None else _ptr("out", out, shape, dt, dev)
+    if dev < 0:
+        _gpu(dev)
+    if po is None:
         out = torch.empty_like(x)
         po = out.data_ptr()
-    _run(dev, "kda_gated_scan_step", px, pz, pa, pb, pi, int(bool(normalize)), ps, po, B, H, D, code)
+    _run(dev, "kda_gated_scan_step", px, pz, pa, pb, pi, 1 if normalize else 0, ps, po, B, H, D, code)
     return out
 
 
