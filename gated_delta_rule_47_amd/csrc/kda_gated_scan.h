@@ -18,6 +18,10 @@
 // tile waits for belongs to a workgroup that already runs and that publishes without waiting, so every wait ends.  (One
 // counter per channel tile, on a line of its own: with a single one the padded batch of 8 x 8 x 4096 x 64 took 48 us for 42.)  Words are written
 // and read by device-scope atomics (past the XCDs' own L2), each record complete before its flag.
+//
+// Bound by memory and next to it by the vector unit (about 52 and 69 instructions an element, transcendentals among them, busy
+// 60 to 70 % of the time).  Measured, bf16 with both gates: forward, 8 x 8192 x 4096, 434 us (4.95 TB/s), 1 x 30011 x 4096, 222 us
+// (4.4); adjoint, 4 x 8192 x 2048, 214 us (4.4); one token of 192 x 4096, 4.6 us.
 #pragma once
 
 #include "kda_launch.h"

