@@ -8,6 +8,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libkda.so")
 
 KDA_OK = 0
+KDA_ERR_SHAPE = -2
 KDA_F32 = 0
 KDA_BF16 = 1
 COUNTER_NAMES = ("gate", "chunk_fwd", "recurrent_step", "chunk_bwd", "rejected", "gate_bwd")

@@ -47,6 +47,20 @@ def _strided(name, t, shape, dtype, dev):
     _refuse(name, t, shape, dtype, dev)
 
 
+_INT = 0x7fffffff
+
+
+def _fits(fn, *sizes):
+    """Sizes are handed over in 32 bits: what has more is refused here, as the library refuses what is too large for it."""
+    if max(sizes) > _INT:
+        raise KdaError(fn, _lib.KDA_ERR_SHAPE)
+
+
+def _need(fn, *sizes):
+    _fits(fn, *sizes)
+    return _bytes(fn, *sizes)
+
+
 _entries = {}
 
 
@@ -88,6 +102,8 @@ def short_conv_fwd(x, weight, bias=None, state_in=None, lengths=None, activation
     W = weight.shape[-1]
     dt, dev = x.dtype, x.get_device()
     code, act = _code(dt), _one_of("activation", activation, _ACTS)
+    if not 0 < x.numel() <= _INT or W > 4:
+        _fits("kda_short_conv_fwd", B, T, C, W)
     if heads < 1 or C % heads:
         raise ValueError("%d channels do not make %r heads" % (C, heads))
     shape, state = (B, heads, T, C // heads), (B, W - 1, C)
@@ -115,6 +131,8 @@ def short_conv_step(x, weight, bias, state, activation="silu", out=None):
     W = weight.shape[-1]
     dt, dev = x.dtype, x.get_device()
     code, act = _code(dt), _one_of("activation", activation, _ACTS)
+    if not 0 < x.numel() <= _INT or W > 4:
+        _fits("kda_short_conv_step", B, C, W)
     px, sx = _strided("x", x, (B, C), dt, dev)
     pw, pb = _ptr("weight", weight, (C, W), _F32, dev), _opt("bias", bias, (C,), _F32, dev)
     ps = _ptr("state", state, (B, W - 1, C), dt, dev)
@@ -129,7 +147,7 @@ def short_conv_step(x, weight, bias, state, activation="silu", out=None):
 
 
 def short_conv_bwd_workspace_bytes(B, H, T, D, W, dtype=torch.bfloat16) -> int:
-    return _bytes("kda_short_conv_bwd_workspace_bytes", B, H, T, D, W, _code(dtype))
+    return _need("kda_short_conv_bwd_workspace_bytes", B, H, T, D, W, _code(dtype))
 
 
 def short_conv_bwd(x, weight, bias, state_in, dy, d_state_out=None, lengths=None, activation="silu", want_params=True,
@@ -141,6 +159,8 @@ def short_conv_bwd(x, weight, bias, state_in, dy, d_state_out=None, lengths=None
     W = weight.shape[-1]
     dt, dev = x.dtype, x.get_device()
     code, act = _code(dt), _one_of("activation", activation, _ACTS)
+    if not 0 < x.numel() <= _INT or W > 4:
+        _fits("kda_short_conv_bwd", B, T, C, W)
     H = dy.shape[1]
     if H < 1 or C % H:
         raise ValueError("%d channels do not make %d heads" % (C, H))
@@ -172,6 +192,8 @@ def rope_frequencies(rot_dim, base=10000.0, scaling=None, factor=1.0, trained_le
     that the slowest pair is slowed by factor; "parts": pairs of more than fast_turns turns over trained_length tokens
     left, those below slow_turns slowed by factor, shares between, rope_scale = 0.1 ln(factor) + 1."""
     n = max(int(rot_dim) // 2, 1)
+    if n > 1 << 19:                            # (the library's limit, before the table is made)
+        raise KdaError("kda_rope_frequencies", _lib.KDA_ERR_SHAPE)
     table, scale = (ctypes.c_double * n)(), ctypes.c_double()
     st = _lib.load().kda_rope_frequencies(table, ctypes.byref(scale), int(rot_dim), float(base),
                                           _one_of("scaling", scaling, _SCALINGS), float(factor), float(trained_length),
@@ -188,6 +210,8 @@ def _side(name, x, B, T, D, weight, dt, dev):
             raise ValueError("%s_weight without %s" % (name, name))
         return 0, 1, None, (0, 0, 0, 1), None
     H = x.shape[2]
+    if not 0 < x.numel() <= _INT:
+        _fits("kda_qk_norm_rope", *x.shape)
     px, sx = _strided(name, x, (B, T, H, D), dt, dev)
     if weight is None:
         return H, 1, px, sx, None
@@ -202,6 +226,8 @@ def _rope(freqs, positions, B, T, dev):
     if freqs is None:
         return 0, None, pp
     n = freqs.shape[0]
+    if n > 128:
+        _fits("kda_qk_norm_rope", 2 * n)
     return 2 * n, _ptr("freqs", freqs, (n,), _F64, dev), pp
 
 
@@ -235,7 +261,7 @@ def qk_norm_rope_fwd(q, k, freqs, positions=None, norm="rms", q_weight=None, k_w
 
 
 def qk_norm_rope_bwd_workspace_bytes(B, T, Hq, Hk, D, q_weight_rows=1, k_weight_rows=1) -> int:
-    return _bytes("kda_qk_norm_rope_bwd_workspace_bytes", B, T, Hq, q_weight_rows, Hk, k_weight_rows, D)
+    return _need("kda_qk_norm_rope_bwd_workspace_bytes", B, T, Hq, q_weight_rows, Hk, k_weight_rows, D)
 
 
 def qk_norm_rope_bwd(q, k, freqs, d_q, d_k, positions=None, norm="rms", q_weight=None, k_weight=None, eps=1e-6,
@@ -279,7 +305,7 @@ def qk_norm_rope_bwd(q, k, freqs, d_q, d_k, positions=None, norm="rms", q_weight
 
 
 def gated_scan_workspace_bytes(B, H, T, D, dtype=torch.bfloat16) -> int:
-    return _bytes("kda_gated_scan_workspace_bytes", B, H, T, D, _code(dtype))
+    return _need("kda_gated_scan_workspace_bytes", B, H, T, D, _code(dtype))
 
 
 def gated_scan_fwd(x, z, A_log, dt_bias=None, state_in=None, input_gate=None, lengths=None, normalize=True,
@@ -293,6 +319,8 @@ def gated_scan_fwd(x, z, A_log, dt_bias=None, state_in=None, input_gate=None, le
     B, H, T, D = x.shape
     dt, dev = x.dtype, x.get_device()
     code = _code(dt)
+    if not 0 < x.numel() <= _INT:
+        _fits("kda_gated_scan_fwd", B, H, T, D)
     shape, state = (B, H, T, D), (B, H, D)
     px, pz = _ptr("x", x, shape, dt, dev), _ptr("z", z, shape, dt, dev)
     pi = _opt("input_gate", input_gate, shape, dt, dev)
@@ -322,6 +350,8 @@ def gated_scan_step(x, z, A_log, dt_bias, state, input_gate=None, normalize=True
     shape, dt, dev = x.shape, x.dtype, x.get_device()
     B, H, D = shape
     code = _code(dt)
+    if not 0 < x.numel() <= _INT:
+        _fits("kda_gated_scan_step", B, H, D)
     pi = None if input_gate is None else _ptr("input_gate", input_gate, shape, dt, dev)
     pb = None if dt_bias is None else _ptr("dt_bias", dt_bias, (H, D), _F32, dev)
     px, pz, pa = _ptr("x", x, shape, dt, dev), _ptr("z", z, shape, dt, dev), _ptr("A_log", A_log, (H,), _F32, dev)
@@ -337,7 +367,7 @@ def gated_scan_step(x, z, A_log, dt_bias, state, input_gate=None, normalize=True
 
 
 def gated_scan_bwd_workspace_bytes(B, H, T, D, dtype=torch.bfloat16) -> int:
-    return _bytes("kda_gated_scan_bwd_workspace_bytes", B, H, T, D, _code(dtype))
+    return _need("kda_gated_scan_bwd_workspace_bytes", B, H, T, D, _code(dtype))
 
 
 def gated_scan_bwd(x, z, A_log, dt_bias, ckpt, dy, d_state_out=None, input_gate=None, lengths=None, normalize=True,
@@ -348,6 +378,8 @@ def gated_scan_bwd(x, z, A_log, dt_bias, ckpt, dy, d_state_out=None, input_gate=
     B, H, T, D = x.shape
     dt, dev = x.dtype, x.get_device()
     code = _code(dt)
+    if not 0 < x.numel() <= _INT:
+        _fits("kda_gated_scan_bwd", B, H, T, D)
     shape, state = (B, H, T, D), (B, H, D)
     px, pz, pd = _ptr("x", x, shape, dt, dev), _ptr("z", z, shape, dt, dev), _ptr("dy", dy, shape, dt, dev)
     pi = _opt("input_gate", input_gate, shape, dt, dev)

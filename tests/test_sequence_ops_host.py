@@ -240,3 +240,27 @@ def test_binding_refuses_before_the_library():
             kda.gated_scan_fwd(**{**dict(x=g, z=g, A_log=torch.zeros(3)), **kw})
     with pytest.raises(ValueError):                              # one chunk's state too few
         kda.gated_scan_bwd(g, g, torch.zeros(3), None, torch.zeros(2, 3, 1, 8), g)
+
+
+def test_sizes_of_more_than_32_bits():
+    """A size that 32 bits would cut to a small one is refused (an expanded tensor holds it in little memory)."""
+    far = (1 << 32) + 16
+    e = lambda *s: torch.zeros((1,) * (len(s) - 1) + (s[-1],)).expand(*s)
+    w, f, A, one = torch.zeros(16, 4), torch.zeros(8, dtype=torch.float64), torch.zeros(1), torch.zeros(1, 2, 1, 16)
+    for call in (lambda: kda.short_conv_fwd(e(1, far, 16), w), lambda: kda.short_conv_fwd(e(far, 0, 16), w),
+                 lambda: kda.short_conv_fwd(e(1, 2, 16), torch.zeros(1, 1).expand(16, far)),
+                 lambda: kda.short_conv_step(e(far, 16), w, None, torch.zeros(1, 3, 16)),
+                 lambda: kda.short_conv_bwd(e(1, far, 16), w, None, None, e(1, 1, far, 16)),
+                 lambda: kda.qk_norm_rope_fwd(e(1, far, 1, 16), None, f), lambda: kda.qk_norm_rope_fwd(one, e(1, 2, far, 16), f),
+                 lambda: kda.qk_norm_rope_fwd(one, None, torch.zeros(1, dtype=torch.float64).expand(far // 2)),
+                 lambda: kda.qk_norm_rope_bwd(e(far, 1, 1, 16), None, f, None, None),
+                 lambda: kda.gated_scan_fwd(e(1, 1, far, 16), e(1, 1, far, 16), A),
+                 lambda: kda.gated_scan_step(e(1, far, 16), e(1, far, 16), A, None, None),
+                 lambda: kda.gated_scan_bwd(e(1, 1, far, 16), e(1, 1, far, 16), A, None, None, None),
+                 lambda: kda.gated_scan_workspace_bytes(1, 1, far, 16), lambda: kda.gated_scan_bwd_workspace_bytes(far, 1, 1, 16),
+                 lambda: kda.short_conv_bwd_workspace_bytes(1, 1, far, 16, 4),
+                 lambda: kda.qk_norm_rope_bwd_workspace_bytes(1, far, 1, 1, 16),
+                 lambda: kda.rope_frequencies(far)):
+        with pytest.raises(kda.KdaError) as err:
+            call()
+        assert err.value.status == SHAPE
