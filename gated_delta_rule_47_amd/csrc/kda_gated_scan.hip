@@ -84,8 +84,9 @@ ScanArgs scan_args(const void* x, const void* z, const float* A_log, const float
   return a;
 }
 
-// Channels per lane: two bf16 that no head's end separates.
-int scan_e(int D, bool bf16) { return bf16 && D % 2 == 0 ? 2 : 1; }
+// Channels per lane: two bf16, for one token only where no head's end separates them.
+int scan_e(int D, bool bf16) { return bf16 && D > 1 ? 2 : 1; }
+int scan_step_e(int D, bool bf16) { return bf16 && D % 2 == 0 ? 2 : 1; }
 
 struct ScanPlan {
   int E, ctiles, tiles;
@@ -96,7 +97,7 @@ ScanPlan scan_plan(int B, int H, int T, int D, bool bf16, bool bwd) {
   ScanPlan p;
   const long long N = (long long)B * H * D;
   p.E = scan_e(D, bf16);
-  p.ctiles = (int)((N + 64 * p.E - 1) / (64 * p.E));
+  p.ctiles = (int)(((long long)B * H * ((D + p.E - 1) / p.E) + 63) / 64);
   const int tokens = bwd ? kScanBwdWaves * kScanBwdTokens : scan_fwd_waves(p.ctiles) * kScanFwdTokens;
   p.tiles = T > tokens ? (T + tokens - 1) / tokens : 1;
   const size_t n = p.tiles > 1 ? (size_t)p.ctiles * p.tiles : 0;
@@ -141,7 +142,7 @@ hipError_t launch_scan_step(const void* x, const void* z, const float* A_log, co
                             int normalize, float* state, void* y, int B, int H, int D, hipStream_t s) {
   ScanArgs a = scan_args(x, z, A_log, dt_bias, i, nullptr, normalize, B, H, 1, D);
   a.state_out = state, a.y = y;
-  const int E = scan_e(D, sizeof(T) == 2);
+  const int E = scan_step_e(D, sizeof(T) == 2);
   const unsigned grid = (unsigned)(((long long)B * H * D / E + kScanThreads - 1) / kScanThreads);
   if constexpr (sizeof(T) == 2)
     if (E == 2) {

@@ -17,7 +17,8 @@ template <int E> struct ScanShared {
   float2 qg[NW][S][E][64];                 // q and g2 of every token, each lane's own: what the last pass alone needs
 };
 
-// FULL: every token of the tile lies inside its sequence, in every lane (the same for all waves).
+// FULL: every token of the tile lies inside its sequence and all channels are their lane's own, in every lane (the same for
+// all waves).
 template <typename T, int E, bool GATE, bool NORM, bool FULL, typename Off>
 __device__ __forceinline__ void scan_bwd_tile(const ScanArgs& a, ScanShared<E>& sh, const ScanTile tile, const ScanLane<E>& l,
                                               int lane, int w) {
@@ -126,9 +127,10 @@ __device__ __forceinline__ void scan_bwd_tile(const ScanArgs& a, ScanShared<E>& 
     if (tile.j + 1 < a.tiles) {
       put_words<E>(a.link.states + rec * (64 * E) + lane, Rt);
       publish(a.link.flags + rec, 2u);
-    } else if (l.on) {
+    } else {
 #pragma unroll
-      for (int e = 0; e < E; ++e) a.d_state_in[l.ch + e] = Rt[e];
+      for (int e = 0; e < E; ++e)
+        if (FULL || l.own(e)) a.d_state_in[l.ch + e] = Rt[e];
     }
   }
   // h in front of this wave's tokens
@@ -178,9 +180,9 @@ __device__ __forceinline__ void scan_bwd_tile(const ScanArgs& a, ScanShared<E>& 
       r[e] = fmaf(v[k][e], r[e], r[e]);
     }
     if (FULL || (l.on && t0 + k < a.T)) {
-      scan_store<T, E>(a.dx, base + k * row, dx);
-      scan_store<T, E>(a.dz, base + k * row, dz);
-      if constexpr (GATE) scan_store<T, E>(a.di, base + k * row, di);
+      scan_store<T, E>(a.dx, base + k * row, dx, !FULL && l.last);
+      scan_store<T, E>(a.dz, base + k * row, dz, !FULL && l.last);
+      if constexpr (GATE) scan_store<T, E>(a.di, base + k * row, di, !FULL && l.last);
     }
   }
   if (!a.parts) return;
@@ -190,10 +192,11 @@ __device__ __forceinline__ void scan_bwd_tile(const ScanArgs& a, ScanShared<E>& 
     sh.qg[w][0][e][lane] = float2{sz[e], sa[e] * kLn2};        // (in the place of the wave's own, which it has used)
   }
   __syncthreads();
-  if (w == 0 && l.on) {
+  if (w == 0) {
     const size_t N = (size_t)a.B * a.H * a.D;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
+      if (!FULL && !l.own(e)) continue;
       float z = 0.f, s = 0.f;
 #pragma unroll
       for (int p = 0; p < NW; ++p) {
@@ -216,14 +219,14 @@ __device__ __forceinline__ void scan_bwd_zeros(const ScanArgs& a, const ScanLane
     const int t = (jt * NW + w) * S + k;
     if (t >= a.T) break;
     const Off off = (((Off)l.bh * a.T + t) * a.D + l.d) * sizeof(T);
-    scan_store<T, E>(a.dx, off, zero);
-    scan_store<T, E>(a.dz, off, zero);
-    if constexpr (GATE) scan_store<T, E>(a.di, off, zero);
+    scan_store<T, E>(a.dx, off, zero, l.last);
+    scan_store<T, E>(a.dz, off, zero, l.last);
+    if constexpr (GATE) scan_store<T, E>(a.di, off, zero, l.last);
   }
   if (a.parts && w == 0)
 #pragma unroll
     for (int e = 0; e < E; ++e)
-      a.parts[(size_t)jt * a.B * a.H * a.D + l.ch + e] = a.parts[((size_t)a.tiles + jt) * a.B * a.H * a.D + l.ch + e] = 0.f;
+      if (l.own(e)) a.parts[(size_t)jt * a.B * a.H * a.D + l.ch + e] = a.parts[((size_t)a.tiles + jt) * a.B * a.H * a.D + l.ch + e] = 0.f;
 }
 
 template <typename T, int E, bool GATE, bool NORM, typename Off>
@@ -234,7 +237,7 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4))) vo
   const ScanLane<E> l = scan_lane<E>(a, tile.c, lane);
   const int jt = a.tiles - 1 - tile.j;
   if (jt > 0 && !__any(l.n > jt * (NW * S))) scan_bwd_zeros<T, E, GATE, Off>(a, l, jt, w);
-  else if (__all((jt + 1) * (NW * S) <= l.n)) scan_bwd_tile<T, E, GATE, NORM, true, Off>(a, sh, tile, l, lane, w);
+  else if (__all((jt + 1) * (NW * S) <= l.n && !l.last)) scan_bwd_tile<T, E, GATE, NORM, true, Off>(a, sh, tile, l, lane, w);
   else scan_bwd_tile<T, E, GATE, NORM, false, Off>(a, sh, tile, l, lane, w);
 }
 

@@ -13,8 +13,8 @@ template <int E, int NW> struct ScanShared {
   float G[NW][E][64], W[NW][E][64], H[NW][E][64], in[E][64];     // sums of g2, the decays over them, states from zero
 };
 
-// FULL: every token of the tile lies inside its sequence, in every lane (the same for all waves, whose lanes are the
-// same channels).
+// FULL: every token of the tile lies inside its sequence and all channels are their lane's own, in every lane (the same for
+// all waves, whose lanes are the same channels).
 template <typename T, int E, int NW, bool GATE, bool NORM, bool FULL, typename Off>
 __device__ __forceinline__ void scan_fwd_tile(const ScanArgs& a, ScanShared<E, NW>& sh, const ScanTile tile, const ScanLane<E>& l,
                                               int lane, int w) {
@@ -79,9 +79,9 @@ __device__ __forceinline__ void scan_fwd_tile(const ScanArgs& a, ScanShared<E, N
 #pragma unroll
     for (int e = 0; e < E; ++e) Wt[e] = word_of(Wt[e]);
     if (tile.j == 0) {
-      if (a.state_in && l.on)
+      if (a.state_in)                      // (another lane's channel may have its last state there by now)
 #pragma unroll
-        for (int e = 0; e < E; ++e) h[e] = a.state_in[l.ch + e];
+        for (int e = 0; e < E; ++e) h[e] = FULL || l.own(e) ? a.state_in[l.ch + e] : 0.f;
     } else {
       float* pair = a.link.pairs + rec * (128 * E) + lane;
       put_words<E>(pair, Wt);
@@ -110,20 +110,22 @@ __device__ __forceinline__ void scan_fwd_tile(const ScanArgs& a, ScanShared<E, N
   if (a.ckpt && t0 % KDA_GATED_SCAN_CHUNK == 0 && t0 < l.n) {
     const int chunks = (a.T + KDA_GATED_SCAN_CHUNK - 1) / KDA_GATED_SCAN_CHUNK;
 #pragma unroll
-    for (int e = 0; e < E; ++e) a.ckpt[((size_t)l.bh * chunks + t0 / KDA_GATED_SCAN_CHUNK) * a.D + l.d + e] = h[e];
+    for (int e = 0; e < E; ++e)
+      if (FULL || l.own(e)) a.ckpt[((size_t)l.bh * chunks + t0 / KDA_GATED_SCAN_CHUNK) * a.D + l.d + e] = h[e];
   }
   asm volatile("" : "+v"(base));           // the stores' offsets are computed anew, not kept in registers since the loads
 #pragma unroll
   for (int k = 0; k < S; ++k) {
 #pragma unroll
     for (int e = 0; e < E; ++e) h[e] = decay_step(v[k][e], h[e], u[k][e]);
-    if (FULL || t0 + k < l.n) scan_store<T, E>(a.y, base + k * row, h);
+    if (FULL || t0 + k < l.n) scan_store<T, E>(a.y, base + k * row, h, !FULL && l.last);
   }
   // the tile of a sequence's last token (or the first one) has its final state: behind it the state stays
   const int start = tile.j * (NW * S);
-  if (w == NW - 1 && a.state_out && l.on && l.n <= start + NW * S && (l.n > start || tile.j == 0))
+  if (w == NW - 1 && a.state_out && l.n <= start + NW * S && (l.n > start || tile.j == 0))
 #pragma unroll
-    for (int e = 0; e < E; ++e) a.state_out[l.ch + e] = h[e];
+    for (int e = 0; e < E; ++e)
+      if (FULL || l.own(e)) a.state_out[l.ch + e] = h[e];
 }
 
 template <typename T, int E, int NW, bool GATE, bool NORM, typename Off>
@@ -133,7 +135,7 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4))) vo
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const ScanLane<E> l = scan_lane<E>(a, tile.c, lane);
   if (tile.j > 0 && !__any(l.n > tile.j * (NW * S))) return;     // behind every lane's sequence, as are the tiles after it
-  if (__all((tile.j + 1) * (NW * S) <= l.n)) scan_fwd_tile<T, E, NW, GATE, NORM, true, Off>(a, sh, tile, l, lane, w);
+  if (__all((tile.j + 1) * (NW * S) <= l.n && !l.last)) scan_fwd_tile<T, E, NW, GATE, NORM, true, Off>(a, sh, tile, l, lane, w);
   else scan_fwd_tile<T, E, NW, GATE, NORM, false, Off>(a, sh, tile, l, lane, w);
 }
 

@@ -362,6 +362,26 @@ def test_options_workspaces_and_state_in_place():
     assert np.linalg.norm(host(same) - ref) <= 2.0 ** -8 * np.linalg.norm(ref)
 
 
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("B,H,D", [(1, 1, 3), (3, 2, 33), (1, 1, 129), (2, 1, 257)])
+def test_odd_heads_with_the_state_in_place(B, H, D, dtype):
+    """An odd head's last lane reads its neighbour's channel too: nothing of that reaches a state that is updated in place."""
+    T = 700
+    d = inputs(B, H, T, D, dtype, 5)
+    lt = torch.tensor([T, 0, 200][:B], dtype=torch.int32, device=DEV)
+    args = (d["x"], d["z"], d["A"], d["b"])
+    y, end, _ = kda.gated_scan_fwd(*args, d["s"], d["i"], lt, out=torch.zeros_like(d["x"]))
+    for _ in range(3):
+        st = d["s"].clone()
+        got, _, _ = kda.gated_scan_fwd(*args, st, d["i"], lt, out=torch.zeros_like(d["x"]), state_out=st)
+        assert torch.equal(got, y) and torch.equal(st, end)
+    for h in range(H):                                             # every head as if it were alone, whatever stands beside it
+        one = lambda t: t[:, h:h + 1].contiguous()
+        g1, e1, _ = kda.gated_scan_fwd(one(d["x"]), one(d["z"]), d["A"][h:h + 1], d["b"][h:h + 1], one(d["s"]), one(d["i"]), lt,
+                                       out=torch.zeros_like(one(d["x"])))
+        assert torch.equal(g1, one(y)) and torch.equal(e1, one(end))
+
+
 @pytest.mark.parametrize("shift", [1, 3])
 def test_rows_off_their_alignment(shift):
     B, H, T, D = 1, 2, 140, 6
