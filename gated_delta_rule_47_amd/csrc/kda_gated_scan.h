@@ -11,15 +11,16 @@
 // with one channel a lane).  Time is cut into tiles of NW waves of S tokens, one workgroup each.  A wave keeps the decays
 // and inputs of its S tokens in registers, so memory is read once: it folds them to one pair (decay over all of them,
 // state from zero), the workgroup's waves put these into LDS, one wave fetches the state in front of the tile from the
-// tiles before it (look_back); then every wave takes that state over the pairs of the waves in front of it and runs over
+// tiles before it (scan_link_tile); then every wave takes that state over the pairs of the waves in front of it and runs over
 // its tokens again from the true one.
 //
 // Tiles hand their states on through the workspace.  Each publishes its own pair as soon as it has it, without
 // waiting for anything, then takes the pairs of the tiles before it from the nearest one on that knows its final state,
 // and publishes its own final state.  A channel tile's workgroups take its tiles by a counter, in time order: whatever a
-// tile waits for belongs to a workgroup that already runs and that publishes without waiting, so every wait ends.  (One
-// counter per channel tile, on a line of its own: with a single one the padded batch of 8 x 8 x 4096 x 64 took 48 us for 42.)  Words are written
-// and read by device-scope atomics (past the XCDs' own L2), each record complete before its flag.
+// tile waits for belongs to a workgroup that already runs, and a pair is published without waiting (a group's pair waits
+// for its tiles' pairs alone), so every wait ends.  (One counter per channel tile, on a line of its own: with a single one
+// the padded batch of 8 x 8 x 4096 x 64 took 48 us for 42.)  Words are written and read by device-scope atomics (past the
+// XCDs' own L2), each record complete before its flag.
 //
 // Bound by memory and next to it by the vector unit (about 52 and 69 instructions an element, transcendentals among them, busy
 // 60 to 70 % of the time).  Measured, bf16 with both gates: forward, 8 x 8192 x 4096, 434 us (4.95 TB/s), 1 x 30011 x 4096, 222 us
@@ -65,6 +66,12 @@ __device__ __forceinline__ float word_of(float g2) {
   const float e = -fabsf(decay_weak(g2)), a = fast_exp2(g2);
   return g2 > kWeak ? e : a;
 }
+// The decay over both: two distances from 1 as long as theirs is below a half.
+__device__ __forceinline__ float word_join(float v, float w) {
+  const bool x = word_weak(v), y = word_weak(w);
+  const float e = fmaf(v, w, v) + w, a = (x ? 1.f + v : v) * (y ? 1.f + w : w);
+  return x && y && e > -0.5f ? -fabsf(e) : a;
+}
 __device__ __forceinline__ float word_step(float w, float h, float u) { return fmaf(w, h, (word_weak(w) ? h : 0.f) + u); }
 
 // A gate's argument (in units of log2(e)) whose softplus is 0, for tokens behind a sequence: g = 0, the state stays, and
@@ -102,12 +109,12 @@ template <typename T, int E, typename Off> __device__ __forceinline__ void scan_
   scan_store<T, E>(p, off, f);
 }
 
-// What links the tiles of a channel tile: a counter (every `every` words), a flag per tile (0 nothing, 1 its pair, 2 its final state too), the
-// records (64 lanes of E pairs, 64 lanes of E states).
+// What links the tiles of a channel tile: a counter (every `every` words), a flag per tile (0 nothing, 1 its pair, 2 its final
+// state too), the records (64 lanes of E pairs, 64 lanes of E states); a flag (1: its pair) and a pair per group of tiles.
 struct ScanLink {
-  uint32_t *tickets, *flags;
-  uint32_t every;
-  float *pairs, *states;
+  uint32_t *tickets, *flags, *group_flags;
+  uint32_t every, groups;                  // groups of a channel tile, 0: none
+  float *pairs, *states, *group_pairs;
 };
 struct ScanArgs {
   const void *x, *z, *i;
@@ -139,45 +146,127 @@ __device__ __forceinline__ void publish(uint32_t* flag, uint32_t value) {
   if ((threadIdx.x & 63) == 0) __hip_atomic_store(flag, value, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// State in front of tile j > 0 (in the order of the tickets) of the channel tile whose first record is `first`; one wave.
-// It starts from the nearest tile that knows its final state and takes the pairs behind it one after the other, as each of
-// those tiles does for its own final state: so the result is the same bit by bit wherever it starts.
-template <int E> __device__ __forceinline__ void look_back(const ScanLink& l, size_t first, int j, int lane, float (&h)[E]) {
-  int from;                                // that tile; the first of its channels always becomes one without waiting
-  for (int at = j - 1;;) {                 // the newest tile of a window of 64; all newer ones have their pairs
-    const int p = at - lane;
-    const uint32_t f = p >= 0 ? __hip_atomic_load(l.flags + first + p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0u;
+// The nearest place p <= at with flag(p) = 2 where all places behind it have theirs (1 or 2); one wave.  A place without
+// one belongs to a workgroup that runs and will publish; nearer places may have finished since, so it starts again.
+template <typename Flag> __device__ __forceinline__ int scan_nearest(int last, int lane, Flag flag) {
+  for (int at = last;;) {                  // the newest place of a window of 64
+    const uint32_t f = flag(at - lane);
     const unsigned long long none = ~__ballot(f >= 1u), final = __ballot(f == 2u);
     const int ready = none ? __builtin_ctzll(none) : 64, stop = final ? __builtin_ctzll(final) : 64;
-    if (stop < ready) {
-      from = at - stop;
-      break;
-    }
+    if (stop < ready) return at - stop;
     if (ready == 64) {
       at -= 64;
-    } else {                               // its workgroup runs and will publish; nearer tiles may have finished since
-      at = j - 1;
+    } else {
+      at = last;
       __builtin_amdgcn_s_sleep(1);
     }
   }
-  asm volatile("" ::: "memory");
-  get_words<E>(l.states + (first + from) * (64 * E) + lane, h);
+}
+__device__ __forceinline__ uint32_t scan_flag(const uint32_t* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+// h taken over the pairs of places k0 .. k1 - 1; with W also the decay over them.
+template <int E, bool WORDS> __device__ __forceinline__ void scan_fold(const float* pairs, int k0, int k1, int lane, float (&h)[E],
+                                                                      float (&W)[E]) {
   constexpr int U = 2;
 #pragma unroll 1
-  for (int k = from + 1; k < j; k += U) {
+  for (int k = k0; k < k1; k += U) {
     float pg[U][E], ph[U][E];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const float* r = l.pairs + (first + min(k + u, j - 1)) * (128 * E) + lane;
+      const float* r = pairs + (size_t)min(k + u, k1 - 1) * (128 * E) + lane;
       get_words<E>(r, pg[u]);
       get_words<E>(r + 64 * E, ph[u]);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (k + u < j)
+      if (k + u < k1)
 #pragma unroll
-        for (int e = 0; e < E; ++e) h[e] = word_step(pg[u][e], h[e], ph[u][e]);
+        for (int e = 0; e < E; ++e) {
+          h[e] = word_step(pg[u][e], h[e], ph[u][e]);
+          if constexpr (WORDS) W[e] = word_join(W[e], pg[u][e]);
+        }
   }
+}
+
+// Tiles of a group: 2^kScanGroupLog2, up to 64.  Few channels over a long time put hundreds of tiles to work at once, which
+// wait for joins one behind the other (0.2 us each); with groups a tile is as many joins away from a known state as there
+// are groups in front of it and tiles in its own.  1 x 32768 x 64, bf16, forward and backward: 26 and 84 us, 56 and 217
+// without; groups of 16: 26 and 79, but 1 x 8192 x 1024 66 for 60 us backward.
+constexpr int kScanGroupLog2 = 3;
+// Where a tile's predecessors have mostly finished, a group's pair is one more wait: 1 x 16384 x 2048 (16 channel tiles),
+// 79 and 167 us with groups, 70 and 156 without; 8 channel tiles (1 x 8192 x 1024), 29 and 60, 29 and 71 without.  Up to 32
+// tiles the two are alike (1 x 4096 x 512 forward: 17.0 and 17.1 us).
+constexpr bool scan_grouped(int ctiles, int tiles) { return ctiles <= 8 && tiles > 32; }
+
+// The links of one channel tile, from its first tile that has tokens on.
+struct ScanChain {
+  uint32_t *flags, *group_flags;
+  float *pairs, *states, *group_pairs;
+};
+template <int E> __device__ __forceinline__ ScanChain scan_chain(const ScanLink& l, int c, int tiles, int skip) {
+  const size_t first = (size_t)c * tiles + skip, g = (size_t)c * l.groups;
+  return {l.flags + first, l.group_flags + g, l.pairs + first * (128 * E), l.states + first * (64 * E),
+          l.group_pairs + g * (128 * E)};
+}
+// State in front of group k > 0: from the nearest group whose last tile knows its final state, over the groups' pairs.
+template <int E> __device__ __forceinline__ void scan_group_start(const ScanChain& c, int k, int lane, float (&h)[E]) {
+  constexpr int shift = kScanGroupLog2;
+  const int from = scan_nearest(k - 1, lane, [&](int q) {
+    if (q < 0) return 0u;
+    if (scan_flag(c.flags + ((q + 1) << shift) - 1) == 2u) return 2u;
+    return q ? scan_flag(c.group_flags + q) : 0u;
+  });
+  asm volatile("" ::: "memory");
+  get_words<E>(c.states + (size_t)(((from + 1) << shift) - 1) * (64 * E) + lane, h);
+  scan_fold<E, false>(c.group_pairs, from + 1, k, lane, h, h);
+}
+// Tile j > 0 of a chain, one wave: publishes its pair (W, H), gives the state h in front of it and in H its final one.
+// It starts from the nearest tile that knows its final state and takes the pairs behind it one after the other, as each of
+// those tiles does for its own final state: so the result is the same bit by bit wherever it starts.
+// With groups this ends at the group's first tile, and the state in front of a group comes from the groups in front of
+// it in the same way: the last tile of a group joins its pairs to one, and its final state is by definition the state in
+// front of the group taken over that.  (Group 0 has no pair: its last tile's state is taken over its tiles.)
+template <int E, bool GROUPS>
+__device__ __forceinline__ void scan_link_tile(const ScanChain& c, int j, bool more, int lane, float (&W)[E], float (&H)[E],
+                                               float (&h)[E]) {
+  constexpr int shift = GROUPS ? kScanGroupLog2 : 31;
+  float* pair = c.pairs + (size_t)j * (128 * E) + lane;
+  put_words<E>(pair, W);
+  put_words<E>(pair + 64 * E, H);
+  publish(c.flags + j, 1u);
+  const int k = j >> shift, j0 = k << shift;
+  const bool closes = GROUPS && k > 0 && more && (j + 1) >> shift > k;
+  int from = j0 - 1;
+  if (closes) {
+    while (__any(lane < j - j0 && scan_flag(c.flags + j0 + lane) == 0u)) __builtin_amdgcn_s_sleep(1);
+    asm volatile("" ::: "memory");
+    float Wg[E], Hg[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) Wg[e] = -0.f, Hg[e] = 0.f;
+    scan_fold<E, true>(c.pairs, j0, j, lane, Hg, Wg);
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      H[e] = word_step(W[e], Hg[e], H[e]);
+      W[e] = word_join(Wg[e], W[e]);
+    }
+    float* gp = c.group_pairs + (size_t)k * (128 * E) + lane;
+    put_words<E>(gp, W);
+    put_words<E>(gp + 64 * E, H);
+    publish(c.group_flags + k, 1u);
+  } else {
+    from = scan_nearest(j - 1, lane, [&](int p) { return p >= j0 ? scan_flag(c.flags + p) : k ? 2u : 0u; });
+    asm volatile("" ::: "memory");
+  }
+  if (!GROUPS || from >= j0) get_words<E>(c.states + (size_t)from * (64 * E) + lane, h);
+  else scan_group_start<E>(c, k, lane, h);
+#pragma unroll
+  for (int e = 0; e < E; ++e)
+    if (closes) H[e] = word_step(W[e], h[e], H[e]);
+  scan_fold<E, false>(c.pairs, from + 1, j, lane, h, h);
+#pragma unroll
+  for (int e = 0; e < E; ++e)
+    if (!closes) H[e] = word_step(W[e], h[e], H[e]);
 }
 
 // The tile of this workgroup: channel tile c, place j in the order of the tickets.

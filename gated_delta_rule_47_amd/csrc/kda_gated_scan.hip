@@ -89,8 +89,8 @@ int scan_e(int D, bool bf16) { return bf16 && D > 1 ? 2 : 1; }
 int scan_step_e(int D, bool bf16) { return bf16 && D % 2 == 0 ? 2 : 1; }
 
 struct ScanPlan {
-  int E, ctiles, tiles;
-  size_t every, flags, clear, pairs, states, parts, sums, total;   // words per counter; offsets and the bytes cleared
+  int E, ctiles, tiles, groups;
+  size_t every, flags, group_flags, clear, pairs, states, group_pairs, parts, sums, total;   // words per counter; offsets and the bytes cleared
 };
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
 ScanPlan scan_plan(int B, int H, int T, int D, bool bf16, bool bwd) {
@@ -103,10 +103,14 @@ ScanPlan scan_plan(int B, int H, int T, int D, bool bf16, bool bwd) {
   const size_t n = p.tiles > 1 ? (size_t)p.ctiles * p.tiles : 0;
   p.every = p.ctiles <= 4096 ? 32 : 1;
   p.flags = up(n ? p.every * p.ctiles * 4 : 0);
-  p.clear = p.flags + n * 4;
+  p.groups = scan_grouped(p.ctiles, p.tiles) ? (p.tiles >> kScanGroupLog2) + 1 : 0;
+  const size_t ng = (size_t)p.ctiles * p.groups;
+  p.group_flags = p.flags + n * 4;
+  p.clear = p.group_flags + ng * 4;
   p.pairs = up(p.clear);
   p.states = p.pairs + n * 128 * p.E * 4;
-  p.parts = p.states + n * 64 * p.E * 4;
+  p.group_pairs = p.states + n * 64 * p.E * 4;
+  p.parts = p.group_pairs + ng * 128 * p.E * 4;
   p.sums = p.parts + (bwd ? up((size_t)p.tiles * N * 8) : 0);
   p.total = p.sums + (bwd ? (size_t)H * D * 4 : 0);
   return p;
@@ -117,6 +121,8 @@ void scan_link(ScanArgs& a, const ScanPlan& p, void* workspace, hipStream_t s) {
   if (!p.clear) return;
   a.link.tickets = (uint32_t*)w, a.link.flags = (uint32_t*)(w + p.flags), a.link.every = (uint32_t)p.every;
   a.link.pairs = (float*)(w + p.pairs), a.link.states = (float*)(w + p.states);
+  a.link.group_flags = (uint32_t*)(w + p.group_flags), a.link.group_pairs = (float*)(w + p.group_pairs);
+  a.link.groups = (uint32_t)p.groups;
   const uint32_t n = (uint32_t)(p.clear / 4);
   scan_clear_kernel<<<(n + kScanThreads - 1) / kScanThreads, kScanThreads, 0, s>>>((uint32_t*)w, n);
 }

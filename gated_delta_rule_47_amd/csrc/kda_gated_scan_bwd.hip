@@ -17,9 +17,16 @@ template <int E> struct ScanShared {
   float2 qg[NW][S][E][64];                 // q and g2 of every token, each lane's own: what the last pass alone needs
 };
 
+// The most tokens of any lane's sequence, at least 1.
+__device__ __forceinline__ int scan_longest(int n) {
+#pragma unroll
+  for (int i = 1; i < 64; i *= 2) n = max(n, __shfl_xor(n, i));
+  return __builtin_amdgcn_readfirstlane(max(n, 1));
+}
+
 // FULL: every token of the tile lies inside its sequence and all channels are their lane's own, in every lane (the same for
 // all waves).
-template <typename T, int E, bool GATE, bool NORM, bool FULL, typename Off>
+template <typename T, int E, bool GATE, bool NORM, bool GROUPS, bool FULL, typename Off>
 __device__ __forceinline__ void scan_bwd_tile(const ScanArgs& a, ScanShared<E>& sh, const ScanTile tile, const ScanLane<E>& l,
                                               int lane, int w) {
   const int jt = a.tiles - 1 - tile.j;     // place in time
@@ -95,7 +102,10 @@ __device__ __forceinline__ void scan_bwd_tile(const ScanArgs& a, ScanShared<E>& 
   __syncthreads();
   float r[E];
   if (w == 0) {
-    const size_t first = (size_t)tile.c * a.tiles, rec = first + tile.j;
+    // the tiles behind every sequence, which the chain starts after
+    const int skip = GROUPS && a.lengths ? a.tiles - (scan_longest(l.n) + NW * S - 1) / (NW * S) : 0;
+    const ScanChain chain = scan_chain<E>(a.link, tile.c, a.tiles, skip);
+    const bool more = tile.j + 1 < a.tiles;
     float Wt[E], Rt[E];                    // the tile's pair
 #pragma unroll
     for (int e = 0; e < E; ++e) Wt[e] = Rt[e] = r[e] = 0.f;
@@ -112,21 +122,16 @@ __device__ __forceinline__ void scan_bwd_tile(const ScanArgs& a, ScanShared<E>& 
       if (a.d_state && l.on)
 #pragma unroll
         for (int e = 0; e < E; ++e) r[e] = a.d_state[l.ch + e];
+#pragma unroll
+      for (int e = 0; e < E; ++e) Rt[e] = word_step(Wt[e], r[e], Rt[e]);
     } else {
-      float* pair = a.link.pairs + rec * (128 * E) + lane;
-      put_words<E>(pair, Wt);
-      put_words<E>(pair + 64 * E, Rt);
-      publish(a.link.flags + rec, 1u);
-      look_back<E>(a.link, first, tile.j, lane, r);
+      scan_link_tile<E, GROUPS>(chain, tile.j - skip, more, lane, Wt, Rt, r);
     }
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      sh.in[e][lane] = r[e];
-      Rt[e] = word_step(Wt[e], r[e], Rt[e]);
-    }
-    if (tile.j + 1 < a.tiles) {
-      put_words<E>(a.link.states + rec * (64 * E) + lane, Rt);
-      publish(a.link.flags + rec, 2u);
+    for (int e = 0; e < E; ++e) sh.in[e][lane] = r[e];
+    if (more) {
+      put_words<E>(chain.states + (size_t)(tile.j - skip) * (64 * E) + lane, Rt);
+      publish(chain.flags + (tile.j - skip), 2u);
     } else {
 #pragma unroll
       for (int e = 0; e < E; ++e)
@@ -229,7 +234,7 @@ __device__ __forceinline__ void scan_bwd_zeros(const ScanArgs& a, const ScanLane
       if (l.own(e)) a.parts[(size_t)jt * a.B * a.H * a.D + l.ch + e] = a.parts[((size_t)a.tiles + jt) * a.B * a.H * a.D + l.ch + e] = 0.f;
 }
 
-template <typename T, int E, bool GATE, bool NORM, typename Off>
+template <typename T, int E, bool GATE, bool NORM, bool GROUPS, typename Off>
 __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4))) void scan_bwd_kernel(ScanArgs a) {
   __shared__ ScanShared<E> sh;
   const ScanTile tile = scan_tile(a, &sh.slot);
@@ -237,16 +242,19 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4))) vo
   const ScanLane<E> l = scan_lane<E>(a, tile.c, lane);
   const int jt = a.tiles - 1 - tile.j;
   if (jt > 0 && !__any(l.n > jt * (NW * S))) scan_bwd_zeros<T, E, GATE, Off>(a, l, jt, w);
-  else if (__all((jt + 1) * (NW * S) <= l.n && !l.last)) scan_bwd_tile<T, E, GATE, NORM, true, Off>(a, sh, tile, l, lane, w);
-  else scan_bwd_tile<T, E, GATE, NORM, false, Off>(a, sh, tile, l, lane, w);
+  else if (__all((jt + 1) * (NW * S) <= l.n && !l.last)) scan_bwd_tile<T, E, GATE, NORM, GROUPS, true, Off>(a, sh, tile, l, lane, w);
+  else scan_bwd_tile<T, E, GATE, NORM, GROUPS, false, Off>(a, sh, tile, l, lane, w);
 }
 
-template <typename T, int E, typename Off> void launch_e(const ScanArgs& a, hipStream_t s) {
+template <typename T, int E, bool GROUPS, typename Off> void launch_groups(const ScanArgs& a, hipStream_t s) {
   const unsigned grid = (unsigned)a.ctiles * (unsigned)a.tiles;
-#define KDA_SCAN(G_, N_) scan_bwd_kernel<T, E, G_, N_, Off><<<grid, NW * 64, 0, s>>>(a)
+#define KDA_SCAN(G_, N_) scan_bwd_kernel<T, E, G_, N_, GROUPS, Off><<<grid, NW * 64, 0, s>>>(a)
   if (a.i) a.normalize ? KDA_SCAN(true, true) : KDA_SCAN(true, false);
   else a.normalize ? KDA_SCAN(false, true) : KDA_SCAN(false, false);
 #undef KDA_SCAN
+}
+template <typename T, int E, typename Off> void launch_e(const ScanArgs& a, hipStream_t s) {
+  a.link.groups ? launch_groups<T, E, true, Off>(a, s) : launch_groups<T, E, false, Off>(a, s);
 }
 
 }  // namespace

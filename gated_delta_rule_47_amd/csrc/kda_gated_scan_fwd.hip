@@ -15,7 +15,7 @@ template <int E, int NW> struct ScanShared {
 
 // FULL: every token of the tile lies inside its sequence and all channels are their lane's own, in every lane (the same for
 // all waves, whose lanes are the same channels).
-template <typename T, int E, int NW, bool GATE, bool NORM, bool FULL, typename Off>
+template <typename T, int E, int NW, bool GATE, bool NORM, bool GROUPS, bool FULL, typename Off>
 __device__ __forceinline__ void scan_fwd_tile(const ScanArgs& a, ScanShared<E, NW>& sh, const ScanTile tile, const ScanLane<E>& l,
                                               int lane, int w) {
   const int t0 = (tile.j * NW + w) * S;
@@ -65,7 +65,8 @@ __device__ __forceinline__ void scan_fwd_tile(const ScanArgs& a, ScanShared<E, N
   __syncthreads();
   float h[E];
   if (w == NW - 1) {
-    const size_t first = (size_t)tile.c * a.tiles, rec = first + tile.j;
+    const ScanChain chain = scan_chain<E>(a.link, tile.c, a.tiles, 0);
+    const bool more = tile.j + 1 < a.tiles;
     float Wt[E], Ht[E];                    // the tile's pair
 #pragma unroll
     for (int e = 0; e < E; ++e) Wt[e] = Ht[e] = h[e] = 0.f;
@@ -82,21 +83,16 @@ __device__ __forceinline__ void scan_fwd_tile(const ScanArgs& a, ScanShared<E, N
       if (a.state_in)                      // (another lane's channel may have its last state there by now)
 #pragma unroll
         for (int e = 0; e < E; ++e) h[e] = FULL || l.own(e) ? a.state_in[l.ch + e] : 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) Ht[e] = word_step(Wt[e], h[e], Ht[e]);
     } else {
-      float* pair = a.link.pairs + rec * (128 * E) + lane;
-      put_words<E>(pair, Wt);
-      put_words<E>(pair + 64 * E, Ht);
-      publish(a.link.flags + rec, 1u);
-      look_back<E>(a.link, first, tile.j, lane, h);
+      scan_link_tile<E, GROUPS>(chain, tile.j, more, lane, Wt, Ht, h);
     }
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      sh.in[e][lane] = h[e];
-      Ht[e] = word_step(Wt[e], h[e], Ht[e]);
-    }
-    if (tile.j + 1 < a.tiles) {
-      put_words<E>(a.link.states + rec * (64 * E) + lane, Ht);
-      publish(a.link.flags + rec, 2u);
+    for (int e = 0; e < E; ++e) sh.in[e][lane] = h[e];
+    if (more) {
+      put_words<E>(chain.states + (size_t)tile.j * (64 * E) + lane, Ht);
+      publish(chain.flags + tile.j, 2u);
     }
   }
   __syncthreads();
@@ -128,26 +124,27 @@ __device__ __forceinline__ void scan_fwd_tile(const ScanArgs& a, ScanShared<E, N
       if (FULL || l.own(e)) a.state_out[l.ch + e] = h[e];
 }
 
-template <typename T, int E, int NW, bool GATE, bool NORM, typename Off>
+template <typename T, int E, int NW, bool GATE, bool NORM, bool GROUPS, typename Off>
 __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4))) void scan_fwd_kernel(ScanArgs a) {
   __shared__ ScanShared<E, NW> sh;
   const ScanTile tile = scan_tile(a, &sh.slot);
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const ScanLane<E> l = scan_lane<E>(a, tile.c, lane);
   if (tile.j > 0 && !__any(l.n > tile.j * (NW * S))) return;     // behind every lane's sequence, as are the tiles after it
-  if (__all((tile.j + 1) * (NW * S) <= l.n && !l.last)) scan_fwd_tile<T, E, NW, GATE, NORM, true, Off>(a, sh, tile, l, lane, w);
-  else scan_fwd_tile<T, E, NW, GATE, NORM, false, Off>(a, sh, tile, l, lane, w);
+  if (__all((tile.j + 1) * (NW * S) <= l.n && !l.last)) scan_fwd_tile<T, E, NW, GATE, NORM, GROUPS, true, Off>(a, sh, tile, l, lane, w);
+  else scan_fwd_tile<T, E, NW, GATE, NORM, GROUPS, false, Off>(a, sh, tile, l, lane, w);
 }
 
-template <typename T, int E, int NW, typename Off> void launch_nw(const ScanArgs& a, hipStream_t s) {
+template <typename T, int E, int NW, bool GROUPS, typename Off> void launch_nw(const ScanArgs& a, hipStream_t s) {
   const unsigned grid = (unsigned)a.ctiles * (unsigned)a.tiles;
-#define KDA_SCAN(G_, N_) scan_fwd_kernel<T, E, NW, G_, N_, Off><<<grid, NW * 64, 0, s>>>(a)
+#define KDA_SCAN(G_, N_) scan_fwd_kernel<T, E, NW, G_, N_, GROUPS, Off><<<grid, NW * 64, 0, s>>>(a)
   if (a.i) a.normalize ? KDA_SCAN(true, true) : KDA_SCAN(true, false);
   else a.normalize ? KDA_SCAN(false, true) : KDA_SCAN(false, false);
 #undef KDA_SCAN
 }
 template <typename T, int E, typename Off> void launch_e(const ScanArgs& a, hipStream_t s) {
-  scan_fwd_waves(a.ctiles) == 4 ? launch_nw<T, E, 4, Off>(a, s) : launch_nw<T, E, 8, Off>(a, s);
+  if (scan_fwd_waves(a.ctiles) == 4) launch_nw<T, E, 4, false, Off>(a, s);
+  else a.link.groups ? launch_nw<T, E, 8, true, Off>(a, s) : launch_nw<T, E, 8, false, Off>(a, s);
 }
 
 }  // namespace

@@ -189,6 +189,24 @@ def test_many_tiles():
     check(3, 1, 200, 6000, BF, lengths=[200, 64, 65], seed=9)
 
 
+@pytest.mark.parametrize("B,H,T,D,dtype,lengths", [
+    (1, 1, 4225, 1, FP, None), (1, 1, 9001, 5, BF, None), (1, 1, 4096 + 128, 128, BF, None), (3, 1, 5000, 64, BF, [5000, 0, 1234]),
+    (2, 2, 4200, 33, FP, [100, 4199]), (2, 1, 4300, 70, BF, [3, 257]), (1, 8, 1056, 64, FP, None), (1, 1, 1057, 1024, BF, None),
+    (4, 1, 1500, 100, FP, [1499, 1056, 1025, 31])])
+def test_long_sequences_of_few_channels(B, H, T, D, dtype, lengths):
+    """Tiles whose states are handed on by groups; bit by bit the same in every run."""
+    d, y, end, ckpt = check(B, H, T, D, dtype, lengths, seed=T, slow=D == 5)
+    lt = None if lengths is None else torch.tensor(lengths, dtype=torch.int32, device=DEV)
+    args = (d["x"], d["z"], d["A"], d["b"])
+    first = None
+    for _ in range(4):
+        got = kda.gated_scan_fwd(*args, d["s"], d["i"], lt, out=torch.full_like(y, 7.0))
+        assert torch.equal(got[0], y) and torch.equal(got[1], end)
+        r = kda.gated_scan_bwd(*args, ckpt, d["dy"], d["ds"], d["i"], lt)
+        first = first or r
+        assert all(torch.equal(r[k], first[k]) for k in r)
+
+
 def test_slow_decays_do_not_drift():
     """A gate that never moves: a decay of 1 - 2^-14 or so, 65536 tokens.  Held as one float it would be off by up to
     2^-25 2^14 of the state.  Rounding errors of either sign: per token three of e / sqrt(3) RMS over 2^14 tokens' memory
