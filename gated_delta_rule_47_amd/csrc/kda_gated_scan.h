@@ -191,12 +191,11 @@ template <int E, bool WORDS> __device__ __forceinline__ void scan_fold(const flo
 
 // Tiles of a group: 2^kScanGroupLog2, up to 64.  Few channels over a long time put hundreds of tiles to work at once, which
 // wait for joins one behind the other (0.2 us each); with groups a tile is as many joins away from a known state as there
-// are groups in front of it and tiles in its own.  1 x 32768 x 64, bf16, forward and backward: 26 and 84 us, 56 and 217
-// without; groups of 16: 26 and 79, but 1 x 8192 x 1024 66 for 60 us backward.
+// are groups in front of it and tiles in its own.  1 x 32768 x 64, bf16, forward and adjoint: 25 and 54 us, 55 and 114 without.
 constexpr int kScanGroupLog2 = 3;
 // Where a tile's predecessors have mostly finished, a group's pair is one more wait: 1 x 16384 x 2048 (16 channel tiles),
-// 79 and 167 us with groups, 70 and 156 without; 8 channel tiles (1 x 8192 x 1024), 29 and 60, 29 and 71 without.  Up to 32
-// tiles the two are alike (1 x 4096 x 512 forward: 17.0 and 17.1 us).
+// 79 and 155 us with groups, 69 and 138 without; 8 channel tiles (1 x 8192 x 1024), 28 and 52 both ways.  Up to 32 tiles the
+// two are alike (1 x 4096 x 512 forward: 17.0 us).
 constexpr bool scan_grouped(int ctiles, int tiles) { return ctiles <= 8 && tiles > 32; }
 
 // The links of one channel tile, from its first tile that has tokens on.
@@ -319,11 +318,14 @@ template <int E> __device__ __forceinline__ ScanLane<E> scan_lane(const ScanArgs
 
 // Tile shapes.  Forward: S = 16 tokens of decay and input are 64 registers at E = 2; eight waves, or four where the channel
 // tiles are many (scan_fwd_waves).  Backward: four values a token in registers and two in LDS.
-constexpr int kScanFwdTokens = 16, kScanBwdWaves = 4, kScanBwdTokens = 8;
+constexpr int kScanFwdTokens = 16, kScanBwdTokens = 8;
 // Five workgroups of four waves fit a CU and two of eight.  The smaller ones overlap better (8 x 8192 x 4096: 434 us for 460) and
 // put twice as many tiles into a channel's line, of which 256 CUs hold more at once the fewer channels there are (1 x
 // 30011 x 4096: 241 us for 222).
 constexpr int scan_fwd_waves(int ctiles) { return ctiles >= 128 ? 4 : 8; }
+// Backward, four workgroups of four waves fit a CU or two of eight, which halve a channel's line of tiles: 1 x 16384 x 4096,
+// 239 us for 264, 2 x 8 x 32768 x 64 in fp32, 268 for 333; from 64 channel tiles on the line is short enough (1 x 4096 x 8192: 126 us for 124).
+constexpr int scan_bwd_waves(int ctiles) { return ctiles >= 64 ? 4 : 8; }
 
 template <typename T> hipError_t launch_scan_fwd_tiles(const ScanArgs& a, bool pairs, hipStream_t s);
 template <typename T> hipError_t launch_scan_bwd_tiles(const ScanArgs& a, bool pairs, hipStream_t s);

@@ -24,9 +24,16 @@ __device__ __forceinline__ void scan_head_sum(const float* in, size_t stride, in
                                               float* dA_log) {
   __shared__ float red[kSumThreads / 64];
   const float* p = in + (size_t)h * D;
-  const long long n = (long long)n_parts * D;
+  const uint32_t q = kSumThreads / (uint32_t)D, r = kSumThreads % (uint32_t)D;       // rows and channels from value to value
+  uint32_t row = threadIdx.x / (uint32_t)D, col = threadIdx.x % (uint32_t)D;
   float s = 0.f;
-  for (long long i = threadIdx.x; i < n; i += kSumThreads) s += p[(size_t)(i / D) * stride + i % D];
+#pragma unroll 8
+  while (row < (uint32_t)n_parts) {
+    s += p[(size_t)row * stride + col];
+    row += q;
+    col += r;
+    if (col >= (uint32_t)D) col -= (uint32_t)D, ++row;
+  }
   s = lane_sum<64>(s);
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
   __syncthreads();
@@ -98,7 +105,7 @@ ScanPlan scan_plan(int B, int H, int T, int D, bool bf16, bool bwd) {
   const long long N = (long long)B * H * D;
   p.E = scan_e(D, bf16);
   p.ctiles = (int)(((long long)B * H * ((D + p.E - 1) / p.E) + 63) / 64);
-  const int tokens = bwd ? kScanBwdWaves * kScanBwdTokens : scan_fwd_waves(p.ctiles) * kScanFwdTokens;
+  const int tokens = bwd ? scan_bwd_waves(p.ctiles) * kScanBwdTokens : scan_fwd_waves(p.ctiles) * kScanFwdTokens;
   p.tiles = T > tokens ? (T + tokens - 1) / tokens : 1;
   const size_t n = p.tiles > 1 ? (size_t)p.ctiles * p.tiles : 0;
   p.every = p.ctiles <= 4096 ? 32 : 1;
@@ -174,8 +181,9 @@ hipError_t launch_scan_bwd(const void* x, const void* z, const float* A_log, con
   hipError_t e = launch_scan_bwd_tiles<T>(a, p.E == 2, s);
   if (e != hipSuccess || !a.parts) return e;
   const int n = H * D;
-  // up to 64 values per thread of a head's workgroup; beyond, the channels are summed over time first, by many workgroups
-  if ((long long)p.tiles * B * D <= 64 * kSumThreads) {
+  // up to 8 values per thread of a head's workgroup (2048 x 256: 21.0 us the whole adjoint, 20.7 in two launches); beyond, the
+  // channels are summed over time first, by many workgroups (2048 x 512: 21.3 us, 23.7 in one launch; 4096 x 1024: 33 and 50)
+  if ((long long)p.tiles * B * D <= 8 * kSumThreads) {
     scan_small_params_kernel<<<(n + 63) / 64 + H, kSumThreads, 0, s>>>(a.parts, (size_t)p.tiles * B * n, p.tiles * B, n, A_log, D,
                                                                        d_dt_bias, dA_log);
     return hipGetLastError();

@@ -1,6 +1,6 @@
 // Adjoint of the gated recurrence (kda_gated_scan.h has the mathematics and the way tiles are linked).  Tiles run from
 // the last token to the first; r crosses them as the state does forward.  h comes from the kept state in front of the
-// tile, one row per tile, so a tile needs its predecessors in one direction only.
+// tile, so a tile needs its predecessors in one direction only.
 #include "kda_gated_scan.h"
 
 #include "../../include/kda.h"
@@ -8,10 +8,9 @@
 namespace kda {
 namespace {
 
-constexpr int NW = kScanBwdWaves, S = kScanBwdTokens;
-static_assert(NW * S == KDA_GATED_SCAN_CHUNK, "one kept state per tile");
+constexpr int S = kScanBwdTokens;
 
-template <int E> struct ScanShared {
+template <int E, int NW> struct ScanShared {
   uint32_t slot;
   float G[NW][E][64], H[NW][E][64], R[NW][E][64], in[E][64];     // sums of g2, states and r from zero
   float2 qg[NW][S][E][64];                 // q and g2 of every token, each lane's own: what the last pass alone needs
@@ -26,8 +25,8 @@ __device__ __forceinline__ int scan_longest(int n) {
 
 // FULL: every token of the tile lies inside its sequence and all channels are their lane's own, in every lane (the same for
 // all waves).
-template <typename T, int E, bool GATE, bool NORM, bool GROUPS, bool FULL, typename Off>
-__device__ __forceinline__ void scan_bwd_tile(const ScanArgs& a, ScanShared<E>& sh, const ScanTile tile, const ScanLane<E>& l,
+template <typename T, int E, int NW, bool GATE, bool NORM, bool GROUPS, bool FULL, typename Off>
+__device__ __forceinline__ void scan_bwd_tile(const ScanArgs& a, ScanShared<E, NW>& sh, const ScanTile tile, const ScanLane<E>& l,
                                               int lane, int w) {
   const int jt = a.tiles - 1 - tile.j;     // place in time
   const int t0 = (jt * NW + w) * S;
@@ -45,9 +44,12 @@ __device__ __forceinline__ void scan_bwd_tile(const ScanArgs& a, ScanShared<E>& 
       rd[k].load(a.dy, base + k * row);
     }
   }
+  static_assert(NW * S % KDA_GATED_SCAN_CHUNK == 0, "a kept state stands in front of a tile");
+  constexpr int per = NW * S / KDA_GATED_SCAN_CHUNK;
+  const int chunks = (a.T + KDA_GATED_SCAN_CHUNK - 1) / KDA_GATED_SCAN_CHUNK;
   float h[E];
 #pragma unroll
-  for (int e = 0; e < E; ++e) h[e] = FULL || jt * NW * S < l.n ? a.ckpt[((size_t)l.bh * a.tiles + jt) * a.D + l.d + e] : 0.f;
+  for (int e = 0; e < E; ++e) h[e] = FULL || jt * NW * S < l.n ? a.ckpt[((size_t)l.bh * chunks + jt * per) * a.D + l.d + e] : 0.f;
 
   const float m = l.m();
   float bias2[E];
@@ -216,7 +218,7 @@ __device__ __forceinline__ void scan_bwd_tile(const ScanArgs& a, ScanShared<E>& 
 }
 
 // A tile behind every lane's sequence: its gradients are zeros.  No other tile waits for it.
-template <typename T, int E, bool GATE, typename Off>
+template <typename T, int E, int NW, bool GATE, typename Off>
 __device__ __forceinline__ void scan_bwd_zeros(const ScanArgs& a, const ScanLane<E>& l, int jt, int w) {
   const float zero[E] = {};
   if (!l.on) return;
@@ -234,27 +236,28 @@ __device__ __forceinline__ void scan_bwd_zeros(const ScanArgs& a, const ScanLane
       if (l.own(e)) a.parts[(size_t)jt * a.B * a.H * a.D + l.ch + e] = a.parts[((size_t)a.tiles + jt) * a.B * a.H * a.D + l.ch + e] = 0.f;
 }
 
-template <typename T, int E, bool GATE, bool NORM, bool GROUPS, typename Off>
+template <typename T, int E, int NW, bool GATE, bool NORM, bool GROUPS, typename Off>
 __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4))) void scan_bwd_kernel(ScanArgs a) {
-  __shared__ ScanShared<E> sh;
+  __shared__ ScanShared<E, NW> sh;
   const ScanTile tile = scan_tile(a, &sh.slot);
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const ScanLane<E> l = scan_lane<E>(a, tile.c, lane);
   const int jt = a.tiles - 1 - tile.j;
-  if (jt > 0 && !__any(l.n > jt * (NW * S))) scan_bwd_zeros<T, E, GATE, Off>(a, l, jt, w);
-  else if (__all((jt + 1) * (NW * S) <= l.n && !l.last)) scan_bwd_tile<T, E, GATE, NORM, GROUPS, true, Off>(a, sh, tile, l, lane, w);
-  else scan_bwd_tile<T, E, GATE, NORM, GROUPS, false, Off>(a, sh, tile, l, lane, w);
+  if (jt > 0 && !__any(l.n > jt * (NW * S))) scan_bwd_zeros<T, E, NW, GATE, Off>(a, l, jt, w);
+  else if (__all((jt + 1) * (NW * S) <= l.n && !l.last)) scan_bwd_tile<T, E, NW, GATE, NORM, GROUPS, true, Off>(a, sh, tile, l, lane, w);
+  else scan_bwd_tile<T, E, NW, GATE, NORM, GROUPS, false, Off>(a, sh, tile, l, lane, w);
 }
 
-template <typename T, int E, bool GROUPS, typename Off> void launch_groups(const ScanArgs& a, hipStream_t s) {
+template <typename T, int E, int NW, bool GROUPS, typename Off> void launch_nw(const ScanArgs& a, hipStream_t s) {
   const unsigned grid = (unsigned)a.ctiles * (unsigned)a.tiles;
-#define KDA_SCAN(G_, N_) scan_bwd_kernel<T, E, G_, N_, GROUPS, Off><<<grid, NW * 64, 0, s>>>(a)
+#define KDA_SCAN(G_, N_) scan_bwd_kernel<T, E, NW, G_, N_, GROUPS, Off><<<grid, NW * 64, 0, s>>>(a)
   if (a.i) a.normalize ? KDA_SCAN(true, true) : KDA_SCAN(true, false);
   else a.normalize ? KDA_SCAN(false, true) : KDA_SCAN(false, false);
 #undef KDA_SCAN
 }
 template <typename T, int E, typename Off> void launch_e(const ScanArgs& a, hipStream_t s) {
-  a.link.groups ? launch_groups<T, E, true, Off>(a, s) : launch_groups<T, E, false, Off>(a, s);
+  if (scan_bwd_waves(a.ctiles) == 4) launch_nw<T, E, 4, false, Off>(a, s);
+  else a.link.groups ? launch_nw<T, E, 8, true, Off>(a, s) : launch_nw<T, E, 8, false, Off>(a, s);
 }
 
 }  // namespace
