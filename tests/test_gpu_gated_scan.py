@@ -460,3 +460,26 @@ def test_offsets_past_32_bits():
     r1 = kda.gated_scan_bwd(last(x), last(z), A[:1], b[:1], c1, last(dy))
     assert tol(last(r["dx"]), r1["dx"]) and tol(last(r["dz"]), r1["dz"]) and not r["dx"][0, 0].any()
     assert np.abs(host(r["ddt_bias"][-1]) - host(r1["ddt_bias"][0])).max() <= 1e-4 * np.abs(host(r1["ddt_bias"])).max()
+
+
+def test_offsets_past_32_bits_by_groups():
+    """The same for few channels, whose tiles hand their states on by groups."""
+    B, H, T, D = 1, 1, 4200000, 512
+    x = torch.zeros((B, H, T, D), dtype=BF, device=DEV)
+    assert x.numel() > 2 ** 31
+    z = torch.zeros_like(x)
+    n = 600
+    x[:, :, -n:].normal_()
+    z[:, :, -n:].normal_()
+    A, b = torch.zeros(H, device=DEV), torch.full((H, D), -1.0, device=DEV)
+    y, end, ckpt = kda.gated_scan_fwd(x, z, A, b, input_gate=z, want_ckpt=True)
+    last = lambda t: t[:, :, -n:].contiguous()
+    y1, end1, c1 = kda.gated_scan_fwd(last(x), last(z), A, b, input_gate=last(z), want_ckpt=True)
+    tol = lambda a, r: np.linalg.norm(host(a) - host(r)) <= 2.0 ** -9 * np.linalg.norm(host(r))
+    assert tol(last(y), y1) and tol(end, end1) and not y[:, :, :-n].any()
+    dy = y.zero_()
+    dy[:, :, -n:].normal_()
+    r = kda.gated_scan_bwd(x, z, A, b, ckpt, dy, input_gate=z)
+    r1 = kda.gated_scan_bwd(last(x), last(z), A, b, c1, last(dy), input_gate=last(z))
+    assert all(tol(last(r[k]), r1[k]) for k in ("dx", "dz", "dinput_gate")) and not r["dz"][:, :, :-n].any()
+    assert np.abs(host(r["ddt_bias"]) - host(r1["ddt_bias"])).max() <= 1e-4 * np.abs(host(r1["ddt_bias"])).max()
