@@ -327,7 +327,8 @@ int kda_rope_frequencies(double* freqs, double* rope_scale, int R, double base, 
   // the pair (not a whole number) that turns `turns` times over the trained length
   const auto pair_of = [=](double turns) { return R * log(trained_length / (turns * 2 * M_PI)) / (2 * log(base)); };
   const double lo = scaling == KDA_ROPE_PARTS ? fmax(floor(pair_of(fast_turns)), 0) : 0;
-  const double hi = scaling == KDA_ROPE_PARTS ? fmin(ceil(pair_of(slow_turns)), n - 1) : 0;
+  // (the first pair behind the ramp may stand behind the table, whose last pair is n - 1: a cut there would steepen the ramp)
+  const double hi = scaling == KDA_ROPE_PARTS ? fmin(ceil(pair_of(slow_turns)), R - 1) : 0;
   for (int p = 0; p < n; ++p) {
     double f = pow(base, -2.0 * p / R);
     if (scaling == KDA_ROPE_LINEAR) f /= factor;

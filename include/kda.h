@@ -488,7 +488,8 @@ int kda_qk_norm_rope_bwd(const void* q, long long q_batch, long long q_token, lo
  *   KDA_ROPE_BASE    base * factor^(R / (R - 2)) in place of base (the slowest pair slowed by factor, the fastest left; R > 2)
  *   KDA_ROPE_PARTS   pairs that turn more than fast_turns times over trained_length tokens are left, those below slow_turns are
  *                    slowed by factor, with a linear share of both between (over the pair's index, from the last whole
- *                    pair in front to the first behind); rope_scale = 0.1 ln(factor) + 1
+ *                    pair in front, pair 0 at least, to the first behind, also where that stands behind the table; R - 1 at
+ *                    most); rope_scale = 0.1 ln(factor) + 1
  * rope_scale is 1 otherwise.  R even and > 0, base > 1, factor >= 1, trained_length > 0, fast_turns > slow_turns > 0
  * (KDA_ERR_SHAPE; the last three only matter to KDA_ROPE_PARTS). */
 typedef enum { KDA_ROPE_PLAIN = 0, KDA_ROPE_LINEAR = 1, KDA_ROPE_BASE = 2, KDA_ROPE_PARTS = 3 } kda_rope_scaling;

@@ -79,7 +79,7 @@ def rope_frequencies(R, base=10000.0, scaling=None, factor=1.0, trained=4096.0, 
         if scaling == "parts":
             # the pair that turns n times: base^(-2 p / R) trained = 2 pi n
             first = max(np.floor(R / 2.0 * np.log(trained / (2 * np.pi * fast)) / np.log(base)), 0.0)
-            last = min(np.ceil(R / 2.0 * np.log(trained / (2 * np.pi * slow)) / np.log(base)), R // 2 - 1.0)
+            last = min(np.ceil(R / 2.0 * np.log(trained / (2 * np.pi * slow)) / np.log(base)), R - 1.0)
             share = min(max((p - first) / max(last - first, 1e-3), 0.0), 1.0)
             f = (1 - share) * f + share * f / factor
         out.append(f)

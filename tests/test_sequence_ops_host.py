@@ -264,3 +264,28 @@ def test_sizes_of_more_than_32_bits():
         with pytest.raises(kda.KdaError) as err:
             call()
         assert err.value.status == SHAPE
+
+
+@pytest.mark.parametrize("R_,base,trained,factor", [(128, 1e4, 65536, 8.0), (128, 1e4, 131072, 8.0), (128, 1e4, 262144, 8.0), (64, 1e4, 1 << 20, 40.0),
+                                                    (8, 500.0, 32768, 4.0), (2, 1e4, 4096, 8.0), (96, 5e5, 8192, 16.0)])
+def test_rotation_by_parts_in_turns(R_, base, trained, factor):
+    """The rule as it is stated: pairs of more than fast_turns turns over the trained length are left, only those below
+    slow_turns take the whole factor, and between the last whole pair in front of the ramp and the first behind it, which may
+    stand behind the table, the share grows by the same step from pair to pair."""
+    fast, slow = 32.0, 1.0
+    f = kda.rope_frequencies(R_, base, "parts", factor, trained, fast, slow)[0].numpy()
+    turns = lambda p: base ** (-2.0 * p / R_) * trained / (2 * np.pi)
+    first = max(p for p in range(R_) if turns(p) >= fast)
+    behind = min(p for p in range(R_) if turns(p) <= slow)
+    assert first >= 0 and behind < R_ - 1 or R_ == 2
+    for p in range(R_ // 2):
+        slowed = turns(p) * 2 * np.pi / trained / f[p]
+        share = min(max((p - first) / (behind - first), 0.0), 1.0)
+        # 1 - share (1 - 1 / factor): a few roundings of 2^-53 times the exponent's logarithm, as above
+        assert abs(1 / slowed - (1 - share * (1 - 1 / factor))) <= 1e-13, p
+        if turns(p) >= fast:
+            assert abs(slowed - 1) <= 1e-13, p
+        if turns(p) > slow:
+            assert slowed < factor * (1 - 1e-6), p
+    rf, _ = R.rope_frequencies(R_, base, "parts", factor, trained)
+    assert np.allclose(f, rf, rtol=1e-13, atol=0)
