@@ -36,10 +36,13 @@ __device__ __forceinline__ float scan_sigmoid(float x) { return fast_rcp(1.0f + 
 
 // log2(1 + 2^x2) for every x2 >= 0 or below: with y = 2^-|x2| and u = fl(1 + y), log2(1 + y) = log2(u) + (y - (u - 1)) / u
 // log2(e) + ..., and the correction only matters where u is next to 1 (y itself where u rounds to 1).
-__device__ __forceinline__ float scan_softplus2(float x2, float& y) {
+// FINITE holds it at 1e20, where any multiplier (e^-10 to e^20) gives a decay of 0 and a finite g2: in the multiplier's gradient
+// dg g2 is then 0, as the limit is, not 0 times infinity (a NaN stays one through y).  The adjoint alone needs that; the
+// forward pass gives the same bits without it, and took 1 % longer with it (1 x 30011 x 4096).
+template <bool FINITE = false> __device__ __forceinline__ float scan_softplus2(float x2, float& y) {
   y = fast_exp2(-fabsf(x2));
   const float u = 1.0f + y;
-  return fmaf(y - (u - 1.0f), kLog2e, fast_log2(u)) + fmaxf(x2, 0.f);
+  return fmaf(y - (u - 1.0f), kLog2e, fast_log2(u)) + (FINITE ? __builtin_amdgcn_fmed3f(x2, 0.f, 1e20f) : fmaxf(x2, 0.f));
 }
 
 // A token's decay e^g, g = g2 ln 2 <= 0, is held as e = e^g - 1.  A decay next to 1 rounded to fp32 would be off to the same

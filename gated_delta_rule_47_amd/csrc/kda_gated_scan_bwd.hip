@@ -65,7 +65,7 @@ __device__ __forceinline__ void scan_bwd_tile(const ScanArgs& a, ScanShared<E, N
     for (int e = 0; e < E; ++e) {
       float y;
       const float p = FULL || t0 + k < l.n ? fmaf(rz[k].at(e), kLog2e, bias2[e]) : kNoDecay;
-      const float g = -m * scan_softplus2(p, y);
+      const float g = -m * scan_softplus2<true>(p, y);
       sh.qg[w][k][e][lane] = float2{m * fast_rcp(1.f + y) * (p >= 0.f ? 1.f : y), g};
       v[k][e] = decay_of(g);
       const float s = GATE ? scan_sigmoid(ri[k].at(e)) : 1.f, x = rx[k].at(e);

@@ -541,7 +541,8 @@ size_t kda_gated_scan_bwd_workspace_bytes(int B, int H, int T, int D, int dtype)
  *             dt_bias is NULL); NULL = not computed.  Fixed order of the sums.
  *   d_state_out (B,H,D) f32 or NULL (= 0);  d_state_in (B,H,D) f32
  * d_input_gate is written exactly when input_gate is given (both or neither: KDA_ERR_NULL).  Where a decay is exactly 1, n = 0
- * and the term with a^2 / n counts as its limit in dz, 0. */
+ * and the term with a^2 / n counts as its limit in dz, 0; where a decay is 0, also one whose g passes fp32 (z of infinity or the
+ * type's largest value: the state is dropped), dg g counts as its limit in dA_log, 0. */
 int kda_gated_scan_bwd(const void* x, const void* z, const float* A_log, const float* dt_bias, const void* input_gate,
                        const int* lengths, int normalize, const float* ckpt, const void* dy, const float* d_state_out,
                        void* dx, void* dz, void* d_input_gate, float* dA_log, float* d_dt_bias, float* d_state_in,

@@ -1,0 +1,52 @@
+"""Gated linear recurrence on the GPU at the ends of its gates, element by element against float64 (the limits are those of
+test_gpu_gated_scan)."""
+import pytest
+import torch
+
+import gated_delta_rule_47_amd as kda
+
+from gpu_helpers import DEV
+from test_gpu_gated_scan import BF, FP, check, inputs
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("normalize", [True, False])
+def test_a_state_dropped_whole_leaves_the_multiplier_s_gradient(normalize, dtype):
+    """A gate so open that its g passes fp32 (z of infinity or the type's largest value: drop the state here): dg g has the
+    limit 0 there, whatever else the head holds, and every gradient is what the largest gate that fp32 holds gives."""
+    B, H, T, D = 2, 2, 150, 10
+    most = torch.finfo(dtype).max
+    d = inputs(B, H, T, D, dtype, 21)
+    # 1e4: a = 0 in float64 too, and nothing overflows anywhere: the definition in float64 has a number there
+    near = {**d, "z": d["z"].clone()}
+    places = ((0, 0, 17, 3), (0, 1, 0, 0), (1, 0, 149, 9), (1, 1, 64, 4), (0, 0, 63, 5))
+    for p in places:
+        near["z"][p] = 1e4
+    check(B, H, T, D, dtype, d=near, normalize=normalize)
+    call = lambda d: kda.gated_scan_fwd(d["x"], d["z"], d["A"], d["b"], d["s"], d["i"], normalize=normalize, want_ckpt=True)
+    back = lambda d, c: kda.gated_scan_bwd(d["x"], d["z"], d["A"], d["b"], c, d["dy"], d["ds"], d["i"], normalize=normalize)
+    y0, e0, c0 = call(near)
+    g0 = back(near, c0)
+    for value in (most, float("inf")):
+        far = {**near, "z": near["z"].clone()}
+        for p in places:
+            far["z"][p] = value
+        y, e, c = call(far)
+        assert torch.equal(y, y0) and torch.equal(e, e0), value
+        g = back(far, c)
+        for name in g0:
+            assert torch.isfinite(g[name]).all(), (name, value)
+            assert torch.equal(g[name], g0[name]), (name, value)
+    # A multiplier at its clamp's end takes a finite z past fp32 as well
+    d["A"] = torch.tensor([19.9, 0.0], device=DEV)
+    d["z"][0, 0, 20, 1] = 1e30
+    y, e, c = call(d)
+    g = back(d, c)
+    assert all(torch.isfinite(t).all() for t in (y, e, *g.values()))
+    # a NaN among the gates still reaches its channel's parameters
+    d["z"][1, 1, 3, 2] = float("nan")
+    g = back(d, call(d)[2])
+    assert torch.isnan(g["dA_log"][1]) and torch.isfinite(g["dA_log"][0])
+    assert torch.isnan(g["ddt_bias"][1, 2]) and torch.isnan(g["ddt_bias"]).sum() == 1
