@@ -73,8 +73,9 @@ __device__ __forceinline__ void scan_bwd_tile(const ScanArgs& a, ScanShared<E, N
       c[k][e] = s;
       k4[k][e] = 0.f;
       if constexpr (NORM) {
-        // n = 0 (a decay of exactly 1): 1 / n is held at 1e18, and q = 0 or tiny takes the term to its limit 0 in dz
-        const float n2 = decay_n2(v[k][e]), rn = __builtin_amdgcn_rsqf(fmaxf(n2, 1e-36f)), av = 1.f + v[k][e];
+        // n = 0 (a decay of exactly 1, or so near it that n^2 is below the normal numbers): the term with 1 / n counts as its
+        // limit in dz, 0
+        const float n2 = decay_n2(v[k][e]), rn = n2 < 0x1p-126f ? 0.f : __builtin_amdgcn_rsqf(n2), av = 1.f + v[k][e];
         c[k][e] = s * (n2 * rn);
         k4[k][e] = av * av * rn * (s * x);
       }

@@ -15,7 +15,7 @@ pytestmark = pytest.mark.gpu
 @pytest.mark.parametrize("normalize", [True, False])
 def test_a_state_dropped_whole_leaves_the_multiplier_s_gradient(normalize, dtype):
     """A gate so open that its g passes fp32 (z of infinity or the type's largest value: drop the state here): dg g has the
-    limit 0 there, whatever else the head holds, and every gradient is what the largest gate that fp32 holds gives."""
+    limit 0 there, whatever else the head holds, and every gradient is what a gate of 1e4 gives, bit by bit."""
     B, H, T, D = 2, 2, 150, 10
     most = torch.finfo(dtype).max
     d = inputs(B, H, T, D, dtype, 21)
@@ -50,3 +50,29 @@ def test_a_state_dropped_whole_leaves_the_multiplier_s_gradient(normalize, dtype
     g = back(d, call(d)[2])
     assert torch.isnan(g["dA_log"][1]) and torch.isfinite(g["dA_log"][0])
     assert torch.isnan(g["ddt_bias"][1, 2]) and torch.isnan(g["ddt_bias"]).sum() == 1
+
+
+def test_input_scales_next_to_nothing():
+    """Decays so close to 1 that 1 - a^2 is 1e-36 and less: n is its root in the adjoint as it is in the forward pass (from
+    z' = -87.3 on, e^z' is below fp32's normal numbers and counts as 0)."""
+    T, D = 40, 16
+    d = inputs(1, 1, T, D, FP, 22, bias=False)
+    d["z"] = torch.linspace(-87.0, -81.0, D, device=DEV).expand(1, 1, T, D).contiguous()
+    d["A"] = torch.zeros(1, device=DEV)
+    check(1, 1, T, D, FP, d=d)
+    # the least multiplier: 1 - a^2 below fp32's normal numbers, where n and all that it scales is at most 2^-63 and may be 0
+    d["A"] = torch.full((1,), -10.0, device=DEV)
+    call = kda.gated_scan_fwd(d["x"], d["z"], d["A"], None, d["s"], d["i"], want_ckpt=True)
+    g = kda.gated_scan_bwd(d["x"], d["z"], d["A"], None, call[2], d["dy"], d["ds"], d["i"])
+    r = float((d["dy"].abs().sum(2) + d["ds"].abs()).max()) * float(d["x"].abs().max() + 1)
+    assert torch.equal(call[0], d["s"].unsqueeze(2).expand_as(call[0]))
+    assert all(torch.isfinite(g[n]).all() for n in g)
+    n = 2.0 ** -63                                                 # (sqrt(2 e^-91) = 2^-65 is the largest)
+    assert g["dx"].abs().max() <= n * r and g["dinput_gate"].abs().max() <= n * r
+    # a decay of exactly 1: the term with 1 / n counts as its limit, 0, for inputs of any size
+    d["z"] = torch.full_like(d["z"], -200.0)
+    d["x"][0, 0, :, 0] = 1e30
+    call = kda.gated_scan_fwd(d["x"], d["z"], d["A"], None, d["s"], d["i"], want_ckpt=True)
+    g = kda.gated_scan_bwd(d["x"], d["z"], d["A"], None, call[2], d["dy"], d["ds"], d["i"])
+    assert all(torch.isfinite(g[n]).all() for n in g)
+    assert not (g["dx"].any() or g["dz"].any() or g["dA_log"].any() or g["dinput_gate"].any())
