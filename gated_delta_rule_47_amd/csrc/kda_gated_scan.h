@@ -149,21 +149,36 @@ __device__ __forceinline__ void publish(uint32_t* flag, uint32_t value) {
   if ((threadIdx.x & 63) == 0) __hip_atomic_store(flag, value, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// The nearest place p <= at with flag(p) = 2 where all places behind it have theirs (1 or 2); one wave.  A place without
+// The flags of 64 places, from place `at` (bit 0) towards the first: which have one (1 or 2), which have 2.
+struct ScanFlags {
+  unsigned long long any, final;
+};
+// The nearest place p <= last with flag 2 where all places behind it have theirs (1 or 2).  A place without
 // one belongs to a workgroup that runs and will publish; nearer places may have finished since, so it starts again.
-template <typename Flag> __device__ __forceinline__ int scan_nearest(int last, int lane, Flag flag) {
+// (Without a GPU in it: read(at) gives the flags of a window, pause() waits a little.)
+template <typename Read, typename Pause> __host__ __device__ __forceinline__ int scan_look_back(int last, Read read, Pause pause) {
   for (int at = last;;) {                  // the newest place of a window of 64
-    const uint32_t f = flag(at - lane);
-    const unsigned long long none = ~__ballot(f >= 1u), final = __ballot(f == 2u);
-    const int ready = none ? __builtin_ctzll(none) : 64, stop = final ? __builtin_ctzll(final) : 64;
+    const ScanFlags f = read(at);
+    const unsigned long long none = ~f.any;
+    const int ready = none ? __builtin_ctzll(none) : 64, stop = f.final ? __builtin_ctzll(f.final) : 64;
     if (stop < ready) return at - stop;
     if (ready == 64) {
       at -= 64;
     } else {
       at = last;
-      __builtin_amdgcn_s_sleep(1);
+      pause();
     }
   }
+}
+// The same over flag(p), by one wave.
+template <typename Flag> __device__ __forceinline__ int scan_nearest(int last, int lane, Flag flag) {
+  return scan_look_back(
+      last,
+      [&](int at) {
+        const uint32_t f = flag(at - lane);
+        return ScanFlags{__ballot(f >= 1u), __ballot(f == 2u)};
+      },
+      [] { __builtin_amdgcn_s_sleep(1); });
 }
 __device__ __forceinline__ uint32_t scan_flag(const uint32_t* p) {
   return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);

@@ -76,3 +76,28 @@ def test_input_scales_next_to_nothing():
     g = kda.gated_scan_bwd(d["x"], d["z"], d["A"], None, call[2], d["dy"], d["ds"], d["i"])
     assert all(torch.isfinite(g[n]).all() for n in g)
     assert not (g["dx"].any() or g["dz"].any() or g["dA_log"].any() or g["dinput_gate"].any())
+
+
+@pytest.mark.parametrize("B,H,T,D,dtype,lengths,backward", [
+    # 10 channel tiles: 71 tiles forward and 141 in the adjoint, one line
+    (1, 1, 9000, 1200, BF, None, True), (2, 1, 9000, 640, BF, [9000, 4321], True),
+    # 66 channel tiles, the adjoint's tiles of four waves: 75
+    (1, 6, 2400, 700, FP, None, True),
+    # 130 channel tiles, the forward pass's too: 66
+    (1, 1, 4200, 8300, FP, None, False),
+    # by groups: 547 tiles in 69 of them forward, 1094 in 137 in the adjoint
+    (1, 1, 70000, 4, FP, None, True), (2, 1, 70000, 3, BF, [70000, 69000], True)])
+def test_lines_of_more_than_64_tiles(B, H, T, D, dtype, lengths, backward):
+    """Every token with its inputs and decays that remember tens of tiles, so that a pair left out or taken twice anywhere in a
+    line shows; bit by bit the same when it runs again, where other tiles have finished."""
+    d, y, end, ckpt = check(B, H, T, D, dtype, lengths, seed=T + D, slow=True, backward=backward)
+    lt = None if lengths is None else torch.tensor(lengths, dtype=torch.int32, device=DEV)
+    args = (d["x"], d["z"], d["A"], d["b"])
+    first = None
+    for _ in range(3):
+        got = kda.gated_scan_fwd(*args, d["s"], d["i"], lt, out=torch.full_like(y, 7.0))
+        assert torch.equal(got[0], y) and torch.equal(got[1], end)
+        if backward:
+            r = kda.gated_scan_bwd(*args, ckpt, d["dy"], d["ds"], d["i"], lt)
+            first = first or r
+            assert all(torch.equal(r[k], first[k]) for k in r)
