@@ -182,7 +182,8 @@ hipError_t launch_scan_bwd(const void* x, const void* z, const float* A_log, con
   if (e != hipSuccess || !a.parts) return e;
   const int n = H * D;
   // up to 8 values per thread of a head's workgroup (2048 x 256: 21.0 us the whole adjoint, 20.7 in two launches); beyond, the
-  // channels are summed over time first, by many workgroups (2048 x 512: 21.3 us, 23.7 in one launch; 4096 x 1024: 33 and 50)
+  // channels are summed over time first, by many workgroups (2048 x 512: 21.3 us, 23.7 in one launch; 4096 x 1024: 33 and 50).
+  // Few channels of many sequences leave all parts to two workgroups: 16 x 32768 x 8, bf16, 27 us of the step's 102.
   if ((long long)p.tiles * B * D <= 8 * kSumThreads) {
     scan_small_params_kernel<<<(n + 63) / 64 + H, kSumThreads, 0, s>>>(a.parts, (size_t)p.tiles * B * n, p.tiles * B, n, A_log, D,
                                                                        d_dt_bias, dA_log);

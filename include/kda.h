@@ -451,7 +451,8 @@ int kda_short_conv_bwd(const void* x, long long x_batch, long long x_token, cons
  *             0;  eps >= 0 and rope_scale finite;  outputs within 2^48 elements (KDA_ERR_SHAPE otherwise).  Pointers need the
  *             alignment of an element only.
  * The angle is formed and reduced in float64 (right to 2^-50 of itself), everything else in fp32 with one rounding to
- * `dtype`.  A row of zeros with eps = 0 gives NaN, as the formula does; a non-finite value reaches its own row only.
+ * `dtype`.  A row of zeros with eps = 0 gives NaN, as the formula does; a row whose sum of squares passes fp32 (values beyond
+ * 2^60 or so) gives zeros; a non-finite value reaches its own row only.
  * Outputs must not overlap inputs or each other. */
 typedef enum { KDA_QK_NONE = 0, KDA_QK_RMS = 1, KDA_QK_L2 = 2 } kda_qk_norm;
 
@@ -509,7 +510,8 @@ int kda_rope_frequencies(double* freqs, double* rope_scale, int R, double base, 
  *   B, H, D >= 1;  T >= 0;  T <= 2^28;  B * H <= 2^20;  B * H * D <= 2^26;  ceil(B * H * D / 64) * ceil(T / 32) <= 2^23
  *             (KDA_ERR_SHAPE; 2^34 elements of many channels).  Pointers need the alignment of an element only.
  * Gates, states and sums are fp32.  A decay is held as its distance from 1: slow ones do not drift over long sequences, and
- * what a strong one leaves of a state is right to 2^-24 of the state before it.  A non-finite value reaches its own channel only, from its token on. */
+ * what a strong one leaves of a state is right to 2^-24 of the state before it.  A non-finite value reaches its own channel only, from its token on.
+ * No output may overlap an input, another output or the workspace (state_out may be state_in; the single token's state is its own). */
 
 /* Tokens between the states that the forward pass keeps for the backward pass. */
 #define KDA_GATED_SCAN_CHUNK 32
